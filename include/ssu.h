@@ -443,6 +443,141 @@ ssu_status ssu_shadow_refresh(const void *state, int32_t state_dtype, int64_t ro
                               int32_t format, void *shadow, float *scale, void *stream);
 
 /*
+ * Linear attention with a decay for each head, on the slot pool.  For every
+ * token t of a sequence and head h of key/value head g = h / (heads /
+ * kv_heads), S the head's state [dim, dstate]:
+ *     S_t   = exp(log_decay[h]) S_{t-1} + v[t,g,:] k[t,g,:]^T
+ *     out_t = scale S_t q[t,h,:]
+ * The pool is the one of the update entry points: [slots, heads, dim,
+ * dstate], any ssu_dtype, slots read and written through the same kind of
+ * tables (ssu_batch_copy moves them).  S is carried in fp32 and rounded once,
+ * to nearest even, into the pool's type; out is computed in fp32 and rounded
+ * into the io type.
+ *
+ * q, k, v and out may be slices of larger tensors: `*_stride` holds the token
+ * and head strides in elements (not negative); the innermost stride is one.
+ * dim and dstate are multiples of 8 in [8, 128] (others return
+ * SSU_ERR_UNSUPPORTED).  log_decay must not be positive (-inf: no memory).
+ */
+typedef struct ssu_linattn_args {
+    int64_t slots, heads, kv_heads, dim, dstate;
+    int64_t rows;                 /* tokens of all sequences; the step has one per sequence   */
+    int32_t io_dtype;             /* ssu_dtype of q, k, v, out                                */
+    int32_t state_dtype;          /* ssu_dtype of the pool                                    */
+    float scale;
+    int32_t reserved0;            /* must be 0                                                */
+    int64_t pad_slot_id;          /* slot id that reads as a zero state and is never written  */
+    void *state;                  /* device [slots, heads, dim, dstate], contiguous, 16-byte aligned */
+    const void *q;                /* device [rows, heads, dstate]                             */
+    const void *k;                /* device [rows, kv_heads, dstate]                          */
+    const void *v;                /* device [rows, kv_heads, dim]                             */
+    const float *log_decay;       /* device [heads]                                           */
+    void *out;                    /* device [rows, heads, dim], output                        */
+    int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+    int32_t *d_status;            /* device int32 or NULL; SSU_DEV_* bits are ORed in         */
+} ssu_linattn_args;
+
+/*
+ * One token per sequence: sequence b is row b, io any ssu_dtype.  The read and
+ * dst tables are those of ssu_update_onetoken, and so are the pad slot and
+ * what a bad entry or slot does.  One kernel launch; rows == 0 launches
+ * nothing.
+ */
+ssu_status ssu_linear_attention_step(const ssu_linattn_args *args, const ssu_slot_table *read,
+                                     const ssu_slot_table *dst, void *stream);
+
+/*
+ * Packed prompts: sequence b holds the rows cu_seqlens[b] .. cu_seqlens[b+1]
+ * (device [nseq + 1], ssu_itype meta_type), starts from the slot at entry
+ * (b, 0) of `read` (pad: from zeros) and leaves its final state in the slot at
+ * entry (b, 0) of `dst` (without `dst`: of `read`; pad: nowhere).  An empty
+ * sequence passes its state on.  io fp16 or bf16; q, k, v and out 16-byte
+ * aligned with strides that are multiples of 8.  Decreasing, negative or too
+ * large cu_seqlens set SSU_DEV_BAD_SEQLEN; such a sequence, and one whose
+ * entry or slot is bad, is skipped: none of its rows and states is written.
+ *
+ * `max_seqlen` is the longest sequence's length if the caller knows it, 0 if
+ * not.  It steers how the work is split over the GPU and never the
+ * result's validity.  `workspace` is caller-owned device memory of at least
+ * ssu_linear_attention_workspace_size() bytes for the same sizes, 256-byte
+ * aligned (NULL where that is 0); its contents need no initialisation.
+ */
+ssu_status ssu_linear_attention_workspace_size(const ssu_linattn_args *args, int64_t nseq, int64_t max_seqlen,
+                                               uint64_t *bytes);
+ssu_status ssu_linear_attention_prefill(const ssu_linattn_args *args, int64_t nseq, const void *cu_seqlens,
+                                        int32_t meta_type, int64_t max_seqlen, const ssu_slot_table *read,
+                                        const ssu_slot_table *dst, void *workspace, uint64_t workspace_bytes,
+                                        void *stream);
+
+/*
+ * RMS norm of `rows` rows of `hidden` columns, with the residual's addition
+ * before it and the output in x's type or in E4M3 codes with scales.  Per row:
+ *     r = x (+ residual)                       fp32; residual_out = r in x's type
+ *     y = r / sqrt(mean(r^2) + eps) * weight   fp32
+ *   SSU_NORM_PLAIN  y in x's type
+ *   SSU_NORM_ROW    codes E4M3(y * (448 / amax)) and scales[row] = amax / 448,
+ *                   amax the largest |y| of the row
+ *   SSU_NORM_BLOCK  the same for every 128 columns (the last block may be
+ *                   shorter), scales[row * ceil(hidden / 128) + block]
+ * with amax = 0 giving scale 1 (the E4M3 read copy's form).  The norm is taken
+ * of the fp32 sum, not of the rounded residual_out.  A row with a NaN, or with
+ * an infinity, gives NaN where the formula does; its scale counts the other
+ * values.  x, residual, residual_out and y have unit column stride and any row
+ * strides (elements); residual_out may be the residual itself.  hidden is in
+ * [1, 32768] (larger returns SSU_ERR_UNSUPPORTED).  One kernel launch; rows ==
+ * 0 launches nothing.
+ */
+#define SSU_NORM_PLAIN 0
+#define SSU_NORM_ROW 1
+#define SSU_NORM_BLOCK 2
+typedef struct ssu_norm_args {
+    int64_t rows, hidden;
+    int32_t dtype;                /* ssu_dtype of x, residual, residual_out (and y when plain) */
+    int32_t weight_dtype;         /* ssu_dtype of weight: x's or SSU_F32                       */
+    int32_t format;               /* SSU_NORM_*                                                */
+    float eps;                    /* > 0                                                       */
+    const void *x;                /* device [rows, hidden]                                     */
+    const void *residual;         /* device [rows, hidden] or NULL                             */
+    const void *weight;           /* device [hidden]                                           */
+    void *residual_out;           /* device [rows, hidden]; NULL exactly when residual is      */
+    void *y;                      /* device [rows, hidden], x's type or one byte a value       */
+    float *scales;                /* device, see above; NULL exactly when plain                */
+    int64_t x_stride, residual_stride, residual_out_stride, y_stride;
+} ssu_norm_args;
+ssu_status ssu_add_rmsnorm(const ssu_norm_args *args, void *stream);
+
+/*
+ * Log probabilities of given tokens under rows of logits, the rows' entropy
+ * and the most likely alternatives -- what drafts verified by
+ * ssu_replay_verify are accepted by.  Per row x, with m = max x and
+ * s = sum exp(x - m):
+ *     logprob = (x[token] - m) - ln s
+ *     entropy = ln s - sum (x - m) exp(x - m) / s
+ *     top_ids = the top_k indices in order of (value, lowest index first),
+ *     top_logprobs = their log probabilities
+ * A logit of -inf has probability 0.  A row of nothing but -inf has logprob
+ * and top_logprobs -inf and entropy 0; a row with a NaN or +inf has NaN for
+ * all three (a NaN orders as -inf among the alternatives).  Token -1 asks for
+ * none: its logprob is 0.  Any other token outside [0, vocab) sets
+ * SSU_DEV_BAD_ENTRY and has logprob NaN.  vocab is in [1, 2^30], top_k in [0,
+ * 32] and at most vocab.  One kernel launch; rows == 0 launches nothing.
+ */
+typedef struct ssu_logprob_args {
+    int64_t rows, vocab, row_stride;  /* row_stride: elements; unit column stride              */
+    int32_t dtype;                /* ssu_dtype of logits                                       */
+    int32_t token_type;           /* ssu_itype of tokens and top_ids                           */
+    int32_t top_k;
+    int32_t reserved0;            /* must be 0                                                 */
+    const void *logits;           /* device [rows, vocab]                                      */
+    const void *tokens;           /* device [rows]                                             */
+    float *logprobs, *entropy;    /* device [rows]                                             */
+    void *top_ids;                /* device [rows, top_k]; NULL when top_k is 0                */
+    float *top_logprobs;          /* device [rows, top_k]; NULL when top_k is 0                */
+    int32_t *d_status;            /* device int32 or NULL                                      */
+} ssu_logprob_args;
+ssu_status ssu_token_logprobs(const ssu_logprob_args *args, void *stream);
+
+/*
  * Get the kernel for one configuration ready before any CUDA graph capture:
  * checks that the configuration is supported, loads the kernel's module on
  * the current device and caches its launch attributes.  MATE "Mamba / SSU",

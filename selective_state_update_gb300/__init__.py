@@ -20,6 +20,12 @@ Entry points (same names as the C ABI):
   ssu_ssd_prefill_static  the same on the library's own device scratch
   ssu_batch_copy       batched state copies with memmove semantics
   ssu_prewarm          load a configuration's kernel before graph capture
+  ssu_linear_attention_step, ssu_linear_attention_prefill
+                       linear attention with a decay for each head on the
+                       same slot pools: single tokens, packed prompts
+  ssu_add_rmsnorm      RMS norm with the residual's addition, E4M3 output
+  ssu_token_logprobs   log probabilities of given tokens, entropy and top
+                       alternatives
 and ``selective_state_update``, the MATE/FlashInfer-shaped call (MATE
 documentation, page "Mamba / SSU", API reference) that picks one of the two
 update entry points from the call shape.
@@ -38,6 +44,7 @@ __all__ = ["ssu_update_onetoken", "ssu_selftest_timeout", "ssu_update_packed", "
            "ssu_batch_copy", "copy_table",
            "slot_copies", "ssu_prewarm",
            "selective_state_update",
+           "ssu_linear_attention_step", "ssu_linear_attention_prefill", "ssu_add_rmsnorm", "ssu_token_logprobs",
            "SLOTS_STRIDED", "SLOTS_PER_ROW", "DEV_BAD_SLOT", "DEV_BAD_ENTRY", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
            "library_path", "lib"]
 
@@ -191,6 +198,7 @@ def lib():
         L.ssu_prewarm.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                   ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]
         L.ssu_prewarm.restype = ctypes.c_int
+        hybrid.bind(L)
         L.ssu_last_error.argtypes = []
         L.ssu_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -746,3 +754,8 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, 
         return ssu_update_packed(state, x, dt, A, B, C, cu_seqlens=cu_seqlens,
                                  num_accepted_tokens=num_accepted_tokens, slot_mode=slot_mode, **common)
     return ssu_update_onetoken(state, x, dt, A, B, C, **common)
+
+
+from . import hybrid  # noqa: E402  (needs the helpers above)
+from .hybrid import (ssu_add_rmsnorm, ssu_linear_attention_prefill, ssu_linear_attention_step,  # noqa: E402
+                     ssu_token_logprobs)

@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "ssu_hybrid.h"
 #include "ssu_internal.h"
 #include "ssu_ssd_params.h"
 #include "ssu_verify.h"
@@ -177,16 +178,16 @@ int32_t packed_bulk_ops(const ssu_args *a) {
 // The kernels launch on the current device: a state pool that lives on
 // another device would be addressed from the wrong one.  Checked right before
 // a launch, after every host check.
-ssu_status check_device(const void *state) {
+ssu_status check_device(const void *state, const char *what = "the state") {
     int dev = -1;
     cudaPointerAttributes pa;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(SSU_ERR_CUDA, "no current CUDA device");
     if (cudaPointerGetAttributes(&pa, state) != cudaSuccess) {
         cudaGetLastError();
-        return fail(SSU_ERR_INVALID, "the state pointer is not one the CUDA runtime knows");
+        return fail(SSU_ERR_INVALID, "the pointer of %s is not one the CUDA runtime knows", what);
     }
     if (pa.type == cudaMemoryTypeDevice && pa.device != dev)
-        return fail(SSU_ERR_INVALID, "the state is on device %d but device %d is current", pa.device, dev);
+        return fail(SSU_ERR_INVALID, "%s is on device %d but device %d is current", what, pa.device, dev);
     return SSU_OK;
 }
 
@@ -501,6 +502,183 @@ ssu_status ssu_shadow_refresh(const void *state, int32_t state_dtype, int64_t ro
         return fail(SSU_ERR_INVALID, "state, shadow (and scale for E4M3 and NVFP4) must not be NULL");
     return launched(ssu::launch_shadow_refresh(state, state_dtype, rows, static_cast<int>(dstate), format, shadow,
                                                scale, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks shared by the two forms of linear attention; fills `lp` except the
+// packed layout.
+static ssu_status linattn_prepare(const ssu_linattn_args *a, const ssu_slot_table *read, const ssu_slot_table *dst,
+                                  ssu::LinattnParams *lp) {
+    if (a == nullptr) return fail(SSU_ERR_INVALID, "args is NULL");
+    if (a->reserved0 != 0) return fail(SSU_ERR_INVALID, "reserved0 must be 0");
+    if (!valid_dtype(a->io_dtype)) return fail(SSU_ERR_INVALID, "io_dtype %d is not an ssu_dtype", a->io_dtype);
+    if (!valid_dtype(a->state_dtype))
+        return fail(SSU_ERR_INVALID, "state_dtype %d is not an ssu_dtype", a->state_dtype);
+    if (a->rows < 0) return fail(SSU_ERR_INVALID, "rows is negative");
+    if (a->slots <= 0) return fail(SSU_ERR_INVALID, "slots must be positive");
+    if (a->heads <= 0 || a->kv_heads <= 0 || a->heads % a->kv_heads != 0)
+        return fail(SSU_ERR_INVALID, "heads (%lld) must be a positive multiple of kv_heads (%lld)", (long long)a->heads,
+                    (long long)a->kv_heads);
+    if (a->heads > 65535) return fail(SSU_ERR_INVALID, "more than 65535 heads");
+    for (const int64_t d : {a->dim, a->dstate})
+        if (d < 8 || d > ssu::kLinattnMaxDim || d % 8 != 0)
+            return fail(SSU_ERR_UNSUPPORTED, "dim %lld, dstate %lld: linear attention takes multiples of 8 from 8 to %d",
+                        (long long)a->dim, (long long)a->dstate, ssu::kLinattnMaxDim);
+    if (!(a->scale == a->scale)) return fail(SSU_ERR_INVALID, "scale is not a number");
+    if (!a->state || !a->log_decay) return fail(SSU_ERR_INVALID, "state and log_decay must not be NULL");
+    if (!aligned16(a->state)) return fail(SSU_ERR_INVALID, "state must be 16-byte aligned");
+    if (a->rows > 0 && (!a->q || !a->k || !a->v || !a->out)) return fail(SSU_ERR_INVALID, "q, k, v and out must not be NULL");
+    if (a->rows > 0 && (a->out == a->q || a->out == a->k || a->out == a->v || a->out == a->state))
+        return fail(SSU_ERR_INVALID, "out must not alias an input");
+    std::memset(lp, 0, sizeof *lp);
+    for (int i = 0; i < 2; ++i) {
+        if (a->q_stride[i] < 0 || a->k_stride[i] < 0 || a->v_stride[i] < 0 || a->out_stride[i] < 0)
+            return fail(SSU_ERR_INVALID, "a stride is negative");
+        lp->qs[i] = a->q_stride[i], lp->ks[i] = a->k_stride[i], lp->vs[i] = a->v_stride[i], lp->os[i] = a->out_stride[i];
+    }
+    ssu_status st;
+    if ((st = check_table("read", read, &lp->rd)) || (st = check_table("destination", dst, &lp->wr))) return st;
+    // a table has one entry per sequence, (b, 0): the mode is ignored
+    lp->rd.per_row = lp->wr.per_row = 0;
+    lp->slots = a->slots;
+    lp->rows = a->rows;
+    lp->H = static_cast<int32_t>(a->heads);
+    lp->G = static_cast<int32_t>(a->kv_heads);
+    lp->share = static_cast<int32_t>(a->heads / a->kv_heads);
+    lp->P = static_cast<int32_t>(a->dim);
+    lp->N = static_cast<int32_t>(a->dstate);
+    lp->io_dtype = a->io_dtype;
+    lp->state_dtype = a->state_dtype;
+    lp->scale = a->scale;
+    lp->pad = a->pad_slot_id;
+    lp->state = a->state;
+    lp->q = a->q, lp->k = a->k, lp->v = a->v;
+    lp->log_decay = a->log_decay;
+    lp->out = a->out;
+    lp->status = a->d_status;
+    return SSU_OK;
+}
+
+ssu_status ssu_linear_attention_step(const ssu_linattn_args *args, const ssu_slot_table *read,
+                                     const ssu_slot_table *dst, void *stream) {
+    ssu::LinattnParams lp;
+    ssu_status st = linattn_prepare(args, read, dst, &lp);
+    if (st != SSU_OK) return st;
+    if (lp.rows == 0) return ok();
+    if (lp.rows > kMaxGrid / (4 * lp.H)) return fail(SSU_ERR_INVALID, "too many sequences and heads for one launch");
+    lp.nseq = lp.rows;
+    if ((st = check_device(args->state)) != SSU_OK) return st;
+    return launched(ssu::launch_linattn_step(lp, static_cast<cudaStream_t>(stream)));
+}
+
+ssu_status ssu_linear_attention_workspace_size(const ssu_linattn_args *args, int64_t nseq, int64_t max_seqlen,
+                                               uint64_t *bytes) {
+    if (!bytes) return fail(SSU_ERR_INVALID, "bytes is NULL");
+    if (nseq < 0 || max_seqlen < 0) return fail(SSU_ERR_INVALID, "nseq and max_seqlen must not be negative");
+    ssu::LinattnParams lp;
+    const ssu_status st = linattn_prepare(args, nullptr, nullptr, &lp);
+    if (st != SSU_OK) return st;
+    *bytes = 0;
+    return ok();
+}
+
+ssu_status ssu_linear_attention_prefill(const ssu_linattn_args *args, int64_t nseq, const void *cu_seqlens,
+                                        int32_t meta_type, int64_t max_seqlen, const ssu_slot_table *read,
+                                        const ssu_slot_table *dst, void *workspace, uint64_t workspace_bytes,
+                                        void *stream) {
+    (void)workspace, (void)workspace_bytes;
+    if (nseq < 0 || max_seqlen < 0) return fail(SSU_ERR_INVALID, "nseq and max_seqlen must not be negative");
+    ssu::LinattnParams lp;
+    ssu_status st = linattn_prepare(args, read, dst, &lp);
+    if (st != SSU_OK) return st;
+    if (!valid_itype(meta_type)) return fail(SSU_ERR_INVALID, "meta_type %d is not an ssu_itype", meta_type);
+    if (args->io_dtype == SSU_F32) return fail(SSU_ERR_UNSUPPORTED, "the prefill takes fp16 or bf16 q, k, v and out");
+    if (nseq == 0) return ok();
+    if (!cu_seqlens) return fail(SSU_ERR_INVALID, "cu_seqlens must not be NULL");
+    if (lp.rows > 0) {
+        for (const void *q : {args->q, args->k, args->v, static_cast<const void *>(args->out)})
+            if (!aligned16(q)) return fail(SSU_ERR_INVALID, "q, k, v and out must be 16-byte aligned");
+        for (int i = 0; i < 2; ++i)
+            if (lp.qs[i] % 8 || lp.ks[i] % 8 || lp.vs[i] % 8 || lp.os[i] % 8)
+                return fail(SSU_ERR_INVALID, "the strides of q, k, v and out must be multiples of 8");
+    }
+    if (lp.rows >= kMaxGrid) return fail(SSU_ERR_INVALID, "more than 2^31-1 tokens");
+    if (nseq > kMaxGrid / (4 * lp.H)) return fail(SSU_ERR_INVALID, "too many sequences and heads for one launch");
+    lp.nseq = nseq;
+    lp.cu = cu_seqlens;
+    lp.meta_is_i64 = meta_type == SSU_I64;
+    if ((st = check_device(args->state)) != SSU_OK) return st;
+    return launched(ssu::launch_linattn_prefill(lp, static_cast<cudaStream_t>(stream)));
+}
+
+ssu_status ssu_add_rmsnorm(const ssu_norm_args *a, void *stream) {
+    if (a == nullptr) return fail(SSU_ERR_INVALID, "args is NULL");
+    if (!valid_dtype(a->dtype)) return fail(SSU_ERR_INVALID, "dtype %d is not an ssu_dtype", a->dtype);
+    if (a->weight_dtype != a->dtype && a->weight_dtype != SSU_F32)
+        return fail(SSU_ERR_INVALID, "weight has x's type or fp32");
+    if (a->format != SSU_NORM_PLAIN && a->format != SSU_NORM_ROW && a->format != SSU_NORM_BLOCK)
+        return fail(SSU_ERR_INVALID, "format %d is not an SSU_NORM_* value", a->format);
+    if (a->rows < 0 || a->hidden < 1) return fail(SSU_ERR_INVALID, "rows must be >= 0 and hidden positive");
+    if (a->hidden > ssu::kNormMaxHidden)
+        return fail(SSU_ERR_UNSUPPORTED, "hidden %lld is not supported (up to %d)", (long long)a->hidden,
+                    ssu::kNormMaxHidden);
+    if (!(a->eps > 0.f)) return fail(SSU_ERR_INVALID, "eps must be positive");
+    if (a->x_stride < 0 || a->residual_stride < 0 || a->residual_out_stride < 0 || a->y_stride < 0)
+        return fail(SSU_ERR_INVALID, "a stride is negative");
+    if (a->rows == 0) return ok();
+    if ((a->residual == nullptr) != (a->residual_out == nullptr))
+        return fail(SSU_ERR_INVALID, "residual and residual_out go together");
+    if ((a->format == SSU_NORM_PLAIN) != (a->scales == nullptr))
+        return fail(SSU_ERR_INVALID, "scales go with the E4M3 formats and only with them");
+    if (!a->x || !a->weight || !a->y) return fail(SSU_ERR_INVALID, "x, weight and y must not be NULL");
+    if (a->rows > kMaxGrid) return fail(SSU_ERR_INVALID, "more than 2^31-1 rows");
+    const int64_t size = a->dtype == SSU_F32 ? 4 : 2;
+    for (const void *q : {a->x, a->residual, static_cast<const void *>(a->residual_out)})
+        if (reinterpret_cast<uintptr_t>(q) % size != 0)
+            return fail(SSU_ERR_INVALID, "x, residual and residual_out must be aligned to their type");
+    if (a->y == a->x || a->y == a->residual || a->y == a->residual_out || (a->residual_out && a->residual_out == a->x))
+        return fail(SSU_ERR_INVALID, "y must not alias x, residual or residual_out, nor residual_out x");
+    ssu_status st = check_device(a->x, "x");
+    if (st != SSU_OK) return st;
+    ssu::NormParams p{};
+    p.rows = a->rows;
+    p.hidden = static_cast<int32_t>(a->hidden);
+    p.dtype = a->dtype, p.weight_dtype = a->weight_dtype, p.quant = a->format;
+    p.eps = a->eps;
+    p.x = a->x, p.residual = a->residual, p.weight = a->weight;
+    p.residual_out = a->residual_out, p.y = a->y, p.scales = a->scales;
+    p.xs = a->x_stride, p.rs = a->residual_stride, p.ros = a->residual_out_stride, p.ys = a->y_stride;
+    return launched(ssu::launch_norm(p, static_cast<cudaStream_t>(stream)));
+}
+
+ssu_status ssu_token_logprobs(const ssu_logprob_args *a, void *stream) {
+    if (a == nullptr) return fail(SSU_ERR_INVALID, "args is NULL");
+    if (a->reserved0 != 0) return fail(SSU_ERR_INVALID, "reserved0 must be 0");
+    if (!valid_dtype(a->dtype)) return fail(SSU_ERR_INVALID, "dtype %d is not an ssu_dtype", a->dtype);
+    if (!valid_itype(a->token_type)) return fail(SSU_ERR_INVALID, "token_type %d is not an ssu_itype", a->token_type);
+    if (a->rows < 0 || a->vocab < 1 || a->vocab > (1 << 30))
+        return fail(SSU_ERR_INVALID, "rows must be >= 0 and vocab in [1, 2^30]");
+    if (a->row_stride < 0) return fail(SSU_ERR_INVALID, "row_stride is negative");
+    if (a->top_k < 0 || a->top_k > ssu::kMaxTopK || a->top_k > a->vocab)
+        return fail(SSU_ERR_INVALID, "top_k %d: from 0 to %d and to vocab", a->top_k, ssu::kMaxTopK);
+    if (a->rows == 0) return ok();
+    if (!a->logits || !a->tokens || !a->logprobs || !a->entropy)
+        return fail(SSU_ERR_INVALID, "logits, tokens, logprobs and entropy must not be NULL");
+    if (a->top_k > 0 && (!a->top_ids || !a->top_logprobs))
+        return fail(SSU_ERR_INVALID, "top_ids and top_logprobs must not be NULL");
+    if (reinterpret_cast<uintptr_t>(a->logits) % (a->dtype == SSU_F32 ? 4 : 2) != 0)
+        return fail(SSU_ERR_INVALID, "logits must be aligned to their type");
+    if (a->rows > kMaxGrid / 8) return fail(SSU_ERR_INVALID, "too many rows for one launch");
+    ssu_status st = check_device(a->logits, "logits");
+    if (st != SSU_OK) return st;
+    ssu::LogprobParams p{};
+    p.rows = a->rows, p.row_stride = a->row_stride;
+    p.vocab = static_cast<int32_t>(a->vocab);
+    p.dtype = a->dtype, p.top_k = a->top_k, p.tok_is_i64 = a->token_type == SSU_I64;
+    p.logits = a->logits, p.tokens = a->tokens;
+    p.logprob = a->logprobs, p.entropy = a->entropy;
+    p.top_ids = a->top_ids, p.top_logprob = a->top_logprobs;
+    p.status = a->d_status;
+    return launched(ssu::launch_logprobs(p, static_cast<cudaStream_t>(stream)));
 }
 
 ssu_status ssu_prewarm(int32_t state_dtype, int32_t io_dtype, int32_t dt_dtype, int64_t heads, int64_t dim,
