@@ -86,8 +86,8 @@ struct Layout {
     static constexpr int kBar = kP + 2 * kPanel;
     static constexpr int kUnits = kBar + 8 * kBars;     // Unit[2]
     static constexpr int kTabA = (kUnits + 2 * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;  // scale l^(i+1), 128 floats
-    static constexpr int kTabB = kTabA + 128 * 4;       // l^n, n = 0 .. 128
-    static constexpr int kRowScale = kTabB + 132 * 4;   // fp16: of the state rows, then of the score rows
+    static constexpr int kTabB = kTabA + 128 * 4;       // l^(127-j), j < 128, then a quarter of zeros
+    static constexpr int kRowScale = kTabB + (128 + 32) * 4;  // fp16: of the state rows, then of the score rows
     static constexpr int kMax = kRowScale + 256 * 4;    // fp16: per warp
     static constexpr int kMisc = kMax + 16;             // tensor-memory address, abort
     static constexpr int kBytes = kMisc + 16;
@@ -195,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     // The launch gives every thread 168 registers (3 groups x 128 x 168 in
-    // all); the two compute groups take 224 each, 56 are left for the third.
+    // all); the two compute groups take 216 each, 72 are left for the third.
     if (warp == 9) {
-        registers<56>();
+        registers<72>();
         // ---------------- units and loads ----------------
         if (lane == 0) {
             int nu = 0, ch = 0;  // units published, chunks loaded
@@ -239,13 +239,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 8) {
-        registers<56>();
+        registers<72>();
         // ---------------- products (one thread) ----------------
         if (lane == 0) {
             constexpr int bf = BF ? 1 : 0;
             constexpr uint32_t kIdScore = idesc_f16(128, 128, 0, 0, bf), kIdEnter = idesc_f16(128, 128, 0, 0, bf);
             constexpr uint32_t kIdInside = idesc_f16(128, 128, 1, 0, bf), kIdGrowth = idesc_f16(128, DK, 0, 1, bf);
-            const uint32_t sP = smem_addr(smem + LY::kP);
+            // Descriptors differ by constants: their address field counts 16 bytes.
+            const uint32_t sQ = smem_addr(smem);
+            const uint64_t dQ = desc_k_sw128(sQ), dK = desc_k_sw128(sQ + LY::kQBytes);
+            const uint64_t dV = desc_mn_sw128(sQ + LY::kQBytes + LY::kKBytes, kPanel);
+            const uint64_t dP = desc_k_sw128(smem_addr(smem + LY::kP));
+            const uint64_t kToMn = desc_mn_sw128(0, kPanel) - desc_k_sw128(0);  // the same K read along its tokens
+            constexpr auto along_k = [](int k) { return static_cast<uint64_t>(((k / 4) * kPanel + (k % 4) * 32) >> 4); };
+            constexpr auto along_mn = [](int k) { return static_cast<uint64_t>((k * 2048) >> 4); };
+            const auto stage = [](int s) { return static_cast<uint64_t>(s * (LY::kStage >> 4)); };
+            const auto scores = [&](int s) {
+                const uint64_t q = dQ + stage(s), k0 = dK + stage(s);
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    mma(tmem + kColScore, q + along_k(k), k0 + along_k(k), kIdScore, k > 0);
+                mma_commit(&bars[kScore]);
+            };
             int nu = 0, ch = 0, tails = 0, quarters = 0;
             for (;;) {
                 if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
@@ -255,37 +270,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (len < 0) break;
                 for (int c = 0; c < len; c += kC, ++ch) {
                     const int s = ch & 1, n = min(kC, len - c), steps = (n + 15) / 16;
-                    const uint32_t sQ = smem_addr(smem + s * LY::kStage), sK = sQ + LY::kQBytes, sV = sK + LY::kKBytes;
-                    if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
-                    tc_fence_after();
-                    for (int k = 0; k < DK / 16; ++k) {
-                        const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-                        mma(tmem + kColScore, desc_k_sw128(sQ + off), desc_k_sw128(sK + off), kIdScore, k > 0);
+                    const uint64_t dQs = dQ + stage(s), dVs = dV + stage(s);
+                    if (c == 0) {
+                        if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
+                        tc_fence_after();
+                        scores(s);
                     }
-                    mma_commit(&bars[kScore]);
                     if (!(ok = mbar_wait_bounded(&bars[kStateFull], ch & 1))) break;
                     if (ch > 0 && !(ok = mbar_wait_bounded(&bars[kOutFree], (ch - 1) & 1))) break;
                     tc_fence_after();
+#pragma unroll
                     for (int part = 0; part < 2; ++part)
+#pragma unroll
                         for (int k = 0; k < DK / 16; ++k)
-                            mma_ts(tmem + kColOut, tmem + kColState + part * (DK / 2) + 8 * k,
-                                   desc_k_sw128(sQ + (k / 4) * kPanel + (k % 4) * 32), kIdEnter, part > 0 || k > 0);
+                            mma_ts(tmem + kColOut, tmem + kColState + part * (DK / 2) + 8 * k, dQs + along_k(k), kIdEnter,
+                                   part > 0 || k > 0);
                     mma_commit(&bars[kEnter]);
                     if (n < kC && !(ok = mbar_wait_bounded(&bars[kTail], tails++ & 1))) break;
                     if (!(ok = mbar_wait_bounded(&bars[kPFull], ch & 1))) break;
                     tc_fence_after();
-                    for (int k = 0; k < steps; ++k)
-                        mma(tmem + kColOut, desc_mn_sw128(sV + k * 2048, kPanel),
-                            desc_k_sw128(sP + (k / 4) * kPanel + (k % 4) * 32), kIdInside, k > 0);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < steps) mma(tmem + kColOut, dVs + along_mn(k), dP + along_k(k), kIdInside, k > 0);
                     mma_commit(&bars[kInside]);
-                    for (int qd = 0; qd * kQuarter < n; ++qd, ++quarters) {
+                    // the next chunk's scores, ahead of this one's growth
+                    if (c + kC < len) {
+                        if (!(ok = mbar_wait_bounded(&bars[kFull0 + (s ^ 1)], ((ch + 1) >> 1) & 1))) break;
+                        tc_fence_after();
+                        scores(s ^ 1);
+                    }
+                    const uint64_t dKn = dK + stage(s) + kToMn;
+#pragma unroll
+                    for (int qd = 0; qd < 4; ++qd) {
+                        if (qd * kQuarter >= n) break;
                         const int r = quarters & 1;
                         if (!(ok = mbar_wait_bounded(&bars[kVFull0 + r], (quarters >> 1) & 1))) break;
+                        ++quarters;
                         tc_fence_after();
-                        for (int k = 2 * qd; k < min(steps, 2 * qd + 2); ++k)
+#pragma unroll
+                        for (int k = 2 * qd; k < 2 * qd + 2; ++k)
+#pragma unroll
                             for (int part = 0; part < kParts; ++part)
-                                mma_ts(tmem + kColGrowth, tmem + kColState + r * kRing + part * 16 + 8 * (k & 1),
-                                       desc_mn_sw128(sK + k * 2048, kPanel), kIdGrowth, k > 0 || part > 0);
+                                if (k < steps)
+                                    mma_ts(tmem + kColGrowth, tmem + kColState + r * kRing + part * 16 + 8 * (k & 1),
+                                           dKn + along_mn(k), kIdGrowth, k > 0 || part > 0);
                         mma_commit(&bars[kVFree0 + r]);
                     }
                     if (!ok) break;
@@ -304,9 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= 10) {
-        registers<56>();
+        registers<72>();
     } else if (warp < 4) {
-        registers<224>();
+        registers<216>();
         // ---------------- P and the outputs ----------------
         const int row = tid;  // score row i; later value dim
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
@@ -418,34 +446,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (fp16) the other rows' scales, by their own arrivals
                 if (!BF && !(ok = mbar_wait_bounded(&bars[kPFull], ch & 1))) break;
                 tc_fence_after();
-                unsigned short *o = out + (un.t0 + c) * p.os[0] + row;
+                // outputs [token][value dim] in P's place, then 16 bytes a
+                // store along each token's row
+                unsigned short *stage = reinterpret_cast<unsigned short *>(smem + LY::kP) + row;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    if (32 * b >= n) continue;
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColOut + 32 * b, r);
                     tmem_wait_ld();
+                    if (b == 3) {
+                        tc_fence_before();
+                        mbar_arrive(&bars[kOutFree]);
+                    }
 #pragma unroll
                     for (int jj = 0; jj < 32; jj += 2) {
                         float s0 = p.scale, s1 = p.scale;
                         if constexpr (!BF) {
-                            s0 = row_scale[128 + 32 * b + jj];
-                            s1 = row_scale[128 + 32 * b + jj + 1];
+                            const float2 two = *reinterpret_cast<const float2 *>(row_scale + 128 + 32 * b + jj);
+                            s0 = two.x;
+                            s1 = two.y;
                         }
                         const uint32_t two = pack2<BF>(fmaf(__uint_as_float(r[jj]), s0, hold[32 * b + jj]),
                                                        fmaf(__uint_as_float(r[jj + 1]), s1, hold[32 * b + jj + 1]));
-                        if (row < p.P) {
-                            if (32 * b + jj < n) o[(32 * b + jj) * p.os[0]] = static_cast<unsigned short>(two);
-                            if (32 * b + jj + 1 < n) o[(32 * b + jj + 1) * p.os[0]] = static_cast<unsigned short>(two >> 16);
-                        }
+                        stage[(32 * b + jj) * 128] = static_cast<unsigned short>(two);
+                        stage[(32 * b + jj + 1) * 128] = static_cast<unsigned short>(two >> 16);
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(&bars[kOutFree]);
-                // fp16: the score rows' scales are read before they are replaced
-                if constexpr (!BF) {
-                    if (!(ok = group_sync(&bars[kSyncA], ph))) break;
+                if (!(ok = group_sync(&bars[kSyncA], ph))) break;
+                const int piece = tid & 15, tok = tid >> 4;
+                unsigned short *o = out + (un.t0 + c + tok) * p.os[0] + 8 * piece;
+                const unsigned char *from = smem + LY::kP + tid * 16;
+                const int64_t step = 8 * p.os[0];
+                if (8 * piece < p.P) {
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i)
+                        if (tok + 8 * i < n)
+                            *reinterpret_cast<uint4 *>(o + i * step) = *reinterpret_cast<const uint4 *>(from + i * 2048);
                 }
+                // P's place, and the score rows' scales, are read
+                if (!(ok = group_sync(&bars[kSyncA], ph))) break;
             }
             if (!ok) break;
         }
@@ -454,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     } else {
-        registers<224>();
+        registers<216>();
         // ---------------- the state and the decayed values ----------------
         const int t = tid - kGroup, w = warp - 4;  // value dim
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
@@ -471,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (un.len < 0) break;
             const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
             if (!(ok = group_sync(&bars[kSyncB], ph))) break;  // the previous unit's table is no longer read
-            tab[t] = expf(g * static_cast<float>(t));
-            if (t == 0) tab[kC] = expf(g * static_cast<float>(kC));
+            tab[t] = expf(g * static_cast<float>(kC - 1 - t));
+            if (t < kQuarter) tab[kC + t] = 0.f;
+            const float lam_chunk = expf(g * static_cast<float>(kC));
             // the entering state: this thread's row
 #pragma unroll
             for (int i = 0; i < DK; ++i) S[i] = 0.f;
@@ -537,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(&bars[kTail]);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;  // every thread's zeros, below
                 }
                 float vs = 1.f, vback = 1.f;
                 if constexpr (!BF) {
@@ -566,33 +607,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the decayed V, 32 tokens at a time, where the parts of S were
                 if (!(ok = mbar_wait_bounded(&bars[kEnter], ch & 1))) break;
                 tc_fence_after();
+                // (column t of V: the swizzle moves its 16-byte piece with the row)
                 const unsigned char *vcol = sV + (t >> 6) * kPanel + (t & 7) * 2;
-                const int piece = (t & 63) >> 3;
+                const int piece = ((t & 63) >> 3) * 16;
+                const float *weight = tab + (kC - n);
                 for (int q0 = 0; q0 < n; q0 += kQuarter, ++quarters) {
                     const int r = quarters & 1;
-                    if (quarters >= 2 && !(ok = mbar_wait_bounded(&bars[kVFree0 + r], ((quarters >> 1) - 1) & 1))) break;
-                    tc_fence_after();
-                    uint32_t part[kParts][16];
+                    float x[kQuarter];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x[2];
+                    for (int j = 0; j < kQuarter; j += 4) {
+                        float we[4];
+                        if (n == kC) {
+                            const float4 wj = *reinterpret_cast<const float4 *>(weight + q0 + j);
+                            we[0] = wj.x, we[1] = wj.y, we[2] = wj.z, we[3] = wj.w;
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = q0 + 2 * i + e;
-                            const unsigned short u = *reinterpret_cast<const unsigned short *>(vcol + j * 128 + ((piece ^ (j & 7)) * 16));
-                            const float v = BF ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u)) * vs;
-                            x[e] = j < n ? v * tab[max(n - 1 - j, 0)] : 0.f;
+                            for (int e = 0; e < 4; ++e) we[e] = weight[q0 + j + e];
                         }
 #pragma unroll
-                        for (int q = 0; q < kParts; ++q) {
-                            part[q][i] = pack2<BF>(x[0], x[1]);
-                            const float2 f = unpack2<BF>(part[q][i]);
-                            x[0] -= f.x;
-                            x[1] -= f.y;
+                        for (int e = 0; e < 4; ++e) {
+                            const unsigned short u = *reinterpret_cast<const unsigned short *>(
+                                vcol + q0 * 128 + (j + e) * 128 + (piece ^ (((j + e) & 7) * 16)));
+                            const float v =
+                                BF ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u)) * vs;
+                            x[j + e] = v * we[e];
                         }
                     }
+                    if (quarters >= 2 && !(ok = mbar_wait_bounded(&bars[kVFree0 + r], ((quarters >> 1) - 1) & 1))) break;
+                    tc_fence_after();
 #pragma unroll
-                    for (int q = 0; q < kParts; ++q) tmem_st16(tmem + lanes + kColState + r * kRing + 16 * q, part[q]);
+                    for (int q = 0; q < kParts; ++q) {
+                        uint32_t part[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if constexpr (BF) {
+                                // the top 8 bits of what is left: three parts hold all 24
+                                const uint32_t a = __float_as_uint(x[2 * i]), c2 = __float_as_uint(x[2 * i + 1]);
+                                part[i] = __byte_perm(a, c2, 0x7632);
+                                x[2 * i] -= __uint_as_float(a & 0xffff0000u);
+                                x[2 * i + 1] -= __uint_as_float(c2 & 0xffff0000u);
+                            } else {
+                                part[i] = pack2<BF>(x[2 * i], x[2 * i + 1]);
+                                const float2 f = unpack2<BF>(part[i]);
+                                x[2 * i] -= f.x;
+                                x[2 * i + 1] -= f.y;
+                            }
+                        }
+                        tmem_st16(tmem + lanes + kColState + r * kRing + 16 * q, part);
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(&bars[kVFull0 + r]);
@@ -601,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kFree0 + s]);
                 if (!(ok = mbar_wait_bounded(&bars[kGrowth], ch & 1))) break;
                 tc_fence_after();
-                const float lam = tab[n];
+                const float lam = n == kC ? lam_chunk : expf(g * static_cast<float>(n));
 #pragma unroll
                 for (int b = 0; b < DK / 32; ++b) {
                     uint32_t r[32];
