@@ -6,29 +6,31 @@
 // state that enters it:
 //     out_i = scale (l^(i+1) S q_i + sum_{j<=i} l^(i-j) (q_i . k_j) v_j)
 //     S'    = l^n S + sum_j l^(n-1-j) v_j k_j^T
-// A work unit is one piece of a sequence (all of it, or an equal part of a long
-// one) for one head; a CTA walks its chunks and carries S in registers.
+// A work unit is one sequence for one head; a CTA walks its chunks and carries
+// S in registers.
 //
 // Four products a chunk, tcgen05.mma with fp32 accumulators in tensor memory:
-//   scores   [i, j]    = Q K^T             Q, K from shared memory, as loaded
-//   entering [p, i]    = S Q^T             S as a high and a low part, from tensor memory
-//   inside   [p, i]    = V^T P^T           P = scores decayed and masked, rounded once
-//   growth   [p, n]    = (V decayed)^T K   the decayed V in three parts (bf16) or two
-//                                          (fp16), from tensor memory
-// Outputs, states and the decayed values thus share lanes: lane p of tensor
-// memory belongs to value dim p, so l^n S + growth, the split of S into parts
-// and the transposition of V (read by columns from shared memory) stay within a
-// thread.  The decay of the entering state is applied to the product, in fp32.
+//   scores   [i, j]  = Q K^T            Q, K from shared memory, as loaded
+//   entering [i, p]  = Q S^T            S as a high and a low part, in shared memory
+//   inside   [i, p] += P V              P = scores decayed and masked, rounded once, from
+//                                       tensor memory; added to the entering product,
+//                                       whose rows have been scaled there by l^(i+1) in fp32
+//   growth   [p, n]  = (V decayed)^T K  the decayed V in three parts (bf16) or two
+//                                       (fp16), transposed, from tensor memory
 // Rounding: P to the io type (2^-8 bf16, 2^-11 fp16, as the output itself); S
 // where it meets Q to two parts (2^-16, 2^-22); the decayed V to three parts
 // (2^-24) or two (2^-22), so that fp32 states keep fp32 accuracy.  fp16 parts are
 // scaled by powers of two (per state row, score row and value tile), so neither
 // overflow nor the subnormals cost accuracy.
 //
-// Warps: 0-3 turn scores into P and store outputs (thread = score row, then
-// value dim); 4-7 own S (thread = value dim), split it, and decay V; 8 issues
-// the products; 9 finds the units and loads Q, K, V (tiled copies, two stages);
-// 10 and 11 only complete the third group, whose registers the others take.
+// Warps, in groups of four (a warp reaches the tensor-memory lanes 32 (warp %
+// 4) ...):
+//   0-3    (thread = token) scores -> P, entering rows scaled, outputs stored;
+//   4-7    (thread = value dim) S: growth added, parts split off, first and last state;
+//   8-11   V decayed, transposed (ldmatrix) and split, 32 tokens at a time;
+//   12     issues the products;  13 finds the units and loads Q, K, V by tiled copies
+//          (K, V in two stages; Q, which only the early products read, in one);
+//   14     stores the outputs by tiled copies;  15 only completes the group.
 #include <cuda.h>
 
 #include "ssu_hybrid.h"
@@ -38,64 +40,64 @@ namespace ssu {
 
 namespace {
 
-constexpr int kC = 128;       // tokens of a chunk
+constexpr int kC = 128;        // tokens of a chunk
 constexpr int kPanel = 16384;  // 128 rows of 128 bytes
-constexpr int kThreads = 384;
-constexpr int kGroup = 128;   // threads of one of the two groups of warps
-constexpr int kQuarter = 32;  // tokens whose decayed V is handed over at a time
+constexpr int kThreads = 512;
+constexpr int kGroup = 128;    // threads of a group of four warps
+constexpr int kQuarter = 32;   // tokens whose decayed V is handed over at a time
 
-// Tensor-memory columns.  The decayed V goes where the parts of S were, once
-// the entering product has read them.
-constexpr uint32_t kColScore = 0, kColOut = 128, kColGrowth = 256, kColState = 384;
+// Tensor-memory columns.  P goes where its scores were.
+constexpr uint32_t kColScore = 0, kColOut = 128, kColGrowth = 256, kColV = 384;
 constexpr uint32_t kRing = 48;  // columns of one quarter: up to 3 parts of 16
 
 struct Unit {
-    int64_t t0;      // first token row
-    int64_t src;     // state entering: pool slot or kZero
-    int64_t dst;     // state leaving: pool slot or kNone
-    int32_t len;     // tokens; -1: no more units
+    int64_t t0;   // first token row
+    int64_t src;  // state entering: pool slot or kZero
+    int64_t dst;  // state leaving: pool slot or kNone
+    int32_t len;  // tokens; -1: no more units
     int32_t h;
 };
 constexpr int64_t kZero = -1, kNone = -1;
 
 enum : int {
-    kFull0, kFull1,    // a stage's Q, K, V have landed
+    kQFull, kQFree,
+    kFull0, kFull1,    // a stage's K and V have landed
     kFree0, kFree1,    // ... and are done with
     kUnitFull0, kUnitFull1, kUnitFree0, kUnitFree1,
     kScore,            // the scores are there
     kStateFull,        // the parts of S are there
-    kEnter,            // the entering product is there (and the parts of S are read)
-    kPFull,            // P is there; the scores and the entering product are read
-    kInside,           // the inside product is there (and P is read)
+    kEnter,            // the entering product is there (the parts of S and Q are read)
+    kPFull,            // P is there, the entering product scaled
+    kInside,           // the outputs are there (P is read)
     kOutFree,          // ... and read
+    kStaged,           // ... and laid out by token, in V's place
     kTail,             // a partial chunk's K and V rows past its end are zeros
     kVFull0, kVFull1, kVFree0, kVFree1,
-    kGrowth,
-    kSyncA, kSyncB,
+    kGrowth, kGrowthFree,
+    kSyncA, kSyncC,
     kFinal,
     kBars
 };
 
 template <int DK>
 struct Layout {
-    static constexpr int kQBytes = DK / 64 * kPanel;
-    static constexpr int kKBytes = kQBytes;
+    static constexpr int kPanels = DK / 64;
+    static constexpr int kKBytes = kPanels * kPanel;
     static constexpr int kVBytes = 2 * kPanel;
-    static constexpr int kStage = kQBytes + kKBytes + kVBytes;
-    static constexpr int kP = 2 * kStage;              // P: two panels
-    static constexpr int kBar = kP + 2 * kPanel;
-    static constexpr int kUnits = kBar + 8 * kBars;     // Unit[2]
-    static constexpr int kTabA = (kUnits + 2 * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;  // scale l^(i+1), 128 floats
-    static constexpr int kTabB = kTabA + 128 * 4;       // l^(127-j), j < 128, then a quarter of zeros
-    static constexpr int kRowScale = kTabB + (128 + 32) * 4;  // fp16: of the state rows, then of the score rows
-    static constexpr int kMax = kRowScale + 256 * 4;    // fp16: per warp
-    static constexpr int kMisc = kMax + 16;             // tensor-memory address, abort
+    static constexpr int kStage = kKBytes + kVBytes;
+    static constexpr int kQ = 2 * kStage;
+    static constexpr int kS = kQ + kKBytes;               // high part, then low part: kPanels panels each
+    static constexpr int kBar = kS + 2 * kKBytes;
+    static constexpr int kUnits = kBar + 8 * kBars;       // Unit[2]
+    static constexpr int kRowScale = (kUnits + 2 * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;  // fp16: state rows, by chunk parity
+    static constexpr int kMax = kRowScale + 2 * 128 * 4;  // fp16: per warp; then the value tiles' scales, four chunks
+    static constexpr int kMisc = kMax + 32;               // tensor-memory address, abort
     static constexpr int kBytes = kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 // A barrier of one group of warps, its waits bounded like every other.
@@ -121,13 +123,53 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
     if constexpr (BF) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     else return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
+// Two floats as parts of the io type, the largest first; x, y are left with
+// the rest.  bf16: the top 16 bits, so that three parts hold all 24 bits of a
+// float's mantissa.
+template <bool BF>
+__device__ __forceinline__ uint32_t split2(float &x, float &y) {
+    if constexpr (BF) {
+        const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+        x -= __uint_as_float(a & 0xffff0000u);
+        y -= __uint_as_float(b & 0xffff0000u);
+        return __byte_perm(a, b, 0x7632);
+    } else {
+        const uint32_t u = pack2<BF>(x, y);
+        const float2 f = unpack2<BF>(u);
+        x -= f.x;
+        y -= f.y;
+        return u;
+    }
+}
 
-// Gives up (N below 168) or takes registers; every warp of a group of four
-// calls it with the same N.
+// Gives up (N below the launch's 128) or takes registers; every warp of a group
+// of four calls it with the same N.
 template <int N>
 __device__ __forceinline__ void registers() {
-    if constexpr (N < 168) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (N == 128) return;
+    else if constexpr (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Four 8 x 8 matrices of 16-bit elements, transposed: the lane's address is row
+// lane % 8 of matrix lane / 8; register m gets, of matrix m, rows 2 (lane % 4)
+// and + 1 of column lane / 4.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+// 16 lanes x 16 columns: register 2 c + i goes to lane 8 i + lane / 4, column
+// 4 c + lane % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    tmem_st16(taddr, r);
+    tmem_st16(taddr + 16, r + 16);
 }
 
 // Finds unit u of the call: the sequence's bounds and slots.  False (and
@@ -165,42 +207,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + LY::kBar);
     Unit *ring = reinterpret_cast<Unit *>(smem + LY::kUnits);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + LY::kMisc);
+    float *row_scale = reinterpret_cast<float *>(smem + LY::kRowScale);
+    float *maxes = reinterpret_cast<float *>(smem + LY::kMax);
     volatile uint32_t *abort_flag = misc + 1;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
-            if (i == kFree0 || i == kFree1) n = 1 + kGroup;
-            if (i == kUnitFree0 || i == kUnitFree1) n = 1 + 2 * kGroup;
-            if (i == kStateFull || i == kPFull || i == kOutFree || i == kTail || i == kVFull0 ||
-                i == kVFull1 || i == kSyncA || i == kSyncB)
+            if (i == kFree0 || i == kFree1) n = 2 + kGroup;
+            if (i == kUnitFree0 || i == kUnitFree1) n = 2 + 3 * kGroup;
+            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail || i == kVFull0 || i == kVFull1 ||
+                i == kGrowthFree || i == kSyncA || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
         *abort_flag = 0;
     }
-    if (p.P <= 64) {
-        // values of dims 64 .. 127 do not exist: their panels stay zero
-        for (int i = tid; i < 2 * kPanel / 16; i += kThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / (kPanel / 16)) * LY::kStage + LY::kQBytes + LY::kKBytes + kPanel +
-                                       (i % (kPanel / 16)) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-    }
-    if (warp == 8) tmem_alloc512(misc);
+    if (warp == 12) tmem_alloc512(misc);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
     bool ok = true;
 
-    // The launch gives every thread 168 registers (3 groups x 128 x 168 in
-    // all); the two compute groups take 216 each, 72 are left for the third.
-    if (warp == 9) {
-        registers<72>();
+    // The launch gives every thread 128 registers (4 x 128 in all); the groups
+    // take 128, 208 and 96, which leaves 80 for the last.
+    if (warp == 13) {
+        registers<80>();
         // ---------------- units and loads ----------------
         if (lane == 0) {
-            int nu = 0, ch = 0;  // units published, chunks loaded
+            int nu = 0, ch = 0, nq = 0;  // units published, chunks loaded (K and V, Q)
             const int vpanels = p.P > 64 ? 2 : 1;
             for (int64_t u = blockIdx.x;; u += gridDim.x) {
                 Unit un;
@@ -214,19 +251,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (end) break;
                 const int g = un.h / p.share;
                 for (int c = 0; c < un.len; c += kC, ++ch) {
-                    const int s = ch & 1;
+                    const int s = ch & 1, row = static_cast<int>(un.t0) + c;
                     if (ch >= 2 && !(ok = mbar_wait_bounded(&bars[kFree0 + s], ((ch >> 1) - 1) & 1))) break;
                     if (*abort_flag) ok = false;
                     if (!ok) break;
                     unsigned char *st = smem + s * LY::kStage;
-                    mbar_arrive_expect(&bars[kFull0 + s], LY::kQBytes + LY::kKBytes + vpanels * kPanel);
-                    const int row = static_cast<int>(un.t0) + c;
-                    for (int i = 0; i < DK / 64; ++i) {
-                        tma_load_3d(st + i * kPanel, &maps.q, 64 * i, un.h, row, &bars[kFull0 + s]);
-                        tma_load_3d(st + LY::kQBytes + i * kPanel, &maps.k, 64 * i, g, row, &bars[kFull0 + s]);
-                    }
+                    mbar_arrive_expect(&bars[kFull0 + s], LY::kKBytes + vpanels * kPanel);
+                    for (int i = 0; i < LY::kPanels; ++i)
+                        tma_load_3d(st + i * kPanel, &maps.k, 64 * i, g, row, &bars[kFull0 + s]);
                     for (int i = 0; i < vpanels; ++i)
-                        tma_load_3d(st + LY::kQBytes + LY::kKBytes + i * kPanel, &maps.v, 64 * i, g, row, &bars[kFull0 + s]);
+                        tma_load_3d(st + LY::kKBytes + i * kPanel, &maps.v, 64 * i, g, row, &bars[kFull0 + s]);
+                    if (ch >= 1 && !(ok = mbar_wait_bounded(&bars[kQFree], (ch - 1) & 1))) {
+                        ++ch;  // its K and V are on their way
+                        break;
+                    }
+                    ++nq;
+                    mbar_arrive_expect(&bars[kQFull], LY::kKBytes);
+                    for (int i = 0; i < LY::kPanels; ++i)
+                        tma_load_3d(smem + LY::kQ + i * kPanel, &maps.q, 64 * i, un.h, row, &bars[kQFull]);
                 }
                 if (!ok) break;
             }
@@ -236,110 +278,149 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // what was loaded has landed before the CTA retires
             for (int k = ch > 2 ? ch - 2 : 0; k < ch; ++k) mbar_wait_bounded(&bars[kFull0 + (k & 1)], (k >> 1) & 1);
+            if (nq > 0) mbar_wait_bounded(&bars[kQFull], (nq - 1) & 1);
         }
         __syncwarp();
-    } else if (warp == 8) {
-        registers<72>();
-        // ---------------- products (one thread) ----------------
-        if (lane == 0) {
-            constexpr int bf = BF ? 1 : 0;
-            constexpr uint32_t kIdScore = idesc_f16(128, 128, 0, 0, bf), kIdEnter = idesc_f16(128, 128, 0, 0, bf);
-            constexpr uint32_t kIdInside = idesc_f16(128, 128, 1, 0, bf), kIdGrowth = idesc_f16(128, DK, 0, 1, bf);
-            // Descriptors differ by constants: their address field counts 16 bytes.
-            const uint32_t sQ = smem_addr(smem);
-            const uint64_t dQ = desc_k_sw128(sQ), dK = desc_k_sw128(sQ + LY::kQBytes);
-            const uint64_t dV = desc_mn_sw128(sQ + LY::kQBytes + LY::kKBytes, kPanel);
-            const uint64_t dP = desc_k_sw128(smem_addr(smem + LY::kP));
-            const uint64_t kToMn = desc_mn_sw128(0, kPanel) - desc_k_sw128(0);  // the same K read along its tokens
-            constexpr auto along_k = [](int k) { return static_cast<uint64_t>(((k / 4) * kPanel + (k % 4) * 32) >> 4); };
-            constexpr auto along_mn = [](int k) { return static_cast<uint64_t>((k * 2048) >> 4); };
-            const auto stage = [](int s) { return static_cast<uint64_t>(s * (LY::kStage >> 4)); };
-            const auto scores = [&](int s) {
-                const uint64_t q = dQ + stage(s), k0 = dK + stage(s);
+    } else if (warp == 12) {
+        registers<80>();
+        // ---------------- products (the warp together, one lane issuing) ----------------
+        // Loop counts and addresses are the same in every lane and known to be
+        // (shuffled from lane 0), so that descriptors stay in uniform registers:
+        // formed per lane, each would be moved there again for every product.
+        constexpr int bf = BF ? 1 : 0;
+        const int ksteps = (p.N + 15) / 16, dims = (p.P + 15) / 16 * 16;
+        const uint32_t id_score = idesc_f16(128, 128, 0, 0, bf), id_enter = idesc_f16(128, dims, 0, 0, bf);
+        const uint32_t id_inside = idesc_f16(128, dims, 0, 1, bf), id_growth = idesc_f16(128, 16 * ksteps, 0, 1, bf);
+        const uint32_t s0 = smem_addr(smem), tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const Desc dK(desc_k_sw128(s0)), dQ(desc_k_sw128(s0 + LY::kQ)), dS(desc_k_sw128(s0 + LY::kS));
+        const Desc dKt(desc_mn_sw128(s0, kPanel)), dV(desc_mn_sw128(s0 + LY::kKBytes, kPanel));
+        constexpr auto along_k = [](int k) { return static_cast<uint32_t>(((k / 4) * kPanel + (k % 4) * 32) >> 4); };
+        constexpr auto along_mn = [](int k) { return static_cast<uint32_t>((k * 2048) >> 4); };
+        const auto wait = [&](int bar, int phase) {
+            const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[bar], phase & 1));
+            tc_fence_after();
+            return got;
+        };
+        int nu = 0, ch = 0, tails = 0, quarters = 0;
+        for (;;) {
+            if (!(ok = wait(kUnitFull0 + (nu & 1), nu >> 1))) break;
+            const int len = __shfl_sync(0xffffffffu, ring[nu & 1].len, 0);
+            if (lane == 0) mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+            ++nu;
+            if (len < 0) break;
+            for (int c = 0; c < len; c += kC, ++ch) {
+                const int s = ch & 1, n = min(kC, len - c), steps = (n + 15) / 16;
+                const uint32_t stage = static_cast<uint32_t>(s * (LY::kStage >> 4));
+                // scores; P of the last chunk, in their place, has been read
+                if (!(ok = wait(kFull0 + s, ch >> 1) && wait(kQFull, ch) && (ch == 0 || wait(kInside, ch - 1)))) break;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    mma(tmem + kColScore, q + along_k(k), k0 + along_k(k), kIdScore, k > 0);
-                mma_commit(&bars[kScore]);
-            };
-            int nu = 0, ch = 0, tails = 0, quarters = 0;
-            for (;;) {
-                if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
-                const int len = ring[nu & 1].len;
-                mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
-                ++nu;
-                if (len < 0) break;
-                for (int c = 0; c < len; c += kC, ++ch) {
-                    const int s = ch & 1, n = min(kC, len - c), steps = (n + 15) / 16;
-                    const uint64_t dQs = dQ + stage(s), dVs = dV + stage(s);
-                    if (c == 0) {
-                        if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
-                        tc_fence_after();
-                        scores(s);
+                    for (int k = 0; k < DK / 16; ++k)
+                        if (k < ksteps) mma(tm + kColScore, dQ + along_k(k), dK + (stage + along_k(k)), id_score, k > 0);
+                    mma_commit(&bars[kScore]);
+                }
+                __syncwarp();
+                if (n < kC && !(ok = wait(kTail, tails++))) break;
+                if (ch > 0 && !(ok = wait(kGrowthFree, ch - 1))) break;
+#pragma unroll
+                for (int qd = 0; qd < 4; ++qd) {
+                    // the entering product in the middle of the growth: the
+                    // group that scales it works while the rest runs
+                    if (qd == 2 || (qd < 2 && qd * kQuarter >= n)) {
+                        if (!(ok = wait(kStateFull, ch) && (ch == 0 || wait(kOutFree, ch - 1)))) break;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int k = 0; k < DK / 16; ++k)
+                                    if (k < ksteps)
+                                        mma(tm + kColOut, dQ + along_k(k), dS + (part * (LY::kKBytes >> 4) + along_k(k)), id_enter,
+                                            part > 0 || k > 0);
+                            mma_commit(&bars[kEnter]);
+                            mma_commit(&bars[kQFree]);
+                        }
+                        __syncwarp();
                     }
-                    if (!(ok = mbar_wait_bounded(&bars[kStateFull], ch & 1))) break;
-                    if (ch > 0 && !(ok = mbar_wait_bounded(&bars[kOutFree], (ch - 1) & 1))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int k = 0; k < DK / 16; ++k)
-                            mma_ts(tmem + kColOut, tmem + kColState + part * (DK / 2) + 8 * k, dQs + along_k(k), kIdEnter,
-                                   part > 0 || k > 0);
-                    mma_commit(&bars[kEnter]);
-                    if (n < kC && !(ok = mbar_wait_bounded(&bars[kTail], tails++ & 1))) break;
-                    if (!(ok = mbar_wait_bounded(&bars[kPFull], ch & 1))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < steps) mma(tmem + kColOut, dVs + along_mn(k), dP + along_k(k), kIdInside, k > 0);
-                    mma_commit(&bars[kInside]);
-                    // the next chunk's scores, ahead of this one's growth
-                    if (c + kC < len) {
-                        if (!(ok = mbar_wait_bounded(&bars[kFull0 + (s ^ 1)], ((ch + 1) >> 1) & 1))) break;
-                        tc_fence_after();
-                        scores(s ^ 1);
-                    }
-                    const uint64_t dKn = dK + stage(s) + kToMn;
-#pragma unroll
-                    for (int qd = 0; qd < 4; ++qd) {
-                        if (qd * kQuarter >= n) break;
-                        const int r = quarters & 1;
-                        if (!(ok = mbar_wait_bounded(&bars[kVFull0 + r], (quarters >> 1) & 1))) break;
-                        ++quarters;
-                        tc_fence_after();
+                    if (qd * kQuarter >= n) break;
+                    const int r = quarters & 1;
+                    if (!(ok = wait(kVFull0 + r, quarters >> 1))) break;
+                    ++quarters;
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 2 * qd; k < 2 * qd + 2; ++k)
 #pragma unroll
                             for (int part = 0; part < kParts; ++part)
                                 if (k < steps)
-                                    mma_ts(tmem + kColGrowth, tmem + kColState + r * kRing + part * 16 + 8 * (k & 1),
-                                           dKn + along_mn(k), kIdGrowth, k > 0 || part > 0);
+                                    mma_ts(tm + kColGrowth, tm + kColV + r * kRing + part * 16 + 8 * (k & 1),
+                                           dKt + (stage + along_mn(k)), id_growth, k > 0 || part > 0);
                         mma_commit(&bars[kVFree0 + r]);
+                        if ((qd + 1) * kQuarter >= n) mma_commit(&bars[kGrowth]);
                     }
-                    if (!ok) break;
-                    mma_commit(&bars[kGrowth]);
+                    __syncwarp();
+                }
+                if (!ok || !(ok = wait(kPFull, ch))) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < steps) mma_ts(tm + kColOut, tm + kColScore + 8 * k, dV + (stage + along_mn(k)), id_inside, 1);
+                    mma_commit(&bars[kInside]);
                     mma_commit(&bars[kFree0 + s]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+        }
+        if (!ok && lane == 0) {
+            flag(p.status, kDevTimeout);
+            *abort_flag = 1;
+        }
+        // every product issued has completed before tensor memory is freed
+        if (elect_one()) mma_commit(&bars[kFinal]);
+        __syncwarp();
+        mbar_wait_bounded(&bars[kFinal], 0);
+        __syncwarp();
+    } else if (warp == 14) {
+        registers<80>();
+        // ---------------- output stores (one thread) ----------------
+        if (lane == 0) {
+            int nu = 0, ch = 0;
+            const int vpanels = p.P > 64 ? 2 : 1;
+            for (;;) {
+                if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
+                const Unit un = ring[nu & 1];
+                mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+                ++nu;
+                if (un.len < 0) break;
+                for (int c = 0; c < un.len; c += kC, ++ch) {
+                    const int s = ch & 1;
+                    if (!(ok = mbar_wait_bounded(&bars[kStaged], ch & 1))) break;
+                    // (a partial chunk's rows have been stored one by one: the
+                    // rows past its end are other tokens')
+                    if (un.len - c >= kC) {
+                        for (int i = 0; i < vpanels; ++i)
+                            tma_store_3d(&maps.out, smem + s * LY::kStage + LY::kKBytes + i * kPanel, 64 * i, un.h,
+                                         static_cast<int>(un.t0) + c);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                    mbar_arrive(&bars[kFree0 + s]);
                 }
                 if (!ok) break;
             }
+            bulk_wait_all();
             if (!ok) {
                 flag(p.status, kDevTimeout);
                 *abort_flag = 1;
             }
-            // every product issued has completed before tensor memory is freed
-            mma_commit(&bars[kFinal]);
-            mbar_wait_bounded(&bars[kFinal], 0);
         }
         __syncwarp();
-    } else if (warp >= 10) {
-        registers<72>();
+    } else if (warp == 15) {
+        registers<80>();
     } else if (warp < 4) {
-        registers<216>();
-        // ---------------- P and the outputs ----------------
-        const int row = tid;  // score row i; later value dim
+        registers<128>();
+        // ---------------- P and the outputs (thread = token) ----------------
+        const int row = tid;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        float *tab = reinterpret_cast<float *>(smem + LY::kTabA);
-        float *row_scale = reinterpret_cast<float *>(smem + LY::kRowScale);
         int nu = 0, ch = 0, ph = 0;
         for (;;) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
@@ -349,142 +430,126 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (un.len < 0) break;
             const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);  // 0 * -inf is no power
             const float g2 = g * 1.4426950408889634f;
-            // the previous unit's table is no longer read (a thread that is
-            // here has stored its last output, the others are past theirs
-            // once all have met)
-            if (!(ok = group_sync(&bars[kSyncA], ph))) break;
-            tab[row] = p.scale * expf(g * static_cast<float>(row + 1));
+            const float enter = p.scale * expf(g * static_cast<float>(row + 1));
             float fall[32];  // l^(31 - jj): from a column of a block to the block's last
 #pragma unroll
             for (int jj = 0; jj < 32; ++jj) fall[jj] = ex2(g2 * static_cast<float>(31 - jj));
-            if (!(ok = group_sync(&bars[kSyncA], ph))) break;
-            unsigned short *out = static_cast<unsigned short *>(p.out) + un.h * p.os[1];
+            unsigned short *out = static_cast<unsigned short *>(p.out) + un.h * p.os[1] + un.t0 * p.os[0];
             for (int c = 0; c < un.len; c += kC, ++ch) {
-                const int n = min(kC, un.len - c);
+                const int s = ch & 1, n = min(kC, un.len - c);
                 if (!(ok = mbar_wait_bounded(&bars[kScore], ch & 1))) break;
                 tc_fence_after();
-                // row i of P: l^(i-j) score for j <= i.  A block of 32 columns
-                // before the warp's rows factors through its last column, both
-                // powers at most 1; the block on the diagonal takes one power
-                // a score.
-                uint32_t pr[64];
-                float mx = 0.f;
-                float pv[BF ? 1 : 128];
+                // Row i of P: scale l^(i-j) score for j <= i.  A block of 32
+                // columns before the warp's rows factors through its last
+                // column, both powers at most 1; the block on the diagonal
+                // takes one power a score.
+                const auto decayed = [&](int b, float *e) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + lanes + kColScore + 32 * b, r);
+                    tmem_wait_ld();
+                    if (b < warp) {
+                        const float f = p.scale * ex2(g2 * static_cast<float>(row - 32 * b - 31));
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b <= warp) {
-                        uint32_t r[32];
-                        tmem_ld32(tmem + lanes + kColScore + 32 * b, r);
-                        tmem_wait_ld();
-                        float e[32];
-                        if (b < warp) {
-                            const float f = ex2(g2 * static_cast<float>(row - 32 * b - 31));
-#pragma unroll
-                            for (int jj = 0; jj < 32; ++jj) e[jj] = __uint_as_float(r[jj]) * (f * fall[jj]);
-                        } else {
-#pragma unroll
-                            for (int jj = 0; jj < 32; ++jj) {
-                                const float w = ex2(g2 * static_cast<float>(max(lane - jj, 0)));
-                                e[jj] = jj <= lane ? __uint_as_float(r[jj]) * w : 0.f;
-                            }
-                        }
-                        if constexpr (BF) {
-#pragma unroll
-                            for (int jj = 0; jj < 16; ++jj) pr[16 * b + jj] = pack2<BF>(e[2 * jj], e[2 * jj + 1]);
-                        } else {
-#pragma unroll
-                            for (int jj = 0; jj < 32; ++jj) {
-                                pv[(32 * b + jj) % (BF ? 1 : 128)] = e[jj];
-                                mx = fmaxf(mx, fabsf(e[jj]));
-                            }
-                        }
+                        for (int jj = 0; jj < 32; ++jj) e[jj] = __uint_as_float(r[jj]) * (f * fall[jj]);
                     } else {
 #pragma unroll
-                        for (int jj = 0; jj < 16; ++jj) pr[16 * b + jj] = 0u;
-                        if constexpr (!BF) {
-#pragma unroll
-                            for (int jj = 0; jj < 32; ++jj) pv[(32 * b + jj) % (BF ? 1 : 128)] = 0.f;
+                        for (int jj = 0; jj < 32; ++jj) {
+                            const float w = p.scale * ex2(g2 * static_cast<float>(max(lane - jj, 0)));
+                            e[jj] = jj <= lane ? __uint_as_float(r[jj]) * w : 0.f;
                         }
                     }
-                }
+                };
+                float up = 1.f, down = 1.f;  // fp16: the row's power of two
                 if constexpr (!BF) {
-                    const int k = fp16_scale_exp(mx);
-                    const float sc = pow2i(k);
+                    float m = 0.f;
 #pragma unroll
-                    for (int jj = 0; jj < 64; ++jj)
-                        pr[jj] = pack2<BF>(pv[(2 * jj) % (BF ? 1 : 128)] * sc, pv[(2 * jj + 1) % (BF ? 1 : 128)] * sc);
-                    row_scale[128 + row] = p.scale * pow2i(-k);
+                    for (int b = 0; b < 4; ++b) {
+                        if (b > warp) break;
+                        float e[32];
+                        decayed(b, e);
+#pragma unroll
+                        for (int jj = 0; jj < 32; ++jj) m = fmaxf(m, fabsf(e[jj]));
+                    }
+                    // (not so far up that the entering product, scaled alike, could overflow)
+                    const int k = min(fp16_scale_exp(m), 40);
+                    up = pow2i(k);
+                    down = pow2i(-k);
                 }
-                unsigned char *prow = smem + LY::kP + row * 128;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    *reinterpret_cast<uint4 *>(prow + (j / 8) * kPanel + (((j % 8) ^ (row & 7)) * 16)) =
-                        make_uint4(pr[4 * j], pr[4 * j + 1], pr[4 * j + 2], pr[4 * j + 3]);
-                fence_proxy_async_smem();
-                // what the entering state contributes
-                if (!(ok = mbar_wait_bounded(&bars[kEnter], ch & 1))) break;
-                tc_fence_after();
-                float hold[128];
-                const float back = BF ? 1.f : row_scale[row];
+                // (block b of P takes columns whose scores, of block b / 2, are read)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
+                    uint32_t pr[16];
+                    if (b <= warp) {
+                        float e[32];
+                        decayed(b, e);
+#pragma unroll
+                        for (int jj = 0; jj < 16; ++jj)
+                            pr[jj] = BF ? pack2<BF>(e[2 * jj], e[2 * jj + 1]) : pack2<BF>(e[2 * jj] * up, e[2 * jj + 1] * up);
+                    } else {
+#pragma unroll
+                        for (int jj = 0; jj < 16; ++jj) pr[jj] = 0u;
+                    }
+                    tmem_st16(tmem + lanes + kColScore + 16 * b, pr);
+                }
+                // the entering product's row, scaled in its place
+                if (!(ok = mbar_wait_bounded(&bars[kEnter], ch & 1))) break;
+                tc_fence_after();
+                const float f = enter * up;
+                // (fp16: value dim p's state row was scaled; written before the
+                // product that has just completed was issued)
+                const float *rs = row_scale + (ch & 1) * 128;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (32 * b >= p.P) break;
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColOut + 32 * b, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int jj = 0; jj < 32; jj += 4) {
-                        const float4 t = *reinterpret_cast<const float4 *>(tab + 32 * b + jj);
-                        hold[32 * b + jj] = __uint_as_float(r[jj]) * back * t.x;
-                        hold[32 * b + jj + 1] = __uint_as_float(r[jj + 1]) * back * t.y;
-                        hold[32 * b + jj + 2] = __uint_as_float(r[jj + 2]) * back * t.z;
-                        hold[32 * b + jj + 3] = __uint_as_float(r[jj + 3]) * back * t.w;
-                    }
+                    for (int jj = 0; jj < 32; ++jj)
+                        r[jj] = __float_as_uint(__uint_as_float(r[jj]) * (BF ? f : f * rs[32 * b + jj]));
+                    tmem_st32(tmem + lanes + kColOut + 32 * b, r);
                 }
+                tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars[kPFull]);
                 if (!(ok = mbar_wait_bounded(&bars[kInside], ch & 1))) break;
-                // (fp16) the other rows' scales, by their own arrivals
-                if (!BF && !(ok = mbar_wait_bounded(&bars[kPFull], ch & 1))) break;
                 tc_fence_after();
-                // outputs [token][value dim] in P's place, then 16 bytes a
-                // store along each token's row
-                unsigned short *stage = reinterpret_cast<unsigned short *>(smem + LY::kP) + row;
+                // Outputs by token where V was (its products are done), laid
+                // out for a tiled copy: a thread's own row, 16 bytes at a time,
+                // would touch 32 lines a store.
+                unsigned char *rows = smem + s * LY::kStage + LY::kKBytes, *mine = rows + row * 128;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
+                    if (32 * b >= p.P) break;
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColOut + 32 * b, r);
                     tmem_wait_ld();
-                    if (b == 3) {
+                    if (32 * b + 32 >= p.P) {
                         tc_fence_before();
                         mbar_arrive(&bars[kOutFree]);
                     }
 #pragma unroll
-                    for (int jj = 0; jj < 32; jj += 2) {
-                        float s0 = p.scale, s1 = p.scale;
-                        if constexpr (!BF) {
-                            const float2 two = *reinterpret_cast<const float2 *>(row_scale + 128 + 32 * b + jj);
-                            s0 = two.x;
-                            s1 = two.y;
-                        }
-                        const uint32_t two = pack2<BF>(fmaf(__uint_as_float(r[jj]), s0, hold[32 * b + jj]),
-                                                       fmaf(__uint_as_float(r[jj + 1]), s1, hold[32 * b + jj + 1]));
-                        stage[(32 * b + jj) * 128] = static_cast<unsigned short>(two);
-                        stage[(32 * b + jj + 1) * 128] = static_cast<unsigned short>(two >> 16);
+                    for (int jj = 0; jj < 16; ++jj) {
+                        float x = __uint_as_float(r[2 * jj]), y = __uint_as_float(r[2 * jj + 1]);
+                        if constexpr (!BF) x *= down, y *= down;
+                        r[jj] = pack2<BF>(x, y);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(mine + (b / 2) * kPanel + (((4 * (b % 2) + j) ^ (row & 7)) * 16)) =
+                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                }
+                fence_proxy_async_smem();
+                if (n < kC) {
+                    if (!(ok = group_sync(&bars[kSyncA], ph))) break;
+                    const int piece = tid & 15;  // 16 threads store a token's row
+                    if (8 * piece < p.P) {
+                        for (int i = tid >> 4; i < n; i += kGroup / 16)
+                            *reinterpret_cast<uint4 *>(out + (c + i) * p.os[0] + 8 * piece) = *reinterpret_cast<const uint4 *>(
+                                rows + (piece / 8) * kPanel + i * 128 + (((piece % 8) ^ (i & 7)) * 16));
                     }
                 }
-                if (!(ok = group_sync(&bars[kSyncA], ph))) break;
-                const int piece = tid & 15, tok = tid >> 4;
-                unsigned short *o = out + (un.t0 + c + tok) * p.os[0] + 8 * piece;
-                const unsigned char *from = smem + LY::kP + tid * 16;
-                const int64_t step = 8 * p.os[0];
-                if (8 * piece < p.P) {
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i)
-                        if (tok + 8 * i < n)
-                            *reinterpret_cast<uint4 *>(o + i * step) = *reinterpret_cast<const uint4 *>(from + i * 2048);
-                }
-                // P's place, and the score rows' scales, are read
-                if (!(ok = group_sync(&bars[kSyncA], ph))) break;
+                mbar_arrive(&bars[kStaged]);
             }
             if (!ok) break;
         }
@@ -492,15 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) flag(p.status, kDevTimeout);
             *abort_flag = 1;
         }
-    } else {
-        registers<216>();
-        // ---------------- the state and the decayed values ----------------
-        const int t = tid - kGroup, w = warp - 4;  // value dim
+    } else if (warp < 8) {
+        registers<208>();
+        // ---------------- the state (thread = value dim) ----------------
+        const int t = tid - kGroup, w = warp - 4;
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-        float *tab = reinterpret_cast<float *>(smem + LY::kTabB);
-        float *row_scale = reinterpret_cast<float *>(smem + LY::kRowScale);
-        float *maxes = reinterpret_cast<float *>(smem + LY::kMax);
-        int nu = 0, ch = 0, quarters = 0, ph = 0;
+        int nu = 0, ch = 0;
         float S[DK];
         for (;;) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
@@ -509,9 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nu;
             if (un.len < 0) break;
             const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
-            if (!(ok = group_sync(&bars[kSyncB], ph))) break;  // the previous unit's table is no longer read
-            tab[t] = expf(g * static_cast<float>(kC - 1 - t));
-            if (t < kQuarter) tab[kC + t] = 0.f;
             const float lam_chunk = expf(g * static_cast<float>(kC));
             // the entering state: this thread's row
 #pragma unroll
@@ -533,11 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i < p.N) StateChunk<__half>::unpack(ld_stream(static_cast<const __half *>(p.state) + at + i), S + i);
                 }
             }
-            if (!(ok = group_sync(&bars[kSyncB], ph))) break;
             for (int c = 0; c < un.len; c += kC, ++ch) {
-                const int s = ch & 1, n = min(kC, un.len - c);
-                // S in two parts, for the entering product (where the last
-                // chunk's decayed V was, which its growth product has read)
+                const int n = min(kC, un.len - c);
+                // S in two parts, once the last entering product has read its own
                 float sc = 1.f;
                 if constexpr (!BF) {
                     float m = 0.f;
@@ -545,134 +602,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < DK; ++i) m = fmaxf(m, fabsf(S[i]));
                     const int k = fp16_scale_exp(m);
                     sc = pow2i(k);
-                    // read before kPFull, which the growth product that this
-                    // thread waits for below comes after
-                    row_scale[t] = pow2i(-k);
+                    row_scale[(ch & 1) * 128 + t] = pow2i(-k);
                 }
+                if (ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
+                unsigned char *srow = smem + LY::kS + t * 128;
 #pragma unroll
-                for (int b = 0; b < DK / 32; ++b) {
-                    uint32_t hi[16], lo[16];
+                for (int j = 0; j < DK / 8; ++j) {
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = S[32 * b + 2 * i] * sc, y = S[32 * b + 2 * i + 1] * sc;
-                        hi[i] = pack2<BF>(x, y);
-                        const float2 f = unpack2<BF>(hi[i]);
-                        lo[i] = pack2<BF>(x - f.x, y - f.y);
+                    for (int i = 0; i < 4; ++i) {
+                        float x = S[8 * j + 2 * i] * sc, y = S[8 * j + 2 * i + 1] * sc;
+                        hi[i] = split2<BF>(x, y);
+                        lo[i] = pack2<BF>(x, y);
                     }
-                    tmem_st16(tmem + lanes + kColState + 16 * b, hi);
-                    tmem_st16(tmem + lanes + kColState + DK / 2 + 16 * b, lo);
+                    unsigned char *d = srow + (j / 8) * kPanel + (((j % 8) ^ (t & 7)) * 16);
+                    *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(d + LY::kKBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
+                fence_proxy_async_smem();
                 mbar_arrive(&bars[kStateFull]);
-                if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
-                unsigned char *sK = smem + s * LY::kStage + LY::kQBytes, *sV = sK + LY::kKBytes;
-                if (n < kC) {
-                    // rows past the piece's end belong to other tokens: a
-                    // weight of zero would still let their NaN through
-                    constexpr int kPanels = DK / 64 + 2;
-                    for (int i = t; i < (kC - n) * 8 * kPanels; i += kGroup) {
-                        const int at = i % ((kC - n) * 8);
-                        *reinterpret_cast<uint4 *>(sK + (i / ((kC - n) * 8)) * kPanel + n * 128 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&bars[kTail]);
-                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;  // every thread's zeros, below
-                }
-                float vs = 1.f, vback = 1.f;
-                if constexpr (!BF) {
-                    // the power of two that brings the tile's largest |v| near fp16's top
-                    uint32_t m2 = 0u;
-                    for (int i = t; i < 2 * kPanel / 16; i += kGroup) {
-                        if ((i % (kPanel / 16)) / 8 >= n) continue;
-                        const uint4 u = *reinterpret_cast<const uint4 *>(sV + i * 16);
-                        const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t a = ws[e] & 0x7fff7fffu;
-                            m2 = __vmaxu2(m2, a);  // magnitudes order as their bits
-                        }
-                    }
-                    float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
-                                    __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    if (lane == 0) maxes[w] = m;
-                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
-                    m = fmaxf(fmaxf(maxes[0], maxes[1]), fmaxf(maxes[2], maxes[3]));
-                    const int k = fp16_scale_exp(m);
-                    vs = pow2i(k);
-                    vback = pow2i(-k);
-                }
-                // the decayed V, 32 tokens at a time, where the parts of S were
-                if (!(ok = mbar_wait_bounded(&bars[kEnter], ch & 1))) break;
-                tc_fence_after();
-                // (column t of V: the swizzle moves its 16-byte piece with the row)
-                const unsigned char *vcol = sV + (t >> 6) * kPanel + (t & 7) * 2;
-                const int piece = ((t & 63) >> 3) * 16;
-                const float *weight = tab + (kC - n);
-                for (int q0 = 0; q0 < n; q0 += kQuarter, ++quarters) {
-                    const int r = quarters & 1;
-                    float x[kQuarter];
-#pragma unroll
-                    for (int j = 0; j < kQuarter; j += 4) {
-                        float we[4];
-                        if (n == kC) {
-                            const float4 wj = *reinterpret_cast<const float4 *>(weight + q0 + j);
-                            we[0] = wj.x, we[1] = wj.y, we[2] = wj.z, we[3] = wj.w;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) we[e] = weight[q0 + j + e];
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const unsigned short u = *reinterpret_cast<const unsigned short *>(
-                                vcol + q0 * 128 + (j + e) * 128 + (piece ^ (((j + e) & 7) * 16)));
-                            const float v =
-                                BF ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u)) * vs;
-                            x[j + e] = v * we[e];
-                        }
-                    }
-                    if (quarters >= 2 && !(ok = mbar_wait_bounded(&bars[kVFree0 + r], ((quarters >> 1) - 1) & 1))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int q = 0; q < kParts; ++q) {
-                        uint32_t part[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if constexpr (BF) {
-                                // the top 8 bits of what is left: three parts hold all 24
-                                const uint32_t a = __float_as_uint(x[2 * i]), c2 = __float_as_uint(x[2 * i + 1]);
-                                part[i] = __byte_perm(a, c2, 0x7632);
-                                x[2 * i] -= __uint_as_float(a & 0xffff0000u);
-                                x[2 * i + 1] -= __uint_as_float(c2 & 0xffff0000u);
-                            } else {
-                                part[i] = pack2<BF>(x[2 * i], x[2 * i + 1]);
-                                const float2 f = unpack2<BF>(part[i]);
-                                x[2 * i] -= f.x;
-                                x[2 * i + 1] -= f.y;
-                            }
-                        }
-                        tmem_st16(tmem + lanes + kColState + r * kRing + 16 * q, part);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&bars[kVFull0 + r]);
-                }
-                if (!ok) break;
-                mbar_arrive(&bars[kFree0 + s]);
                 if (!(ok = mbar_wait_bounded(&bars[kGrowth], ch & 1))) break;
                 tc_fence_after();
                 const float lam = n == kC ? lam_chunk : expf(g * static_cast<float>(n));
+                const float back = BF ? 1.f : maxes[4 + (ch & 3)];
 #pragma unroll
                 for (int b = 0; b < DK / 32; ++b) {
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColGrowth + 32 * b, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(S[32 * b + i], lam, __uint_as_float(r[i]) * vback);
+                    for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(S[32 * b + i], lam, BF ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * back);
                 }
                 tc_fence_before();
+                mbar_arrive(&bars[kGrowthFree]);
             }
             if (!ok) break;
             if (un.dst != kNone && t < p.P) {
@@ -696,11 +658,141 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) flag(p.status, kDevTimeout);
             *abort_flag = 1;
         }
+    } else {
+        registers<96>();
+        // ---------------- the decayed values (warp = 32 value dims) ----------------
+        const int t = tid - 2 * kGroup, w = warp - 8;
+        const bool live = 32 * w < p.P;
+        int nu = 0, ch = 0, quarters = 0, ph = 0;
+        // this lane's row of the matrices it loads: token lane % 8 of token
+        // block lane / 16 of two, 8 value dims of block (lane / 8) % 2; the
+        // swizzle moves the 16-byte piece with the token
+        const int dim0 = 32 * w + 8 * ((lane >> 3) & 1);
+        uint32_t at[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int d = dim0 + 16 * hh;
+            at[hh] = smem_addr(smem) + LY::kKBytes + (d >> 6) * kPanel + ((lane & 7) + 8 * (lane >> 4)) * 128 +
+                     ((((d & 63) >> 3) ^ (lane & 7)) * 16);
+        }
+        for (;;) {
+            if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
+            const Unit un = ring[nu & 1];
+            mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+            ++nu;
+            if (un.len < 0) break;
+            const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
+            float fall[8];  // l^(31 - j) of this lane's tokens j = 8 b + 2 (lane % 4) + e of a quarter
+            float first[4];  // l^(96 - 32 quarter): from a quarter's last token to a full chunk's
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fall[i] = expf(g * static_cast<float>(31 - 8 * (i >> 1) - 2 * (lane & 3) - (i & 1)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) first[i] = expf(g * static_cast<float>(96 - 32 * i));
+            for (int c = 0; c < un.len; c += kC, ++ch) {
+                const int s = ch & 1, n = min(kC, un.len - c);
+                if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
+                unsigned char *sK = smem + s * LY::kStage;
+                if (n < kC) {
+                    // rows past the sequence's end belong to other tokens: a
+                    // weight of zero would still let their NaN through
+                    const int rows = (kC - n) * 8;
+                    for (int i = t; i < rows * (LY::kPanels + 2); i += kGroup)
+                        *reinterpret_cast<uint4 *>(sK + (i / rows) * kPanel + n * 128 + (i % rows) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[kTail]);
+                    if (!(ok = group_sync(&bars[kSyncC], ph))) break;  // every thread's zeros, below
+                }
+                float vs = 1.f;
+                if constexpr (!BF) {
+                    // the power of two that brings the tile's largest |v| near fp16's top
+                    uint32_t m2 = 0u;
+                    const int pieces = (p.P > 64 ? 2 : 1) * (kPanel / 16);
+                    for (int i = t; i < pieces; i += kGroup) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(sK + LY::kKBytes + i * 16);
+                        const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, ws[e] & 0x7fff7fffu);  // magnitudes order as their bits
+                    }
+                    float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
+                                    __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    if (lane == 0) maxes[w] = m;
+                    if (!(ok = group_sync(&bars[kSyncC], ph))) break;
+                    m = fmaxf(fmaxf(maxes[0], maxes[1]), fmaxf(maxes[2], maxes[3]));
+                    const int k = fp16_scale_exp(m);
+                    vs = pow2i(k);
+                    if (t == 0) maxes[4 + (ch & 3)] = pow2i(-k);
+                    if (!(ok = group_sync(&bars[kSyncC], ph))) break;  // the maxima are read
+                }
+                const uint32_t stage = s * LY::kStage;
+#pragma unroll
+                for (int qd = 0; qd < 4; ++qd) {
+                    if (qd * kQuarter >= n) break;
+                    const int r = quarters & 1;
+                    float wt[8];
+                    if (n == kC) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) wt[i] = first[qd] * fall[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int left = n - 1 - (qd * kQuarter + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1));
+                            wt[i] = left >= 0 ? expf(g * static_cast<float>(left)) : 0.f;
+                        }
+                    }
+                    if constexpr (!BF) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) wt[i] *= vs;
+                    }
+                    uint32_t v[2][8];
+                    if (live) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            ldmatrix_x4_trans(at[hh] + stage + qd * kQuarter * 128, v[hh]);
+                            ldmatrix_x4_trans(at[hh] + stage + (qd * kQuarter + 16) * 128, v[hh] + 4);
+                        }
+                    }
+                    if (quarters >= 2 && !(ok = mbar_wait_bounded(&bars[kVFree0 + r], ((quarters >> 1) - 1) & 1))) break;
+                    ++quarters;
+                    tc_fence_after();
+                    if (live) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            float x[8], y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 f = unpack2<BF>(v[hh][i]);
+                                x[i] = f.x * wt[2 * (i >> 1)];
+                                y[i] = f.y * wt[2 * (i >> 1) + 1];
+                            }
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q) {
+                                uint32_t part[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) part[i] = split2<BF>(x[i], y[i]);
+                                tmem_st_16x128b_x4(tmem + (static_cast<uint32_t>(32 * w + 16 * hh) << 16) + kColV + r * kRing + 16 * q, part);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&bars[kVFull0 + r]);
+                }
+                if (!ok) break;
+                mbar_arrive(&bars[kFree0 + s]);
+            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            if (lane == 0) flag(p.status, kDevTimeout);
+            *abort_flag = 1;
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc512(tmem);
+    if (warp == 12) tmem_dealloc512(tmem);
 }
 
 // The driver's tensor-map encoder, looked up once.
@@ -751,7 +843,7 @@ template <int DK, bool BF>
 cudaError_t launch_t(const LinattnParams &p, cudaStream_t stream) {
     Maps maps;
     if (p.rows > 0 && !(encode(&maps.q, p, p.q, p.N, p.H, p.qs) && encode(&maps.k, p, p.k, p.N, p.G, p.ks) &&
-                        encode(&maps.v, p, p.v, p.P, p.G, p.vs)))
+                        encode(&maps.v, p, p.v, p.P, p.G, p.vs) && encode(&maps.out, p, p.out, p.P, p.H, p.os)))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(linattn_prefill_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Layout<DK>::kBytes);

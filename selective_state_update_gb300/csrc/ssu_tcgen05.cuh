@@ -129,14 +129,49 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t panel
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
-// D[tmem] (+)= A[tmem] B[smem]: row m of A in lane m, two 16-bit elements
-// along K a column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// True in one lane of a converged warp.  tcgen05.commit tracks the operations
+// of the thread that issues it: the same lane issues both.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// A matrix descriptor as two words: the high one is the same for every start
+// address, so a loop over K steps adds to the low one only (16-byte units).
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d)
+        : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+    __device__ __forceinline__ Desc operator+(uint32_t units) const {
+        Desc d = *this;
+        d.lo += units;
+        return d;
+    }
+};
+// D[tmem] (+)= A[smem] B[smem].
+__device__ __forceinline__ void mma(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]: row m of A in lane m, two 16-bit elements
+// along K a column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc)
         : "memory");
 }
 
@@ -171,6 +206,13 @@ __device__ __forceinline__ void tma_load_3d(void *dst_smem, const void *map, int
             smem_addr(dst_smem)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
+}
+// Tiled copy shared -> global of a 3-D box, in this thread's bulk group; what
+// lies outside the tensor is not written.  No coordinate is negative.
+__device__ __forceinline__ void tma_store_3d(const void *map, const void *src_smem, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(smem_addr(src_smem))
+                 : "memory");
 }
 
 }  // namespace ssu
