@@ -577,7 +577,7 @@ ssu_status ssu_linear_attention_workspace_size(const ssu_linattn_args *args, int
     ssu::LinattnParams lp;
     const ssu_status st = linattn_prepare(args, nullptr, nullptr, &lp);
     if (st != SSU_OK) return st;
-    *bytes = 0;
+    *bytes = ssu::linattn_split(lp.rows, nseq, lp.H, lp.P, lp.N, max_seqlen).bytes;
     return ok();
 }
 
@@ -585,7 +585,6 @@ ssu_status ssu_linear_attention_prefill(const ssu_linattn_args *args, int64_t ns
                                         int32_t meta_type, int64_t max_seqlen, const ssu_slot_table *read,
                                         const ssu_slot_table *dst, void *workspace, uint64_t workspace_bytes,
                                         void *stream) {
-    (void)workspace, (void)workspace_bytes;
     if (nseq < 0 || max_seqlen < 0) return fail(SSU_ERR_INVALID, "nseq and max_seqlen must not be negative");
     ssu::LinattnParams lp;
     ssu_status st = linattn_prepare(args, read, dst, &lp);
@@ -602,12 +601,19 @@ ssu_status ssu_linear_attention_prefill(const ssu_linattn_args *args, int64_t ns
                 return fail(SSU_ERR_INVALID, "the strides of q, k, v and out must be multiples of 8");
     }
     if (lp.rows >= kMaxGrid) return fail(SSU_ERR_INVALID, "more than 2^31-1 tokens");
-    if (nseq > kMaxGrid / (4 * lp.H)) return fail(SSU_ERR_INVALID, "too many sequences and heads for one launch");
+    if (nseq > kMaxGrid / (4 * lp.H) || lp.rows / 128 > kMaxGrid / (4 * lp.H))
+        return fail(SSU_ERR_INVALID, "too many sequences, tokens and heads for one call");
+    const ssu::LinattnSplit split = ssu::linattn_split(lp.rows, nseq, lp.H, lp.P, lp.N, max_seqlen);
+    if (split.bytes > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+        return fail(SSU_ERR_INVALID, "workspace must be a 256-byte aligned device pointer");
+    if (workspace_bytes < split.bytes)
+        return fail(SSU_ERR_INVALID, "workspace of %llu bytes is smaller than the %llu needed",
+                    (unsigned long long)workspace_bytes, (unsigned long long)split.bytes);
     lp.nseq = nseq;
     lp.cu = cu_seqlens;
     lp.meta_is_i64 = meta_type == SSU_I64;
     if ((st = check_device(args->state)) != SSU_OK) return st;
-    return launched(ssu::launch_linattn_prefill(lp, static_cast<cudaStream_t>(stream)));
+    return launched(ssu::launch_linattn_prefill(lp, split, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 ssu_status ssu_add_rmsnorm(const ssu_norm_args *a, void *stream) {

@@ -35,7 +35,15 @@ struct LinattnParams {
 constexpr int kLinattnMaxDim = 128;  // largest dim and dstate
 
 cudaError_t launch_linattn_step(const LinattnParams &p, cudaStream_t stream);
-cudaError_t launch_linattn_prefill(const LinattnParams &p, cudaStream_t stream);
+// How a prefill is split over the GPU, and the workspace it needs for that:
+// byte offsets of its parts (bytes == 0: none, one unit per CTA).
+struct LinattnSplit {
+    int64_t cut_len;   // sequences longer than this are cut
+    int64_t max_cuts;  // most sequences that can be
+    uint64_t cuts, pieces, states, bytes;
+};
+LinattnSplit linattn_split(int64_t rows, int64_t nseq, int64_t heads, int64_t dim, int64_t dstate, int64_t max_seqlen);
+cudaError_t launch_linattn_prefill(const LinattnParams &p, const LinattnSplit &split, void *workspace, cudaStream_t stream);
 
 // RMS norm (ssu_norm.cu).
 enum : int32_t { kQuantNone = 0, kQuantRow = 1, kQuantBlock = 2 };

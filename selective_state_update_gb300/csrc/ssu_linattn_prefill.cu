@@ -6,8 +6,16 @@
 // state that enters it:
 //     out_i = scale (l^(i+1) S q_i + sum_{j<=i} l^(i-j) (q_i . k_j) v_j)
 //     S'    = l^n S + sum_j l^(n-1-j) v_j k_j^T
-// A work unit is one sequence for one head; a CTA walks its chunks and carries
-// S in registers.
+// A work unit is one piece of a sequence -- the whole of it, or an equal part of
+// a long one -- for one head; a CTA walks its chunks and carries S in registers.
+//
+// Calls with more (sequence, head) pairs than SMs are planned by a small kernel
+// first: it checks the metadata, cuts sequences longer than a given length into
+// pieces and orders the pieces by length, longest first, from where the CTAs
+// take them in turn.  Where sequences are cut, two more kernels run before the
+// main one: this one again for what each piece adds to the state (the growth
+// products alone), and a pass along each cut sequence that turns those into
+// the states that enter its pieces.
 //
 // Four products a chunk, tcgen05.mma with fp32 accumulators in tensor memory:
 //   scores   [i, j]  = Q K^T            Q, K from shared memory, as loaded
@@ -52,12 +60,29 @@ constexpr uint32_t kRing = 48;  // columns of one quarter: up to 3 parts of 16
 
 struct Unit {
     int64_t t0;   // first token row
-    int64_t src;  // state entering: pool slot or kZero
+    int64_t src;  // state entering: pool slot, kZero, or kScratch + state of the workspace
     int64_t dst;  // state leaving: pool slot or kNone
     int32_t len;  // tokens; -1: no more units
-    int32_t h;
+    int32_t h;    // head; in the plan: not the last piece of its sequence
 };
-constexpr int64_t kZero = -1, kNone = -1;
+constexpr int64_t kZero = -1, kNone = -1, kScratch = int64_t(1) << 62;
+
+// The plan in the workspace: counters, the cut sequences, the pieces.
+struct Cut {
+    int32_t state, pieces;  // first workspace state, number of pieces
+    int64_t src, len;       // the sequence's first state and length
+};
+struct PlanHead {
+    int32_t pieces, cuts;
+    int32_t next[2];  // the next unit of the growth pass and of the main one
+};
+struct Plan {
+    PlanHead *head;  // nullptr: a unit is (sequence, head), found on the spot
+    Cut *cuts;
+    Unit *pieces;
+    float *states;   // [state][head][dim][dstate]
+    int64_t cut_len;  // longest piece, a multiple of kC
+};
 
 enum : int {
     kQFull, kQFree,
@@ -172,11 +197,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     tmem_st16(taddr + 16, r + 16);
 }
 
-// Finds unit u of the call: the sequence's bounds and slots.  False (and
-// flagged) when it is to be skipped.
-__device__ __forceinline__ bool find_unit(const LinattnParams &p, int64_t u, Unit &out) {
-    const int64_t b = u / p.H;
-    out.h = static_cast<int>(u - b * p.H);
+// Sequence b: its bounds and slots.  False (and flagged) when it is to be
+// skipped.
+__device__ __forceinline__ bool find_sequence(const LinattnParams &p, int64_t b, Unit &out) {
     const int64_t t0 = load_index(p.cu, b, p.meta_is_i64), t1 = load_index(p.cu, b + 1, p.meta_is_i64);
     KParams kp{};
     kp.slots = p.slots;
@@ -198,9 +221,118 @@ __device__ __forceinline__ bool find_unit(const LinattnParams &p, int64_t u, Uni
     return ok;
 }
 
-template <int DK, bool BF>
+// How a sequence of `len` tokens is cut: pieces of `step` tokens, the last one
+// shorter.
+__device__ __forceinline__ int piece_count(int64_t len, int64_t cut_len) {
+    return len <= cut_len ? 1 : static_cast<int>((len + cut_len - 1) / cut_len);
+}
+__device__ __forceinline__ int64_t piece_step(int64_t len, int pieces) {
+    return ((len + pieces - 1) / pieces + kC - 1) / kC * kC;
+}
+
+// One CTA: pieces counted into buckets by their chunks, then placed, longest
+// first (the order within a bucket is free: it decides who works when, not on
+// what).
+constexpr int kPlanThreads = 1024, kBuckets = 1024;
+__global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const LinattnParams p, const Plan plan, int grid) {
+    __shared__ int start[kBuckets];
+    __shared__ int warp_sum[32];
+    __shared__ int states, cuts;
+    const int tid = threadIdx.x;
+    start[tid] = 0;
+    if (tid == 0) states = cuts = 0;
+    __syncthreads();
+    const auto bucket = [](int64_t len) { return kBuckets - 1 - static_cast<int>(min((len + kC - 1) / kC, int64_t(kBuckets - 1))); };
+    // step s of a cut sequence may leave fewer pieces than counted: n pieces of
+    // `step` tokens, the last of what is left
+    const auto each = [&](const Unit &un, auto f) {
+        const int n0 = piece_count(un.len, plan.cut_len);
+        const int64_t step = n0 == 1 ? un.len : piece_step(un.len, n0);
+        const int n = n0 == 1 ? 1 : static_cast<int>((un.len + step - 1) / step);
+        for (int i = 0; i < n; ++i) f(i, n, min(step, un.len - i * step), i * step);
+    };
+    for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
+        Unit un;
+        if (!find_sequence(p, b, un)) continue;
+        each(un, [&](int, int, int64_t len, int64_t) { atomicAdd(&start[bucket(len)], 1); });
+    }
+    __syncthreads();
+    // exclusive prefix sum of the buckets
+    const int lane = tid & 31, warp = tid >> 5, mine = start[tid];
+    int sum = mine;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    start[tid] = before + sum - mine;
+    __syncthreads();
+    for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
+        Unit un;
+        LinattnParams quiet = p;
+        quiet.status = nullptr;  // flagged above
+        if (!find_sequence(quiet, b, un)) continue;
+        int state = 0, cut = 0;
+        each(un, [&](int i, int n, int64_t len, int64_t off) {
+            if (i == 0 && n > 1) {
+                state = atomicAdd(&states, n);
+                cut = atomicAdd(&cuts, 1);
+                plan.cuts[cut] = Cut{state, n, un.src, un.len};
+            }
+            Unit piece;
+            piece.t0 = un.t0 + off;
+            piece.len = static_cast<int>(len);
+            piece.src = n > 1 ? kScratch + state + i : un.src;
+            piece.dst = i == n - 1 ? un.dst : kNone;
+            piece.h = i < n - 1;
+            plan.pieces[atomicAdd(&start[bucket(len)], 1)] = piece;
+        });
+    }
+    __syncthreads();
+    if (tid == 0) *plan.head = PlanHead{total, cuts, {grid, grid}};
+}
+
+// Along each cut sequence: what its pieces add becomes what enters them.
+__global__ void __launch_bounds__(256) linattn_carry_kernel(const LinattnParams p, const Plan plan) {
+    if (static_cast<int>(blockIdx.z) >= plan.head->cuts) return;
+    const Cut cut = plan.cuts[blockIdx.z];
+    const int h = blockIdx.y;
+    const int64_t elems = static_cast<int64_t>(p.P) * p.N, at = (blockIdx.x * 256 + threadIdx.x) * int64_t(4);
+    if (at >= elems) return;
+    const float g = fmaxf(__ldg(p.log_decay + h), -1e30f);
+    const int64_t step = piece_step(cut.len, piece_count(cut.len, plan.cut_len));
+    const float lam = expf(g * static_cast<float>(step));
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (cut.src != kZero) {
+        const int64_t i = (cut.src * p.H + h) * elems + at;
+        for (int e = 0; e < 4; ++e)
+            s[e] = p.state_dtype == kF32 ? static_cast<const float *>(p.state)[i + e]
+                                         : bits_to_float(static_cast<const unsigned short *>(p.state)[i + e], p.state_dtype);
+    }
+    float4 *w = reinterpret_cast<float4 *>(plan.states + (static_cast<int64_t>(cut.state) * p.H + h) * elems + at);
+    const int64_t stride = p.H * elems / 4;
+#pragma unroll 4
+    for (int i = 0; i < cut.pieces; ++i, w += stride) {
+        float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < cut.pieces - 1) add = *w;
+        *w = make_float4(s[0], s[1], s[2], s[3]);
+        s[0] = fmaf(s[0], lam, add.x);
+        s[1] = fmaf(s[1], lam, add.y);
+        s[2] = fmaf(s[2], lam, add.z);
+        s[3] = fmaf(s[3], lam, add.w);
+    }
+}
+
+// GROW: only what the pieces add to the state, into the workspace.
+template <int DK, bool BF, bool GROW>
 __global__ void __launch_bounds__(kThreads, 1)
-    linattn_prefill_kernel(const LinattnParams p, const __grid_constant__ Maps maps, int64_t units) {
+    linattn_prefill_kernel(const LinattnParams p, const __grid_constant__ Maps maps, const Plan plan) {
     using LY = Layout<DK>;
     constexpr int kParts = BF ? 3 : 2;  // parts of the decayed V
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -215,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
-            if (i == kFree0 || i == kFree1) n = 2 + kGroup;
-            if (i == kUnitFree0 || i == kUnitFree1) n = 2 + 3 * kGroup;
+            if (i == kFree0 || i == kFree1) n = (GROW ? 1 : 2) + kGroup;
+            if (i == kUnitFree0 || i == kUnitFree1) n = GROW ? 1 + 2 * kGroup : 2 + 3 * kGroup;
             if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail || i == kVFull0 || i == kVFull1 ||
                 i == kGrowthFree || i == kSyncA || i == kSyncC)
                 n = kGroup;
@@ -239,11 +371,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int nu = 0, ch = 0, nq = 0;  // units published, chunks loaded (K and V, Q)
             const int vpanels = p.P > 64 ? 2 : 1;
-            for (int64_t u = blockIdx.x;; u += gridDim.x) {
+            const int64_t units = (plan.head ? plan.head->pieces : p.nseq) * p.H;
+            for (int64_t u = blockIdx.x;;
+                 u = plan.head ? atomicAdd(&plan.head->next[GROW ? 0 : 1], 1) : u + gridDim.x) {
                 Unit un;
                 const bool end = u >= units;
-                if (end) un.len = -1;
-                else if (!find_unit(p, u, un)) continue;
+                if (end) {
+                    un.len = -1;
+                } else {
+                    const int64_t b = u / p.H;
+                    if (plan.head) {
+                        un = plan.pieces[b];
+                        if (GROW && un.h == 0) continue;
+                    } else if (!find_sequence(p, b, un)) {
+                        continue;
+                    }
+                    un.h = static_cast<int>(u - b * p.H);
+                }
                 if (nu >= 2 && !(ok = mbar_wait_bounded(&bars[kUnitFree0 + (nu & 1)], ((nu >> 1) - 1) & 1))) break;
                 ring[nu & 1] = un;
                 mbar_arrive(&bars[kUnitFull0 + (nu & 1)]);
@@ -261,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(st + i * kPanel, &maps.k, 64 * i, g, row, &bars[kFull0 + s]);
                     for (int i = 0; i < vpanels; ++i)
                         tma_load_3d(st + LY::kKBytes + i * kPanel, &maps.v, 64 * i, g, row, &bars[kFull0 + s]);
+                    if constexpr (GROW) continue;
                     if (ch >= 1 && !(ok = mbar_wait_bounded(&bars[kQFree], (ch - 1) & 1))) {
                         ++ch;  // its K and V are on their way
                         break;
@@ -312,8 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = ch & 1, n = min(kC, len - c), steps = (n + 15) / 16;
                 const uint32_t stage = static_cast<uint32_t>(s * (LY::kStage >> 4));
                 // scores; P of the last chunk, in their place, has been read
-                if (!(ok = wait(kFull0 + s, ch >> 1) && wait(kQFull, ch) && (ch == 0 || wait(kInside, ch - 1)))) break;
-                if (elect_one()) {
+                if (!(ok = wait(kFull0 + s, ch >> 1))) break;
+                if (!GROW && !(ok = wait(kQFull, ch) && (ch == 0 || wait(kInside, ch - 1)))) break;
+                if (!GROW && elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k)
                         if (k < ksteps) mma(tm + kColScore, dQ + along_k(k), dK + (stage + along_k(k)), id_score, k > 0);
@@ -326,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int qd = 0; qd < 4; ++qd) {
                     // the entering product in the middle of the growth: the
                     // group that scales it works while the rest runs
-                    if (qd == 2 || (qd < 2 && qd * kQuarter >= n)) {
+                    if (!GROW && (qd == 2 || (qd < 2 && qd * kQuarter >= n))) {
                         if (!(ok = wait(kStateFull, ch) && (ch == 0 || wait(kOutFree, ch - 1)))) break;
                         if (elect_one()) {
 #pragma unroll
@@ -355,10 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            dKt + (stage + along_mn(k)), id_growth, k > 0 || part > 0);
                         mma_commit(&bars[kVFree0 + r]);
                         if ((qd + 1) * kQuarter >= n) mma_commit(&bars[kGrowth]);
+                        if (GROW && (qd + 1) * kQuarter >= n) mma_commit(&bars[kFree0 + s]);
                     }
                     __syncwarp();
                 }
-                if (!ok || !(ok = wait(kPFull, ch))) break;
+                if (!ok) break;
+                if constexpr (GROW) continue;
+                if (!(ok = wait(kPFull, ch))) break;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -382,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 14) {
         registers<80>();
         // ---------------- output stores (one thread) ----------------
-        if (lane == 0) {
+        if (!GROW && lane == 0) {
             int nu = 0, ch = 0;
             const int vpanels = p.P > 64 ? 2 : 1;
             for (;;) {
@@ -422,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = tid;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
         int nu = 0, ch = 0, ph = 0;
-        for (;;) {
+        while (!GROW) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
             const Unit un = ring[nu & 1];
             mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
@@ -575,12 +724,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the entering state: this thread's row
 #pragma unroll
             for (int i = 0; i < DK; ++i) S[i] = 0.f;
-            if (un.src != kZero && t < p.P) {
-                const int64_t at = ((un.src * p.H + un.h) * static_cast<int64_t>(p.P) + t) * p.N;
-                if (p.state_dtype == kF32) {
+            const bool scratch = un.src >= kScratch;
+            const int64_t elem = (un.h * static_cast<int64_t>(p.P) + t) * p.N, slot = static_cast<int64_t>(p.H) * p.P * p.N;
+            if (!GROW && un.src != kZero && t < p.P) {
+                const int64_t at = un.src * slot + elem;
+                if (scratch || p.state_dtype == kF32) {
+                    const float *src = scratch ? plan.states + (un.src - kScratch) * slot + elem : static_cast<const float *>(p.state) + at;
 #pragma unroll
                     for (int i = 0; i < DK; i += 4)
-                        if (i < p.N) StateChunk<float>::unpack(ld_stream(static_cast<const float *>(p.state) + at + i), S + i);
+                        if (i < p.N) StateChunk<float>::unpack(ld_stream(src + i), S + i);
                 } else if (p.state_dtype == kBF16) {
 #pragma unroll
                     for (int i = 0; i < DK; i += 8)
@@ -594,33 +746,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int c = 0; c < un.len; c += kC, ++ch) {
                 const int n = min(kC, un.len - c);
-                // S in two parts, once the last entering product has read its own
-                float sc = 1.f;
-                if constexpr (!BF) {
-                    float m = 0.f;
+                if constexpr (!GROW) {
+                    // S in two parts, once the last entering product has read its own
+                    float sc = 1.f;
+                    if constexpr (!BF) {
+                        float m = 0.f;
 #pragma unroll
-                    for (int i = 0; i < DK; ++i) m = fmaxf(m, fabsf(S[i]));
-                    const int k = fp16_scale_exp(m);
-                    sc = pow2i(k);
-                    row_scale[(ch & 1) * 128 + t] = pow2i(-k);
-                }
-                if (ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
-                unsigned char *srow = smem + LY::kS + t * 128;
-#pragma unroll
-                for (int j = 0; j < DK / 8; ++j) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = S[8 * j + 2 * i] * sc, y = S[8 * j + 2 * i + 1] * sc;
-                        hi[i] = split2<BF>(x, y);
-                        lo[i] = pack2<BF>(x, y);
+                        for (int i = 0; i < DK; ++i) m = fmaxf(m, fabsf(S[i]));
+                        const int k = fp16_scale_exp(m);
+                        sc = pow2i(k);
+                        row_scale[(ch & 1) * 128 + t] = pow2i(-k);
                     }
-                    unsigned char *d = srow + (j / 8) * kPanel + (((j % 8) ^ (t & 7)) * 16);
-                    *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(d + LY::kKBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
+                    unsigned char *srow = smem + LY::kS + t * 128;
+#pragma unroll
+                    for (int j = 0; j < DK / 8; ++j) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x = S[8 * j + 2 * i] * sc, y = S[8 * j + 2 * i + 1] * sc;
+                            hi[i] = split2<BF>(x, y);
+                            lo[i] = pack2<BF>(x, y);
+                        }
+                        unsigned char *d = srow + (j / 8) * kPanel + (((j % 8) ^ (t & 7)) * 16);
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(d + LY::kKBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[kStateFull]);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars[kStateFull]);
                 if (!(ok = mbar_wait_bounded(&bars[kGrowth], ch & 1))) break;
                 tc_fence_after();
                 const float lam = n == kC ? lam_chunk : expf(g * static_cast<float>(n));
@@ -637,12 +791,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kGrowthFree]);
             }
             if (!ok) break;
-            if (un.dst != kNone && t < p.P) {
-                const int64_t at = ((un.dst * p.H + un.h) * static_cast<int64_t>(p.P) + t) * p.N;
-                if (p.state_dtype == kF32) {
+            if ((GROW || un.dst != kNone) && t < p.P) {
+                const int64_t at = un.dst * slot + elem;
+                if (GROW || p.state_dtype == kF32) {
+                    float *dst = GROW ? plan.states + (un.src - kScratch) * slot + elem : static_cast<float *>(p.state) + at;
 #pragma unroll
                     for (int i = 0; i < DK; i += 4)
-                        if (i < p.N) st_stream(static_cast<float *>(p.state) + at + i, StateChunk<float>::pack(S + i));
+                        if (i < p.N) st_stream(dst + i, StateChunk<float>::pack(S + i));
                 } else if (p.state_dtype == kBF16) {
 #pragma unroll
                     for (int i = 0; i < DK; i += 8)
@@ -839,29 +994,86 @@ int sm_count() {
     return n;
 }
 
+template <int DK, bool BF, bool GROW>
+cudaError_t launch_one(const LinattnParams &p, const Maps &maps, const Plan &plan, int64_t grid, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(linattn_prefill_kernel<DK, BF, GROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Layout<DK>::kBytes);
+    if (e != cudaSuccess) return e;
+    linattn_prefill_kernel<DK, BF, GROW><<<static_cast<unsigned>(grid), kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan);
+    return cudaGetLastError();
+}
+
 template <int DK, bool BF>
-cudaError_t launch_t(const LinattnParams &p, cudaStream_t stream) {
+cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *workspace, cudaStream_t stream) {
     Maps maps;
     if (p.rows > 0 && !(encode(&maps.q, p, p.q, p.N, p.H, p.qs) && encode(&maps.k, p, p.k, p.N, p.G, p.ks) &&
                         encode(&maps.v, p, p.v, p.P, p.G, p.vs) && encode(&maps.out, p, p.out, p.P, p.H, p.os)))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(linattn_prefill_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Layout<DK>::kBytes);
-    if (e != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int64_t units = p.nseq * p.H;
-    const int64_t grid = units < sms ? units : sms;
-    linattn_prefill_kernel<DK, BF><<<static_cast<unsigned>(grid), kThreads, Layout<DK>::kBytes, stream>>>(p, maps, units);
-    return cudaGetLastError();
+    Plan plan{};
+    int64_t grid = p.nseq * p.H < sms ? p.nseq * p.H : sms;
+    if (split.bytes > 0) {
+        unsigned char *w = static_cast<unsigned char *>(workspace);
+        plan.head = reinterpret_cast<PlanHead *>(w);
+        plan.cuts = reinterpret_cast<Cut *>(w + split.cuts);
+        plan.pieces = reinterpret_cast<Unit *>(w + split.pieces);
+        plan.states = reinterpret_cast<float *>(w + split.states);
+        plan.cut_len = split.cut_len;
+        grid = sms;
+        linattn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, static_cast<int>(grid));
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        if (split.max_cuts > 0) {
+            if ((e = launch_one<DK, BF, true>(p, maps, plan, grid, stream)) != cudaSuccess) return e;
+            const dim3 blocks(static_cast<unsigned>((static_cast<int64_t>(p.P) * p.N + 1023) / 1024), static_cast<unsigned>(p.H),
+                              static_cast<unsigned>(split.max_cuts));
+            linattn_carry_kernel<<<blocks, 256, 0, stream>>>(p, plan);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+    }
+    return launch_one<DK, BF, false>(p, maps, plan, grid, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_linattn_prefill(const LinattnParams &p, cudaStream_t stream) {
+// How a call is split.  Without cuts a call takes at least as long as its
+// longest sequence on one SM, and at least its share of the GPU, `even` chunks
+// an SM; cutting the long ones into pieces of about `even` chunks costs them
+// the growth pass again (half of the main one) and three launches.
+LinattnSplit linattn_split(int64_t rows, int64_t nseq, int64_t heads, int64_t dim, int64_t dstate, int64_t max_seqlen) {
+    constexpr int64_t kSms = 152;
+    constexpr int64_t kLaunches = 6;  // what three launches cost, in chunks (3 us each)
+    LinattnSplit s{};
+    if (nseq == 0 || rows == 0) return s;
+    const auto chunks = [](int64_t n) { return (n + kC - 1) / kC; };
+    // without a hint: the only sequence, or twice the mean
+    int64_t longest = max_seqlen > 0 ? max_seqlen : nseq == 1 ? rows : 2 * ((rows + nseq - 1) / nseq);
+    if (longest > rows) longest = rows;
+    const int64_t even = (chunks(rows) * heads + kSms - 1) / kSms;
+    const bool cut = chunks(longest) > even + even / 2 + kLaunches;
+    if (!cut && nseq * heads <= kSms) return s;  // a CTA each: nothing to order
+    const auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+    // pieces a little longer than even, so that their number stays within a
+    // whole round of the SMs
+    const int64_t piece = even + (even + 15) / 16;
+    s.cut_len = cut ? kC * (piece < 4 ? 4 : piece) : (rows + kC - 1) / kC * kC;
+    s.max_cuts = cut ? rows / s.cut_len : 0;
+    if (s.max_cuts > nseq) s.max_cuts = nseq;
+    if (s.max_cuts > 65535) s.max_cuts = 65535;
+    // sum over cut sequences of ceil(len / cut_len) <= 2 rows / cut_len
+    const uint64_t states = cut ? 2 * (rows / s.cut_len) : 0;
+    s.cuts = up(sizeof(PlanHead));
+    s.pieces = s.cuts + up(s.max_cuts * sizeof(Cut));
+    s.states = s.pieces + up((nseq + states) * sizeof(Unit));
+    s.bytes = s.states + up(states * heads * dim * dstate * sizeof(float));
+    return s;
+}
+
+cudaError_t launch_linattn_prefill(const LinattnParams &p, const LinattnSplit &split, void *workspace, cudaStream_t stream) {
     const bool bf = p.io_dtype == kBF16;
-    if (p.N <= 64) return bf ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
-    return bf ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
+    if (p.N <= 64) return bf ? launch_t<64, true>(p, split, workspace, stream) : launch_t<64, false>(p, split, workspace, stream);
+    return bf ? launch_t<128, true>(p, split, workspace, stream) : launch_t<128, false>(p, split, workspace, stream);
 }
 
 }  // namespace ssu

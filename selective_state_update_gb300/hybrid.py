@@ -151,7 +151,12 @@ def ssu_linear_attention_prefill(state, q, k, v, log_decay, cu_seqlens, scale: O
     rc = lib().ssu_linear_attention_workspace_size(ctypes.byref(a), nseq, longest, ctypes.byref(nbytes))
     if rc != OK:
         _raise(rc)
-    ws = _ssd_workspace(q.device, nbytes.value, stream) if nbytes.value else None
+    ws = None
+    if nbytes.value:
+        # on the current stream a block of the caching allocator (also inside a
+        # graph's own pool); on another one the workspace kept for that stream
+        ws = (torch.empty(nbytes.value, dtype=torch.uint8, device=q.device) if stream is None
+              else _ssd_workspace(q.device, nbytes.value, stream))
     rc = lib().ssu_linear_attention_prefill(ctypes.byref(a), nseq, cu_seqlens.data_ptr(), _ITYPE[cu_seqlens.dtype],
                                             longest, _ref(_table(state_batch_indices, SLOTS_STRIDED)),
                                             _ref(_table(dst_state_batch_indices, SLOTS_STRIDED)), _ptr(ws),

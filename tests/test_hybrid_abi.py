@@ -99,6 +99,29 @@ def test_prefill_refusals(libssu, kw, call, code, needle):
     assert needle in libssu.ssu_last_error().decode()
 
 
+def test_prefill_workspace(libssu):
+    """None for a call that gives every (sequence, head) a CTA; a plan for more of them; states as well where sequences
+    are long for the heads there are.  A call checks what it is given."""
+    n = ctypes.c_uint64(0)
+
+    def size(nseq, longest, **kw):
+        a = linattn(**kw)
+        assert libssu.ssu_linear_attention_workspace_size(ctypes.byref(a), nseq, longest, ctypes.byref(n)) == ssu.OK
+        return n.value
+
+    assert size(2, 0, rows=300) == 0
+    assert 0 < size(100, 0, rows=30000) < 1 << 20
+    long = size(1, 0, rows=100000)
+    assert long >= 2 * 4 * 64 * 128 * 4
+    assert size(2, 300, rows=300) == 0
+    a = linattn(rows=100000)
+    for ws, have in ((None, 1 << 40), (512, long - 1), (520, 1 << 40)):
+        assert libssu.ssu_linear_attention_prefill(ctypes.byref(a), 1, 4096, 0, 0, None, None, ws, have, None) == ssu.ERR_INVALID
+        assert "workspace" in libssu.ssu_last_error().decode()
+    assert libssu.ssu_linear_attention_workspace_size(ctypes.byref(a), -1, 0, ctypes.byref(n)) == ssu.ERR_INVALID
+    assert libssu.ssu_linear_attention_workspace_size(ctypes.byref(a), 1, 0, None) == ssu.ERR_INVALID
+
+
 def test_tables_are_checked(libssu):
     a = linattn()
     t = ssu.SlotTable(entries=128, type=5, mode=0, s0=1, s1=1, extent=2)
