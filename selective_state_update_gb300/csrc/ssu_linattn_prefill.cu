@@ -171,6 +171,9 @@ __device__ __forceinline__ uint32_t split2(float &x, float &y) {
 // of four calls it with the same N.
 template <int N>
 __device__ __forceinline__ void registers() {
+    // (the code of a chunk is kept short -- loops over blocks and quarters
+    // are not unrolled -- because the four groups together would not fit the
+    // instruction cache: unrolled, 384 us instead of XXX us on 32768 tokens x 32 heads)
     if constexpr (N == 128) return;
     else if constexpr (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -611,9 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float up = 1.f, down = 1.f;  // fp16: the row's power of two
                 if constexpr (!BF) {
                     float m = 0.f;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        if (b > warp) break;
+#pragma unroll 1
+                    for (int b = 0; b <= warp; ++b) {
                         float e[32];
                         decayed(b, e);
 #pragma unroll
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     down = pow2i(-k);
                 }
                 // (block b of P takes columns whose scores, of block b / 2, are read)
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     uint32_t pr[16];
                     if (b <= warp) {
@@ -647,9 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (fp16: value dim p's state row was scaled; written before the
                 // product that has just completed was issued)
                 const float *rs = row_scale + (ch & 1) * 128;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (32 * b >= p.P) break;
+#pragma unroll 1
+                for (int b = 0; 32 * b < p.P; ++b) {
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColOut + 32 * b, r);
                     tmem_wait_ld();
@@ -667,9 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // out for a tiled copy: a thread's own row, 16 bytes at a time,
                 // would touch 32 lines a store.
                 unsigned char *rows = smem + s * LY::kStage + LY::kKBytes, *mine = rows + row * 128;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (32 * b >= p.P) break;
+#pragma unroll 1
+                for (int b = 0; 32 * b < p.P; ++b) {
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColOut + 32 * b, r);
                     tmem_wait_ld();
@@ -838,11 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (un.len < 0) break;
             const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
             float fall[8];  // l^(31 - j) of this lane's tokens j = 8 b + 2 (lane % 4) + e of a quarter
-            float first[4];  // l^(96 - 32 quarter): from a quarter's last token to a full chunk's
 #pragma unroll
             for (int i = 0; i < 8; ++i) fall[i] = expf(g * static_cast<float>(31 - 8 * (i >> 1) - 2 * (lane & 3) - (i & 1)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) first[i] = expf(g * static_cast<float>(96 - 32 * i));
             for (int c = 0; c < un.len; c += kC, ++ch) {
                 const int s = ch & 1, n = min(kC, un.len - c);
                 if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
@@ -881,14 +878,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = group_sync(&bars[kSyncC], ph))) break;  // the maxima are read
                 }
                 const uint32_t stage = s * LY::kStage;
-#pragma unroll
-                for (int qd = 0; qd < 4; ++qd) {
-                    if (qd * kQuarter >= n) break;
-                    const int r = quarters & 1;
+#pragma unroll 1
+                for (int qd = 0; qd * kQuarter < n; ++qd) {
+                    const int r = quarters & 1, past = n - (qd + 1) * kQuarter;  // tokens after this quarter
                     float wt[8];
-                    if (n == kC) {
+                    if (past >= 0) {
+                        const float f = expf(g * static_cast<float>(past));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) wt[i] = first[qd] * fall[i];
+                        for (int i = 0; i < 8; ++i) wt[i] = f * fall[i];
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
