@@ -38,7 +38,9 @@
 //   8-11   V decayed, transposed (ldmatrix) and split, 32 tokens at a time;
 //   12     issues the products;  13 finds the units and loads Q, K, V by tiled copies
 //          (K, V in two stages; Q, which only the early products read, in one);
-//   14     stores the outputs by tiled copies;  15 only completes the group.
+//   14-15  only complete their group, whose registers the others take.
+// The groups' code for a chunk is kept short (loops over blocks and quarters are
+// not unrolled): all of it together has to stay in the instruction cache.
 #include <cuda.h>
 
 #include "ssu_hybrid.h"
@@ -95,11 +97,10 @@ enum : int {
     kPFull,            // P is there, the entering product scaled
     kInside,           // the outputs are there (P is read)
     kOutFree,          // ... and read
-    kStaged,           // ... and laid out by token, in V's place
     kTail,             // a partial chunk's K and V rows past its end are zeros
     kVFull0, kVFull1, kVFree0, kVFree1,
     kGrowth, kGrowthFree,
-    kSyncA, kSyncC,
+    kSyncB, kSyncC,
     kFinal,
     kBars
 };
@@ -122,7 +123,7 @@ struct Layout {
 };
 
 struct Maps {
-    CUtensorMap q, k, v, out;
+    CUtensorMap q, k, v;
 };
 
 // A barrier of one group of warps, its waits bounded like every other.
@@ -171,9 +172,6 @@ __device__ __forceinline__ uint32_t split2(float &x, float &y) {
 // of four calls it with the same N.
 template <int N>
 __device__ __forceinline__ void registers() {
-    // (the code of a chunk is kept short -- loops over blocks and quarters
-    // are not unrolled -- because the four groups together would not fit the
-    // instruction cache: unrolled, 384 us instead of XXX us on 32768 tokens x 32 heads)
     if constexpr (N == 128) return;
     else if constexpr (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -195,9 +193,64 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// 32 bytes of this thread, 32-byte aligned.
+__device__ __forceinline__ void store32(void *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     tmem_st16(taddr, r);
     tmem_st16(taddr + 16, r + 16);
+}
+
+// A head's state [P][N] between memory (T, contiguous) and a place in shared
+// memory, 16 bytes a thread along memory, for one group of warps.  Rows there
+// are DK elements apart and their 16-byte pieces swapped by row, so that the
+// threads' own rows are read and written without bank conflicts.
+template <typename T, int DK>
+struct StateRow {
+    static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    __device__ __forceinline__ static int at(int row, int piece) {
+        return row * DK * static_cast<int>(sizeof(T)) + ((piece ^ (row & 7)) * 16);
+    }
+};
+template <typename T, int DK, typename F>
+__device__ __forceinline__ void each_piece(int P, int N, int t, F f) {
+    const int per = N / StateRow<T, DK>::kVec, total = P * per, down = kGroup / per, right = kGroup - down * per;
+    int row = t / per, piece = t - row * per;
+#pragma unroll 4
+    for (int i = t; i < total; i += kGroup) {
+        f(i, StateRow<T, DK>::at(row, piece));
+        row += down;
+        piece += right;
+        if (piece >= per) piece -= per, ++row;
+    }
+}
+template <typename T, int DK>
+__device__ __forceinline__ void stage_in(const T *src, unsigned char *place, int P, int N, int t) {
+    each_piece<T, DK>(P, N, t, [&](int i, int at) { cp16(place + at, src + i * StateRow<T, DK>::kVec, true); });
+    cp_wait_all();
+}
+template <typename T, int DK>
+__device__ __forceinline__ void stage_out(T *dst, const unsigned char *place, int P, int N, int t) {
+    each_piece<T, DK>(P, N, t, [&](int i, int at) {
+        st_stream(dst + i * StateRow<T, DK>::kVec, *reinterpret_cast<const uint4 *>(place + at));
+    });
+}
+template <typename T, int DK>
+__device__ __forceinline__ void row_from(const unsigned char *place, int row, int N, float *S) {
+    constexpr int V = StateRow<T, DK>::kVec;
+#pragma unroll
+    for (int j = 0; j < DK / V; ++j)
+        if (j * V < N) StateChunk<T>::unpack(*reinterpret_cast<const uint4 *>(place + StateRow<T, DK>::at(row, j)), S + j * V);
+}
+template <typename T, int DK>
+__device__ __forceinline__ void row_to(unsigned char *place, int row, const float *S) {
+    constexpr int V = StateRow<T, DK>::kVec;
+#pragma unroll
+    for (int j = 0; j < DK / V; ++j)
+        *reinterpret_cast<uint4 *>(place + StateRow<T, DK>::at(row, j)) = StateChunk<T>::pack(S + j * V);
 }
 
 // Sequence b: its bounds and slots.  False (and flagged) when it is to be
@@ -350,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
-            if (i == kFree0 || i == kFree1) n = (GROW ? 1 : 2) + kGroup;
-            if (i == kUnitFree0 || i == kUnitFree1) n = GROW ? 1 + 2 * kGroup : 2 + 3 * kGroup;
-            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail || i == kVFull0 || i == kVFull1 ||
-                i == kGrowthFree || i == kSyncA || i == kSyncC)
+            if (i == kFree0 || i == kFree1) n = 1 + kGroup;
+            if (i == kUnitFree0 || i == kUnitFree1) n = GROW ? 1 + 2 * kGroup : 1 + 3 * kGroup;
+            if (i == kStateFull || i == kPFull || i == kOutFree || i == kTail || i == kVFull0 || i == kVFull1 ||
+                i == kGrowthFree || i == kSyncB || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
@@ -375,27 +428,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             int nu = 0, ch = 0, nq = 0;  // units published, chunks loaded (K and V, Q)
             const int vpanels = p.P > 64 ? 2 : 1;
             const int64_t units = (plan.head ? plan.head->pieces : p.nseq) * p.H;
-            for (int64_t u = blockIdx.x;;
-                 u = plan.head ? atomicAdd(&plan.head->next[GROW ? 0 : 1], 1) : u + gridDim.x) {
+            int64_t u = blockIdx.x;
+            const auto next_unit = [&] {
                 Unit un;
-                const bool end = u >= units;
-                if (end) {
-                    un.len = -1;
-                } else {
-                    const int64_t b = u / p.H;
+                for (;;) {
+                    const int64_t now = u;
+                    if (now >= units) {
+                        un.len = -1;
+                        return un;
+                    }
+                    u = plan.head ? atomicAdd(&plan.head->next[GROW ? 0 : 1], 1) : u + gridDim.x;
+                    const int64_t b = now / p.H;
                     if (plan.head) {
                         un = plan.pieces[b];
                         if (GROW && un.h == 0) continue;
                     } else if (!find_sequence(p, b, un)) {
                         continue;
                     }
-                    un.h = static_cast<int>(u - b * p.H);
+                    un.h = static_cast<int>(now - b * p.H);
+                    return un;
                 }
-                if (nu >= 2 && !(ok = mbar_wait_bounded(&bars[kUnitFree0 + (nu & 1)], ((nu >> 1) - 1) & 1))) break;
+            };
+            const auto publish = [&](const Unit &un) {
+                if (nu >= 2 && !mbar_wait_bounded(&bars[kUnitFree0 + (nu & 1)], ((nu >> 1) - 1) & 1)) return false;
                 ring[nu & 1] = un;
                 mbar_arrive(&bars[kUnitFull0 + (nu & 1)]);
                 ++nu;
-                if (end) break;
+                return true;
+            };
+            // a unit is announced before the one ahead of it is loaded
+            Unit un = next_unit();
+            ok = publish(un);
+            while (ok && un.len >= 0) {
+                const Unit after = next_unit();
+                if (!(ok = publish(after))) break;
                 const int g = un.h / p.share;
                 for (int c = 0; c < un.len; c += kC, ++ch) {
                     const int s = ch & 1, row = static_cast<int>(un.t0) + c;
@@ -418,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < LY::kPanels; ++i)
                         tma_load_3d(smem + LY::kQ + i * kPanel, &maps.q, 64 * i, un.h, row, &bars[kQFull]);
                 }
-                if (!ok) break;
+                un = after;
             }
             if (!ok) {
                 flag(p.status, kDevTimeout);
@@ -449,78 +515,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return got;
         };
-        int nu = 0, ch = 0, tails = 0, quarters = 0;
-        for (;;) {
-            if (!(ok = wait(kUnitFull0 + (nu & 1), nu >> 1))) break;
-            const int len = __shfl_sync(0xffffffffu, ring[nu & 1].len, 0);
-            if (lane == 0) mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
-            ++nu;
-            if (len < 0) break;
-            for (int c = 0; c < len; c += kC, ++ch) {
-                const int s = ch & 1, n = min(kC, len - c), steps = (n + 15) / 16;
-                const uint32_t stage = static_cast<uint32_t>(s * (LY::kStage >> 4));
-                // scores; P of the last chunk, in their place, has been read
-                if (!(ok = wait(kFull0 + s, ch >> 1))) break;
-                if (!GROW && !(ok = wait(kQFull, ch) && (ch == 0 || wait(kInside, ch - 1)))) break;
-                if (!GROW && elect_one()) {
+        int nu = 0, tails = 0, quarters = 0;
+        struct Chunk {
+            int ch, s, n, steps;  // running number, stage, tokens (0: no more), of them in 16s
+            uint32_t stage;
+        };
+        int len = 0, c = 0, count = 0;  // the current unit's length, tokens begun, chunks begun
+        const auto next_chunk = [&](Chunk &k) {
+            while (c >= len) {
+                if (!wait(kUnitFull0 + (nu & 1), nu >> 1)) return false;
+                len = __shfl_sync(0xffffffffu, ring[nu & 1].len, 0);
+                if (lane == 0) mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+                ++nu;
+                c = 0;
+                if (len < 0) {
+                    k.n = 0;
+                    return true;
+                }
+            }
+            k.ch = count++;
+            k.s = k.ch & 1;
+            k.n = min(kC, len - c);
+            k.steps = (k.n + 15) / 16;
+            k.stage = static_cast<uint32_t>(k.s * (LY::kStage >> 4));
+            c += kC;
+            return true;
+        };
+        const auto growth = [&](const Chunk &k, int qd) {  // quarter qd, if there is one
+            if (qd * kQuarter >= k.n) return true;
+            if (qd == 0) {
+                if (!wait(kFull0 + k.s, k.ch >> 1)) return false;
+                if (k.n < kC && !wait(kTail, tails++)) return false;
+                if (k.ch > 0 && !wait(kGrowthFree, k.ch - 1)) return false;
+            }
+            const int r = quarters & 1;
+            if (!wait(kVFull0 + r, quarters >> 1)) return false;
+            ++quarters;
+            if (elect_one()) {
+                const uint32_t a = tm + kColV + r * kRing;
+                const Desc b = dKt + (k.stage + qd * along_mn(2));
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        if (k < ksteps) mma(tm + kColScore, dQ + along_k(k), dK + (stage + along_k(k)), id_score, k > 0);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+                        if (2 * qd + i < k.steps)
+                            mma_ts(tm + kColGrowth, a + part * 16 + 8 * i, b + along_mn(i), id_growth, qd > 0 || i > 0 || part > 0);
+                mma_commit(&bars[kVFree0 + r]);
+                if ((qd + 1) * kQuarter >= k.n) {
+                    mma_commit(&bars[kGrowth]);
+                    if (GROW) mma_commit(&bars[kFree0 + k.s]);
+                }
+            }
+            __syncwarp();
+            return true;
+        };
+        // The order keeps the pipe busy: the first half of the growth runs
+        // while the outputs of the chunk before are read and the state is
+        // split, the second while the entering rows are scaled.
+        Chunk k;
+        while ((ok = next_chunk(k)) && k.n > 0) {
+            if (!(ok = growth(k, 0) && growth(k, 1))) break;
+            if constexpr (!GROW) {
+                // (P of the last chunk, in the scores' place, has been read)
+                if (!(ok = wait(kQFull, k.ch) && (k.ch == 0 || wait(kInside, k.ch - 1)))) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < DK / 16; ++i)
+                        if (i < ksteps) mma(tm + kColScore, dQ + along_k(i), dK + (k.stage + along_k(i)), id_score, i > 0);
                     mma_commit(&bars[kScore]);
                 }
                 __syncwarp();
-                if (n < kC && !(ok = wait(kTail, tails++))) break;
-                if (ch > 0 && !(ok = wait(kGrowthFree, ch - 1))) break;
-#pragma unroll
-                for (int qd = 0; qd < 4; ++qd) {
-                    // the entering product in the middle of the growth: the
-                    // group that scales it works while the rest runs
-                    if (!GROW && (qd == 2 || (qd < 2 && qd * kQuarter >= n))) {
-                        if (!(ok = wait(kStateFull, ch) && (ch == 0 || wait(kOutFree, ch - 1)))) break;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                                for (int k = 0; k < DK / 16; ++k)
-                                    if (k < ksteps)
-                                        mma(tm + kColOut, dQ + along_k(k), dS + (part * (LY::kKBytes >> 4) + along_k(k)), id_enter,
-                                            part > 0 || k > 0);
-                            mma_commit(&bars[kEnter]);
-                            mma_commit(&bars[kQFree]);
-                        }
-                        __syncwarp();
-                    }
-                    if (qd * kQuarter >= n) break;
-                    const int r = quarters & 1;
-                    if (!(ok = wait(kVFull0 + r, quarters >> 1))) break;
-                    ++quarters;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 2 * qd; k < 2 * qd + 2; ++k)
-#pragma unroll
-                            for (int part = 0; part < kParts; ++part)
-                                if (k < steps)
-                                    mma_ts(tm + kColGrowth, tm + kColV + r * kRing + part * 16 + 8 * (k & 1),
-                                           dKt + (stage + along_mn(k)), id_growth, k > 0 || part > 0);
-                        mma_commit(&bars[kVFree0 + r]);
-                        if ((qd + 1) * kQuarter >= n) mma_commit(&bars[kGrowth]);
-                        if (GROW && (qd + 1) * kQuarter >= n) mma_commit(&bars[kFree0 + s]);
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                if constexpr (GROW) continue;
-                if (!(ok = wait(kPFull, ch))) break;
+                if (!(ok = wait(kStateFull, k.ch) && (k.ch == 0 || wait(kOutFree, k.ch - 1)))) break;
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < steps) mma_ts(tm + kColOut, tm + kColScore + 8 * k, dV + (stage + along_mn(k)), id_inside, 1);
-                    mma_commit(&bars[kInside]);
-                    mma_commit(&bars[kFree0 + s]);
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < DK / 16; ++i)
+                            if (i < ksteps)
+                                mma(tm + kColOut, dQ + along_k(i), dS + (part * (LY::kKBytes >> 4) + along_k(i)), id_enter,
+                                    part > 0 || i > 0);
+                    mma_commit(&bars[kEnter]);
+                    mma_commit(&bars[kQFree]);
                 }
                 __syncwarp();
             }
-            if (!ok) break;
+            if (!(ok = growth(k, 2) && growth(k, 3))) break;
+            if constexpr (!GROW) {
+                if (!(ok = wait(kPFull, k.ch))) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < k.steps)
+                            mma_ts(tm + kColOut, tm + kColScore + 8 * i, dV + (k.stage + along_mn(i)), id_inside, 1);
+                    mma_commit(&bars[kInside]);
+                    mma_commit(&bars[kFree0 + k.s]);
+                }
+                __syncwarp();
+            }
         }
         if (!ok && lane == 0) {
             flag(p.status, kDevTimeout);
@@ -531,49 +622,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait_bounded(&bars[kFinal], 0);
         __syncwarp();
-    } else if (warp == 14) {
-        registers<80>();
-        // ---------------- output stores (one thread) ----------------
-        if (!GROW && lane == 0) {
-            int nu = 0, ch = 0;
-            const int vpanels = p.P > 64 ? 2 : 1;
-            for (;;) {
-                if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
-                const Unit un = ring[nu & 1];
-                mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
-                ++nu;
-                if (un.len < 0) break;
-                for (int c = 0; c < un.len; c += kC, ++ch) {
-                    const int s = ch & 1;
-                    if (!(ok = mbar_wait_bounded(&bars[kStaged], ch & 1))) break;
-                    // (a partial chunk's rows have been stored one by one: the
-                    // rows past its end are other tokens')
-                    if (un.len - c >= kC) {
-                        for (int i = 0; i < vpanels; ++i)
-                            tma_store_3d(&maps.out, smem + s * LY::kStage + LY::kKBytes + i * kPanel, 64 * i, un.h,
-                                         static_cast<int>(un.t0) + c);
-                        bulk_commit();
-                        bulk_wait_read<0>();
-                    }
-                    mbar_arrive(&bars[kFree0 + s]);
-                }
-                if (!ok) break;
-            }
-            bulk_wait_all();
-            if (!ok) {
-                flag(p.status, kDevTimeout);
-                *abort_flag = 1;
-            }
-        }
-        __syncwarp();
-    } else if (warp == 15) {
+    } else if (warp >= 14) {
         registers<80>();
     } else if (warp < 4) {
         registers<128>();
         // ---------------- P and the outputs (thread = token) ----------------
         const int row = tid;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        int nu = 0, ch = 0, ph = 0;
+        const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.P % 16 == 0 && p.os[0] % 16 == 0 && p.os[1] % 16 == 0;
+        int nu = 0, ch = 0;
         while (!GROW) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
             const Unit un = ring[nu & 1];
@@ -588,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int jj = 0; jj < 32; ++jj) fall[jj] = ex2(g2 * static_cast<float>(31 - jj));
             unsigned short *out = static_cast<unsigned short *>(p.out) + un.h * p.os[1] + un.t0 * p.os[0];
             for (int c = 0; c < un.len; c += kC, ++ch) {
-                const int s = ch & 1, n = min(kC, un.len - c);
+                const int n = min(kC, un.len - c);
                 if (!(ok = mbar_wait_bounded(&bars[kScore], ch & 1))) break;
                 tc_fence_after();
                 // Row i of P: scale l^(i-j) score for j <= i.  A block of 32
@@ -664,10 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kPFull]);
                 if (!(ok = mbar_wait_bounded(&bars[kInside], ch & 1))) break;
                 tc_fence_after();
-                // Outputs by token where V was (its products are done), laid
-                // out for a tiled copy: a thread's own row, 16 bytes at a time,
-                // would touch 32 lines a store.
-                unsigned char *rows = smem + s * LY::kStage + LY::kKBytes, *mine = rows + row * 128;
+                // the token's outputs, 32 bytes a store (16 where their rows do
+                // not begin on such a boundary)
 #pragma unroll 1
                 for (int b = 0; 32 * b < p.P; ++b) {
                     uint32_t r[32];
@@ -683,22 +738,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (!BF) x *= down, y *= down;
                         r[jj] = pack2<BF>(x, y);
                     }
+                    if (row < n) {
+                        unsigned short *o = out + (c + row) * p.os[0] + 32 * b;
+                        if (wide) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4 *>(mine + (b / 2) * kPanel + (((4 * (b % 2) + j) ^ (row & 7)) * 16)) =
-                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                }
-                fence_proxy_async_smem();
-                if (n < kC) {
-                    if (!(ok = group_sync(&bars[kSyncA], ph))) break;
-                    const int piece = tid & 15;  // 16 threads store a token's row
-                    if (8 * piece < p.P) {
-                        for (int i = tid >> 4; i < n; i += kGroup / 16)
-                            *reinterpret_cast<uint4 *>(out + (c + i) * p.os[0] + 8 * piece) = *reinterpret_cast<const uint4 *>(
-                                rows + (piece / 8) * kPanel + i * 128 + (((piece % 8) ^ (i & 7)) * 16));
+                            for (int j = 0; j < 2; ++j)
+                                if (32 * b + 16 * j < p.P) store32(o + 16 * j, r + 8 * j);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (32 * b + 8 * j < p.P)
+                                    *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        }
                     }
                 }
-                mbar_arrive(&bars[kStaged]);
             }
             if (!ok) break;
         }
@@ -711,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- the state (thread = value dim) ----------------
         const int t = tid - kGroup, w = warp - 4;
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-        int nu = 0, ch = 0;
+        int nu = 0, ch = 0, ph = 0;
         float S[DK];
         for (;;) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
@@ -721,28 +774,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (un.len < 0) break;
             const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
             const float lam_chunk = expf(g * static_cast<float>(kC));
-            // the entering state: this thread's row
+            const int64_t slot = static_cast<int64_t>(p.H) * p.P * p.N, head = static_cast<int64_t>(un.h) * p.P * p.N;
 #pragma unroll
             for (int i = 0; i < DK; ++i) S[i] = 0.f;
-            const bool scratch = un.src >= kScratch;
-            const int64_t elem = (un.h * static_cast<int64_t>(p.P) + t) * p.N, slot = static_cast<int64_t>(p.H) * p.P * p.N;
-            if (!GROW && un.src != kZero && t < p.P) {
-                const int64_t at = un.src * slot + elem;
-                if (scratch || p.state_dtype == kF32) {
-                    const float *src = scratch ? plan.states + (un.src - kScratch) * slot + elem : static_cast<const float *>(p.state) + at;
-#pragma unroll
-                    for (int i = 0; i < DK; i += 4)
-                        if (i < p.N) StateChunk<float>::unpack(ld_stream(src + i), S + i);
-                } else if (p.state_dtype == kBF16) {
-#pragma unroll
-                    for (int i = 0; i < DK; i += 8)
-                        if (i < p.N)
-                            StateChunk<__nv_bfloat16>::unpack(ld_stream(static_cast<const __nv_bfloat16 *>(p.state) + at + i), S + i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < DK; i += 8)
-                        if (i < p.N) StateChunk<__half>::unpack(ld_stream(static_cast<const __half *>(p.state) + at + i), S + i);
+            // the entering state, by way of the parts' place (which the last
+            // entering product has read)
+            if (!GROW && ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
+            if (!GROW && un.src != kZero) {
+                const bool scratch = un.src >= kScratch;
+                const int64_t at = (scratch ? un.src - kScratch : un.src) * slot + head;
+                const void *src = scratch ? plan.states : p.state;
+                unsigned char *const place = smem + LY::kS;
+                if (scratch || p.state_dtype == kF32) stage_in<float, DK>(static_cast<const float *>(src) + at, place, p.P, p.N, t);
+                else stage_in<__half, DK>(static_cast<const __half *>(src) + at, place, p.P, p.N, t);  // any 16 bits
+                if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                if (t < p.P) {
+                    if (scratch || p.state_dtype == kF32) row_from<float, DK>(place, t, p.N, S);
+                    else if (p.state_dtype == kBF16) row_from<__nv_bfloat16, DK>(place, t, p.N, S);
+                    else row_from<__half, DK>(place, t, p.N, S);
                 }
+                if (!(ok = group_sync(&bars[kSyncB], ph))) break;
             }
             for (int c = 0; c < un.len; c += kC, ++ch) {
                 const int n = min(kC, un.len - c);
@@ -791,22 +842,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kGrowthFree]);
             }
             if (!ok) break;
-            if ((GROW || un.dst != kNone) && t < p.P) {
-                const int64_t at = un.dst * slot + elem;
-                if (GROW || p.state_dtype == kF32) {
-                    float *dst = GROW ? plan.states + (un.src - kScratch) * slot + elem : static_cast<float *>(p.state) + at;
-#pragma unroll
-                    for (int i = 0; i < DK; i += 4)
-                        if (i < p.N) st_stream(dst + i, StateChunk<float>::pack(S + i));
-                } else if (p.state_dtype == kBF16) {
-#pragma unroll
-                    for (int i = 0; i < DK; i += 8)
-                        if (i < p.N) st_stream(static_cast<__nv_bfloat16 *>(p.state) + at + i, StateChunk<__nv_bfloat16>::pack(S + i));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < DK; i += 8)
-                        if (i < p.N) st_stream(static_cast<__half *>(p.state) + at + i, StateChunk<__half>::pack(S + i));
-                }
+            if (GROW || un.dst != kNone) {
+                // out the same way
+                if (!GROW && ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
+                const int64_t at = (GROW ? un.src - kScratch : un.dst) * slot + head;
+                unsigned char *const place = smem + LY::kS;
+                if (GROW || p.state_dtype == kF32) row_to<float, DK>(place, t, S);
+                else if (p.state_dtype == kBF16) row_to<__nv_bfloat16, DK>(place, t, S);
+                else row_to<__half, DK>(place, t, S);
+                if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                void *dst = GROW ? plan.states : p.state;
+                if (GROW || p.state_dtype == kF32) stage_out<float, DK>(static_cast<float *>(dst) + at, place, p.P, p.N, t);
+                else stage_out<__half, DK>(static_cast<__half *>(dst) + at, place, p.P, p.N, t);
+                if (!(ok = group_sync(&bars[kSyncB], ph))) break;
             }
         }
         if (!ok) {
@@ -1004,7 +1052,7 @@ template <int DK, bool BF>
 cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *workspace, cudaStream_t stream) {
     Maps maps;
     if (p.rows > 0 && !(encode(&maps.q, p, p.q, p.N, p.H, p.qs) && encode(&maps.k, p, p.k, p.N, p.G, p.ks) &&
-                        encode(&maps.v, p, p.v, p.P, p.G, p.vs) && encode(&maps.out, p, p.out, p.P, p.H, p.os)))
+                        encode(&maps.v, p, p.v, p.P, p.G, p.vs)))
         return cudaErrorInvalidValue;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
