@@ -100,7 +100,7 @@ enum : int {
     kTail,             // a partial chunk's K and V rows past its end are zeros
     kVFull0, kVFull1, kVFree0, kVFree1,
     kGrowth, kGrowthFree,
-    kSyncB, kSyncC,
+    kSyncA, kSyncB, kSyncC,
     kFinal,
     kBars
 };
@@ -116,8 +116,8 @@ struct Layout {
     static constexpr int kBar = kS + 2 * kKBytes;
     static constexpr int kUnits = kBar + 8 * kBars;       // Unit[2]
     static constexpr int kRowScale = (kUnits + 2 * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;  // fp16: state rows, by chunk parity
-    static constexpr int kMax = kRowScale + 2 * 128 * 4;  // fp16: per warp; then the value tiles' scales, four chunks
-    static constexpr int kMisc = kMax + 32;               // tensor-memory address, abort
+    static constexpr int kMax = kRowScale + 2 * 128 * 4;  // fp16: per warp; the value tiles' scales, four chunks; per warp of the growth pass's helpers
+    static constexpr int kMisc = kMax + 48;               // tensor-memory address, abort
     static constexpr int kBytes = kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -307,10 +307,13 @@ __global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const Linatt
         const int n = n0 == 1 ? 1 : static_cast<int>((un.len + step - 1) / step);
         for (int i = 0; i < n; ++i) f(i, n, min(step, un.len - i * step), i * step);
     };
+    Unit own;  // this thread's first sequence is looked up once
+    bool have = false;
     for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
         Unit un;
-        if (!find_sequence(p, b, un)) continue;
-        each(un, [&](int, int, int64_t len, int64_t) { atomicAdd(&start[bucket(len)], 1); });
+        const bool ok = find_sequence(p, b, un);
+        if (b == tid) own = un, have = ok;
+        if (ok) each(un, [&](int, int, int64_t len, int64_t) { atomicAdd(&start[bucket(len)], 1); });
     }
     __syncthreads();
     // exclusive prefix sum of the buckets
@@ -330,10 +333,13 @@ __global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const Linatt
     start[tid] = before + sum - mine;
     __syncthreads();
     for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
-        Unit un;
-        LinattnParams quiet = p;
-        quiet.status = nullptr;  // flagged above
-        if (!find_sequence(quiet, b, un)) continue;
+        Unit un = own;
+        if (b != tid) {
+            LinattnParams quiet = p;
+            quiet.status = nullptr;  // flagged above
+            have = find_sequence(quiet, b, un);
+        }
+        if (!have) continue;
         int state = 0, cut = 0;
         each(un, [&](int i, int n, int64_t len, int64_t off) {
             if (i == 0 && n > 1) {
@@ -373,15 +379,21 @@ __global__ void __launch_bounds__(256) linattn_carry_kernel(const LinattnParams 
     }
     float4 *w = reinterpret_cast<float4 *>(plan.states + (static_cast<int64_t>(cut.state) * p.H + h) * elems + at);
     const int64_t stride = p.H * elems / 4;
-#pragma unroll 4
-    for (int i = 0; i < cut.pieces; ++i, w += stride) {
-        float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < cut.pieces - 1) add = *w;
-        *w = make_float4(s[0], s[1], s[2], s[3]);
-        s[0] = fmaf(s[0], lam, add.x);
-        s[1] = fmaf(s[1], lam, add.y);
-        s[2] = fmaf(s[2], lam, add.z);
-        s[3] = fmaf(s[3], lam, add.w);
+    constexpr int kBatch = 8;  // loads in flight; the sums along the pieces depend on one another
+    for (int i0 = 0; i0 < cut.pieces; i0 += kBatch, w += kBatch * stride) {
+        float4 add[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            add[i] = i0 + i < cut.pieces - 1 ? w[i * stride] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i0 + i >= cut.pieces) break;
+            w[i * stride] = make_float4(s[0], s[1], s[2], s[3]);
+            s[0] = fmaf(s[0], lam, add[i].x);
+            s[1] = fmaf(s[1], lam, add[i].y);
+            s[2] = fmaf(s[2], lam, add[i].z);
+            s[3] = fmaf(s[3], lam, add[i].w);
+        }
     }
 }
 
@@ -403,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
-            if (i == kFree0 || i == kFree1) n = 1 + kGroup;
-            if (i == kUnitFree0 || i == kUnitFree1) n = GROW ? 1 + 2 * kGroup : 1 + 3 * kGroup;
+            if (i == kFree0 || i == kFree1) n = 1 + (GROW ? 2 : 1) * kGroup;
+            if (i == kUnitFree0 || i == kUnitFree1) n = 1 + 3 * kGroup;
             if (i == kStateFull || i == kPFull || i == kOutFree || i == kTail || i == kVFull0 || i == kVFull1 ||
-                i == kGrowthFree || i == kSyncB || i == kSyncC)
+                i == kGrowthFree || i == kSyncA || i == kSyncB || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
@@ -418,6 +430,141 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = misc[0];
     bool ok = true;
+
+    // The decayed values (warp = 32 value dims), by the third group of warps; in
+    // the growth pass the first one, `helper` 1, takes every second quarter.
+    const auto decay_values = [&](int helper) {
+        const int sync = helper ? kSyncA : kSyncC;
+        float *tile_max = maxes + (helper ? 8 : 0);
+        const int t = tid % kGroup, w = warp % 4;
+        const bool live = 32 * w < p.P;
+        int nu = 0, ch = 0, quarters = 0, ph = 0;
+        // this lane's row of the matrices it loads: token lane % 8 of token
+        // block lane / 16 of two, 8 value dims of block (lane / 8) % 2; the
+        // swizzle moves the 16-byte piece with the token
+        const int dim0 = 32 * w + 8 * ((lane >> 3) & 1);
+        uint32_t at[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int d = dim0 + 16 * hh;
+            at[hh] = smem_addr(smem) + LY::kKBytes + (d >> 6) * kPanel + ((lane & 7) + 8 * (lane >> 4)) * 128 +
+                     ((((d & 63) >> 3) ^ (lane & 7)) * 16);
+        }
+        for (;;) {
+            if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
+            const Unit un = ring[nu & 1];
+            mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+            ++nu;
+            if (un.len < 0) break;
+            const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
+            float fall[8];  // l^(31 - j) of this lane's tokens j = 8 b + 2 (lane % 4) + e of a quarter
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fall[i] = expf(g * static_cast<float>(31 - 8 * (i >> 1) - 2 * (lane & 3) - (i & 1)));
+            for (int c = 0; c < un.len; c += kC, ++ch) {
+                const int s = ch & 1, n = min(kC, un.len - c);
+                if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
+                unsigned char *sK = smem + s * LY::kStage;
+                if (n < kC) {
+                    // rows past the sequence's end belong to other tokens: a
+                    // weight of zero would still let their NaN through
+                    const int rows = (kC - n) * 8;
+                    for (int i = t; i < rows * (LY::kPanels + 2); i += kGroup)
+                        *reinterpret_cast<uint4 *>(sK + (i / rows) * kPanel + n * 128 + (i % rows) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[kTail]);
+                    if (!(ok = group_sync(&bars[sync], ph))) break;  // every thread's zeros, below
+                }
+                float vs = 1.f;
+                if constexpr (!BF) {
+                    // the power of two that brings the tile's largest |v| near fp16's top
+                    uint32_t m2 = 0u;
+                    const int pieces = (p.P > 64 ? 2 : 1) * (kPanel / 16);
+                    for (int i = t; i < pieces; i += kGroup) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(sK + LY::kKBytes + i * 16);
+                        const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, ws[e] & 0x7fff7fffu);  // magnitudes order as their bits
+                    }
+                    float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
+                                    __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    if (lane == 0) tile_max[w] = m;
+                    if (!(ok = group_sync(&bars[sync], ph))) break;
+                    m = fmaxf(fmaxf(tile_max[0], tile_max[1]), fmaxf(tile_max[2], tile_max[3]));
+                    const int k = fp16_scale_exp(m);
+                    vs = pow2i(k);
+                    if (helper == 0 && t == 0) maxes[4 + (ch & 3)] = pow2i(-k);
+                    if (!(ok = group_sync(&bars[sync], ph))) break;  // the maxima are read
+                }
+                const uint32_t stage = s * LY::kStage;
+#pragma unroll 1
+                for (int qd = 0; qd * kQuarter < n; ++qd) {
+                    if (GROW && (qd & 1) != helper) {  // (growth pass: whole chunks, so each group keeps to one slot)
+                        ++quarters;
+                        continue;
+                    }
+                    const int r = quarters & 1, past = n - (qd + 1) * kQuarter;  // tokens after this quarter
+                    float wt[8];
+                    if (past >= 0) {
+                        const float f = expf(g * static_cast<float>(past));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) wt[i] = f * fall[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int left = n - 1 - (qd * kQuarter + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1));
+                            wt[i] = left >= 0 ? expf(g * static_cast<float>(left)) : 0.f;
+                        }
+                    }
+                    if constexpr (!BF) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) wt[i] *= vs;
+                    }
+                    uint32_t v[2][8];
+                    if (live) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            ldmatrix_x4_trans(at[hh] + stage + qd * kQuarter * 128, v[hh]);
+                            ldmatrix_x4_trans(at[hh] + stage + (qd * kQuarter + 16) * 128, v[hh] + 4);
+                        }
+                    }
+                    if (quarters >= 2 && !(ok = mbar_wait_bounded(&bars[kVFree0 + r], ((quarters >> 1) - 1) & 1))) break;
+                    ++quarters;
+                    tc_fence_after();
+                    if (live) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            float x[8], y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 f = unpack2<BF>(v[hh][i]);
+                                x[i] = f.x * wt[2 * (i >> 1)];
+                                y[i] = f.y * wt[2 * (i >> 1) + 1];
+                            }
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q) {
+                                uint32_t part[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) part[i] = split2<BF>(x[i], y[i]);
+                                tmem_st_16x128b_x4(tmem + (static_cast<uint32_t>(32 * w + 16 * hh) << 16) + kColV + r * kRing + 16 * q, part);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&bars[kVFull0 + r]);
+                }
+                if (!ok) break;
+                mbar_arrive(&bars[kFree0 + s]);
+            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            if (lane == 0) flag(p.status, kDevTimeout);
+            *abort_flag = 1;
+        }
+    };
 
     // The launch gives every thread 128 registers (4 x 128 in all); the groups
     // take 128, 208 and 96, which leaves 80 for the last.
@@ -626,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         registers<80>();
     } else if (warp < 4) {
         registers<128>();
+        if constexpr (GROW) decay_values(1);
         // ---------------- P and the outputs (thread = token) ----------------
         const int row = tid;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
@@ -863,131 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         registers<96>();
-        // ---------------- the decayed values (warp = 32 value dims) ----------------
-        const int t = tid - 2 * kGroup, w = warp - 8;
-        const bool live = 32 * w < p.P;
-        int nu = 0, ch = 0, quarters = 0, ph = 0;
-        // this lane's row of the matrices it loads: token lane % 8 of token
-        // block lane / 16 of two, 8 value dims of block (lane / 8) % 2; the
-        // swizzle moves the 16-byte piece with the token
-        const int dim0 = 32 * w + 8 * ((lane >> 3) & 1);
-        uint32_t at[2];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int d = dim0 + 16 * hh;
-            at[hh] = smem_addr(smem) + LY::kKBytes + (d >> 6) * kPanel + ((lane & 7) + 8 * (lane >> 4)) * 128 +
-                     ((((d & 63) >> 3) ^ (lane & 7)) * 16);
-        }
-        for (;;) {
-            if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
-            const Unit un = ring[nu & 1];
-            mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
-            ++nu;
-            if (un.len < 0) break;
-            const float g = fmaxf(__ldg(p.log_decay + un.h), -1e30f);
-            float fall[8];  // l^(31 - j) of this lane's tokens j = 8 b + 2 (lane % 4) + e of a quarter
-#pragma unroll
-            for (int i = 0; i < 8; ++i) fall[i] = expf(g * static_cast<float>(31 - 8 * (i >> 1) - 2 * (lane & 3) - (i & 1)));
-            for (int c = 0; c < un.len; c += kC, ++ch) {
-                const int s = ch & 1, n = min(kC, un.len - c);
-                if (!(ok = mbar_wait_bounded(&bars[kFull0 + s], (ch >> 1) & 1))) break;
-                unsigned char *sK = smem + s * LY::kStage;
-                if (n < kC) {
-                    // rows past the sequence's end belong to other tokens: a
-                    // weight of zero would still let their NaN through
-                    const int rows = (kC - n) * 8;
-                    for (int i = t; i < rows * (LY::kPanels + 2); i += kGroup)
-                        *reinterpret_cast<uint4 *>(sK + (i / rows) * kPanel + n * 128 + (i % rows) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    mbar_arrive(&bars[kTail]);
-                    if (!(ok = group_sync(&bars[kSyncC], ph))) break;  // every thread's zeros, below
-                }
-                float vs = 1.f;
-                if constexpr (!BF) {
-                    // the power of two that brings the tile's largest |v| near fp16's top
-                    uint32_t m2 = 0u;
-                    const int pieces = (p.P > 64 ? 2 : 1) * (kPanel / 16);
-                    for (int i = t; i < pieces; i += kGroup) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(sK + LY::kKBytes + i * 16);
-                        const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, ws[e] & 0x7fff7fffu);  // magnitudes order as their bits
-                    }
-                    float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
-                                    __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    if (lane == 0) maxes[w] = m;
-                    if (!(ok = group_sync(&bars[kSyncC], ph))) break;
-                    m = fmaxf(fmaxf(maxes[0], maxes[1]), fmaxf(maxes[2], maxes[3]));
-                    const int k = fp16_scale_exp(m);
-                    vs = pow2i(k);
-                    if (t == 0) maxes[4 + (ch & 3)] = pow2i(-k);
-                    if (!(ok = group_sync(&bars[kSyncC], ph))) break;  // the maxima are read
-                }
-                const uint32_t stage = s * LY::kStage;
-#pragma unroll 1
-                for (int qd = 0; qd * kQuarter < n; ++qd) {
-                    const int r = quarters & 1, past = n - (qd + 1) * kQuarter;  // tokens after this quarter
-                    float wt[8];
-                    if (past >= 0) {
-                        const float f = expf(g * static_cast<float>(past));
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) wt[i] = f * fall[i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int left = n - 1 - (qd * kQuarter + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1));
-                            wt[i] = left >= 0 ? expf(g * static_cast<float>(left)) : 0.f;
-                        }
-                    }
-                    if constexpr (!BF) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) wt[i] *= vs;
-                    }
-                    uint32_t v[2][8];
-                    if (live) {
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            ldmatrix_x4_trans(at[hh] + stage + qd * kQuarter * 128, v[hh]);
-                            ldmatrix_x4_trans(at[hh] + stage + (qd * kQuarter + 16) * 128, v[hh] + 4);
-                        }
-                    }
-                    if (quarters >= 2 && !(ok = mbar_wait_bounded(&bars[kVFree0 + r], ((quarters >> 1) - 1) & 1))) break;
-                    ++quarters;
-                    tc_fence_after();
-                    if (live) {
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            float x[8], y[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 f = unpack2<BF>(v[hh][i]);
-                                x[i] = f.x * wt[2 * (i >> 1)];
-                                y[i] = f.y * wt[2 * (i >> 1) + 1];
-                            }
-#pragma unroll
-                            for (int q = 0; q < kParts; ++q) {
-                                uint32_t part[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) part[i] = split2<BF>(x[i], y[i]);
-                                tmem_st_16x128b_x4(tmem + (static_cast<uint32_t>(32 * w + 16 * hh) << 16) + kColV + r * kRing + 16 * q, part);
-                            }
-                        }
-                        tmem_wait_st();
-                    }
-                    tc_fence_before();
-                    mbar_arrive(&bars[kVFull0 + r]);
-                }
-                if (!ok) break;
-                mbar_arrive(&bars[kFree0 + s]);
-            }
-            if (!ok) break;
-        }
-        if (!ok) {
-            if (lane == 0) flag(p.status, kDevTimeout);
-            *abort_flag = 1;
-        }
+        decay_values(0);
     }
     tc_fence_before();
     __syncthreads();
