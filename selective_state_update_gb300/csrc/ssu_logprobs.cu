@@ -8,6 +8,12 @@
 // its log probability.  s, t and m are fp32; a thread carries its own running
 // maximum and rescales its sums when that grows:
 //     d = m - m' <= 0:  s' = s e^d,  t' = (t + d s) e^d.
+// The sums are taken in powers of two against M, m log2(e) rounded to fp32:
+// x log2(e) - M is one FMA, and as M is the reference everywhere its rounding
+// drops out.  The product would overflow beyond 2.3e38: logits below -1e38
+// count as nothing, as they do beside any other, and a row that comes out with
+// nothing or with a NaN (masked altogether, or with infinities) is gone through
+// again with the difference x - m taken first.
 //
 // HBM-bound: every logit is read once.  A row is split over the CTAs of a
 // cluster when there are few rows, and the parts are joined through
@@ -96,50 +102,171 @@ __device__ __forceinline__ uint64_t merge_lists(const uint64_t *base, int lists)
     return v;
 }
 
-// Sums of one thread, warp or CTA.
+// Sums of one thread, warp or CTA: the reference m, s = sum 2^d and t = sum d
+// 2^d of the exponents d = (x log2(e) - m), or with `unit` log2(e) those of a
+// reference in the logits' own unit.
 struct Stats {
-    float m, s, t;  // t in units of ln 2: sum of log2(e) (x - m) e^(x - m)
+    float m, s, t;
 };
-__device__ __forceinline__ void rescale(Stats &a, float m) {
-    // never below -1e4: the exponential is zero long before, and the product
-    // with s stays finite
-    const float d = fmaxf((a.m - m) * kLog2e, -1e4f);
+__device__ __forceinline__ void rescale(Stats &a, float m, float unit) {
+    // never below -1e4: the power is zero long before, and the product with s
+    // stays finite
+    const float d = fmaxf((a.m - m) * unit, -1e4f);
     const float c = ex2(d);
     a.t = (a.t + d * a.s) * c;
     a.s *= c;
     a.m = m;
 }
-__device__ __forceinline__ Stats join(Stats a, Stats b) {
+__device__ __forceinline__ Stats join(Stats a, Stats b, float unit) {
     const float m = fmaxf(a.m, b.m);
-    rescale(a, m);
-    rescale(b, m);
+    rescale(a, m, unit);
+    rescale(b, m, unit);
     return {m, a.s + b.s, a.t + b.t};
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void unpack_vec(const T *p, float *v) {
-    if constexpr (VEC == 1) v[0] = to_float(*p);
-    else StateChunk<T>::unpack(*reinterpret_cast<const uint4 *>(p), v);
+// Running maxima start at kFloor and elements are raised to kLow, below it:
+// what is masked has the exponential zero, its product with the exponent is
+// zero and not NaN, and a row of nothing else sums to zero.
+constexpr float kFloor = -0.9e38f, kLow = -1e38f;
+__device__ __forceinline__ float raise(float v) {  // a NaN stays
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(kLow));
+    return r;
 }
 
-// A part of a row: the vectors [v0, v1) of VEC elements, and for the last
-// part the `tail` elements that fill no vector, as vectors of one element
-// after v1.  Vector v belongs to thread (v - v0) % kLpThreads.
-template <typename T, int VEC>
-struct Part {
-    const T *x;
-    int v0, v1, tail;
-    __device__ __forceinline__ int count() const { return v1 - v0 + tail; }
-    // element index of vector v0 + i, and how many elements it has
-    __device__ __forceinline__ int first(int i) const {
-        const int v = v0 + i;
-        return v < v1 ? v * VEC : v1 * VEC + (v - v1);
+// VEC elements as loaded; the largest of them; as floats.
+template <typename T>
+struct Logits;
+template <>
+struct Logits<float> {
+    uint4 u;
+    __device__ __forceinline__ void none() { u.x = u.y = u.z = u.w = 0xff800000u; }
+    __device__ __forceinline__ float largest() const {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
     }
-    __device__ __forceinline__ int size(int i) const { return v0 + i < v1 ? VEC : 1; }
+    __device__ __forceinline__ void floats(float *v) const {
+        StateChunk<float>::unpack(u, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = raise(v[j]);
+    }
+};
+template <>
+struct Logits<__half> {
+    uint4 u;
+    __device__ __forceinline__ void none() { u.x = u.y = u.z = u.w = 0xfc00fc00u; }
+    __device__ __forceinline__ float largest() const {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+        const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ void floats(float *v) const {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(h[j]);
+            v[2 * j] = raise(f.x);
+            v[2 * j + 1] = raise(f.y);
+        }
+    }
+};
+template <>
+struct Logits<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void none() { u.x = u.y = u.z = u.w = 0xff80ff80u; }
+    __device__ __forceinline__ float largest() const {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ void floats(float *v) const {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+        const __nv_bfloat162 low = __float2bfloat162_rn(kLow);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 c = __hmax2_nan(h[j], low);
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(&c);
+            v[2 * j] = __uint_as_float(w << 16);
+            v[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    }
 };
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobParams p, int parts) {
+// A part of a row: vectors i < nv of VEC elements from element e0 on, and the
+// `extra` elements outside the row's whole, aligned vectors -- those before
+// (`head` of them, from element 0) and those after (from element `tail`).
+// Vector i belongs to thread i % kLpThreads, extra e to thread e.
+template <typename T>
+struct Part {
+    static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    const T *x;
+    int nv, e0, extra, head, tail;
+    __device__ __forceinline__ Part(const LogprobParams &p, const T *row, int rank, int parts) : x(row) {
+        int before = static_cast<int>((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(T));
+        if (before > p.vocab) before = p.vocab;
+        const int all = (p.vocab - before) / VEC;
+        const int v0 = static_cast<int>(static_cast<int64_t>(all) * rank / parts);
+        nv = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / parts) - v0;
+        e0 = before + v0 * VEC;
+        head = rank == 0 ? before : 0;
+        tail = before + all * VEC;
+        extra = head + (rank == parts - 1 ? p.vocab - tail : 0);
+    }
+    __device__ __forceinline__ int extra_at(int e) const { return e < head ? e : tail + e - head; }
+    __device__ __forceinline__ int owner(int elem) const {
+        const int i = elem - e0;
+        if (i >= 0 && i < nv * VEC) return (i / VEC) % kLpThreads;
+        return elem < head ? elem : head + elem - tail;
+    }
+    __device__ __forceinline__ Logits<T> load(int i) const {
+        Logits<T> l;
+        l.u = *reinterpret_cast<const uint4 *>(x + e0 + i * VEC);
+        return l;
+    }
+    // the largest key of vector i
+    __device__ __forceinline__ uint64_t key(int i, int j) const { return make_key(to_float(x[e0 + i * VEC + j]), e0 + i * VEC + j); }
+};
+
+constexpr int kUnroll = 4;  // vectors a thread has in flight
+
+// The sums over the CTA, in every lane of its first warp.
+__device__ __forceinline__ Stats block_join(Stats a, Stats *wstats, float unit) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const Stats o = {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
+                         __shfl_xor_sync(0xffffffffu, a.t, off)};
+        a = join(a, o, unit);
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) wstats[warp] = a;
+    __syncthreads();
+    a = wstats[lane % kLpWarps];
+#pragma unroll
+    for (int off = kLpWarps / 2; off > 0; off >>= 1) {
+        const Stats o = {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
+                         __shfl_xor_sync(0xffffffffu, a.t, off)};
+        a = join(a, o, unit);
+    }
+    return a;
+}
+
+// The sums of a whole row with the difference taken before the product: for
+// rows with nothing but values near the type's lowest, or with infinities.
+template <typename T>
+__device__ __noinline__ Stats careful_row(const T *x, int vocab, Stats *wstats) {
+    Stats a = {-3.402823466e38f, 0.f, 0.f};
+    for (int i = threadIdx.x; i < vocab; i += kLpThreads) {
+        const float v = to_float(x[i]);
+        if (v > a.m) rescale(a, v, kLog2e);
+        const float d = (v - a.m) * kLog2e, e = ex2(d);
+        a.s += e;
+        a.t = fmaf(fmaxf(d, -1e4f), e, a.t);
+    }
+    return block_join(a, wstats, kLog2e);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobParams p, int parts) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     __shared__ Stats wstats[kLpWarps];
     __shared__ uint64_t lists[kLpWarps * 32];
     __shared__ Stats part_stats;
@@ -147,58 +274,63 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobParam
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / parts;
     const int rank = static_cast<int>(blockIdx.x - row * parts);
-    const int nvec = p.vocab / VEC;
-    Part<T, VEC> pt;
-    pt.x = static_cast<const T *>(p.logits) + row * p.row_stride;
-    pt.v0 = static_cast<int>(static_cast<int64_t>(nvec) * rank / parts);
-    pt.v1 = static_cast<int>(static_cast<int64_t>(nvec) * (rank + 1) / parts);
-    pt.tail = rank == parts - 1 ? p.vocab - nvec * VEC : 0;
-    const int n = pt.count();
+    const T *const x = static_cast<const T *>(p.logits) + row * p.row_stride;
+    const Part<T> pt(p, x, rank, parts);
 
-    Stats a = {-3.402823466e38f, 0.f, 0.f};  // the floor keeps x - m defined for rows of -inf
+    float m = kFloor;  // the largest so far
+    Stats a = {kFloor * kLog2e, 0.f, 0.f};
     float best = -INFINITY;
-    int best_i = -1;
-    for (int i = tid; i < n; i += kLpThreads) {
-        float v[VEC];
-        if (pt.size(i) == VEC) {
-            unpack_vec<T, VEC>(pt.x + pt.first(i), v);
-        } else {
-            v[0] = to_float(pt.x[pt.first(i)]);
+    int best_i = tid < pt.nv ? tid : -1;  // the group of vectors with this thread's largest logit
+    for (int i = tid; i < pt.nv; i += kUnroll * kLpThreads) {
+        Logits<T> l[kUnroll];
 #pragma unroll
-            for (int j = 1; j < VEC; ++j) v[j] = -INFINITY;
+        for (int u = 0; u < kUnroll; ++u) {
+            if (i + u * kLpThreads < pt.nv) l[u] = pt.load(i + u * kLpThreads);
+            else l[u].none();
         }
-        float vm = -INFINITY;
+        float vm = l[0].largest();
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) vm = fmaxf(vm, v[j]);
-        if (vm > best || best_i < 0) {
+        for (int u = 1; u < kUnroll; ++u) vm = fmaxf(vm, l[u].largest());
+        if (vm > best) {
             best = vm;
             best_i = i;
         }
-        if (vm > a.m) rescale(a, vm);
+        if (vm > m) {
+            m = vm;
+            rescale(a, m * kLog2e, 1.f);
+        }
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const float d = (v[j] - a.m) * kLog2e;
-            const float e = ex2(d);
-            a.s += e;
-            a.t = fmaf(fmaxf(d, -1e4f), e, a.t);  // -inf * 0 would be NaN
+        for (int u = 0; u < kUnroll; ++u) {
+            float v[VEC];
+            l[u].floats(v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float d = fmaf(v[j], kLog2e, -a.m), e = ex2(d);
+                a.s += e;
+                a.t = fmaf(d, e, a.t);
+            }
         }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const Stats o = {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
-                         __shfl_xor_sync(0xffffffffu, a.t, off)};
-        a = join(a, o);
+    uint64_t key = 0;  // this thread's largest
+    if (tid < pt.extra) {
+        const float v = to_float(x[pt.extra_at(tid)]);
+        key = make_key(v, pt.extra_at(tid));
+        if (v > m) rescale(a, v * kLog2e, 1.f);
+        const float d = fmaf(raise(v), kLog2e, -a.m), e = ex2(d);
+        a.s += e;
+        a.t = fmaf(d, e, a.t);
     }
-    if (lane == 0) wstats[warp] = a;
 
     if (p.top_k > 0) {
-        // this thread's largest key
-        uint64_t key = 0;
         if (best_i >= 0) {
-            const int e0 = pt.first(best_i), ne = pt.size(best_i);
-            for (int j = 0; j < ne; ++j) {
-                const uint64_t kj = make_key(to_float(pt.x[e0 + j]), e0 + j);
-                key = kj > key ? kj : key;
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = best_i + u * kLpThreads;
+                if (i >= pt.nv) break;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const uint64_t kj = pt.key(i, j);
+                    key = kj > key ? kj : key;
+                }
             }
         }
         lists[tid] = warp_sort(key);
@@ -211,15 +343,16 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobParam
         for (int o = warp; o < p.top_k; o += kLpWarps) {
             const uint64_t ok = __shfl_sync(0xffffffffu, owners, o);
             if (ok == 0) break;  // fewer threads with elements than k
-            // the owner's vectors: those congruent to its own
-            const int e = key_index(ok);
-            const int i0 = (e < pt.v1 * VEC ? e / VEC : pt.v1 + (e - pt.v1 * VEC)) - pt.v0;
-            for (int base = i0 % kLpThreads; base < n; base += 32 * kLpThreads) {
+            const int owner = pt.owner(key_index(ok));
+            if (owner < pt.extra) {
+                uint64_t kj = lane == 0 ? make_key(to_float(x[pt.extra_at(owner)]), pt.extra_at(owner)) : 0;
+                if (kj < bound) kj = 0;
+                mine = warp_merge(mine, warp_sort(kj));
+            }
+            for (int base = owner; base < pt.nv; base += 32 * kLpThreads) {
                 const int i = base + lane * kLpThreads;
-                const int ne = i < n ? pt.size(i) : 0;
                 for (int j = 0; j < VEC; ++j) {
-                    uint64_t kj = 0;
-                    if (j < ne) kj = make_key(to_float(pt.x[pt.first(i) + j]), pt.first(i) + j);
+                    uint64_t kj = i < pt.nv ? pt.key(i, j) : 0;
                     if (kj < bound) kj = 0;
                     if (__any_sync(0xffffffffu, kj != 0)) mine = warp_merge(mine, warp_sort(kj));
                 }
@@ -227,54 +360,60 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobParam
         }
         lists[tid] = mine;
     }
-    __syncthreads();
+    a = block_join(a, wstats, 1.f);  // (its barrier also completes the lists)
     if (warp == 0) {
-        Stats b = lane < kLpWarps ? wstats[lane] : Stats{-3.402823466e38f, 0.f, 0.f};
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const Stats o = {__shfl_xor_sync(0xffffffffu, b.m, off), __shfl_xor_sync(0xffffffffu, b.s, off),
-                             __shfl_xor_sync(0xffffffffu, b.t, off)};
-            b = join(b, o);
-        }
-        if (lane == 0) part_stats = b;
+        if (lane == 0) part_stats = a;
         if (p.top_k > 0) part_top[lane] = merge_lists(lists, kLpWarps);
     }
     if (parts > 1) cg::this_cluster().sync();
-    if (rank == 0 && warp == 0) {
-        __syncwarp();
+    else __syncthreads();
+    if (rank == 0) {
         Stats b = part_stats;
-        uint64_t top = p.top_k > 0 ? part_top[lane] : 0;
-        for (int c = 1; c < parts; ++c) {
-            b = join(b, *cg::this_cluster().map_shared_rank(&part_stats, c));
-            if (p.top_k > 0) top = warp_merge(top, cg::this_cluster().map_shared_rank(part_top, c)[lane]);
-        }
-        const bool none = b.s == 0.f;  // every logit is -inf
-        const float lse = logf(b.s);
-        if (lane == 0) {
-            const int64_t tok = load_index(p.tokens, row, p.tok_is_i64);
-            float lp = 0.f;
-            if (tok >= 0 && tok < p.vocab) lp = none ? -INFINITY : (to_float(pt.x[tok]) - b.m) - lse;
-            else if (tok != -1) {
-                flag(p.status, kDevBadEntry);
-                lp = __int_as_float(0x7fc00000);
+        for (int c = 1; c < parts; ++c) b = join(b, *cg::this_cluster().map_shared_rank(&part_stats, c), 1.f);
+        const bool careful = !(b.s > 0.f);  // (the same in every thread)
+        if (careful) b = careful_row(x, p.vocab, wstats);
+        if (warp == 0) {
+            uint64_t top = p.top_k > 0 ? part_top[lane] : 0;
+            if (p.top_k > 0)
+                for (int c = 1; c < parts; ++c) top = warp_merge(top, cg::this_cluster().map_shared_rank(part_top, c)[lane]);
+            const bool none = b.s == 0.f;  // every logit is -inf
+            const float ls = log2f(b.s);
+            const auto logprob = [&](float v) {
+                if (none) return -INFINITY;
+                if (careful) return (v - b.m) - kLn2 * ls;
+                // far below the fast sums' range the logit itself is all that counts
+                if (v < kLow && v > -INFINITY) return v - kLn2 * b.m;
+                return kLn2 * (fmaf(v, kLog2e, -b.m) - ls);
+            };
+            if (lane == 0) {
+                const int64_t tok = load_index(p.tokens, row, p.tok_is_i64);
+                float lp = 0.f;
+                if (tok >= 0 && tok < p.vocab) {
+                    lp = logprob(to_float(x[tok]));
+                } else if (tok != -1) {
+                    flag(p.status, kDevBadEntry);
+                    lp = __int_as_float(0x7fc00000);
+                }
+                p.logprob[row] = lp;
+                p.entropy[row] = none ? 0.f : kLn2 * (ls - b.t / b.s);
             }
-            p.logprob[row] = lp;
-            p.entropy[row] = none ? 0.f : lse - kLn2 * (b.t / b.s);
-        }
-        if (lane < p.top_k) {
-            const int64_t at = row * p.top_k + lane;
-            const int idx = key_index(top);
-            if (p.tok_is_i64) static_cast<int64_t *>(p.top_ids)[at] = idx;
-            else static_cast<int32_t *>(p.top_ids)[at] = idx;
-            p.top_logprob[at] = none ? -INFINITY : (key_value(top) - b.m) - lse;
+            if (lane < p.top_k) {
+                const int64_t at = row * p.top_k + lane;
+                const int idx = key_index(top);
+                if (p.tok_is_i64) static_cast<int64_t *>(p.top_ids)[at] = idx;
+                else static_cast<int32_t *>(p.top_ids)[at] = idx;
+                p.top_logprob[at] = logprob(key_value(top));
+            }
         }
     }
     // the others' shared memory stays until rank 0 has read it
     if (parts > 1) cg::this_cluster().sync();
 }
 
-template <typename T, int VEC>
-cudaError_t launch_lp(const LogprobParams &p, int parts, cudaStream_t stream) {
+template <typename T>
+cudaError_t launch_lp_t(const LogprobParams &p, cudaStream_t stream) {
+    int parts = 1;
+    while (parts < kMaxCluster && p.rows * parts * 2 <= 304) parts *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * parts));
     cfg.blockDim = dim3(kLpThreads);
@@ -285,16 +424,7 @@ cudaError_t launch_lp(const LogprobParams &p, int parts, cudaStream_t stream) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, VEC>, p, parts);
-}
-
-template <typename T>
-cudaError_t launch_lp_t(const LogprobParams &p, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
-    int parts = 1;
-    while (parts < kMaxCluster && p.rows * parts * 2 <= 304) parts *= 2;
-    const bool vec = p.row_stride % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
-    return vec ? launch_lp<T, V>(p, parts, stream) : launch_lp<T, 1>(p, parts, stream);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, p, parts);
 }
 
 }  // namespace

@@ -10,9 +10,11 @@
 // taken of the fp32 sum, not of the stored residual: one rounding less.  Sum,
 // mean and maximum are fp32.
 //
-// HBM-bound: every operand is read once and every output written once.  One
-// CTA holds a row in registers between the two reductions (the sum of
-// squares, the maximum), kEpt elements a thread.
+// HBM-bound: every operand is read once and every output written once.  A CTA
+// holds a row in registers between the two reductions (the sum of squares, the
+// maximum), EPT elements a thread.  The grid is as large as the GPU holds at
+// once; a CTA walks rows and has the next row's loads in flight while it reduces
+// and stores the current one.
 #include "ssu_device.cuh"
 #include "ssu_hybrid.h"
 
@@ -29,15 +31,21 @@ __device__ __forceinline__ __half from_float<__half>(float v) { return __float2h
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// VEC consecutive elements <-> floats (VEC = 1, or 16 bytes of T).
+// VEC consecutive elements (VEC = 1, or 16 bytes of T) as loaded, and as floats.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float *v) {
-    if constexpr (VEC == 1) {
-        v[0] = to_float(*p);
-    } else {
-        StateChunk<T>::unpack(ld_stream(p), v);
-    }
-}
+struct Raw {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void zero() { v = from_float<T>(0.f); }
+    __device__ __forceinline__ void unpack(float *f) const { f[0] = to_float(v); }
+};
+template <typename T>
+struct Raw<T, 16 / sizeof(T)> {
+    uint4 v;
+    __device__ __forceinline__ void load(const T *p) { v = ld_stream(p); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void unpack(float *f) const { StateChunk<T>::unpack(v, f); }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *v) {
     if constexpr (VEC == 1) {
@@ -94,139 +102,182 @@ __device__ __forceinline__ float block_reduce(float v, float *part) {
     return v;
 }
 
-// T: element type of x; VEC: elements a load; EPT: elements a thread.
-template <typename T, int VEC, int EPT>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
+// Elements a thread holds by the row's width, and the threads that makes at most.
+constexpr int elements_per_thread(int hidden) { return hidden <= 2048 ? 8 : hidden <= 8192 ? 16 : 32; }
+constexpr int ept_threads(int ept) { return ept == 8 ? 2048 / 8 : ept == 16 ? 8192 / 16 : kNormMaxHidden / 32; }
+
+// T: element type of x; VEC: elements a load; EPT: elements a thread; RES:
+// with a residual.
+template <typename T, int VEC, int EPT, bool RES>
+__global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) norm_kernel(const NormParams p) {
     constexpr int NV = EPT / VEC;
+    constexpr bool kAhead = EPT < 32;  // a second row does not fit the registers of 1024 threads
     __shared__ float part[2][32];
     __shared__ int bmax[kNormMaxHidden / kNormBlock];  // VEC == 1: the blocks' maxima (bits of non-negative floats)
-    const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, nthr = blockDim.x;
-    const T *x = static_cast<const T *>(p.x) + row * p.xs;
-    const T *res = p.residual ? static_cast<const T *>(p.residual) + row * p.rs : nullptr;
-    float r[EPT];
+    Raw<T, VEC> xr[NV], er[RES ? NV : 1];
+    const auto fetch = [&](int64_t row) {
+        const T *x = static_cast<const T *>(p.x) + row * p.xs;
+        const T *res = RES ? static_cast<const T *>(p.residual) + row * p.rs : nullptr;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int col = (tid + j * nthr) * VEC;
-        if (col < p.hidden) {
-            load_vec<T, VEC>(x + col, r + j * VEC);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) r[j * VEC + i] = 0.f;
+        for (int j = 0; j < NV; ++j) {
+            const int col = (tid + j * nthr) * VEC;
+            if (row < p.rows && col < p.hidden) {
+                xr[j].load(x + col);
+                if constexpr (RES) er[j].load(res + col);
+            } else {
+                xr[j].zero();
+                if constexpr (RES) er[j].zero();
+            }
         }
-    }
-    if (res) {
-        float e[EPT];
+    };
+    if (kAhead) fetch(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        if (!kAhead) fetch(row);
+        float r[EPT];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            xr[j].unpack(r + j * VEC);
+            if constexpr (RES) {
+                float e[VEC];
+                er[j].unpack(e);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) r[j * VEC + i] += e[i];
+            }
+        }
+        if (kAhead) fetch(row + gridDim.x);
+        if constexpr (RES) {
+            T *ro = static_cast<T *>(p.residual_out) + row * p.ros;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (tid + j * nthr) * VEC;
+                if (col < p.hidden) store_vec<T, VEC>(ro + col, r + j * VEC);
+            }
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) ss = fmaf(r[i], r[i], ss);
+        ss = block_reduce<false>(ss, part[0]);
+        const float inv = __frsqrt_rn(ss / static_cast<float>(p.hidden) + p.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (tid + j * nthr) * VEC;
             if (col < p.hidden) {
-                load_vec<T, VEC>(res + col, e + j * VEC);
-            } else {
+                float w[VEC];
+                load_weight<VEC>(p, col, w);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) e[j * VEC + i] = 0.f;
+                for (int i = 0; i < VEC; ++i) r[j * VEC + i] = r[j * VEC + i] * inv * w[i];
             }
         }
-        T *ro = static_cast<T *>(p.residual_out) + row * p.ros;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (tid + j * nthr) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) r[j * VEC + i] += e[j * VEC + i];
-            if (col < p.hidden) store_vec<T, VEC>(ro + col, r + j * VEC);
-        }
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) ss = fmaf(r[i], r[i], ss);
-    ss = block_reduce<false>(ss, part[0]);
-    const float inv = __frsqrt_rn(ss / static_cast<float>(p.hidden) + p.eps);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int col = (tid + j * nthr) * VEC;
-        if (col < p.hidden) {
-            float w[VEC];
-            load_weight<VEC>(p, col, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) r[j * VEC + i] = r[j * VEC + i] * inv * w[i];
-        }
-    }
-    if (p.quant == kQuantNone) {
-        T *y = static_cast<T *>(p.y) + row * p.ys;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (tid + j * nthr) * VEC;
-            if (col < p.hidden) store_vec<T, VEC>(y + col, r + j * VEC);
-        }
-        return;
-    }
-    // Maxima of the groups, per vector j.
-    float amax[NV];
-    if (p.quant == kQuantRow) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) m = fmaxf(m, fabsf(r[i]));
-        m = block_reduce<true>(m, part[1]);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) amax[j] = m;
-        if (tid == 0) p.scales[row] = shadow_scale_of(m);
-    } else {
-        const int nblk = (p.hidden + kNormBlock - 1) / kNormBlock;
-        float *scales = p.scales + row * nblk;
-        if constexpr (VEC == 1) {
-            for (int b = tid; b < nblk; b += nthr) bmax[b] = 0;
-            __syncthreads();
+        if (p.quant == kQuantNone) {
+            T *y = static_cast<T *>(p.y) + row * p.ys;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int col = tid + j * nthr;
-                // a NaN counts as no magnitude, as in fmaxf
-                if (col < p.hidden && r[j] == r[j]) atomicMax(&bmax[col / kNormBlock], __float_as_int(fabsf(r[j])));
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = tid + j * nthr;
-                amax[j] = col < p.hidden ? __int_as_float(bmax[col / kNormBlock]) : 0.f;
-            }
-            for (int b = tid; b < nblk; b += nthr) scales[b] = shadow_scale_of(__int_as_float(bmax[b]));
-        } else {
-            // 128 / VEC neighbouring lanes hold a block
-            constexpr int L = kNormBlock / VEC;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(r[j * VEC + i]));
-#pragma unroll
-                for (int off = L / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                amax[j] = m;
                 const int col = (tid + j * nthr) * VEC;
-                if (col < p.hidden && tid % L == 0) scales[col / kNormBlock] = shadow_scale_of(m);
+                if (col < p.hidden) store_vec<T, VEC>(y + col, r + j * VEC);
             }
+            __syncthreads();  // `part` is read
+            continue;
         }
-    }
-    unsigned char *y = static_cast<unsigned char *>(p.y) + row * p.ys;
+        // Maxima of the groups, per vector j.
+        float amax[NV];
+        if (p.quant == kQuantRow) {
+            float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int col = (tid + j * nthr) * VEC;
-        if (col >= p.hidden) continue;
-        const float f = shadow_factor_of(amax[j]);
-        if constexpr (VEC == 1) {
-            y[col] = e4m3_code(r[j] * f);
+            for (int i = 0; i < EPT; ++i) m = fmaxf(m, fabsf(r[i]));
+            m = block_reduce<true>(m, part[1]);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) amax[j] = m;
+            if (tid == 0) p.scales[row] = shadow_scale_of(m);
         } else {
-            uint32_t w[VEC / 4];
+            const int nblk = (p.hidden + kNormBlock - 1) / kNormBlock;
+            float *scales = p.scales + row * nblk;
+            if constexpr (VEC == 1) {
+                for (int b = tid; b < nblk; b += nthr) bmax[b] = 0;
+                __syncthreads();
 #pragma unroll
-            for (int i = 0; i < VEC / 4; ++i) {
-                const float *v = r + j * VEC + 4 * i;
-                w[i] = e4m3x2_codes(v[0] * f, v[1] * f) | (e4m3x2_codes(v[2] * f, v[3] * f) << 16);
+                for (int j = 0; j < NV; ++j) {
+                    const int col = tid + j * nthr;
+                    // a NaN counts as no magnitude, as in fmaxf
+                    if (col < p.hidden && r[j] == r[j]) atomicMax(&bmax[col / kNormBlock], __float_as_int(fabsf(r[j])));
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int col = tid + j * nthr;
+                    amax[j] = col < p.hidden ? __int_as_float(bmax[col / kNormBlock]) : 0.f;
+                }
+                for (int b = tid; b < nblk; b += nthr) scales[b] = shadow_scale_of(__int_as_float(bmax[b]));
+            } else {
+                // 128 / VEC neighbouring lanes hold a block
+                constexpr int L = kNormBlock / VEC;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(r[j * VEC + i]));
+#pragma unroll
+                    for (int off = L / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    amax[j] = m;
+                    const int col = (tid + j * nthr) * VEC;
+                    if (col < p.hidden && tid % L == 0) scales[col / kNormBlock] = shadow_scale_of(m);
+                }
             }
-            if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(y + col) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(y + col) = w[0];
         }
+        unsigned char *y = static_cast<unsigned char *>(p.y) + row * p.ys;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = (tid + j * nthr) * VEC;
+            if (col >= p.hidden) continue;
+            const float f = shadow_factor_of(amax[j]);
+            if constexpr (VEC == 1) {
+                y[col] = e4m3_code(r[j] * f);
+            } else {
+                uint32_t w[VEC / 4];
+#pragma unroll
+                for (int i = 0; i < VEC / 4; ++i) {
+                    const float *v = r + j * VEC + 4 * i;
+                    w[i] = e4m3x2_codes(v[0] * f, v[1] * f) | (e4m3x2_codes(v[2] * f, v[3] * f) << 16);
+                }
+                if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(y + col) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint32_t *>(y + col) = w[0];
+            }
+        }
+        __syncthreads();  // `part` and `bmax` are read
     }
 }
 
 bool aligned(const void *q, int64_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; }
+
+// CTAs of this kernel that the GPU holds at once, by threads (cached).
+template <typename T, int VEC, int EPT, bool RES>
+int resident(int threads) {
+    static int cache[33];
+    int n = __atomic_load_n(&cache[threads / 32], __ATOMIC_RELAXED);
+    if (n == 0) {
+        int dev = 0, sms = 0, per = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, norm_kernel<T, VEC, EPT, RES>, threads, 0) != cudaSuccess || per <= 0)
+            return 0;
+        n = per * sms;
+        __atomic_store_n(&cache[threads / 32], n, __ATOMIC_RELAXED);
+    }
+    return n;
+}
+
+template <typename T, int VEC, int EPT, bool RES>
+cudaError_t launch_norm_r(const NormParams &p, cudaStream_t stream) {
+    const int threads = ((p.hidden + EPT - 1) / EPT + 31) / 32 * 32;
+    const int most = resident<T, VEC, EPT, RES>(threads);
+    if (most <= 0) return cudaErrorInvalidConfiguration;
+    const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
+    norm_kernel<T, VEC, EPT, RES><<<grid, threads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, int VEC, int EPT>
+cudaError_t launch_norm_k(const NormParams &p, cudaStream_t stream) {
+    return p.residual ? launch_norm_r<T, VEC, EPT, true>(p, stream) : launch_norm_r<T, VEC, EPT, false>(p, stream);
+}
 
 template <typename T>
 cudaError_t launch_norm_t(const NormParams &p, cudaStream_t stream) {
@@ -236,19 +287,15 @@ cudaError_t launch_norm_t(const NormParams &p, cudaStream_t stream) {
     const bool vec = p.hidden % V == 0 && p.xs % V == 0 && aligned(p.x, 16) && p.ys % V == 0 && aligned(p.y, V * ye) &&
                      aligned(p.weight, 16) && (p.weight_dtype == kF32 || V == 8) &&
                      (!p.residual || (p.rs % V == 0 && p.ros % V == 0 && aligned(p.residual, 16) && aligned(p.residual_out, 16)));
-    const int ept = p.hidden <= 2048 ? 8 : p.hidden <= 8192 ? 16 : 32;
-    const int threads = ((p.hidden + ept - 1) / ept + 31) / 32 * 32;
-    const unsigned grid = static_cast<unsigned>(p.rows);
+    const int ept = elements_per_thread(p.hidden);
     if (vec) {
-        if (ept == 8) norm_kernel<T, V, 8><<<grid, threads, 0, stream>>>(p);
-        else if (ept == 16) norm_kernel<T, V, 16><<<grid, threads, 0, stream>>>(p);
-        else norm_kernel<T, V, 32><<<grid, threads, 0, stream>>>(p);
-    } else {
-        if (ept == 8) norm_kernel<T, 1, 8><<<grid, threads, 0, stream>>>(p);
-        else if (ept == 16) norm_kernel<T, 1, 16><<<grid, threads, 0, stream>>>(p);
-        else norm_kernel<T, 1, 32><<<grid, threads, 0, stream>>>(p);
+        if (ept == 8) return launch_norm_k<T, V, 8>(p, stream);
+        if (ept == 16) return launch_norm_k<T, V, 16>(p, stream);
+        return launch_norm_k<T, V, 32>(p, stream);
     }
-    return cudaGetLastError();
+    if (ept == 8) return launch_norm_k<T, 1, 8>(p, stream);
+    if (ept == 16) return launch_norm_k<T, 1, 16>(p, stream);
+    return launch_norm_k<T, 1, 32>(p, stream);
 }
 
 }  // namespace

@@ -7,12 +7,12 @@ exported by the package."""
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
 
-from . import (_DTYPE, _ITYPE, _need, _on_device_of_first, _ptr, _raise, _ssd_workspace, _stream, _table, OK,
-               SLOTS_STRIDED, lib)
+from . import _DTYPE, _ITYPE, _need, _raise, _ssd_workspace, _stream, _table, OK, SLOTS_STRIDED, SlotTable, lib
 
 _I64x2 = ctypes.c_int64 * 2
 
@@ -57,9 +57,19 @@ class LogprobArgs(ctypes.Structure):
     ]
 
 
+def _packer(cls) -> struct.Struct:
+    """The C layout of a ctypes structure for one struct.pack call: filling the
+    structure field by field costs more than some of the kernels take."""
+    code = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "Q", _I64x2: "2q"}
+    return struct.Struct("@" + "".join(code[f[1]] for f in cls._fields_))
+
+
+_LINATTN, _NORM, _LOGPROB, _SLOTS = (_packer(c) for c in (LinattnArgs, NormArgs, LogprobArgs, SlotTable))
+
+
 def bind(L) -> None:
     """Argument types of these entry points on the loaded library."""
-    p = ctypes.c_void_p
+    p = ctypes.c_void_p  # structures are passed as their packed bytes
     L.ssu_linear_attention_step.argtypes = [p, p, p, p]
     L.ssu_linear_attention_workspace_size.argtypes = [p, ctypes.c_int64, ctypes.c_int64, p]
     L.ssu_linear_attention_prefill.argtypes = [p, ctypes.c_int64, p, ctypes.c_int32, ctypes.c_int64, p, p, p,
@@ -71,42 +81,62 @@ def bind(L) -> None:
         fn.restype = ctypes.c_int
 
 
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
+def _launch(fn, device: int, stream, *args) -> None:
+    """fn(*args, stream) with the operands' device current; raises what it reports."""
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != OK:
+        _raise(rc)
 
 
-def _status(status: Optional[torch.Tensor]):
-    if status is None:
+def _slots(t: Optional[torch.Tensor]):
+    """A slot table's packed structure."""
+    if t is None:
         return None
+    if t.dim() == 1 and t.is_cuda and t.dtype in _ITYPE:
+        n, s = t.shape[0], t.stride(0)
+        return _SLOTS.pack(t.data_ptr(), _ITYPE[t.dtype], SLOTS_STRIDED, s, s, (n - 1) * s + 1 if n else 0)
+    return ctypes.byref(_table(t, SLOTS_STRIDED))
+
+
+def _status(status: Optional[torch.Tensor]) -> int:
+    if status is None:
+        return 0
     _need(status.dtype == torch.int32 and status.numel() >= 1 and status.is_cuda, "status must be an int32 CUDA tensor")
     return status.data_ptr()
 
 
-def _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status) -> LinattnArgs:
+def _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status):
+    """(packed arguments, out)."""
     _need(state.dim() == 4 and state.is_contiguous(), "state must be a contiguous [slots, heads, dim, dstate] tensor")
-    slots, heads, dim, dstate = state.shape
     _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k and v are [rows, heads, head size]")
-    rows, kv_heads = q.shape[0], k.shape[1]
-    _need(q.shape[1] == heads and q.shape[2] == dstate, "q must be [rows, heads, dstate]")
-    _need(k.shape[0] == rows and k.shape[2] == dstate, "k must be [rows, kv_heads, dstate]")
-    _need(v.shape[0] == rows and v.shape[1] == kv_heads and v.shape[2] == dim, "v must be [rows, kv_heads, dim]")
-    dtype = q.dtype
+    slots, heads, dim, dstate = state.shape
+    rows, kv_heads, dtype = q.shape[0], k.shape[1], q.dtype
+    _need(q.shape == (rows, heads, dstate), "q must be [rows, heads, dstate]")
+    _need(k.shape == (rows, kv_heads, dstate), "k must be [rows, kv_heads, dstate]")
+    _need(v.shape == (rows, kv_heads, dim), "v must be [rows, kv_heads, dim]")
     _need(state.dtype in _DTYPE and dtype in _DTYPE, "unsupported dtype")
     _need(k.dtype == dtype and v.dtype == dtype, "k and v must have the dtype of q")
-    _need(out.shape == (rows, heads, dim) and out.dtype == dtype, "out must be [rows, heads, dim] in q's dtype")
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device)
+    else:
+        _need(out.shape == (rows, heads, dim) and out.dtype == dtype, "out must be [rows, heads, dim] in q's dtype")
     qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
     _need(qs[2] == ks[2] == vs[2] == os[2] == 1, "the last dimension of q, k, v and out must have unit stride")
     _need(log_decay.dtype == torch.float32 and log_decay.shape == (heads,) and log_decay.is_contiguous(),
           "log_decay must be a contiguous fp32 [heads] tensor")
     _need(state.is_cuda and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and log_decay.is_cuda,
           "all tensors must be CUDA tensors")
-    return LinattnArgs(slots, heads, kv_heads, dim, dstate, rows, _DTYPE[dtype], _DTYPE[state.dtype],
-                       dstate ** -0.5 if scale is None else scale, 0, pad_slot_id,
-                       state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                       out.data_ptr(), qs[:2], ks[:2], vs[:2], os[:2], _status(status))
+    return _LINATTN.pack(slots, heads, kv_heads, dim, dstate, rows, _DTYPE[dtype], _DTYPE[state.dtype],
+                         dstate ** -0.5 if scale is None else scale, 0, pad_slot_id, state.data_ptr(), q.data_ptr(),
+                         k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1],
+                         vs[0], vs[1], os[0], os[1], _status(status)), out
 
 
-@_on_device_of_first
 def ssu_linear_attention_step(state, q, k, v, log_decay, scale: Optional[float] = None, state_batch_indices=None,
                               dst_state_batch_indices=None, pad_slot_id: int = -1, out=None, status=None,
                               stream=None) -> torch.Tensor:
@@ -118,17 +148,12 @@ def ssu_linear_attention_step(state, q, k, v, log_decay, scale: Optional[float] 
     ``[batch, kv_heads, dim]`` (slices of a fused projection are fine),
     ``log_decay`` fp32 ``[heads]``; ``scale`` defaults to ``dstate ** -0.5``.
     Returns out ``[batch, heads, dim]`` in q's dtype."""
-    if out is None:
-        out = torch.empty((q.shape[0], state.shape[1], state.shape[2]), dtype=q.dtype, device=q.device)
-    a = _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status)
-    rc = lib().ssu_linear_attention_step(ctypes.byref(a), _ref(_table(state_batch_indices, SLOTS_STRIDED)),
-                                         _ref(_table(dst_state_batch_indices, SLOTS_STRIDED)), _stream(stream))
-    if rc != OK:
-        _raise(rc)
+    a, out = _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status)
+    _launch(lib().ssu_linear_attention_step, state.get_device(), stream, a, _slots(state_batch_indices),
+            _slots(dst_state_batch_indices))
     return out
 
 
-@_on_device_of_first
 def ssu_linear_attention_prefill(state, q, k, v, log_decay, cu_seqlens, scale: Optional[float] = None,
                                  state_batch_indices=None, dst_state_batch_indices=None, pad_slot_id: int = -1,
                                  max_seqlen: Optional[int] = None, out=None, status=None, stream=None) -> torch.Tensor:
@@ -143,30 +168,25 @@ def ssu_linear_attention_prefill(state, q, k, v, log_decay, cu_seqlens, scale: O
     split.  Returns out ``[tokens, heads, dim]`` in q's dtype."""
     _need(cu_seqlens.dtype in _ITYPE and cu_seqlens.is_cuda and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()
           and cu_seqlens.numel() >= 1, "cu_seqlens must be a contiguous int32/int64 [nseq + 1] CUDA tensor")
-    if out is None:
-        out = torch.empty((q.shape[0], state.shape[1], state.shape[2]), dtype=q.dtype, device=q.device)
-    a = _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status)
-    nseq, longest = cu_seqlens.numel() - 1, 0 if max_seqlen is None else max_seqlen
+    a, out = _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status)
+    nseq, longest = cu_seqlens.shape[0] - 1, 0 if max_seqlen is None else max_seqlen
     nbytes = ctypes.c_uint64(0)
-    rc = lib().ssu_linear_attention_workspace_size(ctypes.byref(a), nseq, longest, ctypes.byref(nbytes))
+    L = lib()
+    rc = L.ssu_linear_attention_workspace_size(a, nseq, longest, ctypes.byref(nbytes))
     if rc != OK:
         _raise(rc)
-    ws = None
-    if nbytes.value:
+    need, ws = nbytes.value, None
+    if need:
         # on the current stream a block of the caching allocator (also inside a
         # graph's own pool); on another one the workspace kept for that stream
-        ws = (torch.empty(nbytes.value, dtype=torch.uint8, device=q.device) if stream is None
-              else _ssd_workspace(q.device, nbytes.value, stream))
-    rc = lib().ssu_linear_attention_prefill(ctypes.byref(a), nseq, cu_seqlens.data_ptr(), _ITYPE[cu_seqlens.dtype],
-                                            longest, _ref(_table(state_batch_indices, SLOTS_STRIDED)),
-                                            _ref(_table(dst_state_batch_indices, SLOTS_STRIDED)), _ptr(ws),
-                                            0 if ws is None else ws.numel(), _stream(stream))
-    if rc != OK:
-        _raise(rc)
+        ws = (torch.empty(need, dtype=torch.uint8, device=q.device) if stream is None
+              else _ssd_workspace(q.device, need, stream))
+    _launch(L.ssu_linear_attention_prefill, state.get_device(), stream, a, nseq, cu_seqlens.data_ptr(),
+            _ITYPE[cu_seqlens.dtype], longest, _slots(state_batch_indices), _slots(dst_state_batch_indices),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out
 
 
-@_on_device_of_first
 def ssu_add_rmsnorm(x, weight, eps: float = 1e-5, residual=None, quant: str = "none", residual_out=None, out=None,
                     scales=None, stream=None):
     """RMS norm of the rows of x ``[rows, hidden]``, with the residual's
@@ -205,19 +225,18 @@ def ssu_add_rmsnorm(x, weight, eps: float = 1e-5, residual=None, quant: str = "n
         shape = (rows,) if fmt == NORM_ROW else (rows, -(-hidden // NORM_BLOCK_COLUMNS))
         if scales is None:
             scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-        _need(scales.shape == shape and scales.dtype == torch.float32 and scales.is_contiguous() and scales.is_cuda,
-              f"scales must be a contiguous fp32 CUDA tensor of shape {shape}")
-    a = NormArgs(rows, hidden, _DTYPE[x.dtype], _DTYPE[weight.dtype], fmt, eps, x.data_ptr(), _ptr(residual),
-                 weight.data_ptr(), _ptr(residual_out), out.data_ptr(), _ptr(scales), x.stride(0),
-                 0 if residual is None else residual.stride(0), 0 if residual is None else residual_out.stride(0),
-                 out.stride(0))
-    rc = lib().ssu_add_rmsnorm(ctypes.byref(a), _stream(stream))
-    if rc != OK:
-        _raise(rc)
+        else:
+            _need(scales.shape == shape and scales.dtype == torch.float32 and scales.is_contiguous() and scales.is_cuda,
+                  f"scales must be a contiguous fp32 CUDA tensor of shape {shape}")
+    res, res_out = (0, 0) if residual is None else (residual.data_ptr(), residual_out.data_ptr())
+    a = _NORM.pack(rows, hidden, _DTYPE[x.dtype], _DTYPE[weight.dtype], fmt, eps, x.data_ptr(), res, weight.data_ptr(),
+                   res_out, out.data_ptr(), 0 if scales is None else scales.data_ptr(), x.stride(0),
+                   0 if residual is None else residual.stride(0), 0 if residual is None else residual_out.stride(0),
+                   out.stride(0))
+    _launch(lib().ssu_add_rmsnorm, x.get_device(), stream, a)
     return out, scales, residual_out
 
 
-@_on_device_of_first
 def ssu_token_logprobs(logits, tokens, top_k: int = 0, status=None, stream=None):
     """Log probabilities of ``tokens`` ``[rows]`` under ``logits`` ``[rows,
     vocab]``, the rows' entropy and the ``top_k`` most likely alternatives
@@ -231,15 +250,15 @@ def ssu_token_logprobs(logits, tokens, top_k: int = 0, status=None, stream=None)
     rows, vocab = logits.shape
     _need(tokens.shape == (rows,) and tokens.dtype in _ITYPE and tokens.is_cuda and tokens.is_contiguous(),
           "tokens must be a contiguous int32/int64 [rows] CUDA tensor")
-    both = torch.empty((2, rows), dtype=torch.float32, device=logits.device)
+    device = logits.device
+    logprobs = torch.empty(rows, dtype=torch.float32, device=device)
+    entropy = torch.empty(rows, dtype=torch.float32, device=device)
     ids = top = None
     if top_k > 0:
-        ids = torch.empty((rows, top_k), dtype=tokens.dtype, device=logits.device)
-        top = torch.empty((rows, top_k), dtype=torch.float32, device=logits.device)
-    a = LogprobArgs(rows, vocab, logits.stride(0), _DTYPE[logits.dtype], _ITYPE[tokens.dtype], top_k, 0,
-                    logits.data_ptr(), tokens.data_ptr(), both.data_ptr(), both.data_ptr() + 4 * rows, _ptr(ids),
-                    _ptr(top), _status(status))
-    rc = lib().ssu_token_logprobs(ctypes.byref(a), _stream(stream))
-    if rc != OK:
-        _raise(rc)
-    return both[0], both[1], ids, top
+        ids = torch.empty((rows, top_k), dtype=tokens.dtype, device=device)
+        top = torch.empty((rows, top_k), dtype=torch.float32, device=device)
+    a = _LOGPROB.pack(rows, vocab, logits.stride(0), _DTYPE[logits.dtype], _ITYPE[tokens.dtype], top_k, 0, logits.data_ptr(),
+                      tokens.data_ptr(), logprobs.data_ptr(), entropy.data_ptr(), 0 if ids is None else ids.data_ptr(),
+                      0 if top is None else top.data_ptr(), _status(status))
+    _launch(lib().ssu_token_logprobs, logits.get_device(), stream, a)
+    return logprobs, entropy, ids, top
