@@ -19,14 +19,16 @@
 // cluster when there are few rows, and the parts are joined through
 // distributed shared memory, so a call is one launch without a workspace.
 //
-// The largest logits take no second pass.  Keys (value made monotone, then
-// the index downwards) are unique.  While streaming, a thread only notes its
-// largest value (which the softmax needs anyway) and the vector it came from.
-// The k-th largest of the threads' maxima is a lower bound of the k-th
-// largest key, and only the k threads whose maximum reaches it can hold any
-// key that does: those threads' vectors are read again (k / threads of the
-// row, out of L2), and what reaches the bound goes through a sorted list of 32
-// keys a warp.
+// The largest logits take no second pass.  While streaming, a thread only
+// notes its largest value, which the softmax needs anyway, and the vectors it
+// came from.  The k-th largest of the threads' maxima is a lower bound of the
+// k-th largest logit, and only threads whose maximum reaches it can hold any
+// logit that does: those threads' vectors (about k / threads of the row) are
+// read again, out of L2.  What reaches the bound is collected, a little more
+// than k as a rule, and placed by counting what is larger, by unique keys of
+// value and index.  If too many tie with the bound for the collection, the
+// threads' largest keys take the place of their values, which leaves k threads;
+// if those alone hold too many, sorted lists of 32 keys a warp are kept instead.
 #include <cooperative_groups.h>
 
 #include "ssu_device.cuh"
@@ -50,33 +52,35 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Unique keys: larger values first, then lower indices; never 0.  -0 equals
-// 0, a NaN orders as -inf.
-__device__ __forceinline__ uint64_t make_key(float x, int idx) {
-    const float c = fmaxf(x, -INFINITY) + 0.f;
-    const uint32_t b = __float_as_uint(c);
-    const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return (static_cast<uint64_t>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(idx));
+// Values as integers in their order, never 0.  -0 equals 0, a NaN orders as
+// -inf.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(fmaxf(x, -INFINITY) + 0.f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t o = static_cast<uint32_t>(key >> 32);
+__device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
+// Unique keys: larger values first, then lower indices; never 0.
+__device__ __forceinline__ uint64_t make_key(float x, int idx) {
+    return (static_cast<uint64_t>(ordered(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(idx));
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return value_of(static_cast<uint32_t>(key >> 32)); }
 __device__ __forceinline__ int key_index(uint64_t key) {
     return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m) { return __shfl_xor_sync(0xffffffffu, v, m); }
-
 // One compare-exchange step of a bitonic network over the lanes, descending
 // where `desc`.
-__device__ __forceinline__ uint64_t exchange(uint64_t v, int m, bool desc) {
-    const uint64_t o = shfl_xor64(v, m);
+template <typename K>
+__device__ __forceinline__ K exchange(K v, int m, bool desc) {
+    const K o = __shfl_xor_sync(0xffffffffu, v, m);
     const bool upper = (threadIdx.x & m) != 0;
     return (v > o) == (upper != desc) ? v : o;
 }
 // The warp's 32 keys sorted downwards over the lanes.
-__device__ __forceinline__ uint64_t warp_sort(uint64_t v) {
+template <typename K>
+__device__ __forceinline__ K warp_sort(K v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 2; k <= 32; k <<= 1) {
@@ -86,20 +90,27 @@ __device__ __forceinline__ uint64_t warp_sort(uint64_t v) {
     return v;
 }
 // The 32 largest of two downward-sorted lists, sorted downwards.
-__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
-    const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - (threadIdx.x & 31));
-    uint64_t v = a > r ? a : r;
+template <typename K>
+__device__ __forceinline__ K warp_merge(K a, K b) {
+    const K r = __shfl_sync(0xffffffffu, b, 31 - (threadIdx.x & 31));
+    K v = a > r ? a : r;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) v = exchange(v, m, true);
     return v;
 }
-// The 32 largest keys of `lists` downward-sorted lists of 32 (list i at
-// base + 32 i) by one warp, sorted downwards over its lanes.
-__device__ __forceinline__ uint64_t merge_lists(const uint64_t *base, int lists) {
-    const int lane = threadIdx.x & 31;
-    uint64_t v = base[lane];
-    for (int i = 1; i < lists; ++i) v = warp_merge(v, base[32 * i + lane]);
-    return v;
+// The 32 largest of the CTA's keys, one a thread, sorted downwards at the
+// start of `lists`; begins and ends with a barrier.
+template <typename K>
+__device__ __forceinline__ void largest_of_threads(K key, K *lists) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    lists[threadIdx.x] = warp_sort(key);
+    __syncthreads();
+#pragma unroll 1
+    for (int half = kLpWarps / 2; half > 0; half >>= 1) {
+        if (warp < half) lists[32 * warp + lane] = warp_merge(lists[32 * warp + lane], lists[32 * (warp + half) + lane]);
+        __syncthreads();
+    }
 }
 
 // Sums of one thread, warp or CTA: the reference m, s = sum 2^d and t = sum d
@@ -212,21 +223,16 @@ struct Part {
         extra = head + (rank == parts - 1 ? p.vocab - tail : 0);
     }
     __device__ __forceinline__ int extra_at(int e) const { return e < head ? e : tail + e - head; }
-    __device__ __forceinline__ int owner(int elem) const {
-        const int i = elem - e0;
-        if (i >= 0 && i < nv * VEC) return (i / VEC) % kLpThreads;
-        return elem < head ? elem : head + elem - tail;
-    }
     __device__ __forceinline__ Logits<T> load(int i) const {
         Logits<T> l;
         l.u = *reinterpret_cast<const uint4 *>(x + e0 + i * VEC);
         return l;
     }
-    // the largest key of vector i
-    __device__ __forceinline__ uint64_t key(int i, int j) const { return make_key(to_float(x[e0 + i * VEC + j]), e0 + i * VEC + j); }
+    __device__ __forceinline__ int element(int i, int j) const { return e0 + i * VEC + j; }
 };
 
 constexpr int kUnroll = 4;  // vectors a thread has in flight
+constexpr int kMaxHits = 512;  // candidates collected before the sorted lists take over
 
 // The sums over the CTA, in every lane of its first warp.
 __device__ __forceinline__ Stats block_join(Stats a, Stats *wstats, float unit) {
@@ -264,13 +270,94 @@ __device__ __noinline__ Stats careful_row(const T *x, int vocab, Stats *wstats) 
     return block_join(a, wstats, kLog2e);
 }
 
+// Shared memory of the search for the largest.
+struct TopSearch {
+    uint64_t lists[kLpThreads];
+    uint64_t found[kMaxHits];
+    int hits;
+    uint64_t top[32];
+};
+
+// Collects the keys of a part that reach `bound`, from the lanes in `owners` of
+// each warp (and every thread's extra element); true if they fitted, and then
+// the 32 largest are in ts->top.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobParams p, int parts) {
+__device__ __forceinline__ bool collect_top(const Part<T> &pt, uint64_t bound, bool owner, uint64_t extra_key, TopSearch *ts) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const float low = bound == 0 ? -INFINITY : key_value(bound);
+    const auto collect = [&](uint64_t k) {
+        const int h = atomicAdd(&ts->hits, 1);
+        if (h < kMaxHits) ts->found[h] = k;
+    };
+    if (tid == 0) ts->hits = 0;
+    if (tid < 32) ts->top[tid] = 0;  // (with fewer than 32 the other places stay empty)
+    __syncthreads();
+    if (extra_key != 0 && extra_key >= bound) collect(extra_key);
+    for (uint32_t rest = __ballot_sync(0xffffffffu, owner); rest; rest &= rest - 1) {
+        for (int i = 32 * warp + __ffs(rest) - 1 + lane * kLpThreads; i < pt.nv; i += 32 * kLpThreads) {
+            float v[Part<T>::VEC];
+            StateChunk<T>::unpack(pt.load(i).u, v);
+#pragma unroll
+            for (int j = 0; j < Part<T>::VEC; ++j)
+                if (!(v[j] < low)) {
+                    const uint64_t k = make_key(v[j], pt.element(i, j));
+                    if (k >= bound) collect(k);
+                }
+        }
+    }
+    __syncthreads();
+    const int n = ts->hits;
+    if (n > kMaxHits) return false;
+    for (int i = tid; i < n; i += kLpThreads) {
+        const uint64_t k = ts->found[i];
+        int larger = 0;
+        for (int j = 0; j < n; ++j) larger += ts->found[j] > k;
+        if (larger < 32) ts->top[larger] = k;
+    }
+    return true;
+}
+
+// The same by the threads' largest keys, for rows with many ties.
+template <typename T>
+__device__ __noinline__ void tied_top(const Part<T> &pt, int top_k, float best, int best_i, uint64_t extra_key, TopSearch *ts) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t key = extra_key;
+    if (best_i >= 0) {
+        // the first element that is this thread's largest (where nothing is
+        // above -inf, the first of all)
+        int at = pt.element(best_i, 0);
+        for (int u = kUnroll - 1; u >= 0 && best > -INFINITY; --u)
+            for (int j = Part<T>::VEC - 1; j >= 0; --j)
+                if (best_i + u * kLpThreads < pt.nv && to_float(pt.x[pt.element(best_i + u * kLpThreads, j)]) == best)
+                    at = pt.element(best_i + u * kLpThreads, j);
+        const uint64_t kb = make_key(best, at);
+        key = kb > key ? kb : key;
+    }
+    largest_of_threads(key, ts->lists);
+    const uint64_t bound = ts->lists[top_k - 1];
+    if (collect_top(pt, bound, key >= bound, extra_key, ts)) return;
+    // each warp keeps its owners' 32 largest in a sorted list over the lanes
+    uint64_t mine = warp_sort(extra_key >= bound ? extra_key : uint64_t(0));
+    for (uint32_t rest = __ballot_sync(0xffffffffu, key >= bound); rest; rest &= rest - 1) {
+        for (int base = 32 * warp + __ffs(rest) - 1; base < pt.nv; base += 32 * kLpThreads) {
+            const int i = base + lane * kLpThreads;
+            for (int j = 0; j < Part<T>::VEC; ++j) {
+                uint64_t k = i < pt.nv ? make_key(to_float(pt.x[pt.element(i, j)]), pt.element(i, j)) : 0;
+                if (k < bound) k = 0;
+                if (__any_sync(0xffffffffu, k != 0)) mine = warp_merge(mine, warp_sort(k));
+            }
+        }
+    }
+    largest_of_threads(mine, ts->lists);
+    if (tid < 32) ts->top[tid] = ts->lists[tid];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel(const LogprobParams p, int parts) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     __shared__ Stats wstats[kLpWarps];
-    __shared__ uint64_t lists[kLpWarps * 32];
+    __shared__ TopSearch ts;
     __shared__ Stats part_stats;
-    __shared__ uint64_t part_top[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / parts;
     const int rank = static_cast<int>(blockIdx.x - row * parts);
@@ -322,48 +409,19 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
     }
 
     if (p.top_k > 0) {
-        if (best_i >= 0) {
-            for (int u = 0; u < kUnroll; ++u) {
-                const int i = best_i + u * kLpThreads;
-                if (i >= pt.nv) break;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const uint64_t kj = pt.key(i, j);
-                    key = kj > key ? kj : key;
-                }
-            }
-        }
-        lists[tid] = warp_sort(key);
-        __syncthreads();
-        // every warp: the 32 largest of the threads' maxima, their k-th as the bound
-        const uint64_t owners = merge_lists(lists, kLpWarps);
-        const uint64_t bound = __shfl_sync(0xffffffffu, owners, p.top_k - 1);
-        __syncthreads();
-        uint64_t mine = 0;  // this warp's list, sorted downwards over the lanes
-        for (int o = warp; o < p.top_k; o += kLpWarps) {
-            const uint64_t ok = __shfl_sync(0xffffffffu, owners, o);
-            if (ok == 0) break;  // fewer threads with elements than k
-            const int owner = pt.owner(key_index(ok));
-            if (owner < pt.extra) {
-                uint64_t kj = lane == 0 ? make_key(to_float(x[pt.extra_at(owner)]), pt.extra_at(owner)) : 0;
-                if (kj < bound) kj = 0;
-                mine = warp_merge(mine, warp_sort(kj));
-            }
-            for (int base = owner; base < pt.nv; base += 32 * kLpThreads) {
-                const int i = base + lane * kLpThreads;
-                for (int j = 0; j < VEC; ++j) {
-                    uint64_t kj = i < pt.nv ? pt.key(i, j) : 0;
-                    if (kj < bound) kj = 0;
-                    if (__any_sync(0xffffffffu, kj != 0)) mine = warp_merge(mine, warp_sort(kj));
-                }
-            }
-        }
-        lists[tid] = mine;
+        // by value: the bound's own ties are all collected
+        uint32_t mine = best_i >= 0 ? ordered(best) : 0u;
+        const uint32_t from_extra = static_cast<uint32_t>(key >> 32);
+        mine = mine > from_extra ? mine : from_extra;
+        uint32_t *lists = reinterpret_cast<uint32_t *>(ts.lists);
+        largest_of_threads(mine, lists);
+        const uint32_t bound = lists[p.top_k - 1];
+        if (!collect_top(pt, static_cast<uint64_t>(bound) << 32, mine >= bound, key, &ts))
+            tied_top(pt, p.top_k, best, best_i, key, &ts);
     }
-    a = block_join(a, wstats, 1.f);  // (its barrier also completes the lists)
+    a = block_join(a, wstats, 1.f);  // (its barrier also completes ts.top)
     if (warp == 0) {
         if (lane == 0) part_stats = a;
-        if (p.top_k > 0) part_top[lane] = merge_lists(lists, kLpWarps);
     }
     if (parts > 1) cg::this_cluster().sync();
     else __syncthreads();
@@ -373,9 +431,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprobs_kernel(const LogprobPa
         const bool careful = !(b.s > 0.f);  // (the same in every thread)
         if (careful) b = careful_row(x, p.vocab, wstats);
         if (warp == 0) {
-            uint64_t top = p.top_k > 0 ? part_top[lane] : 0;
+            uint64_t top = p.top_k > 0 ? ts.top[lane] : 0;
             if (p.top_k > 0)
-                for (int c = 1; c < parts; ++c) top = warp_merge(top, cg::this_cluster().map_shared_rank(part_top, c)[lane]);
+                for (int c = 1; c < parts; ++c) top = warp_merge(top, cg::this_cluster().map_shared_rank(ts.top, c)[lane]);
             const bool none = b.s == 0.f;  // every logit is -inf
             const float ls = log2f(b.s);
             const auto logprob = [&](float v) {
