@@ -19,26 +19,28 @@
 //
 // Four products a chunk, tcgen05.mma with fp32 accumulators in tensor memory:
 //   scores   [i, j]  = Q K^T            Q, K from shared memory, as loaded
-//   entering [i, p]  = Q S^T            S as a high and a low part, in shared memory
+//   entering [i, p]  = Q S^T            S rounded to the io type, in shared memory
 //   inside   [i, p] += P V              P = scores decayed and masked, rounded once, from
 //                                       tensor memory; added to the entering product,
 //                                       whose rows have been scaled there by l^(i+1) in fp32
 //   growth   [p, n]  = (V decayed)^T K  the decayed V in three parts (bf16) or two
 //                                       (fp16), transposed, from tensor memory
-// Rounding: P to the io type (2^-8 bf16, 2^-11 fp16, as the output itself); S
-// where it meets Q to two parts (2^-16, 2^-22); the decayed V to three parts
-// (2^-24) or two (2^-22), so that fp32 states keep fp32 accuracy.  fp16 parts are
-// scaled by powers of two (per state row, score row and value tile), so neither
-// overflow nor the subnormals cost accuracy.
+// Rounding: P and, where it meets Q, S to the io type (2^-8 bf16, 2^-11 fp16,
+// each once, as the output itself: together they take the output's error from
+// one rounding's to at most sqrt(2) of it); the decayed V to three parts
+// (2^-24) or two (2^-22), so that fp32 states keep fp32 accuracy.  S as two
+// parts as well measured 255 us instead of XXX on 32768 tokens x 32 heads.
+// fp16 operands are scaled by powers of two (per state row, score row and value
+// tile), so neither overflow nor the subnormals cost accuracy.
 //
 // Warps, in groups of four (a warp reaches the tensor-memory lanes 32 (warp %
 // 4) ...):
 //   0-3    (thread = token) scores -> P, entering rows scaled, outputs stored;
 //   4-7    (thread = value dim) S: growth added, parts split off, first and last state;
 //   8-11   V decayed, transposed (ldmatrix) and split, 32 tokens at a time;
-//   12     issues the products;  13 finds the units and loads Q, K, V by tiled copies
-//          (K, V in two stages; Q, which only the early products read, in one);
-//   14-15  only complete their group, whose registers the others take.
+//   12     issues the products;  13 finds the units and loads Q, K, V by tiled copies,
+//          two chunks ahead of the outputs, which leave through Q's place;
+//   14     stores the outputs by tiled copies;  15 only completes the group.
 // The groups' code for a chunk is kept short (loops over blocks and quarters are
 // not unrolled): all of it together has to stay in the instruction cache.
 #include <cuda.h>
@@ -87,16 +89,18 @@ struct Plan {
 };
 
 enum : int {
-    kQFull, kQFree,
+    kQFull0, kQFull1,  // a Q has landed
+    kQFree0, kQFree1,  // ... and is done with, and the outputs in its place are stored
     kFull0, kFull1,    // a stage's K and V have landed
     kFree0, kFree1,    // ... and are done with
     kUnitFull0, kUnitFull1, kUnitFree0, kUnitFree1,
     kScore,            // the scores are there
-    kStateFull,        // the parts of S are there
-    kEnter,            // the entering product is there (the parts of S and Q are read)
+    kStateFull,        // the rounded S is there
+    kEnter,            // the entering product is there (S and Q are read)
     kPFull,            // P is there, the entering product scaled
     kInside,           // the outputs are there (P is read)
     kOutFree,          // ... and read
+    kStaged,           // ... and laid out by token, in Q's place
     kTail,             // a partial chunk's K and V rows past its end are zeros
     kVFull0, kVFull1, kVFree0, kVFree1,
     kGrowth, kGrowthFree,
@@ -111,9 +115,10 @@ struct Layout {
     static constexpr int kKBytes = kPanels * kPanel;
     static constexpr int kVBytes = 2 * kPanel;
     static constexpr int kStage = kKBytes + kVBytes;
-    static constexpr int kQ = 2 * kStage;
-    static constexpr int kS = kQ + kKBytes;               // high part, then low part: kPanels panels each
-    static constexpr int kBar = kS + 2 * kKBytes;
+    static constexpr int kQ = 2 * kStage;                 // two, each with room for two panels of outputs
+    static constexpr int kQBytes = 2 * kPanel;
+    static constexpr int kS = kQ + 2 * kQBytes;           // kPanels panels
+    static constexpr int kBar = kS + kKBytes;
     static constexpr int kUnits = kBar + 8 * kBars;       // Unit[2]
     static constexpr int kRowScale = (kUnits + 2 * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;  // fp16: state rows, by chunk parity
     static constexpr int kMax = kRowScale + 2 * 128 * 4;  // fp16: per warp; the value tiles' scales, four chunks; per warp of the growth pass's helpers
@@ -123,7 +128,7 @@ struct Layout {
 };
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 // A barrier of one group of warps, its waits bounded like every other.
@@ -193,64 +198,59 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-// 32 bytes of this thread, 32-byte aligned.
-__device__ __forceinline__ void store32(void *p, const uint32_t *r) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     tmem_st16(taddr, r);
     tmem_st16(taddr + 16, r + 16);
 }
 
-// A head's state [P][N] between memory (T, contiguous) and a place in shared
-// memory, 16 bytes a thread along memory, for one group of warps.  Rows there
-// are DK elements apart and their 16-byte pieces swapped by row, so that the
-// threads' own rows are read and written without bank conflicts.
+// A head's state [P][N] between memory (T, contiguous) and the state's place in
+// shared memory, 16 bytes a thread along memory, for one group of warps.  The
+// place holds kCols columns of every row at a time; its 16-byte pieces are swapped
+// by row, so that the threads' own rows are read and written without bank
+// conflicts.
 template <typename T, int DK>
 struct StateRow {
     static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-    __device__ __forceinline__ static int at(int row, int piece) {
-        return row * DK * static_cast<int>(sizeof(T)) + ((piece ^ (row & 7)) * 16);
-    }
+    static constexpr int kCols = 2 * DK / static_cast<int>(sizeof(T));  // the place has 2 DK bytes a row
+    __device__ __forceinline__ static int at(int row, int piece) { return row * 2 * DK + ((piece ^ (row & 7)) * 16); }
 };
 template <typename T, int DK, typename F>
-__device__ __forceinline__ void each_piece(int P, int N, int t, F f) {
-    const int per = N / StateRow<T, DK>::kVec, total = P * per, down = kGroup / per, right = kGroup - down * per;
+__device__ __forceinline__ void each_piece(int P, int N, int c0, int t, F f) {
+    using R = StateRow<T, DK>;
+    const int per = min(R::kCols, N - c0) / R::kVec, total = P * per, down = kGroup / per, right = kGroup - down * per;
     int row = t / per, piece = t - row * per;
 #pragma unroll 4
     for (int i = t; i < total; i += kGroup) {
-        f(i, StateRow<T, DK>::at(row, piece));
+        f(row * N + c0 + piece * R::kVec, R::at(row, piece));
         row += down;
         piece += right;
         if (piece >= per) piece -= per, ++row;
     }
 }
 template <typename T, int DK>
-__device__ __forceinline__ void stage_in(const T *src, unsigned char *place, int P, int N, int t) {
-    each_piece<T, DK>(P, N, t, [&](int i, int at) { cp16(place + at, src + i * StateRow<T, DK>::kVec, true); });
+__device__ __forceinline__ void stage_in(const T *src, unsigned char *place, int P, int N, int c0, int t) {
+    each_piece<T, DK>(P, N, c0, t, [&](int i, int at) { cp16(place + at, src + i, true); });
     cp_wait_all();
 }
 template <typename T, int DK>
-__device__ __forceinline__ void stage_out(T *dst, const unsigned char *place, int P, int N, int t) {
-    each_piece<T, DK>(P, N, t, [&](int i, int at) {
-        st_stream(dst + i * StateRow<T, DK>::kVec, *reinterpret_cast<const uint4 *>(place + at));
-    });
+__device__ __forceinline__ void stage_out(T *dst, const unsigned char *place, int P, int N, int c0, int t) {
+    each_piece<T, DK>(P, N, c0, t, [&](int i, int at) { st_stream(dst + i, *reinterpret_cast<const uint4 *>(place + at)); });
 }
-template <typename T, int DK>
+// Columns C0 ... of this thread's row.
+template <typename T, int DK, int C0>
 __device__ __forceinline__ void row_from(const unsigned char *place, int row, int N, float *S) {
-    constexpr int V = StateRow<T, DK>::kVec;
+    using R = StateRow<T, DK>;
 #pragma unroll
-    for (int j = 0; j < DK / V; ++j)
-        if (j * V < N) StateChunk<T>::unpack(*reinterpret_cast<const uint4 *>(place + StateRow<T, DK>::at(row, j)), S + j * V);
+    for (int j = 0; j < R::kCols / R::kVec; ++j)
+        if (C0 + j * R::kVec < N)
+            StateChunk<T>::unpack(*reinterpret_cast<const uint4 *>(place + R::at(row, j)), S + C0 + j * R::kVec);
 }
-template <typename T, int DK>
+template <typename T, int DK, int C0>
 __device__ __forceinline__ void row_to(unsigned char *place, int row, const float *S) {
-    constexpr int V = StateRow<T, DK>::kVec;
+    using R = StateRow<T, DK>;
 #pragma unroll
-    for (int j = 0; j < DK / V; ++j)
-        *reinterpret_cast<uint4 *>(place + StateRow<T, DK>::at(row, j)) = StateChunk<T>::pack(S + j * V);
+    for (int j = 0; j < R::kCols / R::kVec; ++j)
+        *reinterpret_cast<uint4 *>(place + R::at(row, j)) = StateChunk<T>::pack(S + C0 + j * R::kVec);
 }
 
 // Sequence b: its bounds and slots.  False (and flagged) when it is to be
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
             if (i == kFree0 || i == kFree1) n = 1 + (GROW ? 2 : 1) * kGroup;
-            if (i == kUnitFree0 || i == kUnitFree1) n = 1 + 3 * kGroup;
-            if (i == kStateFull || i == kPFull || i == kOutFree || i == kTail || i == kVFull0 || i == kVFull1 ||
+            if (i == kUnitFree0 || i == kUnitFree1) n = (GROW ? 1 : 2) + 3 * kGroup;
+            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail || i == kVFull0 || i == kVFull1 ||
                 i == kGrowthFree || i == kSyncA || i == kSyncB || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
@@ -622,15 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < vpanels; ++i)
                         tma_load_3d(st + LY::kKBytes + i * kPanel, &maps.v, 64 * i, g, row, &bars[kFull0 + s]);
                     if constexpr (GROW) continue;
-                    if (ch >= 1 && !(ok = mbar_wait_bounded(&bars[kQFree], (ch - 1) & 1))) {
+                    if (ch >= 2 && !(ok = mbar_wait_bounded(&bars[kQFree0 + s], ((ch >> 1) - 1) & 1))) {
                         ++ch;  // its K and V are on their way
                         break;
                     }
                     ++nq;
-                    mbar_arrive_expect(&bars[kQFull], LY::kKBytes);
+                    mbar_arrive_expect(&bars[kQFull0 + s], LY::kKBytes);
                     for (int i = 0; i < LY::kPanels; ++i)
-                        tma_load_3d(smem + LY::kQ + i * kPanel, &maps.q, 64 * i, un.h, row, &bars[kQFull]);
+                        tma_load_3d(smem + LY::kQ + s * LY::kQBytes + i * kPanel, &maps.q, 64 * i, un.h, row, &bars[kQFull0 + s]);
                 }
+                if (!ok) break;
                 un = after;
             }
             if (!ok) {
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // what was loaded has landed before the CTA retires
             for (int k = ch > 2 ? ch - 2 : 0; k < ch; ++k) mbar_wait_bounded(&bars[kFull0 + (k & 1)], (k >> 1) & 1);
-            if (nq > 0) mbar_wait_bounded(&bars[kQFull], (nq - 1) & 1);
+            for (int k = nq > 2 ? nq - 2 : 0; k < nq; ++k) mbar_wait_bounded(&bars[kQFull0 + (k & 1)], (k >> 1) & 1);
         }
         __syncwarp();
     } else if (warp == 12) {
@@ -716,37 +717,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return true;
         };
-        // The order keeps the pipe busy: the first half of the growth runs
-        // while the outputs of the chunk before are read and the state is
-        // split, the second while the entering rows are scaled.
+        // The order keeps the pipe busy: most of the growth runs while the
+        // outputs of the chunk before are read and the state is rounded, the
+        // rest of it while the entering rows are scaled.
         Chunk k;
         while ((ok = next_chunk(k)) && k.n > 0) {
-            if (!(ok = growth(k, 0) && growth(k, 1))) break;
+            const uint32_t q = static_cast<uint32_t>(k.s * (LY::kQBytes >> 4));
+            if (!(ok = growth(k, 0) && growth(k, 1) && growth(k, 2))) break;
             if constexpr (!GROW) {
                 // (P of the last chunk, in the scores' place, has been read)
-                if (!(ok = wait(kQFull, k.ch) && (k.ch == 0 || wait(kInside, k.ch - 1)))) break;
+                if (!(ok = wait(kQFull0 + k.s, k.ch >> 1) && (k.ch == 0 || wait(kInside, k.ch - 1)))) break;
                 if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < DK / 16; ++i)
-                        if (i < ksteps) mma(tm + kColScore, dQ + along_k(i), dK + (k.stage + along_k(i)), id_score, i > 0);
+                        if (i < ksteps) mma(tm + kColScore, dQ + (q + along_k(i)), dK + (k.stage + along_k(i)), id_score, i > 0);
                     mma_commit(&bars[kScore]);
                 }
                 __syncwarp();
                 if (!(ok = wait(kStateFull, k.ch) && (k.ch == 0 || wait(kOutFree, k.ch - 1)))) break;
                 if (elect_one()) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int i = 0; i < DK / 16; ++i)
-                            if (i < ksteps)
-                                mma(tm + kColOut, dQ + along_k(i), dS + (part * (LY::kKBytes >> 4) + along_k(i)), id_enter,
-                                    part > 0 || i > 0);
+                    for (int i = 0; i < DK / 16; ++i)
+                        if (i < ksteps) mma(tm + kColOut, dQ + (q + along_k(i)), dS + along_k(i), id_enter, i > 0);
                     mma_commit(&bars[kEnter]);
-                    mma_commit(&bars[kQFree]);
                 }
                 __syncwarp();
             }
-            if (!(ok = growth(k, 2) && growth(k, 3))) break;
+            if (!(ok = growth(k, 3))) break;
             if constexpr (!GROW) {
                 if (!(ok = wait(kPFull, k.ch))) break;
                 if (elect_one()) {
@@ -769,7 +766,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait_bounded(&bars[kFinal], 0);
         __syncwarp();
-    } else if (warp >= 14) {
+    } else if (warp == 14) {
+        registers<80>();
+        // ---------------- output stores (one thread) ----------------
+        if (!GROW && lane == 0) {
+            int nu = 0, ch = 0;
+            const int panels = p.P > 64 ? 2 : 1;
+            for (;;) {
+                if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
+                const Unit un = ring[nu & 1];
+                mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+                ++nu;
+                if (un.len < 0) break;
+                for (int c = 0; c < un.len; c += kC, ++ch) {
+                    if (!(ok = mbar_wait_bounded(&bars[kStaged], ch & 1))) break;
+                    if (un.len - c >= kC) {  // (a partial chunk's rows are stored one by one)
+                        for (int i = 0; i < panels; ++i)
+                            tma_store_3d(&maps.out, smem + LY::kQ + (ch & 1) * LY::kQBytes + i * kPanel, 64 * i, un.h,
+                                         static_cast<int>(un.t0) + c);
+                        bulk_commit();
+                        bulk_wait_read<0>();
+                    }
+                    mbar_arrive(&bars[kQFree0 + (ch & 1)]);
+                }
+                if (!ok) break;
+            }
+            bulk_wait_all();
+            if (!ok) {
+                flag(p.status, kDevTimeout);
+                *abort_flag = 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 15) {
         registers<80>();
     } else if (warp < 4) {
         registers<128>();
@@ -777,8 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- P and the outputs (thread = token) ----------------
         const int row = tid;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const bool wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.P % 16 == 0 && p.os[0] % 16 == 0 && p.os[1] % 16 == 0;
-        int nu = 0, ch = 0;
+        int nu = 0, ch = 0, ph = 0;
         while (!GROW) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
             const Unit un = ring[nu & 1];
@@ -869,8 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kPFull]);
                 if (!(ok = mbar_wait_bounded(&bars[kInside], ch & 1))) break;
                 tc_fence_after();
-                // the token's outputs, 32 bytes a store (16 where their rows do
-                // not begin on such a boundary)
+                // Outputs by token where Q was (its products are done), laid out
+                // for a tiled copy: a thread's own row, 16 or 32 bytes at a
+                // time, would touch 32 lines a store.
+                unsigned char *rows = smem + LY::kQ + (ch & 1) * LY::kQBytes, *mine = rows + row * 128;
 #pragma unroll 1
                 for (int b = 0; 32 * b < p.P; ++b) {
                     uint32_t r[32];
@@ -886,20 +916,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (!BF) x *= down, y *= down;
                         r[jj] = pack2<BF>(x, y);
                     }
-                    if (row < n) {
-                        unsigned short *o = out + (c + row) * p.os[0] + 32 * b;
-                        if (wide) {
 #pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                if (32 * b + 16 * j < p.P) store32(o + 16 * j, r + 8 * j);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (32 * b + 8 * j < p.P)
-                                    *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                        }
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(mine + (b / 2) * kPanel + (((4 * (b % 2) + j) ^ (row & 7)) * 16)) =
+                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                }
+                fence_proxy_async_smem();
+                if (n < kC) {
+                    // the rows past the end are other tokens'
+                    if (!(ok = group_sync(&bars[kSyncA], ph))) break;
+                    const int piece = tid & 15;  // 16 threads store a token's row
+                    if (8 * piece < p.P) {
+                        for (int i = tid >> 4; i < n; i += kGroup / 16)
+                            *reinterpret_cast<uint4 *>(out + (c + i) * p.os[0] + 8 * piece) = *reinterpret_cast<const uint4 *>(
+                                rows + (piece / 8) * kPanel + i * 128 + (((piece % 8) ^ (i & 7)) * 16));
                     }
                 }
+                mbar_arrive(&bars[kStaged]);
             }
             if (!ok) break;
         }
@@ -925,28 +958,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t slot = static_cast<int64_t>(p.H) * p.P * p.N, head = static_cast<int64_t>(un.h) * p.P * p.N;
 #pragma unroll
             for (int i = 0; i < DK; ++i) S[i] = 0.f;
-            // the entering state, by way of the parts' place (which the last
-            // entering product has read)
+            // the entering state, by way of its place for the products (which
+            // the last entering product has read)
             if (!GROW && ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
             if (!GROW && un.src != kZero) {
                 const bool scratch = un.src >= kScratch;
                 const int64_t at = (scratch ? un.src - kScratch : un.src) * slot + head;
                 const void *src = scratch ? plan.states : p.state;
                 unsigned char *const place = smem + LY::kS;
-                if (scratch || p.state_dtype == kF32) stage_in<float, DK>(static_cast<const float *>(src) + at, place, p.P, p.N, t);
-                else stage_in<__half, DK>(static_cast<const __half *>(src) + at, place, p.P, p.N, t);  // any 16 bits
-                if (!(ok = group_sync(&bars[kSyncB], ph))) break;
-                if (t < p.P) {
-                    if (scratch || p.state_dtype == kF32) row_from<float, DK>(place, t, p.N, S);
-                    else if (p.state_dtype == kBF16) row_from<__nv_bfloat16, DK>(place, t, p.N, S);
-                    else row_from<__half, DK>(place, t, p.N, S);
+                if (scratch || p.state_dtype == kF32) {
+                    const float *from = static_cast<const float *>(src) + at;
+                    stage_in<float, DK>(from, place, p.P, p.N, 0, t);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    if (t < p.P) row_from<float, DK, 0>(place, t, p.N, S);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    if (p.N > DK / 2) stage_in<float, DK>(from, place, p.P, p.N, DK / 2, t);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    if (t < p.P) row_from<float, DK, DK / 2>(place, t, p.N, S);
+                } else {
+                    stage_in<__half, DK>(static_cast<const __half *>(src) + at, place, p.P, p.N, 0, t);  // any 16 bits
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    if (t < p.P) {
+                        if (p.state_dtype == kBF16) row_from<__nv_bfloat16, DK, 0>(place, t, p.N, S);
+                        else row_from<__half, DK, 0>(place, t, p.N, S);
+                    }
                 }
                 if (!(ok = group_sync(&bars[kSyncB], ph))) break;
             }
             for (int c = 0; c < un.len; c += kC, ++ch) {
                 const int n = min(kC, un.len - c);
                 if constexpr (!GROW) {
-                    // S in two parts, once the last entering product has read its own
+                    // S rounded, once the last entering product has read its own
                     float sc = 1.f;
                     if constexpr (!BF) {
                         float m = 0.f;
@@ -960,16 +1002,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unsigned char *srow = smem + LY::kS + t * 128;
 #pragma unroll
                     for (int j = 0; j < DK / 8; ++j) {
-                        uint32_t hi[4], lo[4];
+                        uint32_t u[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x = S[8 * j + 2 * i] * sc, y = S[8 * j + 2 * i + 1] * sc;
-                            hi[i] = split2<BF>(x, y);
-                            lo[i] = pack2<BF>(x, y);
-                        }
-                        unsigned char *d = srow + (j / 8) * kPanel + (((j % 8) ^ (t & 7)) * 16);
-                        *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(d + LY::kKBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int i = 0; i < 4; ++i) u[i] = pack2<BF>(S[8 * j + 2 * i] * sc, S[8 * j + 2 * i + 1] * sc);
+                        *reinterpret_cast<uint4 *>(srow + (j / 8) * kPanel + (((j % 8) ^ (t & 7)) * 16)) =
+                            make_uint4(u[0], u[1], u[2], u[3]);
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(&bars[kStateFull]);
@@ -995,13 +1032,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!GROW && ch > 0 && !(ok = mbar_wait_bounded(&bars[kEnter], (ch - 1) & 1))) break;
                 const int64_t at = (GROW ? un.src - kScratch : un.dst) * slot + head;
                 unsigned char *const place = smem + LY::kS;
-                if (GROW || p.state_dtype == kF32) row_to<float, DK>(place, t, S);
-                else if (p.state_dtype == kBF16) row_to<__nv_bfloat16, DK>(place, t, S);
-                else row_to<__half, DK>(place, t, S);
-                if (!(ok = group_sync(&bars[kSyncB], ph))) break;
                 void *dst = GROW ? plan.states : p.state;
-                if (GROW || p.state_dtype == kF32) stage_out<float, DK>(static_cast<float *>(dst) + at, place, p.P, p.N, t);
-                else stage_out<__half, DK>(static_cast<__half *>(dst) + at, place, p.P, p.N, t);
+                if (GROW || p.state_dtype == kF32) {
+                    float *to = static_cast<float *>(dst) + at;
+                    row_to<float, DK, 0>(place, t, S);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    stage_out<float, DK>(to, place, p.P, p.N, 0, t);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    row_to<float, DK, DK / 2>(place, t, S);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    if (p.N > DK / 2) stage_out<float, DK>(to, place, p.P, p.N, DK / 2, t);
+                } else {
+                    if (p.state_dtype == kBF16) row_to<__nv_bfloat16, DK, 0>(place, t, S);
+                    else row_to<__half, DK, 0>(place, t, S);
+                    if (!(ok = group_sync(&bars[kSyncB], ph))) break;
+                    stage_out<__half, DK>(static_cast<__half *>(dst) + at, place, p.P, p.N, 0, t);
+                }
                 if (!(ok = group_sync(&bars[kSyncB], ph))) break;
             }
         }
@@ -1076,7 +1122,7 @@ template <int DK, bool BF>
 cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *workspace, cudaStream_t stream) {
     Maps maps;
     if (p.rows > 0 && !(encode(&maps.q, p, p.q, p.N, p.H, p.qs) && encode(&maps.k, p, p.k, p.N, p.G, p.ks) &&
-                        encode(&maps.v, p, p.v, p.P, p.G, p.vs)))
+                        encode(&maps.v, p, p.v, p.P, p.G, p.vs) && encode(&maps.out, p, p.out, p.P, p.H, p.os)))
         return cudaErrorInvalidValue;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;

@@ -208,4 +208,12 @@ __device__ __forceinline__ void tma_load_3d(void *dst_smem, const void *map, int
         : "memory");
 }
 
+// Tiled copy shared -> global of a 3-D box, in this thread's bulk group; what
+// lies outside the tensor is not written.  No coordinate is negative.
+__device__ __forceinline__ void tma_store_3d(const void *map, const void *src_smem, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(smem_addr(src_smem))
+                 : "memory");
+}
+
 }  // namespace ssu

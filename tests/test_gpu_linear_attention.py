@@ -9,12 +9,14 @@ in fp32, so |dS| <= 2^-20 (|e^g S| + |v k|) + us |S|; the output sums at most 12
 products of it: |dy| <= 2^-16 scale sum |S q| + u |y|.
 
 Prefill.  The scores q . k and every sum are fp32 (2^-15 of the sum of the
-magnitudes, covering sums over a few thousand terms); a score times its decay is
-rounded once to the io type before it meets v: u of the magnitudes |q . k| e^.. |v|;
-the state and the decayed v enter products in two parts of the io type, 2^-16
-of the magnitudes.  So, with A = scale sum_j e^{g(i-j)} |q_i . k_j| |v_j| over the
-tokens of the prompt, B the same with (|q_i| . |k_j|) and the first state's part:
-|dy| <= u |y| + u A + 2^-15 B, and |dS| <= 2^-15 (sum of magnitudes) + us |S|.
+magnitudes, covering sums over a few thousand terms).  Two operands are rounded
+once to the io type: a score times its decay before it meets v, u of the
+magnitudes |q . k| e^.. |v|; and the state S_c that enters a chunk of 128 tokens
+before it meets q, u of |S_c| |q|.  The decayed v enters the state in parts that
+hold 22 bits and more.  So, with A = scale sum_j e^{g(i-j)} |q_i . k_j| |v_j| over the
+tokens of the prompt, E = scale e^{g(i-c+1)} |S_c| |q_i| and B the magnitudes of all
+(A with |q_i| . |k_j| and the first state's part): |dy| <= u (|y| + A + E) + 2^-15 B,
+and |dS| <= 2^-15 (sum of magnitudes) + us |S|.
 Values below the types' normal ranges add 2^-24 (fp16) absolutely."""
 import pytest
 import torch
@@ -23,6 +25,7 @@ import selective_state_update_gb300 as ssu
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+CHUNK = 128  # tokens of the prefill's chunks
 HALF_ULP = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
 TINY = {torch.float32: 0.0, torch.float16: 2.0 ** -24, torch.bfloat16: 0.0}
 
@@ -41,7 +44,7 @@ def problem(seed, rows, heads, kv_heads, dim, dstate, io, state, slots, decays=N
 
 
 def reference(q, k, v, log_decay, lengths, first, scale):
-    """(y, A, B, states, their magnitudes) in 64 bits by the quadratic form; first: [nseq, heads, dim, dstate]."""
+    """(y, A + E, B, states, their magnitudes) in 64 bits by the quadratic form; first: [nseq, heads, dim, dstate]."""
     heads = q.shape[1]
     kv = torch.arange(heads, device=q.device) // (heads // k.shape[1])
     q, k, v = q.double().transpose(0, 1), k.double()[:, kv].transpose(0, 1), v.double()[:, kv].transpose(0, 1)
@@ -57,7 +60,13 @@ def reference(q, k, v, log_decay, lengths, first, scale):
         score = (qb @ kb.transpose(1, 2)) * w
         reach = power(i + 1)[..., None]
         ys.append(scale * (score @ vb + reach * (qb @ s0.transpose(1, 2))))
-        As.append(scale * (score.abs() @ vb.abs()))
+        E = torch.zeros_like(ys[-1])
+        for c in range(0, n, CHUNK):
+            left = power(c - 1 - i[:c])[..., None]
+            s_c = power(torch.tensor(c, device=q.device))[:, None, None] * s0 + (vb[:, :c] * left).transpose(1, 2) @ kb[:, :c]
+            e = slice(c, c + CHUNK)
+            E[:, e] = scale * power(i[e] - c + 1)[..., None] * (qb[:, e].abs() @ s_c.abs().transpose(1, 2))
+        As.append(scale * (score.abs() @ vb.abs()) + E)
         Bs.append(scale * (((qb.abs() @ kb.abs().transpose(1, 2)) * w) @ vb.abs() + reach * (qb.abs() @ s0.abs().transpose(1, 2))))
         left = power(n - 1 - i)[..., None]
         lam = power(torch.tensor(n, device=q.device))[:, None, None]
