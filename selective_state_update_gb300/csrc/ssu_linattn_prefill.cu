@@ -717,13 +717,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return true;
         };
-        // The order keeps the pipe busy: most of the growth runs while the
-        // outputs of the chunk before are read and the state is rounded, the
-        // rest of it while the entering rows are scaled.
+        // The quarters of the growth lie between the other products so that
+        // each finds its decayed V prepared (two fit tensor memory at a time),
+        // the scores become P meanwhile, and no product waits for the one
+        // just before it.
         Chunk k;
         while ((ok = next_chunk(k)) && k.n > 0) {
             const uint32_t q = static_cast<uint32_t>(k.s * (LY::kQBytes >> 4));
-            if (!(ok = growth(k, 0) && growth(k, 1) && growth(k, 2))) break;
+            if (!(ok = growth(k, 0))) break;
             if constexpr (!GROW) {
                 // (P of the last chunk, in the scores' place, has been read)
                 if (!(ok = wait(kQFull0 + k.s, k.ch >> 1) && (k.ch == 0 || wait(kInside, k.ch - 1)))) break;
@@ -734,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&bars[kScore]);
                 }
                 __syncwarp();
+                if (!(ok = growth(k, 1))) break;
                 if (!(ok = wait(kStateFull, k.ch) && (k.ch == 0 || wait(kOutFree, k.ch - 1)))) break;
                 if (elect_one()) {
 #pragma unroll
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (!(ok = growth(k, 3))) break;
+            if (!(ok = (!GROW || growth(k, 1)) && growth(k, 2) && growth(k, 3))) break;
             if constexpr (!GROW) {
                 if (!(ok = wait(kPFull, k.ch))) break;
                 if (elect_one()) {
@@ -1093,7 +1095,7 @@ bool encode(CUtensorMap *m, const LinattnParams &p, const void *base, int n, int
     const cuuint32_t box[3] = {64, 1, kC}, unit[3] = {1, 1, 1};
     const CUtensorMapDataType type = p.io_dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     return fn(m, type, 3, const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count() {
