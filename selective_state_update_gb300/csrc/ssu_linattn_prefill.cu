@@ -253,6 +253,11 @@ __device__ __forceinline__ void row_to(unsigned char *place, int row, const floa
         *reinterpret_cast<uint4 *>(place + R::at(row, j)) = StateChunk<T>::pack(S + C0 + j * R::kVec);
 }
 
+// `bytes` (a multiple of 16, 16-byte aligned) into L2.
+__device__ __forceinline__ void bulk_prefetch(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Sequence b: its bounds and slots.  False (and flagged) when it is to be
 // skipped.
 __device__ __forceinline__ bool find_sequence(const LinattnParams &p, int64_t b, Unit &out) {
@@ -597,6 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             const auto publish = [&](const Unit &un) {
+                // its first state on the way to L2
+                if (!GROW && un.len >= 0 && un.src != kZero) {
+                    const bool scratch = un.src >= kScratch;
+                    const int64_t head = static_cast<int64_t>(p.P) * p.N, size = scratch || p.state_dtype == kF32 ? 4 : 2;
+                    const unsigned char *state = scratch ? reinterpret_cast<const unsigned char *>(plan.states)
+                                                         : static_cast<const unsigned char *>(p.state);
+                    bulk_prefetch(state + ((scratch ? un.src - kScratch : un.src) * p.H + un.h) * head * size,
+                                  static_cast<uint32_t>(head * size));
+                }
                 if (nu >= 2 && !mbar_wait_bounded(&bars[kUnitFree0 + (nu & 1)], ((nu >> 1) - 1) & 1)) return false;
                 ring[nu & 1] = un;
                 mbar_arrive(&bars[kUnitFull0 + (nu & 1)]);
