@@ -472,9 +472,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n < kC) {
                     // rows past the sequence's end belong to other tokens: a
                     // weight of zero would still let their NaN through
-                    const int rows = (kC - n) * 8;
-                    for (int i = t; i < rows * (LY::kPanels + 2); i += kGroup)
-                        *reinterpret_cast<uint4 *>(sK + (i / rows) * kPanel + n * 128 + (i % rows) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    // (as far as a product or the decay below reads them)
+                    const int pieces = ((n + kQuarter - 1) / kQuarter * kQuarter - n) * 8;
+                    for (int panel = 0; panel < LY::kPanels + (p.P > 64 ? 2 : 1); ++panel)
+                        for (int i = t; i < pieces; i += kGroup)
+                            *reinterpret_cast<uint4 *>(sK + panel * kPanel + n * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                     mbar_arrive(&bars[kTail]);
                     if (!(ok = group_sync(&bars[sync], ph))) break;  // every thread's zeros, below
@@ -844,37 +846,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // columns before the warp's rows factors through its last
                 // column, both powers at most 1; the block on the diagonal
                 // takes one power a score.
+                float up = 1.f, down = 1.f;  // fp16: the row's power of two
+                if constexpr (!BF) {
+                    // from the largest score before its decay, which bounds
+                    // the decayed ones: P stays in fp16's normal range down to
+                    // 2^-27 of it
+                    float m = 0.f;
+#pragma unroll 1
+                    for (int b = 0; b <= warp; ++b) {
+                        uint32_t r[32];
+                        tmem_ld32(tmem + lanes + kColScore + 32 * b, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int jj = 0; jj < 32; ++jj) m = fmaxf(m, fabsf(__uint_as_float(r[jj])));
+                    }
+                    // (not so far up that the entering product, scaled alike, could overflow)
+                    const int k = min(fp16_scale_exp(m * fabsf(p.scale)), 40);
+                    up = pow2i(k);
+                    down = pow2i(-k);
+                }
+                const float scale_up = p.scale * up;
                 const auto decayed = [&](int b, float *e) {
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + kColScore + 32 * b, r);
                     tmem_wait_ld();
                     if (b < warp) {
-                        const float f = p.scale * ex2(g2 * static_cast<float>(row - 32 * b - 31));
+                        const float f = scale_up * ex2(g2 * static_cast<float>(row - 32 * b - 31));
 #pragma unroll
                         for (int jj = 0; jj < 32; ++jj) e[jj] = __uint_as_float(r[jj]) * (f * fall[jj]);
                     } else {
 #pragma unroll
                         for (int jj = 0; jj < 32; ++jj) {
-                            const float w = p.scale * ex2(g2 * static_cast<float>(max(lane - jj, 0)));
+                            const float w = scale_up * ex2(g2 * static_cast<float>(max(lane - jj, 0)));
                             e[jj] = jj <= lane ? __uint_as_float(r[jj]) * w : 0.f;
                         }
                     }
                 };
-                float up = 1.f, down = 1.f;  // fp16: the row's power of two
-                if constexpr (!BF) {
-                    float m = 0.f;
-#pragma unroll 1
-                    for (int b = 0; b <= warp; ++b) {
-                        float e[32];
-                        decayed(b, e);
-#pragma unroll
-                        for (int jj = 0; jj < 32; ++jj) m = fmaxf(m, fabsf(e[jj]));
-                    }
-                    // (not so far up that the entering product, scaled alike, could overflow)
-                    const int k = min(fp16_scale_exp(m), 40);
-                    up = pow2i(k);
-                    down = pow2i(-k);
-                }
                 // (block b of P takes columns whose scores, of block b / 2, are read)
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
@@ -884,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         decayed(b, e);
 #pragma unroll
                         for (int jj = 0; jj < 16; ++jj)
-                            pr[jj] = BF ? pack2<BF>(e[2 * jj], e[2 * jj + 1]) : pack2<BF>(e[2 * jj] * up, e[2 * jj + 1] * up);
+                            pr[jj] = pack2<BF>(e[2 * jj], e[2 * jj + 1]);
                     } else {
 #pragma unroll
                         for (int jj = 0; jj < 16; ++jj) pr[jj] = 0u;
