@@ -177,8 +177,7 @@ __device__ __forceinline__ uint32_t split2(float &x, float &y) {
 // of four calls it with the same N.
 template <int N>
 __device__ __forceinline__ void registers() {
-    if constexpr (N == 128) return;
-    else if constexpr (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
@@ -574,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // The launch gives every thread 128 registers (4 x 128 in all); the groups
-    // take 128, 208 and 96, which leaves 80 for the last.
+    // take 120, 216 and 96, which leaves 80 for the last.
     if (warp == 13) {
         registers<80>();
         // ---------------- units and loads ----------------
@@ -819,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 15) {
         registers<80>();
     } else if (warp < 4) {
-        registers<128>();
+        registers<120>();
         if constexpr (GROW) decay_values(1);
         // ---------------- P and the outputs (thread = token) ----------------
         const int row = tid;
@@ -964,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     } else if (warp < 8) {
-        registers<208>();
+        registers<216>();
         // ---------------- the state (thread = value dim) ----------------
         const int t = tid - kGroup, w = warp - 4;
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
