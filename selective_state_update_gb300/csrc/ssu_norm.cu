@@ -41,11 +41,29 @@ struct Raw {
 };
 template <typename T>
 struct Raw<T, 16 / sizeof(T)> {
-    uint4 v;
+    static constexpr int kN = 16 / static_cast<int>(sizeof(T));
+    union {
+        uint4 v;
+        T e[kN];
+    };
+    __device__ __forceinline__ Raw() {}
+    // elements c of a row of n, c = col + i, that exist
+    __device__ __forceinline__ void load_some(const T *row, int col, int n) {
+        v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (col + i >= 0 && col + i < n) e[i] = row[col + i];
+    }
     __device__ __forceinline__ void load(const T *p) { v = ld_stream(p); }
     __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void unpack(float *f) const { StateChunk<T>::unpack(v, f); }
 };
+template <typename T, int VEC>
+__device__ __forceinline__ void store_some(T *row, int col, int n, const float *v) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        if (col + i >= 0 && col + i < n) row[col + i] = from_float<T>(v[i]);
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T *p, const float *v) {
     if constexpr (VEC == 1) {
@@ -107,33 +125,57 @@ constexpr int elements_per_thread(int hidden) { return hidden <= 2048 ? 8 : hidd
 constexpr int ept_threads(int ept) { return ept == 8 ? 2048 / 8 : ept == 16 ? 8192 / 16 : kNormMaxHidden / 32; }
 
 // T: element type of x; VEC: elements a load; EPT: elements a thread; RES:
-// with a residual.
-template <typename T, int VEC, int EPT, bool RES>
+// with a residual; LOOSE: rows that begin anywhere.  With VEC > 1 a loose row is
+// still taken in aligned vectors (x, residual and outputs begin at the same
+// place within one, `shift` elements in), the first and the last in part.
+template <typename T, int VEC, int EPT, bool RES, bool LOOSE>
 __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) norm_kernel(const NormParams p) {
     constexpr int NV = EPT / VEC;
     constexpr bool kAhead = EPT < 32;  // a second row does not fit the registers of 1024 threads
     __shared__ float part[2][32];
-    __shared__ int bmax[kNormMaxHidden / kNormBlock];  // VEC == 1: the blocks' maxima (bits of non-negative floats)
+    __shared__ int bmax[kNormMaxHidden / kNormBlock];  // LOOSE: the blocks' maxima (bits of non-negative floats)
     const int tid = threadIdx.x, nthr = blockDim.x;
+    const auto shift_of = [&](int64_t row) {
+        if constexpr (!LOOSE || VEC == 1) return 0;
+        else return static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T *>(p.x) + row * p.xs) / sizeof(T) % VEC);
+    };
+    const auto whole = [&](int col) { return !LOOSE || VEC == 1 ? col < p.hidden : col >= 0 && col + VEC <= p.hidden; };
     Raw<T, VEC> xr[NV], er[RES ? NV : 1];
     const auto fetch = [&](int64_t row) {
         const T *x = static_cast<const T *>(p.x) + row * p.xs;
         const T *res = RES ? static_cast<const T *>(p.residual) + row * p.rs : nullptr;
+        const int shift = shift_of(row);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (tid + j * nthr) * VEC;
-            if (row < p.rows && col < p.hidden) {
+            const int col = (tid + j * nthr) * VEC - shift;
+            if (row < p.rows && whole(col)) {
                 xr[j].load(x + col);
                 if constexpr (RES) er[j].load(res + col);
             } else {
                 xr[j].zero();
                 if constexpr (RES) er[j].zero();
+                if constexpr (LOOSE && VEC > 1) {
+                    if (row < p.rows && col < p.hidden) {
+                        xr[j].load_some(x, col, p.hidden);
+                        if constexpr (RES) er[j].load_some(res, col, p.hidden);
+                    }
+                }
             }
         }
     };
     if (kAhead) fetch(blockIdx.x);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         if (!kAhead) fetch(row);
+        const int shift = shift_of(row);
+        // a row of an output in T
+        const auto store_row = [&](T *y, const float *v) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int col = (tid + j * nthr) * VEC - shift;
+                if (whole(col)) store_vec<T, VEC>(y + col, v + j * VEC);
+                else if (LOOSE && VEC > 1) store_some<T, VEC>(y, col, p.hidden, v + j * VEC);
+            }
+        };
         float r[EPT];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -146,14 +188,7 @@ __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) nor
             }
         }
         if (kAhead) fetch(row + gridDim.x);
-        if constexpr (RES) {
-            T *ro = static_cast<T *>(p.residual_out) + row * p.ros;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (tid + j * nthr) * VEC;
-                if (col < p.hidden) store_vec<T, VEC>(ro + col, r + j * VEC);
-            }
-        }
+        if constexpr (RES) store_row(static_cast<T *>(p.residual_out) + row * p.ros, r);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) ss = fmaf(r[i], r[i], ss);
@@ -161,51 +196,78 @@ __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) nor
         const float inv = __frsqrt_rn(ss / static_cast<float>(p.hidden) + p.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int col = (tid + j * nthr) * VEC;
-            if (col < p.hidden) {
-                float w[VEC];
-                load_weight<VEC>(p, col, w);
+            const int col = (tid + j * nthr) * VEC - shift;
+            float w[VEC];
+            if constexpr (LOOSE) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) r[j * VEC + i] = r[j * VEC + i] * inv * w[i];
+                for (int i = 0; i < VEC; ++i) {
+                    w[i] = 0.f;
+                    if (col + i >= 0 && col + i < p.hidden) load_weight<1>(p, col + i, w + i);
+                }
+            } else if (col < p.hidden) {
+                load_weight<VEC>(p, col, w);
+            } else {
+                continue;
             }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) r[j * VEC + i] = r[j * VEC + i] * inv * w[i];
         }
         if (p.quant == kQuantNone) {
-            T *y = static_cast<T *>(p.y) + row * p.ys;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int col = (tid + j * nthr) * VEC;
-                if (col < p.hidden) store_vec<T, VEC>(y + col, r + j * VEC);
-            }
+            store_row(static_cast<T *>(p.y) + row * p.ys, r);
             __syncthreads();  // `part` is read
             continue;
         }
-        // Maxima of the groups, per vector j.
-        float amax[NV];
+        unsigned char *y = static_cast<unsigned char *>(p.y) + row * p.ys;
+        // E4M3 codes of vector j, the factor of element i given
+        const auto store_codes = [&](int j, auto factor) {
+            const int col = (tid + j * nthr) * VEC - shift;
+            const float *v = r + j * VEC;
+            if (VEC > 1 && whole(col)) {
+                uint32_t w[VEC / 4 + 1];
+#pragma unroll
+                for (int i = 0; i < VEC / 4; ++i)
+                    w[i] = e4m3x2_codes(v[4 * i] * factor(4 * i), v[4 * i + 1] * factor(4 * i + 1)) |
+                           (e4m3x2_codes(v[4 * i + 2] * factor(4 * i + 2), v[4 * i + 3] * factor(4 * i + 3)) << 16);
+                if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(y + col) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint32_t *>(y + col) = w[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (col + i >= 0 && col + i < p.hidden) y[col + i] = e4m3_code(v[i] * factor(i));
+            }
+        };
         if (p.quant == kQuantRow) {
             float m = 0.f;
 #pragma unroll
             for (int i = 0; i < EPT; ++i) m = fmaxf(m, fabsf(r[i]));
             m = block_reduce<true>(m, part[1]);
-#pragma unroll
-            for (int j = 0; j < NV; ++j) amax[j] = m;
             if (tid == 0) p.scales[row] = shadow_scale_of(m);
+            const float f = shadow_factor_of(m);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) store_codes(j, [&](int) { return f; });
         } else {
             const int nblk = (p.hidden + kNormBlock - 1) / kNormBlock;
             float *scales = p.scales + row * nblk;
-            if constexpr (VEC == 1) {
+            if constexpr (LOOSE) {
                 for (int b = tid; b < nblk; b += nthr) bmax[b] = 0;
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const int col = tid + j * nthr;
-                    // a NaN counts as no magnitude, as in fmaxf
-                    if (col < p.hidden && r[j] == r[j]) atomicMax(&bmax[col / kNormBlock], __float_as_int(fabsf(r[j])));
+                    const int col = (tid + j * nthr) * VEC - shift;
+                    // (a NaN counts as no magnitude, as in fmaxf)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (col + i >= 0 && col + i < p.hidden && r[j * VEC + i] == r[j * VEC + i])
+                            atomicMax(&bmax[(col + i) / kNormBlock], __float_as_int(fabsf(r[j * VEC + i])));
                 }
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const int col = tid + j * nthr;
-                    amax[j] = col < p.hidden ? __int_as_float(bmax[col / kNormBlock]) : 0.f;
+                    const int col = (tid + j * nthr) * VEC - shift;
+                    store_codes(j, [&](int i) {
+                        const int c = min(max(col + i, 0), p.hidden - 1);
+                        return shadow_factor_of(__int_as_float(bmax[c / kNormBlock]));
+                    });
                 }
                 for (int b = tid; b < nblk; b += nthr) scales[b] = shadow_scale_of(__int_as_float(bmax[b]));
             } else {
@@ -218,29 +280,11 @@ __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) nor
                     for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(r[j * VEC + i]));
 #pragma unroll
                     for (int off = L / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    amax[j] = m;
                     const int col = (tid + j * nthr) * VEC;
                     if (col < p.hidden && tid % L == 0) scales[col / kNormBlock] = shadow_scale_of(m);
+                    const float f = shadow_factor_of(m);
+                    if (col < p.hidden) store_codes(j, [&](int) { return f; });
                 }
-            }
-        }
-        unsigned char *y = static_cast<unsigned char *>(p.y) + row * p.ys;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int col = (tid + j * nthr) * VEC;
-            if (col >= p.hidden) continue;
-            const float f = shadow_factor_of(amax[j]);
-            if constexpr (VEC == 1) {
-                y[col] = e4m3_code(r[j] * f);
-            } else {
-                uint32_t w[VEC / 4];
-#pragma unroll
-                for (int i = 0; i < VEC / 4; ++i) {
-                    const float *v = r + j * VEC + 4 * i;
-                    w[i] = e4m3x2_codes(v[0] * f, v[1] * f) | (e4m3x2_codes(v[2] * f, v[3] * f) << 16);
-                }
-                if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(y + col) = make_uint2(w[0], w[1]);
-                else *reinterpret_cast<uint32_t *>(y + col) = w[0];
             }
         }
         __syncthreads();  // `part` and `bmax` are read
@@ -250,14 +294,15 @@ __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) nor
 bool aligned(const void *q, int64_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; }
 
 // CTAs of this kernel that the GPU holds at once, by threads (cached).
-template <typename T, int VEC, int EPT, bool RES>
+template <typename T, int VEC, int EPT, bool RES, bool LOOSE>
 int resident(int threads) {
     static int cache[33];
     int n = __atomic_load_n(&cache[threads / 32], __ATOMIC_RELAXED);
     if (n == 0) {
         int dev = 0, sms = 0, per = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, norm_kernel<T, VEC, EPT, RES>, threads, 0) != cudaSuccess || per <= 0)
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, norm_kernel<T, VEC, EPT, RES, LOOSE>, threads, 0) != cudaSuccess ||
+            per <= 0)
             return 0;
         n = per * sms;
         __atomic_store_n(&cache[threads / 32], n, __ATOMIC_RELAXED);
@@ -265,37 +310,48 @@ int resident(int threads) {
     return n;
 }
 
-template <typename T, int VEC, int EPT, bool RES>
+template <typename T, int VEC, int EPT, bool RES, bool LOOSE>
 cudaError_t launch_norm_r(const NormParams &p, cudaStream_t stream) {
-    const int threads = ((p.hidden + EPT - 1) / EPT + 31) / 32 * 32;
-    const int most = resident<T, VEC, EPT, RES>(threads);
+    const int columns = p.hidden + (LOOSE ? VEC - 1 : 0);  // (whatever the shift)
+    const int threads = ((columns + EPT - 1) / EPT + 31) / 32 * 32;
+    const int most = resident<T, VEC, EPT, RES, LOOSE>(threads);
     if (most <= 0) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
-    norm_kernel<T, VEC, EPT, RES><<<grid, threads, 0, stream>>>(p);
+    // as many rows for every CTA, or one less
+    const int64_t turns = (p.rows + most - 1) / most;
+    const unsigned grid = static_cast<unsigned>((p.rows + turns - 1) / turns);
+    norm_kernel<T, VEC, EPT, RES, LOOSE><<<grid, threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool LOOSE>
 cudaError_t launch_norm_k(const NormParams &p, cudaStream_t stream) {
-    return p.residual ? launch_norm_r<T, VEC, EPT, true>(p, stream) : launch_norm_r<T, VEC, EPT, false>(p, stream);
+    return p.residual ? launch_norm_r<T, VEC, EPT, true, LOOSE>(p, stream) : launch_norm_r<T, VEC, EPT, false, LOOSE>(p, stream);
+}
+template <typename T, int VEC, bool LOOSE>
+cudaError_t launch_norm_v(const NormParams &p, cudaStream_t stream) {
+    const int ept = elements_per_thread(p.hidden + (LOOSE ? VEC - 1 : 0));
+    if (ept == 8) return launch_norm_k<T, VEC, 8, LOOSE>(p, stream);
+    if (ept == 16) return launch_norm_k<T, VEC, 16, LOOSE>(p, stream);
+    return launch_norm_k<T, VEC, 32, LOOSE>(p, stream);
 }
 
+// How the rows of the operands lie: all on 16-byte boundaries; all alike within
+// 16 bytes, so that aligned vectors cover them; or neither, element by element
+// (1001 rows of 2565 fp16 values: 12.6 us element by element).
 template <typename T>
 cudaError_t launch_norm_t(const NormParams &p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    // 16-byte accesses need every row of every operand to start on its vector's boundary
     const int64_t ye = p.quant == kQuantNone ? sizeof(T) : 1;  // bytes of an output element
-    const bool vec = p.hidden % V == 0 && p.xs % V == 0 && aligned(p.x, 16) && p.ys % V == 0 && aligned(p.y, V * ye) &&
-                     aligned(p.weight, 16) && (p.weight_dtype == kF32 || V == 8) &&
-                     (!p.residual || (p.rs % V == 0 && p.ros % V == 0 && aligned(p.residual, 16) && aligned(p.residual_out, 16)));
-    const int ept = elements_per_thread(p.hidden);
-    if (vec) {
-        if (ept == 8) return launch_norm_k<T, V, 8>(p, stream);
-        if (ept == 16) return launch_norm_k<T, V, 16>(p, stream);
-        return launch_norm_k<T, V, 32>(p, stream);
-    }
-    if (ept == 8) return launch_norm_k<T, 1, 8>(p, stream);
-    if (ept == 16) return launch_norm_k<T, 1, 16>(p, stream);
-    return launch_norm_k<T, 1, 32>(p, stream);
+    const auto place = [](const void *q, int64_t size) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(q) / size % V); };
+    const auto step = [&](int64_t stride) { return p.rows > 1 ? stride % V : 0; };
+    const int64_t at = place(p.x, sizeof(T)), xstep = step(p.xs);
+    const bool alike = reinterpret_cast<uintptr_t>(p.y) % ye == 0 && place(p.y, ye) == at && step(p.ys) == xstep &&
+                       (!p.residual || (place(p.residual, sizeof(T)) == at && step(p.rs) == xstep &&
+                                        place(p.residual_out, sizeof(T)) == at && step(p.ros) == xstep));
+    const bool vec = alike && at == 0 && xstep == 0 && p.hidden % V == 0 && aligned(p.weight, 16) &&
+                     (p.weight_dtype == kF32 || V == 8);
+    if (vec) return launch_norm_v<T, V, false>(p, stream);
+    if (alike && p.hidden + V - 1 <= kNormMaxHidden) return launch_norm_v<T, V, true>(p, stream);
+    return launch_norm_v<T, 1, true>(p, stream);
 }
 
 }  // namespace

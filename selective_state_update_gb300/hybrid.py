@@ -208,11 +208,13 @@ def ssu_add_rmsnorm(x, weight, eps: float = 1e-5, residual=None, quant: str = "n
     if residual is None:
         _need(residual_out is None, "residual_out needs a residual")
     else:
+        _need(residual.shape == x.shape and residual.dtype == x.dtype and residual.is_cuda and residual.stride(1) == 1,
+              "residual must match x and have unit column stride")
         if residual_out is None:
             residual_out = torch.empty((rows, hidden), dtype=x.dtype, device=x.device)
-        for t in (residual, residual_out):
-            _need(t.shape == x.shape and t.dtype == x.dtype and t.is_cuda and t.stride(1) == 1,
-                  "residual and residual_out must match x and have unit column stride")
+        else:
+            _need(residual_out.shape == x.shape and residual_out.dtype == x.dtype and residual_out.is_cuda
+                  and residual_out.stride(1) == 1, "residual_out must match x and have unit column stride")
     y_dtype = x.dtype if fmt == NORM_PLAIN else torch.float8_e4m3fn
     if out is None:
         out = torch.empty((rows, hidden), dtype=y_dtype, device=x.device)
