@@ -39,7 +39,7 @@ cudaError_t launch_linattn_step(const LinattnParams &p, cudaStream_t stream);
 // byte offsets of its parts (bytes == 0: none, one unit per CTA).
 struct LinattnSplit {
     int64_t cut_len;   // sequences longer than this are cut
-    int64_t max_cuts;  // most sequences that can be
+    int64_t max_cuts, max_states;  // most sequences that can be, and pieces that makes
     uint64_t cuts, pieces, states, bytes;
 };
 LinattnSplit linattn_split(int64_t rows, int64_t nseq, int64_t heads, int64_t dim, int64_t dstate, int64_t max_seqlen);

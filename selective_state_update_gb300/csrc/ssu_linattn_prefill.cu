@@ -86,6 +86,7 @@ struct Plan {
     Unit *pieces;
     float *states;   // [state][head][dim][dstate]
     int64_t cut_len;  // longest piece, a multiple of kC
+    int64_t max_cuts, max_states;  // what the workspace has room for
 };
 
 enum : int {
@@ -106,6 +107,7 @@ enum : int {
     kGrowth, kGrowthFree,
     kSyncA, kSyncB, kSyncC,
     kFinal,
+    kGrowth1, kGrowthFree1,  // the growth pass's second growth
     kBars
 };
 
@@ -298,26 +300,49 @@ __global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const Linatt
     __shared__ int start[kBuckets];
     __shared__ int warp_sum[32];
     __shared__ int states, cuts;
+    __shared__ unsigned long long want_states, want_cuts;
     const int tid = threadIdx.x;
     start[tid] = 0;
-    if (tid == 0) states = cuts = 0;
+    if (tid == 0) states = cuts = 0, want_states = want_cuts = 0;
     __syncthreads();
-    const auto bucket = [](int64_t len) { return kBuckets - 1 - static_cast<int>(min((len + kC - 1) / kC, int64_t(kBuckets - 1))); };
-    // step s of a cut sequence may leave fewer pieces than counted: n pieces of
-    // `step` tokens, the last of what is left
-    const auto each = [&](const Unit &un, auto f) {
-        const int n0 = piece_count(un.len, plan.cut_len);
-        const int64_t step = n0 == 1 ? un.len : piece_step(un.len, n0);
-        const int n = n0 == 1 ? 1 : static_cast<int>((un.len + step - 1) / step);
-        for (int i = 0; i < n; ++i) f(i, n, min(step, un.len - i * step), i * step);
-    };
     Unit own;  // this thread's first sequence is looked up once
     bool have = false;
     for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
         Unit un;
         const bool ok = find_sequence(p, b, un);
         if (b == tid) own = un, have = ok;
-        if (ok) each(un, [&](int, int, int64_t len, int64_t) { atomicAdd(&start[bucket(len)], 1); });
+        const int n = ok ? piece_count(un.len, plan.cut_len) : 1;
+        if (n > 1) {
+            atomicAdd(&want_cuts, 1ull);
+            atomicAdd(&want_states, static_cast<unsigned long long>(n));
+        }
+    }
+    __syncthreads();
+    // Sequences that follow one another fit the workspace.  Bounds that go back
+    // and forth may name more tokens than there are: then none is cut.
+    const int64_t cut_len =
+        want_cuts <= static_cast<unsigned long long>(plan.max_cuts) && want_states <= static_cast<unsigned long long>(plan.max_states)
+            ? plan.cut_len
+            : int64_t(1) << 40;
+    LinattnParams quiet = p;
+    quiet.status = nullptr;  // flagged above
+    const auto sequence = [&](int64_t b, Unit &un) {
+        if (b != tid) return find_sequence(quiet, b, un);
+        un = own;
+        return have;
+    };
+    const auto bucket = [](int64_t len) { return kBuckets - 1 - static_cast<int>(min((len + kC - 1) / kC, int64_t(kBuckets - 1))); };
+    // step s of a cut sequence may leave fewer pieces than counted: n pieces of
+    // `step` tokens, the last of what is left
+    const auto each = [&](const Unit &un, auto f) {
+        const int n0 = piece_count(un.len, cut_len);
+        const int64_t step = n0 == 1 ? un.len : piece_step(un.len, n0);
+        const int n = n0 == 1 ? 1 : static_cast<int>((un.len + step - 1) / step);
+        for (int i = 0; i < n; ++i) f(i, n, min(step, un.len - i * step), i * step);
+    };
+    for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
+        Unit un;
+        if (sequence(b, un)) each(un, [&](int, int, int64_t len, int64_t) { atomicAdd(&start[bucket(len)], 1); });
     }
     __syncthreads();
     // exclusive prefix sum of the buckets
@@ -337,13 +362,8 @@ __global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const Linatt
     start[tid] = before + sum - mine;
     __syncthreads();
     for (int64_t b = tid; b < p.nseq; b += kPlanThreads) {
-        Unit un = own;
-        if (b != tid) {
-            LinattnParams quiet = p;
-            quiet.status = nullptr;  // flagged above
-            have = find_sequence(quiet, b, un);
-        }
-        if (!have) continue;
+        Unit un;
+        if (!sequence(b, un)) continue;
         int state = 0, cut = 0;
         each(un, [&](int i, int n, int64_t len, int64_t off) {
             if (i == 0 && n > 1) {
@@ -407,6 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     linattn_prefill_kernel(const LinattnParams p, const __grid_constant__ Maps maps, const Plan plan) {
     using LY = Layout<DK>;
     constexpr int kParts = BF ? 3 : 2;  // parts of the decayed V
+    // The growth pass has the outputs' columns free and lets the chunks' growths
+    // take turns there, so that one is read while the next is formed.
+    const auto growth_at = [](int ch) { return GROW && (ch & 1) ? kColOut : kColGrowth; };
+    const auto growth_bar = [](int ch) { return GROW && (ch & 1) ? kGrowth1 : kGrowth; };
+    const auto growth_free = [](int ch) { return GROW && (ch & 1) ? kGrowthFree1 : kGrowthFree; };
+    const auto growth_phase = [](int ch) { return GROW ? ch >> 1 : ch; };
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + LY::kBar);
     Unit *ring = reinterpret_cast<Unit *>(smem + LY::kUnits);
@@ -422,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == kFree0 || i == kFree1) n = 1 + (GROW ? 2 : 1) * kGroup;
             if (i == kUnitFree0 || i == kUnitFree1) n = (GROW ? 1 : 2) + 3 * kGroup;
             if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail || i == kVFull0 || i == kVFull1 ||
-                i == kGrowthFree || i == kSyncA || i == kSyncB || i == kSyncC)
+                i == kGrowthFree || i == kGrowthFree1 || i == kSyncA || i == kSyncB || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
@@ -709,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (qd == 0) {
                 if (!wait(kFull0 + k.s, k.ch >> 1)) return false;
                 if (k.n < kC && !wait(kTail, tails++)) return false;
-                if (k.ch > 0 && !wait(kGrowthFree, k.ch - 1)) return false;
+                if (k.ch > (GROW ? 1 : 0) && !wait(growth_free(k.ch), growth_phase(k.ch) - 1)) return false;
             }
             const int r = quarters & 1;
             if (!wait(kVFull0 + r, quarters >> 1)) return false;
@@ -722,10 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int part = 0; part < kParts; ++part)
                         if (2 * qd + i < k.steps)
-                            mma_ts(tm + kColGrowth, a + part * 16 + 8 * i, b + along_mn(i), id_growth, qd > 0 || i > 0 || part > 0);
+                            mma_ts(tm + growth_at(k.ch), a + part * 16 + 8 * i, b + along_mn(i), id_growth, qd > 0 || i > 0 || part > 0);
                 mma_commit(&bars[kVFree0 + r]);
                 if ((qd + 1) * kQuarter >= k.n) {
-                    mma_commit(&bars[kGrowth]);
+                    mma_commit(&bars[growth_bar(k.ch)]);
                     if (GROW) mma_commit(&bars[kFree0 + k.s]);
                 }
             }
@@ -1033,20 +1059,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     mbar_arrive(&bars[kStateFull]);
                 }
-                if (!(ok = mbar_wait_bounded(&bars[kGrowth], ch & 1))) break;
+                if (!(ok = mbar_wait_bounded(&bars[growth_bar(ch)], growth_phase(ch) & 1))) break;
                 tc_fence_after();
                 const float lam = n == kC ? lam_chunk : expf(g * static_cast<float>(n));
                 const float back = BF ? 1.f : maxes[4 + (ch & 3)];
 #pragma unroll
                 for (int b = 0; b < DK / 32; ++b) {
                     uint32_t r[32];
-                    tmem_ld32(tmem + lanes + kColGrowth + 32 * b, r);
+                    tmem_ld32(tmem + lanes + growth_at(ch) + 32 * b, r);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(S[32 * b + i], lam, BF ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * back);
                 }
                 tc_fence_before();
-                mbar_arrive(&bars[kGrowthFree]);
+                mbar_arrive(&bars[growth_free(ch)]);
             }
             if (!ok) break;
             if (GROW || un.dst != kNone) {
@@ -1157,6 +1183,8 @@ cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *wo
         plan.pieces = reinterpret_cast<Unit *>(w + split.pieces);
         plan.states = reinterpret_cast<float *>(w + split.states);
         plan.cut_len = split.cut_len;
+        plan.max_cuts = split.max_cuts;
+        plan.max_states = split.max_states;
         grid = sms;
         linattn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, static_cast<int>(grid));
         cudaError_t e = cudaGetLastError();
@@ -1199,7 +1227,8 @@ LinattnSplit linattn_split(int64_t rows, int64_t nseq, int64_t heads, int64_t di
     if (s.max_cuts > nseq) s.max_cuts = nseq;
     if (s.max_cuts > 65535) s.max_cuts = 65535;
     // sum over cut sequences of ceil(len / cut_len) <= 2 rows / cut_len
-    const uint64_t states = cut ? 2 * (rows / s.cut_len) : 0;
+    s.max_states = cut ? 2 * (rows / s.cut_len) : 0;
+    const uint64_t states = static_cast<uint64_t>(s.max_states);
     s.cuts = up(sizeof(PlanHead));
     s.pieces = s.cuts + up(s.max_cuts * sizeof(Cut));
     s.states = s.pieces + up((nseq + states) * sizeof(Unit));

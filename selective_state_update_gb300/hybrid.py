@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import _DTYPE, _ITYPE, _need, _raise, _ssd_workspace, _stream, _table, OK, SLOTS_STRIDED, SlotTable, lib
+from . import _DTYPE, _ITYPE, _raise, _ssd_workspace, _stream, _table, OK, SLOTS_STRIDED, SlotTable, lib
 
 _I64x2 = ctypes.c_int64 * 2
 
@@ -106,31 +106,41 @@ def _slots(t: Optional[torch.Tensor]):
 def _status(status: Optional[torch.Tensor]) -> int:
     if status is None:
         return 0
-    _need(status.dtype == torch.int32 and status.numel() >= 1 and status.is_cuda, "status must be an int32 CUDA tensor")
+    if not (status.dtype == torch.int32 and status.numel() >= 1 and status.is_cuda):
+        raise ValueError("status must be an int32 CUDA tensor")
     return status.data_ptr()
 
 
 def _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status):
     """(packed arguments, out)."""
-    _need(state.dim() == 4 and state.is_contiguous(), "state must be a contiguous [slots, heads, dim, dstate] tensor")
-    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k and v are [rows, heads, head size]")
+    if not (state.dim() == 4 and state.is_contiguous()):
+        raise ValueError("state must be a contiguous [slots, heads, dim, dstate] tensor")
+    if not (q.dim() == 3 and k.dim() == 3 and v.dim() == 3):
+        raise ValueError("q, k and v are [rows, heads, head size]")
     slots, heads, dim, dstate = state.shape
     rows, kv_heads, dtype = q.shape[0], k.shape[1], q.dtype
-    _need(q.shape == (rows, heads, dstate), "q must be [rows, heads, dstate]")
-    _need(k.shape == (rows, kv_heads, dstate), "k must be [rows, kv_heads, dstate]")
-    _need(v.shape == (rows, kv_heads, dim), "v must be [rows, kv_heads, dim]")
-    _need(state.dtype in _DTYPE and dtype in _DTYPE, "unsupported dtype")
-    _need(k.dtype == dtype and v.dtype == dtype, "k and v must have the dtype of q")
+    if q.shape != (rows, heads, dstate):
+        raise ValueError("q must be [rows, heads, dstate]")
+    if k.shape != (rows, kv_heads, dstate):
+        raise ValueError("k must be [rows, kv_heads, dstate]")
+    if v.shape != (rows, kv_heads, dim):
+        raise ValueError("v must be [rows, kv_heads, dim]")
+    if not (state.dtype in _DTYPE and dtype in _DTYPE):
+        raise ValueError("unsupported dtype")
+    if not (k.dtype == dtype and v.dtype == dtype):
+        raise ValueError("k and v must have the dtype of q")
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=dtype, device=q.device)
     else:
-        _need(out.shape == (rows, heads, dim) and out.dtype == dtype, "out must be [rows, heads, dim] in q's dtype")
+        if not (out.shape == (rows, heads, dim) and out.dtype == dtype):
+            raise ValueError("out must be [rows, heads, dim] in q's dtype")
     qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
-    _need(qs[2] == ks[2] == vs[2] == os[2] == 1, "the last dimension of q, k, v and out must have unit stride")
-    _need(log_decay.dtype == torch.float32 and log_decay.shape == (heads,) and log_decay.is_contiguous(),
-          "log_decay must be a contiguous fp32 [heads] tensor")
-    _need(state.is_cuda and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and log_decay.is_cuda,
-          "all tensors must be CUDA tensors")
+    if not (qs[2] == ks[2] == vs[2] == os[2] == 1):
+        raise ValueError("the last dimension of q, k, v and out must have unit stride")
+    if not (log_decay.dtype == torch.float32 and log_decay.shape == (heads,) and log_decay.is_contiguous()):
+        raise ValueError("log_decay must be a contiguous fp32 [heads] tensor")
+    if not (state.is_cuda and q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and log_decay.is_cuda):
+        raise ValueError("all tensors must be CUDA tensors")
     return _LINATTN.pack(slots, heads, kv_heads, dim, dstate, rows, _DTYPE[dtype], _DTYPE[state.dtype],
                          dstate ** -0.5 if scale is None else scale, 0, pad_slot_id, state.data_ptr(), q.data_ptr(),
                          k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1],
@@ -166,8 +176,9 @@ def ssu_linear_attention_prefill(state, q, k, v, log_decay, cu_seqlens, scale: O
     ``dst_state_batch_indices[b]`` (default: the slot it started from).  Pass
     ``max_seqlen`` where it is known on the host; it only steers how the work is
     split.  Returns out ``[tokens, heads, dim]`` in q's dtype."""
-    _need(cu_seqlens.dtype in _ITYPE and cu_seqlens.is_cuda and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()
-          and cu_seqlens.numel() >= 1, "cu_seqlens must be a contiguous int32/int64 [nseq + 1] CUDA tensor")
+    if not (cu_seqlens.dtype in _ITYPE and cu_seqlens.is_cuda and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()
+            and cu_seqlens.numel() >= 1):
+        raise ValueError("cu_seqlens must be a contiguous int32/int64 [nseq + 1] CUDA tensor")
     a, out = _linattn_args(state, q, k, v, log_decay, scale, pad_slot_id, out, status)
     nseq, longest = cu_seqlens.shape[0] - 1, 0 if max_seqlen is None else max_seqlen
     nbytes = ctypes.c_uint64(0)
@@ -198,38 +209,42 @@ def ssu_add_rmsnorm(x, weight, eps: float = 1e-5, residual=None, quant: str = "n
     the residual itself (default: a new tensor).  Returns (out, scales,
     residual_out); scales is None for "none", residual_out without a
     residual."""
-    _need(x.dim() == 2 and x.dtype in _DTYPE and x.is_cuda and x.stride(1) == 1,
-          "x must be a [rows, hidden] CUDA tensor with unit column stride")
+    if not (x.dim() == 2 and x.dtype in _DTYPE and x.is_cuda and x.stride(1) == 1):
+        raise ValueError("x must be a [rows, hidden] CUDA tensor with unit column stride")
     rows, hidden = x.shape
     fmt = _NORM_FORMAT.get(quant)
-    _need(fmt is not None, "quant is 'none', 'row' or 'block'")
-    _need(weight.shape == (hidden,) and weight.dtype in (x.dtype, torch.float32) and weight.is_contiguous()
-          and weight.is_cuda, "weight must be a contiguous [hidden] CUDA tensor in x's dtype or fp32")
+    if fmt is None:
+        raise ValueError("quant is 'none', 'row' or 'block'")
+    if not (weight.shape == (hidden,) and weight.dtype in (x.dtype, torch.float32) and weight.is_contiguous() and weight.is_cuda):
+        raise ValueError("weight must be a contiguous [hidden] CUDA tensor in x's dtype or fp32")
     if residual is None:
-        _need(residual_out is None, "residual_out needs a residual")
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
     else:
-        _need(residual.shape == x.shape and residual.dtype == x.dtype and residual.is_cuda and residual.stride(1) == 1,
-              "residual must match x and have unit column stride")
+        if not (residual.shape == x.shape and residual.dtype == x.dtype and residual.is_cuda and residual.stride(1) == 1):
+            raise ValueError("residual must match x and have unit column stride")
         if residual_out is None:
             residual_out = torch.empty((rows, hidden), dtype=x.dtype, device=x.device)
         else:
-            _need(residual_out.shape == x.shape and residual_out.dtype == x.dtype and residual_out.is_cuda
-                  and residual_out.stride(1) == 1, "residual_out must match x and have unit column stride")
+            if not (residual_out.shape == x.shape and residual_out.dtype == x.dtype and residual_out.is_cuda
+                    and residual_out.stride(1) == 1):
+                raise ValueError("residual_out must match x and have unit column stride")
     y_dtype = x.dtype if fmt == NORM_PLAIN else torch.float8_e4m3fn
     if out is None:
         out = torch.empty((rows, hidden), dtype=y_dtype, device=x.device)
     else:
-        _need(out.shape == x.shape and out.dtype == y_dtype and out.is_cuda and out.stride(1) == 1,
-              f"out must be a [rows, hidden] {y_dtype} CUDA tensor with unit column stride")
+        if not (out.shape == x.shape and out.dtype == y_dtype and out.is_cuda and out.stride(1) == 1):
+            raise ValueError(f"out must be a [rows, hidden] {y_dtype} CUDA tensor with unit column stride")
     if fmt == NORM_PLAIN:
-        _need(scales is None, "scales go with an 8-bit output")
+        if scales is not None:
+            raise ValueError("scales go with an 8-bit output")
     else:
         shape = (rows,) if fmt == NORM_ROW else (rows, -(-hidden // NORM_BLOCK_COLUMNS))
         if scales is None:
             scales = torch.empty(shape, dtype=torch.float32, device=x.device)
         else:
-            _need(scales.shape == shape and scales.dtype == torch.float32 and scales.is_contiguous() and scales.is_cuda,
-                  f"scales must be a contiguous fp32 CUDA tensor of shape {shape}")
+            if not (scales.shape == shape and scales.dtype == torch.float32 and scales.is_contiguous() and scales.is_cuda):
+                raise ValueError(f"scales must be a contiguous fp32 CUDA tensor of shape {shape}")
     res, res_out = (0, 0) if residual is None else (residual.data_ptr(), residual_out.data_ptr())
     a = _NORM.pack(rows, hidden, _DTYPE[x.dtype], _DTYPE[weight.dtype], fmt, eps, x.data_ptr(), res, weight.data_ptr(),
                    res_out, out.data_ptr(), 0 if scales is None else scales.data_ptr(), x.stride(0),
@@ -247,11 +262,11 @@ def ssu_token_logprobs(logits, tokens, top_k: int = 0, status=None, stream=None)
     Returns (logprobs ``[rows]``, entropy ``[rows]``, top_ids ``[rows, top_k]``
     in tokens' dtype, top_logprobs ``[rows, top_k]``), the floating ones fp32;
     the last two are None without ``top_k``.  Token -1 asks for none."""
-    _need(logits.dim() == 2 and logits.dtype in _DTYPE and logits.is_cuda and logits.stride(1) == 1,
-          "logits must be a [rows, vocab] CUDA tensor with unit column stride")
+    if not (logits.dim() == 2 and logits.dtype in _DTYPE and logits.is_cuda and logits.stride(1) == 1):
+        raise ValueError("logits must be a [rows, vocab] CUDA tensor with unit column stride")
     rows, vocab = logits.shape
-    _need(tokens.shape == (rows,) and tokens.dtype in _ITYPE and tokens.is_cuda and tokens.is_contiguous(),
-          "tokens must be a contiguous int32/int64 [rows] CUDA tensor")
+    if not (tokens.shape == (rows,) and tokens.dtype in _ITYPE and tokens.is_cuda and tokens.is_contiguous()):
+        raise ValueError("tokens must be a contiguous int32/int64 [rows] CUDA tensor")
     device = logits.device
     logprobs = torch.empty(rows, dtype=torch.float32, device=device)
     entropy = torch.empty(rows, dtype=torch.float32, device=device)

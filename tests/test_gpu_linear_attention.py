@@ -207,6 +207,22 @@ def test_prefill_bad_metadata_is_flagged_and_skipped(libssu):
     assert st == ssu.DEV_BAD_SEQLEN and torch.equal(out[100:], good[100:]) and (out[:100] == 7).all()
 
 
+@pytest.mark.parametrize("heads,times", [(1, 40), (2, 200)])
+def test_prefill_bounds_that_go_back(libssu, heads, times):
+    """Bounds that name the same rows again and again, more tokens than the call has: flagged, each rising pair computed
+    (here all of the same rows, to the same outputs), nothing out of bounds."""
+    pool, q, k, v, g = problem(96, 2500, heads, 1, 64, 64, torch.bfloat16, torch.float32, times * 2)
+    cu = torch.tensor([0, 2500] * times, dtype=torch.int32, device=DEV)
+    none = torch.full((2 * times - 1,), -1, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu, state_batch_indices=none, max_seqlen=2500, status=status)
+    assert int(status.item()) == ssu.DEV_BAD_SEQLEN
+    one = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu[:2].contiguous(), state_batch_indices=none[:1])
+    yr, A, B, _, _ = reference(q, k, v, g, [2500], torch.zeros(1, heads, 64, 64, device=DEV), 64 ** -0.5)
+    for out in (y, one):
+        close(out, yr, 2.0 ** -8 * (yr.abs() + A) + 2.0 ** -15 * B, "y")
+
+
 def test_prefill_then_step_is_one_sequence(libssu):
     """A prompt's state goes on token by token: the same as the longer prompt, within the tolerance of each."""
     pool, q, k, v, g = problem(97, 140, 4, 2, 64, 64, torch.bfloat16, torch.float32, 2)
