@@ -28,9 +28,9 @@
 // Rounding: P and, where it meets Q, S to the io type (2^-8 bf16, 2^-11 fp16,
 // each once, as the output itself: together they take the output's error from
 // one rounding's to at most sqrt(2) of it); the decayed V to three parts
-// (2^-24) or two (2^-22), so that fp32 states keep fp32 accuracy.  S as two
-// parts as well measured 255 us instead of XXX on 32768 tokens x 32 heads.
-// fp16 operands are scaled by powers of two (per state row, score row and value
+// (2^-24) or two (2^-22), so that fp32 states keep fp32 accuracy.  S in two
+// parts as well took 260 us where one takes 235 (32768 tokens x 32 heads): eight
+// more products, and the shared memory that the second Q now has.  fp16 operands are scaled by powers of two (per state row, score row and value
 // tile), so neither overflow nor the subnormals cost accuracy.
 //
 // Warps, in groups of four (a warp reaches the tensor-memory lanes 32 (warp %
@@ -42,7 +42,18 @@
 //          two chunks ahead of the outputs, which leave through Q's place;
 //   14     stores the outputs by tiled copies;  15 only completes the group.
 // The groups' code for a chunk is kept short (loops over blocks and quarters are
-// not unrolled): all of it together has to stay in the instruction cache.
+// not unrolled): all of it together has to stay in the instruction cache
+// (unrolled, 384 us instead of 257 at that stage).
+//
+// What it takes: 32768 tokens in 16 sequences x 32 heads of 128 x 128 (bf16, fp32
+// states, some read) 218 us, 5.1 TB/s of the bytes that have to move, 0.76 of the
+// copy rate; one sequence of 40001 tokens x 16 heads (4 of keys) 183 us, of which
+// the growth pass 58.  A chunk takes 4.9 to 5.2 thousand cycles: 48 products of
+// 128 x 128 x 16 and more keep the tensor pipe at work for 3.1 thousand of them, the
+// others go to the hand-overs between the groups; its 450 KB of shared-memory
+// traffic would take 3.5 thousand.  A unit costs 5 to 7 thousand cycles beside its
+// chunks (its state in and out, the partial chunk), the first one of a CTA 10 more
+// (cold instructions).
 #include <cuda.h>
 
 #include "ssu_hybrid.h"

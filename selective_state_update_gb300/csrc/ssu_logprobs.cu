@@ -18,6 +18,9 @@
 // HBM-bound: every logit is read once.  A row is split over the CTAs of a
 // cluster when there are few rows, and the parts are joined through
 // distributed shared memory, so a call is one launch without a workspace.
+// 4096 x 131072 bf16 with 20 alternatives: 214 us, 5.0 TB/s, 0.74 of the copy rate;
+// without alternatives 194 us: a row's sums and search at its end take 1.3 and
+// 1.6 us of its SM, and three CTAs an SM cover them only in part.
 //
 // The largest logits take no second pass.  While streaming, a thread only
 // notes its largest value, which the softmax needs anyway, and the vectors it
@@ -470,6 +473,8 @@ __global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel
 
 template <typename T>
 cudaError_t launch_lp_t(const LogprobParams &p, cudaStream_t stream) {
+    // Two CTAs an SM are enough to split for: 256 rows of 100352 in one part
+    // each take 22.9 us, in two 28.8; 40 rows in four parts 19.4 us, in two 24.6.
     int parts = 1;
     while (parts < kMaxCluster && p.rows * parts * 2 <= 304) parts *= 2;
     cudaLaunchConfig_t cfg{};

@@ -14,7 +14,9 @@
 // holds a row in registers between the two reductions (the sum of squares, the
 // maximum), EPT elements a thread.  The grid is as large as the GPU holds at
 // once; a CTA walks rows and has the next row's loads in flight while it reduces
-// and stores the current one.
+// and stores the current one (rows of up to 4096 columns; wider ones leave no
+// registers for it).  16384 x 8192 bf16 with residual and block scales: 155 us,
+// 6.1 TB/s, 0.90 of the copy rate.
 #include "ssu_device.cuh"
 #include "ssu_hybrid.h"
 
@@ -341,7 +343,7 @@ cudaError_t launch_norm_v(const NormParams &p, cudaStream_t stream) {
 
 // How the rows of the operands lie: all on 16-byte boundaries; all alike within
 // 16 bytes, so that aligned vectors cover them; or neither, element by element
-// (1001 rows of 2565 fp16 values: 12.6 us element by element).
+// (1001 rows of 2565 fp16 values: 9.3 us in vectors, 14.8 by element).
 template <typename T>
 cudaError_t launch_norm_t(const NormParams &p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
