@@ -348,3 +348,27 @@ def test_capture(libssu):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(pool, after)
+
+
+@pytest.mark.parametrize("lengths,heads", [([40] * 60 + [300], 4), ([3000, 5, 700], 2)])
+def test_planned_calls_on_streams_and_in_graphs(libssu, lengths, heads):
+    """Calls with a workspace (many sequences; a cut one): on another stream, and on a graph's replays, as on this one."""
+    pool, q, k, v, g = problem(180, sum(lengths), heads, 1, 64, 64, torch.bfloat16, torch.float32, len(lengths))
+    cu = torch.tensor([0, *lengths]).cumsum(0).to(DEV, torch.int32)
+    start, kw = pool.clone(), dict(max_seqlen=max(lengths))
+    want = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu, **kw)
+    after = pool.clone()
+    pool.copy_(start)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(want)
+    ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu, out=out, stream=side, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want) and torch.equal(pool, after)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu, **kw)
+    for _ in range(2):
+        pool.copy_(start)
+        graph.replay()
+        assert torch.equal(got, want) and torch.equal(pool, after)
