@@ -18,20 +18,24 @@
 // HBM-bound: every logit is read once.  A row is split over the CTAs of a
 // cluster when there are few rows, and the parts are joined through
 // distributed shared memory, so a call is one launch without a workspace.
-// 4096 x 131072 bf16 with 20 alternatives: 214 us, 5.0 TB/s, 0.74 of the copy rate;
-// without alternatives 194 us: a row's sums and search at its end take 1.3 and
-// 1.6 us of its SM, and three CTAs an SM cover them only in part.
+// 4096 x 131072 bf16 with 20 alternatives: 188 us, 5.7 TB/s, 0.84 of the copy rate;
+// without alternatives 168 us.  A row's end (sums, search) leaves its CTA's loads
+// idle, so CTAs are small and many: of 512 threads, three an SM, four vectors in
+// flight a thread it took 208 us, of 256 threads, six an SM 192, four an SM with
+// eight vectors 188.
 //
-// The largest logits take no second pass.  While streaming, a thread only
-// notes its largest value, which the softmax needs anyway, and the vectors it
-// came from.  The k-th largest of the threads' maxima is a lower bound of the
-// k-th largest logit, and only threads whose maximum reaches it can hold any
-// logit that does: those threads' vectors (about k / threads of the row) are
-// read again, out of L2.  What reaches the bound is collected, a little more
-// than k as a rule, and placed by counting what is larger, by unique keys of
-// value and index.  If too many tie with the bound for the collection, the
-// threads' largest keys take the place of their values, which leaves k threads;
-// if those alone hold too many, sorted lists of 32 keys a warp are kept instead.
+// The largest logits take no second pass.  While streaming, a thread notes its
+// largest value, which the softmax needs anyway, and that of each group of
+// vectors that it had in flight at once.  Threads 64 apart form a set; the k-th
+// largest of the 64 sets' maxima is a lower bound of the k-th largest logit, and
+// hardly more than k groups reach it (the k-th largest of the threads' maxima is
+// a closer bound, but sorting all of them costs more).  Those groups are read
+// again, all at once; what reaches the bound is collected and placed by
+// counting what is larger, by unique keys of value and index.  (Reading all of
+// such a thread's vectors again, one thread after the other, took 6 us more of
+// the 188.)  If too many tie with the bound for the collection, the threads'
+// largest keys take the place of their values, which leaves k threads; if those
+// alone hold too many, sorted lists of 32 keys a warp are kept instead.
 #include <cooperative_groups.h>
 
 #include "ssu_device.cuh"
@@ -43,8 +47,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpSmThreads = 1024;  // resident a SM
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -103,14 +106,14 @@ __device__ __forceinline__ K warp_merge(K a, K b) {
 }
 // The 32 largest of the CTA's keys, one a thread, sorted downwards at the
 // start of `lists`; begins and ends with a barrier.
-template <typename K>
+template <int NT, typename K>
 __device__ __forceinline__ void largest_of_threads(K key, K *lists) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
     lists[threadIdx.x] = warp_sort(key);
     __syncthreads();
 #pragma unroll 1
-    for (int half = kLpWarps / 2; half > 0; half >>= 1) {
+    for (int half = NT / 64; half > 0; half >>= 1) {
         if (warp < half) lists[32 * warp + lane] = warp_merge(lists[32 * warp + lane], lists[32 * (warp + half) + lane]);
         __syncthreads();
     }
@@ -208,7 +211,7 @@ struct Logits<__nv_bfloat16> {
 // A part of a row: vectors i < nv of VEC elements from element e0 on, and the
 // `extra` elements outside the row's whole, aligned vectors -- those before
 // (`head` of them, from element 0) and those after (from element `tail`).
-// Vector i belongs to thread i % kLpThreads, extra e to thread e.
+// Vector i belongs to thread i % NT, extra e to thread e.
 template <typename T>
 struct Part {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
@@ -234,10 +237,12 @@ struct Part {
     __device__ __forceinline__ int element(int i, int j) const { return e0 + i * VEC + j; }
 };
 
-constexpr int kUnroll = 4;  // vectors a thread has in flight
-constexpr int kMaxHits = 512;  // candidates collected before the sorted lists take over
+constexpr int kUnroll = 8;  // vectors a thread has in flight: a group
+constexpr int kMaxGroups = 8;  // largest values noted a thread
+constexpr int kMaxHits = 256;  // candidates collected before the sorted lists take over
 
 // The sums over the CTA, in every lane of its first warp.
+template <int NT>
 __device__ __forceinline__ Stats block_join(Stats a, Stats *wstats, float unit) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -248,9 +253,9 @@ __device__ __forceinline__ Stats block_join(Stats a, Stats *wstats, float unit) 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) wstats[warp] = a;
     __syncthreads();
-    a = wstats[lane % kLpWarps];
+    a = wstats[lane % (NT / 32)];
 #pragma unroll
-    for (int off = kLpWarps / 2; off > 0; off >>= 1) {
+    for (int off = NT / 64; off > 0; off >>= 1) {
         const Stats o = {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
                          __shfl_xor_sync(0xffffffffu, a.t, off)};
         a = join(a, o, unit);
@@ -260,44 +265,60 @@ __device__ __forceinline__ Stats block_join(Stats a, Stats *wstats, float unit) 
 
 // The sums of a whole row with the difference taken before the product: for
 // rows with nothing but values near the type's lowest, or with infinities.
-template <typename T>
+template <typename T, int NT>
 __device__ __noinline__ Stats careful_row(const T *x, int vocab, Stats *wstats) {
     Stats a = {-3.402823466e38f, 0.f, 0.f};
-    for (int i = threadIdx.x; i < vocab; i += kLpThreads) {
+    for (int i = threadIdx.x; i < vocab; i += NT) {
         const float v = to_float(x[i]);
         if (v > a.m) rescale(a, v, kLog2e);
         const float d = (v - a.m) * kLog2e, e = ex2(d);
         a.s += e;
         a.t = fmaf(fmaxf(d, -1e4f), e, a.t);
     }
-    return block_join(a, wstats, kLog2e);
+    return block_join<NT>(a, wstats, kLog2e);
 }
 
-// Shared memory of the search for the largest.
+// Shared memory of the search for the largest.  `groups` holds the largest of
+// every 1 << shift groups of kUnroll vectors, in order, for each thread.
+template <int NT>
 struct TopSearch {
-    uint64_t lists[kLpThreads];
+    uint64_t lists[NT];
     uint64_t found[kMaxHits];
-    int hits;
+    uint32_t spots[kMaxHits];
+    float groups[kMaxGroups][NT];
+    int hits, nspots;
+    uint32_t bound;
     uint64_t top[32];
 };
 
-// Collects the keys of a part that reach `bound`, from the lanes in `owners` of
-// each warp (and every thread's extra element); true if they fitted, and then
-// the 32 largest are in ts->top.
-template <typename T>
-__device__ __forceinline__ bool collect_top(const Part<T> &pt, uint64_t bound, bool owner, uint64_t extra_key, TopSearch *ts) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// Collects the keys of a part that reach `bound`, from the groups of the
+// threads that are `owner` (and every thread's extra element); true if they
+// fitted, and then the 32 largest are in ts->top.  The counters are zero and
+// ts->top is empty before.
+template <typename T, int NT>
+__device__ __forceinline__ bool collect_top(const Part<T> &pt, int shift, uint64_t bound, bool owner, uint64_t extra_key,
+                                            TopSearch<NT> *ts) {
+    const int tid = threadIdx.x;
     const float low = bound == 0 ? -INFINITY : key_value(bound);
     const auto collect = [&](uint64_t k) {
         const int h = atomicAdd(&ts->hits, 1);
         if (h < kMaxHits) ts->found[h] = k;
     };
-    if (tid == 0) ts->hits = 0;
-    if (tid < 32) ts->top[tid] = 0;  // (with fewer than 32 the other places stay empty)
-    __syncthreads();
     if (extra_key != 0 && extra_key >= bound) collect(extra_key);
-    for (uint32_t rest = __ballot_sync(0xffffffffu, owner); rest; rest &= rest - 1) {
-        for (int i = 32 * warp + __ffs(rest) - 1 + lane * kLpThreads; i < pt.nv; i += 32 * kLpThreads) {
+    if (owner) {
+        for (int g = 0; tid + (g << shift) * (kUnroll * NT) < pt.nv; ++g) {
+            if (ts->groups[g][tid] < low) continue;
+            const int h = atomicAdd(&ts->nspots, 1);
+            if (h < kMaxHits) ts->spots[h] = static_cast<uint32_t>(g * NT + tid);
+        }
+    }
+    __syncthreads();
+    const int spots = ts->nspots;
+    if (spots > kMaxHits) return false;
+    for (int w = tid / kUnroll; w < spots; w += NT / kUnroll) {
+        const int g = static_cast<int>(ts->spots[w]) / NT, owner_tid = static_cast<int>(ts->spots[w]) % NT;
+        int i = owner_tid + ((g << shift) * kUnroll + tid % kUnroll) * NT;
+        for (int r = 0; r < 1 << shift && i < pt.nv; ++r, i += kUnroll * NT) {
             float v[Part<T>::VEC];
             StateChunk<T>::unpack(pt.load(i).u, v);
 #pragma unroll
@@ -311,7 +332,7 @@ __device__ __forceinline__ bool collect_top(const Part<T> &pt, uint64_t bound, b
     __syncthreads();
     const int n = ts->hits;
     if (n > kMaxHits) return false;
-    for (int i = tid; i < n; i += kLpThreads) {
+    for (int i = tid; i < n; i += NT) {
         const uint64_t k = ts->found[i];
         int larger = 0;
         for (int j = 0; j < n; ++j) larger += ts->found[j] > k;
@@ -321,8 +342,9 @@ __device__ __forceinline__ bool collect_top(const Part<T> &pt, uint64_t bound, b
 }
 
 // The same by the threads' largest keys, for rows with many ties.
-template <typename T>
-__device__ __noinline__ void tied_top(const Part<T> &pt, int top_k, float best, int best_i, uint64_t extra_key, TopSearch *ts) {
+template <typename T, int NT>
+__device__ __noinline__ void tied_top(const Part<T> &pt, int shift, int top_k, float best, int best_i, uint64_t extra_key,
+                                     TopSearch<NT> *ts) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t key = extra_key;
     if (best_i >= 0) {
@@ -331,19 +353,21 @@ __device__ __noinline__ void tied_top(const Part<T> &pt, int top_k, float best, 
         int at = pt.element(best_i, 0);
         for (int u = kUnroll - 1; u >= 0 && best > -INFINITY; --u)
             for (int j = Part<T>::VEC - 1; j >= 0; --j)
-                if (best_i + u * kLpThreads < pt.nv && to_float(pt.x[pt.element(best_i + u * kLpThreads, j)]) == best)
-                    at = pt.element(best_i + u * kLpThreads, j);
+                if (best_i + u * NT < pt.nv && to_float(pt.x[pt.element(best_i + u * NT, j)]) == best)
+                    at = pt.element(best_i + u * NT, j);
         const uint64_t kb = make_key(best, at);
         key = kb > key ? kb : key;
     }
-    largest_of_threads(key, ts->lists);
+    __syncthreads();
+    if (tid == 0) ts->hits = ts->nspots = 0;
+    largest_of_threads<NT>(key, ts->lists);
     const uint64_t bound = ts->lists[top_k - 1];
-    if (collect_top(pt, bound, key >= bound, extra_key, ts)) return;
+    if (collect_top(pt, shift, bound, key >= bound, extra_key, ts)) return;
     // each warp keeps its owners' 32 largest in a sorted list over the lanes
     uint64_t mine = warp_sort(extra_key >= bound ? extra_key : uint64_t(0));
     for (uint32_t rest = __ballot_sync(0xffffffffu, key >= bound); rest; rest &= rest - 1) {
-        for (int base = 32 * warp + __ffs(rest) - 1; base < pt.nv; base += 32 * kLpThreads) {
-            const int i = base + lane * kLpThreads;
+        for (int base = 32 * warp + __ffs(rest) - 1; base < pt.nv; base += 32 * NT) {
+            const int i = base + lane * NT;
             for (int j = 0; j < Part<T>::VEC; ++j) {
                 uint64_t k = i < pt.nv ? make_key(to_float(pt.x[pt.element(i, j)]), pt.element(i, j)) : 0;
                 if (k < bound) k = 0;
@@ -351,36 +375,52 @@ __device__ __noinline__ void tied_top(const Part<T> &pt, int top_k, float best, 
             }
         }
     }
-    largest_of_threads(mine, ts->lists);
+    largest_of_threads<NT>(mine, ts->lists);
     if (tid < 32) ts->top[tid] = ts->lists[tid];
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel(const LogprobParams p, int parts) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, kLpSmThreads / NT) logprobs_kernel(const LogprobParams p, int parts) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-    __shared__ Stats wstats[kLpWarps];
-    __shared__ TopSearch ts;
+    __shared__ Stats wstats[(NT / 32)];
+    __shared__ TopSearch<NT> ts;
     __shared__ Stats part_stats;
+    __shared__ alignas(8) int32_t token[2];  // low half first
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / parts;
     const int rank = static_cast<int>(blockIdx.x - row * parts);
     const T *const x = static_cast<const T *>(p.logits) + row * p.row_stride;
     const Part<T> pt(p, x, rank, parts);
 
+    // The token is asked for now, by a copy that holds up no warp, and its
+    // logit before the search, so that the row's end waits for neither.
+    if (rank == 0 && tid == 0) {
+        const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(token));
+        if (p.tok_is_i64)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(static_cast<const int64_t *>(p.tokens) + row) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(static_cast<const int32_t *>(p.tokens) + row) : "memory");
+    }
+    int shift = 0;
+    while ((pt.nv - 1) / (kUnroll * NT) >> shift >= kMaxGroups) ++shift;
+
     float m = kFloor;  // the largest so far
     Stats a = {kFloor * kLog2e, 0.f, 0.f};
     float best = -INFINITY;
     int best_i = tid < pt.nv ? tid : -1;  // the group of vectors with this thread's largest logit
-    for (int i = tid; i < pt.nv; i += kUnroll * kLpThreads) {
+    float group = -INFINITY;
+    for (int i = tid, step = 0; i < pt.nv; i += kUnroll * NT, ++step) {
         Logits<T> l[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (i + u * kLpThreads < pt.nv) l[u] = pt.load(i + u * kLpThreads);
+            if (i + u * NT < pt.nv) l[u] = pt.load(i + u * NT);
             else l[u].none();
         }
         float vm = l[0].largest();
 #pragma unroll
         for (int u = 1; u < kUnroll; ++u) vm = fmaxf(vm, l[u].largest());
+        group = (step & ((1 << shift) - 1)) == 0 ? vm : fmaxf(group, vm);
+        ts.groups[step >> shift][tid] = group;
         if (vm > best) {
             best = vm;
             best_i = i;
@@ -411,18 +451,40 @@ __global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel
         a.t = fmaf(d, e, a.t);
     }
 
+    int64_t tok = -1;
+    float tok_x = 0.f;
+    if (rank == 0 && tid == 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        tok = p.tok_is_i64 ? *reinterpret_cast<const volatile int64_t *>(token) : *static_cast<const volatile int32_t *>(token);
+        if (tok >= 0 && tok < p.vocab) tok_x = to_float(x[tok]);
+    }
     if (p.top_k > 0) {
-        // by value: the bound's own ties are all collected
+        // Threads 64 apart are a set; the k-th largest of the sets' largest is a
+        // bound.  By value: the bound's own ties are all collected.
         uint32_t mine = best_i >= 0 ? ordered(best) : 0u;
         const uint32_t from_extra = static_cast<uint32_t>(key >> 32);
         mine = mine > from_extra ? mine : from_extra;
         uint32_t *lists = reinterpret_cast<uint32_t *>(ts.lists);
-        largest_of_threads(mine, lists);
-        const uint32_t bound = lists[p.top_k - 1];
-        if (!collect_top(pt, static_cast<uint64_t>(bound) << 32, mine >= bound, key, &ts))
-            tied_top(pt, p.top_k, best, best_i, key, &ts);
+        lists[tid] = mine;
+        if (tid == 0) ts.hits = ts.nspots = 0;
+        if (tid < 32) ts.top[tid] = 0;  // (with fewer than 32 the other places stay empty)
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t s0 = lists[lane], s1 = lists[lane + 32];
+#pragma unroll
+            for (int j = 64; j < NT; j += 64) {
+                s0 = max(s0, lists[lane + j]);
+                s1 = max(s1, lists[lane + 32 + j]);
+            }
+            const uint32_t sorted = warp_merge(warp_sort(s0), warp_sort(s1));
+            if (lane == p.top_k - 1) ts.bound = sorted;
+        }
+        __syncthreads();
+        const uint32_t bound = ts.bound;
+        if (!collect_top(pt, shift, static_cast<uint64_t>(bound) << 32, mine >= bound, key, &ts))
+            tied_top(pt, shift, p.top_k, best, best_i, key, &ts);
     }
-    a = block_join(a, wstats, 1.f);  // (its barrier also completes ts.top)
+    a = block_join<NT>(a, wstats, 1.f);  // (its barrier also completes ts.top)
     if (warp == 0) {
         if (lane == 0) part_stats = a;
     }
@@ -432,7 +494,7 @@ __global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel
         Stats b = part_stats;
         for (int c = 1; c < parts; ++c) b = join(b, *cg::this_cluster().map_shared_rank(&part_stats, c), 1.f);
         const bool careful = !(b.s > 0.f);  // (the same in every thread)
-        if (careful) b = careful_row(x, p.vocab, wstats);
+        if (careful) b = careful_row<T, NT>(x, p.vocab, wstats);
         if (warp == 0) {
             uint64_t top = p.top_k > 0 ? ts.top[lane] : 0;
             if (p.top_k > 0)
@@ -447,10 +509,9 @@ __global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel
                 return kLn2 * (fmaf(v, kLog2e, -b.m) - ls);
             };
             if (lane == 0) {
-                const int64_t tok = load_index(p.tokens, row, p.tok_is_i64);
                 float lp = 0.f;
                 if (tok >= 0 && tok < p.vocab) {
-                    lp = logprob(to_float(x[tok]));
+                    lp = logprob(tok_x);
                 } else if (tok != -1) {
                     flag(p.status, kDevBadEntry);
                     lp = __int_as_float(0x7fc00000);
@@ -471,15 +532,11 @@ __global__ void __launch_bounds__(kLpThreads, 1536 / kLpThreads) logprobs_kernel
     if (parts > 1) cg::this_cluster().sync();
 }
 
-template <typename T>
-cudaError_t launch_lp_t(const LogprobParams &p, cudaStream_t stream) {
-    // Two CTAs an SM are enough to split for: 256 rows of 100352 in one part
-    // each take 22.9 us, in two 28.8; 40 rows in four parts 19.4 us, in two 24.6.
-    int parts = 1;
-    while (parts < kMaxCluster && p.rows * parts * 2 <= 304) parts *= 2;
+template <typename T, int NT>
+cudaError_t launch_lp_t(const LogprobParams &p, int parts, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * parts));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(NT);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -487,16 +544,33 @@ cudaError_t launch_lp_t(const LogprobParams &p, cudaStream_t stream) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, p, parts);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT>, p, parts);
+}
+
+// Of 128 threads a CTA, eight an SM, where rows are short and enough to fill the
+// SMs: 20000 rows of 32000 bf16 take 253 us (of 256 threads 300), 1216 18.5
+// (20.3), 2432 of 65536 63 (66), but 304 of 32000 8.8 (7.9), 4096 of 131072 193 (186).
+constexpr int64_t kSmallRows = 8 * 152, kSmallRowBytes = 131072;
+
+template <typename T>
+cudaError_t launch_lp(const LogprobParams &p, cudaStream_t stream) {
+    // Two CTAs an SM are enough to split for: 256 rows of 100352 in one part each take
+    // 15.2 us, in two 16.9; 40 rows in four parts 8.9, in eight 9.5 (100 rows of
+    // 131072, 11.7 in two and 11.0 in four, are the other way round).
+    int parts = 1;
+    while (parts < kMaxCluster && p.rows * parts * 2 <= 304) parts *= 2;
+    const int64_t bytes = static_cast<int64_t>(p.vocab) * static_cast<int64_t>(sizeof(T));
+    if (p.rows >= kSmallRows && bytes <= kSmallRowBytes) return launch_lp_t<T, 128>(p, parts, stream);
+    return launch_lp_t<T, 256>(p, parts, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t stream) {
     switch (p.dtype) {
-    case kF32: return launch_lp_t<float>(p, stream);
-    case kF16: return launch_lp_t<__half>(p, stream);
-    case kBF16: return launch_lp_t<__nv_bfloat16>(p, stream);
+    case kF32: return launch_lp<float>(p, stream);
+    case kF16: return launch_lp<__half>(p, stream);
+    case kBF16: return launch_lp<__nv_bfloat16>(p, stream);
     }
     return cudaErrorInvalidValue;
 }

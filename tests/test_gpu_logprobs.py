@@ -185,3 +185,30 @@ def test_refusals_on_device(libssu):
         ssu.ssu_token_logprobs(x.t(), tok)
     with pytest.raises(ValueError, match="logits"):
         ssu.ssu_token_logprobs(x.double(), tok)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [31, 257, 2049, 32003])
+def test_many_rows(libssu, vocab, dtype):
+    """Enough rows for small CTAs; among them masked ones, with fewer left than are asked for, just as many, and ties."""
+    x, tok = logits(60 + vocab, 1301, vocab, dtype)
+    k = min(32, vocab)
+    g = torch.Generator(device=DEV).manual_seed(61)
+    for row, left in enumerate((1, k // 2, k, k + 3)):
+        hidden = torch.randperm(vocab, generator=g, device=DEV)[left:]
+        x[row, hidden] = -float("inf")
+        tok[row] = x[row].argmax()
+        x[row + 4, hidden] = torch.finfo(dtype).min
+        tok[row + 4] = x[row + 4].argmax()
+    x[8] = 0.25
+    x[9] = x[9].round()
+    check(x, tok, k)
+    check(x, tok.int(), 0)
+
+
+def test_more_steps_than_groups(libssu):
+    """A row in one part, longer than the noted groups hold one by one; sorted rows crowd the last of them."""
+    x, tok = logits(70, 160, 110003, torch.float32)
+    x[0] = torch.arange(110003, device=DEV) / 1e4
+    x[1] = x[0].flip(0)
+    check(x, tok, 32)
