@@ -46,8 +46,8 @@
 // (unrolled, 384 us instead of 257 at that stage).
 //
 // What it takes: 32768 tokens in 16 sequences x 32 heads of 128 x 128 (bf16, fp32
-// states, some read) 218 us, 5.1 TB/s of the bytes that have to move, 0.76 of the
-// copy rate; one sequence of 40001 tokens x 16 heads (4 of keys) 183 us, of which
+// states, some read) 220 us, 5.1 TB/s of the bytes that have to move, 0.75 of the
+// copy rate; one sequence of 40001 tokens x 16 heads (4 of keys) 182 us, of which
 // the growth pass 58.  A chunk takes 4.9 to 5.2 thousand cycles: 48 products of
 // 128 x 128 x 16 and more keep the tensor pipe at work for 3.1 thousand of them, the
 // others go to the hand-overs between the groups; its 450 KB of shared-memory
