@@ -113,7 +113,8 @@ enum : int {
     kInside,           // the outputs are there (P is read)
     kOutFree,          // ... and read
     kStaged,           // ... and laid out by token, in Q's place
-    kTail,             // a partial chunk's K and V rows past its end are zeros
+    kTail0, kTail1,    // a stage's partial chunk has zeros past its end; one for each stage, whose kFree keeps
+                       // the next such chunk from completing it before this one has been waited for
     kVFull0, kVFull1, kVFree0, kVFree1,
     kGrowth, kGrowthFree,
     kSyncA, kSyncB, kSyncC,
@@ -458,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 1;
             if (i == kFree0 || i == kFree1) n = 1 + (GROW ? 2 : 1) * kGroup;
             if (i == kUnitFree0 || i == kUnitFree1) n = (GROW ? 1 : 2) + 3 * kGroup;
-            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail || i == kVFull0 || i == kVFull1 ||
-                i == kGrowthFree || i == kGrowthFree1 || i == kSyncA || i == kSyncB || i == kSyncC)
+            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail0 || i == kTail1 || i == kVFull0 ||
+                i == kVFull1 || i == kGrowthFree || i == kGrowthFree1 || i == kSyncA || i == kSyncB || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = t; i < pieces; i += kGroup)
                             *reinterpret_cast<uint4 *>(sK + panel * kPanel + n * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
-                    mbar_arrive(&bars[kTail]);
+                    mbar_arrive(&bars[kTail0 + s]);
                     if (!(ok = group_sync(&bars[sync], ph))) break;  // every thread's zeros, below
                 }
                 float vs = 1.f;
@@ -715,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return got;
         };
-        int nu = 0, tails = 0, quarters = 0;
+        int nu = 0, quarters = 0;
+        uint32_t tails = 0;  // bit s: phase of stage s's partial chunks
         struct Chunk {
             int ch, s, n, steps;  // running number, stage, tokens (0: no more), of them in 16s
             uint32_t stage;
@@ -745,7 +747,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (qd * kQuarter >= k.n) return true;
             if (qd == 0) {
                 if (!wait(kFull0 + k.s, k.ch >> 1)) return false;
-                if (k.n < kC && !wait(kTail, tails++)) return false;
+                if (k.n < kC) {
+                    if (!wait(kTail0 + k.s, static_cast<int>(tails >> k.s))) return false;
+                    tails ^= 1u << k.s;
+                }
                 if (k.ch > (GROW ? 1 : 0) && !wait(growth_free(k.ch), growth_phase(k.ch) - 1)) return false;
             }
             const int r = quarters & 1;
