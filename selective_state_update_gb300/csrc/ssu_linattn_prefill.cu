@@ -112,7 +112,8 @@ enum : int {
     kPFull,            // P is there, the entering product scaled
     kInside,           // the outputs are there (P is read)
     kOutFree,          // ... and read
-    kStaged,           // ... and laid out by token, in Q's place
+    kStaged0, kStaged1,  // ... and laid out by token, in Q's place; one for each stage, as the outputs of the next
+                       // chunk may come before the store of this one's has been begun
     kTail0, kTail1,    // a stage's partial chunk has zeros past its end; one for each stage, whose kFree keeps
                        // the next such chunk from completing it before this one has been waited for
     kVFull0, kVFull1, kVFree0, kVFree1,
@@ -459,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 1;
             if (i == kFree0 || i == kFree1) n = 1 + (GROW ? 2 : 1) * kGroup;
             if (i == kUnitFree0 || i == kUnitFree1) n = (GROW ? 1 : 2) + 3 * kGroup;
-            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged || i == kTail0 || i == kTail1 || i == kVFull0 ||
-                i == kVFull1 || i == kGrowthFree || i == kGrowthFree1 || i == kSyncA || i == kSyncB || i == kSyncC)
+            if (i == kStateFull || i == kPFull || i == kOutFree || i == kStaged0 || i == kStaged1 || i == kTail0 || i == kTail1 ||
+                i == kVFull0 || i == kVFull1 || i == kGrowthFree || i == kGrowthFree1 || i == kSyncA || i == kSyncB || i == kSyncC)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++nu;
                 if (un.len < 0) break;
                 for (int c = 0; c < un.len; c += kC, ++ch) {
-                    if (!(ok = mbar_wait_bounded(&bars[kStaged], ch & 1))) break;
+                    if (!(ok = mbar_wait_bounded(&bars[kStaged0 + (ch & 1)], (ch >> 1) & 1))) break;
                     if (un.len - c >= kC) {  // (a partial chunk's rows are stored one by one)
                         for (int i = 0; i < panels; ++i)
                             tma_store_3d(&maps.out, smem + LY::kQ + (ch & 1) * LY::kQBytes + i * kPanel, 64 * i, un.h,
@@ -996,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 rows + (piece / 8) * kPanel + i * 128 + (((piece % 8) ^ (i & 7)) * 16));
                     }
                 }
-                mbar_arrive(&bars[kStaged]);
+                mbar_arrive(&bars[kStaged0 + (ch & 1)]);
             }
             if (!ok) break;
         }

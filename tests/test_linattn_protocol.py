@@ -1,13 +1,14 @@
 """The hand-overs of the linear-attention prefill kernel, as a model on the CPU.
 
-A wait names a barrier's phase by its parity, so it must be looked at before
-the barrier has passed one phase more: a wait that comes after that never sees
-its phase and runs into its time limit.  The model has the kernel's groups of
+A wait names a barrier's phase by its parity, so it must not begin before the
+phase ahead of its own is over (it would take that one's end for its own), and
+must be looked at before the barrier has passed one phase more (it would never
+see its phase and run into its time limit).  The model has the kernel's groups of
 warps, its tiled copies and its products as actors that wait for and complete
 the same barriers, and lets them run in random orders, each actor in turn held
-back for as long as the others can go on.  In no order may a wait be overrun,
+back for as long as the others can go on.  In no order may a wait be early or overrun,
 and every order has to come to its end.  How many barriers the partial chunks
-have is read from the kernel's source."""
+and the staged outputs have is read from the kernel's source."""
 import os
 import random
 import re
@@ -35,17 +36,17 @@ class Overrun(Exception):
 class Model:
     """One CTA that works on `units` (their lengths in tokens).  An actor yields (barrier, phase) to wait, None otherwise."""
 
-    def __init__(self, units, grow, tails=2):
-        self.units, self.grow, self.tails = [*units, -1], grow, tails
+    def __init__(self, units, grow, tails=2, staged=2):
+        self.units, self.grow, self.tails, self.staged = [*units, -1], grow, tails, staged
         self.need, self.left, self.done = {}, {}, {}
         self.ring, self.products, self.copies = [None, None], [], []
         helpers = 2 if grow else 1
         for s in (0, 1):
             for name, count in (("QFull", 1), ("QFree", 1), ("Full", 1), ("Free", 1 + helpers), ("UnitFull", 1),
-                                ("UnitFree", 4 if grow else 5), ("VFull", 1), ("VFree", 1), ("Tail", 1),
+                                ("UnitFree", 4 if grow else 5), ("VFull", 1), ("VFree", 1), ("Tail", 1), ("Staged", 1),
                                 ("Growth", 1), ("GrowthFree", 1)):
                 self.barrier(f"{name}{s}", count)
-        for name in ("Score", "State", "Enter", "P", "Inside", "OutFree", "Staged"):
+        for name in ("Score", "State", "Enter", "P", "Inside", "OutFree"):
             self.barrier(name, 1)
         self.actors = {"loads": self.loads(), "products": self.issue(), "state": self.state(), "values": self.values(0)}
         if grow:
@@ -194,14 +195,14 @@ class Model:
             yield "Inside", ch
             self.arrive("OutFree")
             yield
-            self.arrive("Staged")
+            self.arrive(f"Staged{ch & 1 if self.staged == 2 else 0}")
             yield
 
         yield from self.each_chunk(chunk)
 
     def stores(self):
         def chunk(ch, n):
-            yield "Staged", ch
+            yield (f"Staged{ch & 1}", ch >> 1) if self.staged == 2 else ("Staged0", ch)
             self.arrive(f"QFree{ch & 1}")
             yield
 
@@ -225,14 +226,14 @@ class Model:
         yield from self.each_chunk(chunk, place_free)
 
     def run(self, seed, late, watched):
-        """`late` goes on only where nothing else can.  Raises where a wait on a barrier of `watched` is overrun; other
+        """`late` goes on only where nothing else can.  Raises where a wait on a barrier of `watched` is early or overrun; other
         waits are taken as they are meant."""
         rng = random.Random(seed)
         at = {name: next(actor) for name, actor in self.actors.items()}
         engines = {"tensor cores": self.products, "copy engine": self.copies}
         while True:
             for name, where in at.items():
-                if where and where[0].rstrip("01") in watched and self.done[where[0]] > where[1] + 1:
+                if where and where[0].rstrip("01") in watched and self.done[where[0]] not in (where[1], where[1] + 1):
                     raise Overrun(f"{name} waits for phase {where[1]} of {where[0]}, which is in phase {self.done[where[0]]}")
             able = [n for n, w in at.items() if w is None or self.done[w[0]] > w[1]] + [n for n, q in engines.items() if q]
             if not able:
@@ -251,7 +252,7 @@ class Model:
 ACTORS = [None, "loads", "products", "state", "values", "rows", "stores", "tensor cores", "copy engine"]
 LENGTHS = [[5] * 12, [40] * 8, [128] * 6, [130, 3, 1, 256, 31, 0, 0, 7, 128, 129, 33], [1, 128, 1, 128, 1],
            [64, 5, 70, 20, 300, 9, 9, 9], [0, 1, 0, 1, 0, 1, 2, 3]]
-WATCHED = ["Tail", "Score", "State", "Enter", "P", "Inside", "OutFree", "QFull", "QFree", "Full", "Free", "UnitFull", "UnitFree",
+WATCHED = ["Tail", "Staged", "Score", "State", "Enter", "P", "Inside", "OutFree", "QFull", "QFree", "Full", "Free", "UnitFull", "UnitFree",
            "VFull", "VFree", "Growth", "GrowthFree"]
 
 
@@ -259,7 +260,7 @@ WATCHED = ["Tail", "Score", "State", "Enter", "P", "Inside", "OutFree", "QFull",
 def test_no_wait_is_overrun(late):
     for lengths in LENGTHS:
         for seed in range(30):
-            Model(lengths, False, barriers("Tail")).run(seed, late, WATCHED)
+            Model(lengths, False, barriers("Tail"), barriers("Staged")).run(seed, late, WATCHED)
 
 
 @pytest.mark.parametrize("late", [None, "loads", "products", "state", "values", "values 1", "tensor cores", "copy engine"])
@@ -270,7 +271,8 @@ def test_no_wait_is_overrun_in_the_growth_pass(late):
             Model(lengths, True).run(seed, late, WATCHED)
 
 
-def test_one_barrier_for_the_partial_chunks_of_both_stages_is_overrun():
+@pytest.mark.parametrize("name,late", [("Tail", "products"), ("Staged", "stores")])
+def test_one_barrier_for_both_stages_is_overrun(name, late):
     """The model tells the difference."""
-    with pytest.raises(Overrun, match="Tail"):
-        Model([5] * 12, False, 1).run(0, "products", WATCHED)
+    with pytest.raises(Overrun, match=name):
+        Model([5] * 12, False, 1 if name == "Tail" else 2, 1 if name == "Staged" else 2).run(0, late, WATCHED)
