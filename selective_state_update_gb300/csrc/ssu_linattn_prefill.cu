@@ -1085,8 +1085,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + growth_at(ch) + 32 * b, r);
                     tmem_wait_ld();
+                    // Columns past dstate stay zeros: the products write at most
+                    // the first multiple of 16, the others hold what an earlier
+                    // kernel left there, and fp16 scales a row by its largest.
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(S[32 * b + i], lam, BF ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * back);
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * b + i / 8 * 8 < p.N)
+                            S[32 * b + i] = fmaf(S[32 * b + i], lam, BF ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * back);
                 }
                 tc_fence_before();
                 mbar_arrive(&bars[growth_free(ch)]);
