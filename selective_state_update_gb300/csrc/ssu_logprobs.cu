@@ -10,10 +10,11 @@
 //     d = m - m' <= 0:  s' = s e^d,  t' = (t + d s) e^d.
 // The sums are taken in powers of two against M, m log2(e) rounded to fp32:
 // x log2(e) - M is one FMA, and as M is the reference everywhere its rounding
-// drops out.  The product would overflow beyond 2.3e38: logits below -1e38
-// count as nothing, as they do beside any other, and a row that comes out with
-// nothing or with a NaN (masked altogether, or with infinities) is gone through
-// again with the difference x - m taken first.
+// drops out -- as long as it is small: it is the largest logit's exponent, and
+// from |M| = 2^31 on may overflow the power.  Logits below -1e38 count as nothing,
+// as they do beside any other.  A row whose |M| is above 2^26 (logits of 4.6e7; a
+// row that a mask covers altogether), or that comes out with nothing or with a
+// NaN, is gone through again with the difference x - m taken first.
 //
 // HBM-bound: every logit is read once.  A row is split over the CTAs of a
 // cluster when there are few rows, and the parts are joined through
@@ -145,6 +146,14 @@ __device__ __forceinline__ Stats join(Stats a, Stats b, float unit) {
 // what is masked has the exponential zero, its product with the exponent is
 // zero and not NaN, and a row of nothing else sums to zero.
 constexpr float kFloor = -0.9e38f, kLow = -1e38f;
+// The largest reference whose rounding (at most 4 there) leaves the sums exact.
+constexpr float kMostReference = 67108864.f;
+// Sums against a larger one may have overflowed.  They are nothing beside a
+// smaller one, and not looked at where the row's own is no smaller; a NaN among
+// the logits stays.
+__device__ __forceinline__ void drop_unusable(Stats &a) {
+    if (fabsf(a.m) > kMostReference) a.s = a.t = a.s == a.s ? 0.f : a.s;
+}
 __device__ __forceinline__ float raise(float v) {  // a NaN stays
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(kLow));
@@ -264,7 +273,7 @@ __device__ __forceinline__ Stats block_join(Stats a, Stats *wstats, float unit) 
 }
 
 // The sums of a whole row with the difference taken before the product: for
-// rows with nothing but values near the type's lowest, or with infinities.
+// rows whose largest logit is large in size, or with infinities.
 template <typename T, int NT>
 __device__ __noinline__ Stats careful_row(const T *x, int vocab, Stats *wstats) {
     Stats a = {-3.402823466e38f, 0.f, 0.f};
@@ -427,6 +436,7 @@ __global__ void __launch_bounds__(NT, kLpSmThreads / NT) logprobs_kernel(const L
         }
         if (vm > m) {
             m = vm;
+            drop_unusable(a);
             rescale(a, m * kLog2e, 1.f);
         }
 #pragma unroll
@@ -445,11 +455,15 @@ __global__ void __launch_bounds__(NT, kLpSmThreads / NT) logprobs_kernel(const L
     if (tid < pt.extra) {
         const float v = to_float(x[pt.extra_at(tid)]);
         key = make_key(v, pt.extra_at(tid));
-        if (v > m) rescale(a, v * kLog2e, 1.f);
+        if (v > m) {
+            drop_unusable(a);
+            rescale(a, v * kLog2e, 1.f);
+        }
         const float d = fmaf(raise(v), kLog2e, -a.m), e = ex2(d);
         a.s += e;
         a.t = fmaf(d, e, a.t);
     }
+    drop_unusable(a);
 
     int64_t tok = -1;
     float tok_x = 0.f;
@@ -493,7 +507,7 @@ __global__ void __launch_bounds__(NT, kLpSmThreads / NT) logprobs_kernel(const L
     if (rank == 0) {
         Stats b = part_stats;
         for (int c = 1; c < parts; ++c) b = join(b, *cg::this_cluster().map_shared_rank(&part_stats, c), 1.f);
-        const bool careful = !(b.s > 0.f);  // (the same in every thread)
+        const bool careful = !(b.s > 0.f && fabsf(b.m) <= kMostReference);  // (the same in every thread)
         if (careful) b = careful_row<T, NT>(x, p.vocab, wstats);
         if (warp == 0) {
             uint64_t top = p.top_k > 0 ? ts.top[lane] : 0;
