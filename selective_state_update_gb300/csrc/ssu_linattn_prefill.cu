@@ -521,15 +521,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float vs = 1.f;
                 if constexpr (!BF) {
-                    // the power of two that brings the tile's largest |v| near fp16's top
+                    // the power of two that brings the chunk's largest |v| near
+                    // fp16's top (the rows past its end are zeros as far as the
+                    // last quarter goes, and after it other tokens')
                     uint32_t m2 = 0u;
-                    const int pieces = (p.P > 64 ? 2 : 1) * (kPanel / 16);
-                    for (int i = t; i < pieces; i += kGroup) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(sK + LY::kKBytes + i * 16);
-                        const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+                    const int pieces = (n + kQuarter - 1) / kQuarter * kQuarter * 8;
+                    for (int panel = 0; panel < (p.P > 64 ? 2 : 1); ++panel)
+                        for (int i = t; i < pieces; i += kGroup) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(sK + LY::kKBytes + panel * kPanel + i * 16);
+                            const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, ws[e] & 0x7fff7fffu);  // magnitudes order as their bits
-                    }
+                            for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, ws[e] & 0x7fff7fffu);  // magnitudes order as their bits
+                        }
                     float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
                                     __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
 #pragma unroll

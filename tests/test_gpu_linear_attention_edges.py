@@ -24,3 +24,34 @@ def test_prefill_fp16_after_large_growths(libssu, before, dstate):
     """Nothing of an earlier call is left in what the state's rows are scaled by."""
     fill_tensor_memory(before)
     check_prefill(200 + dstate, [300, 131], 80, 80, 64, dstate, torch.float16, torch.float32)
+
+
+@pytest.mark.parametrize("poison", [6e4, float("inf"), float("nan")])
+@pytest.mark.parametrize("lengths", [[70, 200, 61], [1, 140, 33], [128, 3, 97]])
+def test_prefill_fp16_keeps_sequences_apart(libssu, lengths, poison):
+    """Values beside a sequence in the packed tokens change no bit of its outputs and states."""
+    pool, q, k, v, g = problem(210, sum(lengths), 2, 1, 64, 64, torch.float16, torch.float32, 3, std=1e-3)
+    a, b = lengths[0], lengths[0] + lengths[1]
+    cu = torch.tensor([0, a, b, sum(lengths)], dtype=torch.int32, device=DEV)
+    for t in (q, k, v):
+        t[a:b] = 0
+    clean_pool, dirty_pool = pool.clone(), pool.clone()
+    want = ssu.ssu_linear_attention_prefill(clean_pool, q, k, v, g, cu)
+    for t in (q, k, v):
+        t[a:b] = poison
+    got = ssu.ssu_linear_attention_prefill(dirty_pool, q, k, v, g, cu)
+    keep = [*range(a), *range(b, sum(lengths))]
+    assert torch.equal(got[keep], want[keep])
+    assert torch.equal(dirty_pool[[0, 2]], clean_pool[[0, 2]])
+
+
+def test_prefill_fp16_rows_past_the_end(libssu):
+    """The same for rows that belong to no sequence."""
+    pool, q, k, v, g = problem(215, 200, 2, 1, 64, 64, torch.float16, torch.float32, 1, std=1e-3)
+    cu = torch.tensor([0, 133], dtype=torch.int32, device=DEV)
+    first = pool.clone()
+    v[133:] = 0
+    want = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu)
+    v[133:] = 6e4
+    got = ssu.ssu_linear_attention_prefill(first, q, k, v, g, cu)
+    assert torch.equal(got[:133], want[:133]) and torch.equal(first, pool)
