@@ -193,7 +193,7 @@ __device__ __forceinline__ uint32_t split2(float &x, float &y) {
 template <int N>
 __device__ __forceinline__ void registers() {
     if constexpr (N < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else if constexpr (N > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Four 8 x 8 matrices of 16-bit elements, transposed: the lane's address is row
@@ -615,7 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // The launch gives every thread 128 registers (4 x 128 in all); the groups
-    // take 120, 216 and 96, which leaves 80 for the last.
+    // take 120, 216 and 96 (fp16, whose rows have their power of two besides: 128,
+    // 208 and 96), which leaves 80 for the last: no spills.
+    constexpr int kRowRegs = BF ? 120 : 128, kStateRegs = BF ? 216 : 208;
     if (warp == 13) {
         registers<80>();
         // ---------------- units and loads ----------------
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 15) {
         registers<80>();
     } else if (warp < 4) {
-        registers<120>();
+        registers<kRowRegs>();
         if constexpr (GROW) decay_values(1);
         // ---------------- P and the outputs (thread = token) ----------------
         const int row = tid;
@@ -1009,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     } else if (warp < 8) {
-        registers<216>();
+        registers<kStateRegs>();
         // ---------------- the state (thread = value dim) ----------------
         const int t = tid - kGroup, w = warp - 4;
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
