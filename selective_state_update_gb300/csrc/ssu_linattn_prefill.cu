@@ -1017,6 +1017,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
         int nu = 0, ch = 0, ph = 0;
         float S[DK];
+        if constexpr (!GROW && !BF) {
+            // fp16 scales a row of S by its largest, and S takes in all DK
+            // columns of the growth, of which the products write dstate,
+            // rounded up to 16.  The others, with what an earlier kernel left
+            // in them, are zeros from here on (leaving them out of every sum
+            // instead takes 10 % longer: 242 us for 217, 32768 tokens x 32 heads).
+            const uint32_t zeros[16] = {};
+            for (int c = (p.N + 15) / 16 * 16; c < DK; c += 16) tmem_st16(tmem + lanes + kColGrowth + c, zeros);
+            tmem_wait_st();
+        }
         for (;;) {
             if (!(ok = mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) break;
             const Unit un = ring[nu & 1];
@@ -1090,13 +1100,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t r[32];
                     tmem_ld32(tmem + lanes + growth_at(ch) + 32 * b, r);
                     tmem_wait_ld();
-                    // Columns past dstate stay zeros: the products write at most
-                    // the first multiple of 16, the others hold what an earlier
-                    // kernel left there, and fp16 scales a row by its largest.
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * b + i / 8 * 8 < p.N)
-                            S[32 * b + i] = fmaf(S[32 * b + i], lam, BF ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * back);
+                    for (int i = 0; i < 32; ++i) S[32 * b + i] = fmaf(S[32 * b + i], lam, BF ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * back);
                 }
                 tc_fence_before();
                 mbar_arrive(&bars[growth_free(ch)]);
