@@ -525,14 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // fp16's top (the rows past its end are zeros as far as the
                     // last quarter goes, and after it other tokens')
                     uint32_t m2 = 0u;
-                    const int pieces = (n + kQuarter - 1) / kQuarter * kQuarter * 8;
-                    for (int panel = 0; panel < (p.P > 64 ? 2 : 1); ++panel)
-                        for (int i = t; i < pieces; i += kGroup) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(sK + LY::kKBytes + panel * kPanel + i * 16);
-                            const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) m2 = __vmaxu2(m2, ws[e] & 0x7fff7fffu);  // magnitudes order as their bits
-                        }
+                    const int turns = (n + kQuarter - 1) / kQuarter * 2;  // a turn takes 16 rows of 8 pieces
+                    const auto largest = [](uint4 u) {                    // magnitudes order as their bits
+                        return __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+                    };
+                    for (int panel = 0; panel < (p.P > 64 ? 2 : 1); ++panel) {
+                        const unsigned char *from = sK + LY::kKBytes + panel * kPanel + t * 16;
+#pragma unroll 1
+                        for (int i = 0; i < turns; i += 2, from += 2 * kGroup * 16)
+                            m2 = __vmaxu2(m2, __vmaxu2(largest(*reinterpret_cast<const uint4 *>(from)),
+                                                       largest(*reinterpret_cast<const uint4 *>(from + kGroup * 16))));
+                    }
                     float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
                                     __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
 #pragma unroll
