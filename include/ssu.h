@@ -495,6 +495,9 @@ ssu_status ssu_linear_attention_step(const ssu_linattn_args *args, const ssu_slo
  * aligned with strides that are multiples of 8.  Decreasing, negative or too
  * large cu_seqlens set SSU_DEV_BAD_SEQLEN; such a sequence, and one whose
  * entry or slot is bad, is skipped: none of its rows and states is written.
+ * A NaN or an infinity in v[t,g,p] makes out[.,h,p] from t on and row p of the
+ * state NaN (an infinity is not followed with its sign, as the recurrence would);
+ * it reaches no earlier token, no other row and no other sequence.
  *
  * `max_seqlen` is the longest sequence's length if the caller knows it, 0 if
  * not.  It steers how the work is split over the GPU and never the

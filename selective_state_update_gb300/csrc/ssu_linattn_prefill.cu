@@ -138,7 +138,9 @@ struct Layout {
     static constexpr int kRowScale = (kUnits + 2 * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;  // fp16: state rows, by chunk parity
     static constexpr int kMax = kRowScale + 2 * 128 * 4;  // fp16: per warp; the value tiles' scales, four chunks; per warp of the growth pass's helpers
     static constexpr int kMisc = kMax + 48;               // tensor-memory address, abort
-    static constexpr int kBytes = kMisc + 16;
+    static constexpr int kOdd = kMisc + 16;               // by chunk, of four, and warp of value dims: the last chunk with
+    static constexpr int kFirst = kOdd + 4 * 16;          // values that are no numbers; of every dim the token of its first
+    static constexpr int kBytes = kFirst + 4 * 128;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -215,6 +217,34 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     tmem_st16(taddr, r);
     tmem_st16(taddr + 16, r + 16);
+}
+
+// Where element `dim` of row `row` lies in panels of 64 16-bit elements a row.
+__device__ __forceinline__ int swizzled(int row, int dim) {
+    return (dim >> 6) * kPanel + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) * 16) + (dim & 7) * 2;
+}
+// sum += 0 v, two bf16 each: a NaN from the first v on that is no number.
+__device__ __forceinline__ void add_zero_times(uint32_t &sum, uint32_t v) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(v), "r"(0u));
+}
+// A NaN or an infinity among a chunk's values would reach the outputs of the
+// tokens before it, by a zero of P.  So they are made zeros in shared memory, where
+// P meets them, once they have been read for the state; and the rows' group
+// makes the outputs of a dim NaN from the first one's token on, which this returns
+// (kC where there is none).  Looking for them and the room that this takes in the
+// instruction cache cost 2 to 4 %: 233 us for 225, 32768 tokens x 32 heads.
+template <bool BF>
+__device__ __forceinline__ int take_out(unsigned char *values, int dim, int tokens) {
+    int first = kC;
+#pragma unroll 1
+    for (int row = tokens - 1; row >= 0; --row) {
+        unsigned short *v = reinterpret_cast<unsigned short *>(values + swizzled(row, dim));
+        if ((*v & 0x7fff) < (BF ? 0x7f80 : 0x7c00)) continue;
+        *v = 0;
+        first = row;
+    }
+    fence_proxy_async_smem();
+    return first;
 }
 
 // A head's state [P][N] between memory (T, contiguous) and the state's place in
@@ -453,6 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *row_scale = reinterpret_cast<float *>(smem + LY::kRowScale);
     float *maxes = reinterpret_cast<float *>(smem + LY::kMax);
     volatile uint32_t *abort_flag = misc + 1;
+    int *odd_chunk = reinterpret_cast<int *>(smem + LY::kOdd);
+    unsigned char *first_odd = smem + LY::kFirst;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
@@ -465,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n = kGroup;
             mbar_init(&bars[i], n);
         }
+        for (int i = 0; i < 16; ++i) odd_chunk[i] = -1;
         *abort_flag = 0;
     }
     if (warp == 12) tmem_alloc512(misc);
@@ -478,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the growth pass the first one, `helper` 1, takes every second quarter.
     const auto decay_values = [&](int helper) {
         const int sync = helper ? kSyncA : kSyncC;
-        float *tile_max = maxes + (helper ? 8 : 0);
+        uint32_t *tile_max = reinterpret_cast<uint32_t *>(maxes + (helper ? 8 : 0));
         const int t = tid % kGroup, w = warp % 4;
         const bool live = 32 * w < p.P;
         int nu = 0, ch = 0, quarters = 0, ph = 0;
@@ -520,11 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = group_sync(&bars[sync], ph))) break;  // every thread's zeros, below
                 }
                 float vs = 1.f;
+                bool odd = false;  // some of the warp's values (fp16: of the chunk's) are no numbers
                 if constexpr (!BF) {
                     // the power of two that brings the chunk's largest |v| near
                     // fp16's top (the rows past its end are zeros as far as the
                     // last quarter goes, and after it other tokens')
-                    uint32_t m2 = 0u;
+                    uint32_t pair = 0u;
                     const int turns = (n + kQuarter - 1) / kQuarter * 2;  // a turn takes 16 rows of 8 pieces
                     const auto largest = [](uint4 u) {                    // magnitudes order as their bits
                         return __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
@@ -533,17 +567,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const unsigned char *from = sK + LY::kKBytes + panel * kPanel + t * 16;
 #pragma unroll 1
                         for (int i = 0; i < turns; i += 2, from += 2 * kGroup * 16)
-                            m2 = __vmaxu2(m2, __vmaxu2(largest(*reinterpret_cast<const uint4 *>(from)),
-                                                       largest(*reinterpret_cast<const uint4 *>(from + kGroup * 16))));
+                            pair = __vmaxu2(pair, __vmaxu2(largest(*reinterpret_cast<const uint4 *>(from)),
+                                                           largest(*reinterpret_cast<const uint4 *>(from + kGroup * 16))));
                     }
-                    float m = fmaxf(__half2float(__ushort_as_half(static_cast<unsigned short>(m2))),
-                                    __half2float(__ushort_as_half(static_cast<unsigned short>(m2 >> 16))));
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    if (lane == 0) tile_max[w] = m;
+                    uint32_t m = max(pair & 0xffffu, pair >> 16);
+                    if (__builtin_expect(m >= 0x7c00u, 0)) {  // no number: the largest of the others, and a mark
+                        m = 0u;
+#pragma unroll 1
+                        for (int i = t * 8; i < (p.P > 64 ? 2 : 1) * (kPanel / 2); i += (i & 7) == 7 ? kGroup * 8 - 7 : 1) {
+                            const uint32_t x = reinterpret_cast<const unsigned short *>(sK + LY::kKBytes)[i] & 0x7fffu;
+                            if ((i / 64 & (kC - 1)) < n && x < 0x7c00u) m = max(m, x);
+                        }
+                        m |= 0x10000u;
+                    }
+                    odd = __any_sync(0xffffffffu, m > 0xffffu);
+                    m = __reduce_max_sync(0xffffffffu, m & 0xffffu);
+                    if (lane == 0) tile_max[w] = odd ? m | 0x10000u : m;
                     if (!(ok = group_sync(&bars[sync], ph))) break;
-                    m = fmaxf(fmaxf(tile_max[0], tile_max[1]), fmaxf(tile_max[2], tile_max[3]));
-                    const int k = fp16_scale_exp(m);
+                    const uint32_t m0 = tile_max[0], m1 = tile_max[1], m2 = tile_max[2], m3 = tile_max[3];
+                    odd = ((m0 | m1 | m2 | m3) >> 16) != 0u;
+                    const uint32_t top = max(max(m0 & 0xffffu, m1 & 0xffffu), max(m2 & 0xffffu, m3 & 0xffffu));
+                    const int k = fp16_scale_exp(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
                     vs = pow2i(k);
                     if (helper == 0 && t == 0) maxes[4 + (ch & 3)] = pow2i(-k);
                     if (!(ok = group_sync(&bars[sync], ph))) break;  // the maxima are read
@@ -601,7 +645,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st_16x128b_x4(tmem + (static_cast<uint32_t>(32 * w + 16 * hh) << 16) + kColV + r * kRing + 16 * q, part);
                             }
                         }
+                        if constexpr (BF && !GROW) {
+                            uint32_t zeros[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) add_zero_times(zeros[i & 3], v[i >> 3][i & 7]);
+                            odd = odd || __any_sync(0xffffffffu, ((zeros[0] | zeros[1] | zeros[2] | zeros[3]) & 0x7fff7fffu) != 0u);
+                        }
                         tmem_wait_st();
+                        if (!GROW && __builtin_expect(odd && past <= 0, 0)) {  // (the warp has read all of its values)
+                            const int dim = 32 * w + lane, slot = ch & 3;
+                            first_odd[slot * 128 + dim] = static_cast<unsigned char>(take_out<BF>(sK + LY::kKBytes, dim, n));
+                            if (lane == 0) odd_chunk[4 * slot + w] = ch;
+                        }
                     }
                     tc_fence_before();
                     mbar_arrive(&bars[kVFull0 + r]);
@@ -993,6 +1048,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j)
                         *reinterpret_cast<uint4 *>(mine + (b / 2) * kPanel + (((4 * (b % 2) + j) ^ (row & 7)) * 16)) =
                             make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                }
+                const int4 odd = reinterpret_cast<const int4 *>(odd_chunk)[ch & 3];
+                if (__builtin_expect(odd.x == ch || odd.y == ch || odd.z == ch || odd.w == ch, 0)) {
+                    const unsigned char *first = first_odd + (ch & 3) * 128;
+#pragma unroll 1
+                    for (int dim = 0; dim < p.P; ++dim)
+                        if (odd_chunk[4 * (ch & 3) + dim / 32] == ch && row >= first[dim])
+                            *reinterpret_cast<unsigned short *>(rows + swizzled(row, dim)) = 0x7fff;
                 }
                 fence_proxy_async_smem();
                 if (n < kC) {

@@ -55,3 +55,52 @@ def test_prefill_fp16_rows_past_the_end(libssu):
     v[133:] = 6e4
     got = ssu.ssu_linear_attention_prefill(first, q, k, v, g, cu)
     assert torch.equal(got[:133], want[:133]) and torch.equal(first, pool)
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("rows,at,heads", [(100, 0, 4), (100, 99, 4), (300, 140, 4), (300, 127, 4), (300, 128, 4),
+                                           (2600, 1333, 2)])
+def test_prefill_values_that_are_no_numbers(libssu, rows, at, heads, poison, io):
+    """A NaN or an infinity in v at token t, value dim p: the outputs of dim p are NaN from t on, and so is row p of the
+    state; no bit of anything else changes."""
+    dim = 13
+    pool, q, k, v, _ = problem(220 + at, rows, heads, 1, 64, 96, io, torch.float32, 1)
+    g = torch.full((heads,), -1e-4, device=DEV)
+    cu = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    v[at, 0, dim] = 0
+    dirty_pool = pool.clone()
+    want = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu)
+    v[at, 0, dim] = poison
+    got = ssu.ssu_linear_attention_prefill(dirty_pool, q, k, v, g, cu)
+    assert torch.equal(got[:at], want[:at])
+    others = [p for p in range(64) if p != dim]
+    assert torch.equal(got[:, :, others], want[:, :, others])
+    assert torch.equal(dirty_pool[:, :, others], pool[:, :, others])
+    assert torch.isnan(got[at:, :, dim].float()).all()
+    assert torch.isnan(dirty_pool[0, :, dim]).all()
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16])
+def test_prefill_many_values_that_are_no_numbers(libssu, io):
+    """Several of them in one chunk: each dim from its first one on."""
+    pool, q, k, v, _ = problem(230, 250, 2, 1, 80, 64, io, torch.float32, 1)
+    g = torch.full((2,), -1e-3, device=DEV)
+    cu = torch.tensor([0, 250], dtype=torch.int32, device=DEV)
+    where = [(5, 3), (9, 3), (40, 70), (127, 0), (128, 1), (249, 79), (200, 33), (131, 33)]
+    for t, p in where:
+        v[t, 0, p] = 0
+    dirty_pool = pool.clone()
+    want = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu)
+    for n, (t, p) in enumerate(where):
+        v[t, 0, p] = (float("nan"), float("inf"), -float("inf"))[n % 3]
+    got = ssu.ssu_linear_attention_prefill(dirty_pool, q, k, v, g, cu)
+    first = {}
+    for t, p in where:
+        first[p] = min(t, first.get(p, 250))
+    for p in range(80):
+        t = first.get(p, 250)
+        assert torch.equal(got[:t, :, p], want[:t, :, p]), p
+        assert torch.isnan(got[t:, :, p].float()).all(), p
+        if t == 250:
+            assert torch.equal(dirty_pool[:, :, p], pool[:, :, p])
