@@ -955,15 +955,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!BF) {
                     // from the largest score before its decay, which bounds
                     // the decayed ones: P stays in fp16's normal range down to
-                    // 2^-27 of it
+                    // 2^-27 of it (of the scores up to the row's own token: a
+                    // later one may be any number or none)
                     float m = 0.f;
 #pragma unroll 1
                     for (int b = 0; b <= warp; ++b) {
                         uint32_t r[32];
                         tmem_ld32(tmem + lanes + kColScore + 32 * b, r);
                         tmem_wait_ld();
+                        const int last = b < warp ? 31 : lane;
 #pragma unroll
-                        for (int jj = 0; jj < 32; ++jj) m = fmaxf(m, fabsf(__uint_as_float(r[jj])));
+                        for (int jj = 0; jj < 32; ++jj)
+                            if (jj <= last) m = fmaxf(m, fabsf(__uint_as_float(r[jj])));
                     }
                     // (not so far up that the entering product, scaled alike, could overflow)
                     const int k = min(fp16_scale_exp(m * fabsf(p.scale)), 40);

@@ -104,3 +104,20 @@ def test_prefill_many_values_that_are_no_numbers(libssu, io):
         assert torch.isnan(got[t:, :, p].float()).all(), p
         if t == 250:
             assert torch.equal(dirty_pool[:, :, p], pool[:, :, p])
+
+
+@pytest.mark.parametrize("late", [6e4, float("inf"), float("nan")])
+def test_prefill_fp16_later_keys_leave_earlier_outputs(libssu, late):
+    """A key however large or bad changes no bit of the outputs of tokens before it."""
+    pool, q, k, v, g = problem(240, 128, 4, 1, 64, 64, torch.float16, torch.float32, 1)
+    k.copy_(torch.sign(k.float()) * 2.0 ** -18)  # far below it: 2^33 of the products
+    v.mul_(1000)
+    pool.zero_()
+    cu = torch.tensor([0, 128], dtype=torch.int32, device=DEV)
+    for at in (20, 33, 95):
+        kk = k.clone()
+        kk[at] = 0
+        want = ssu.ssu_linear_attention_prefill(pool.clone(), q, kk, v, g, cu, scale=1.0)
+        kk[at] = late
+        got = ssu.ssu_linear_attention_prefill(pool.clone(), q, kk, v, g, cu, scale=1.0)
+        assert torch.equal(got[:at], want[:at])
