@@ -75,6 +75,11 @@ ssu_status check_strides(const char *name, const int64_t *s) {
     return SSU_OK;
 }
 
+// A pointer that the device reads elements of `size` bytes through.
+bool aligned(const void *q, int64_t size) { return reinterpret_cast<uintptr_t>(q) % size == 0; }
+int64_t dtype_size(int32_t dtype) { return dtype == SSU_F32 ? 4 : 2; }
+int64_t itype_size(int32_t type) { return type == SSU_I64 ? 8 : 4; }
+
 ssu_status check_table(const char *name, const ssu_slot_table *t, ssu::SlotTab *out) {
     std::memset(out, 0, sizeof *out);
     if (t == nullptr || t->entries == nullptr) return SSU_OK;
@@ -83,6 +88,8 @@ ssu_status check_table(const char *name, const ssu_slot_table *t, ssu::SlotTab *
         return fail(SSU_ERR_INVALID, "%s table: mode %d is not an ssu_slot_mode", name, t->mode);
     if (t->extent < 0) return fail(SSU_ERR_INVALID, "%s table: negative extent", name);
     if (t->s0 < 0 || t->s1 < 0) return fail(SSU_ERR_INVALID, "%s table: negative stride", name);
+    if (!aligned(t->entries, itype_size(t->type)))
+        return fail(SSU_ERR_INVALID, "%s table: entries must be aligned to their type", name);
     out->entries = t->entries;
     out->s0 = t->s0;
     out->s1 = t->s1;
@@ -526,6 +533,10 @@ static ssu_status linattn_prepare(const ssu_linattn_args *a, const ssu_slot_tabl
     if (!(a->scale == a->scale)) return fail(SSU_ERR_INVALID, "scale is not a number");
     if (!a->state || !a->log_decay) return fail(SSU_ERR_INVALID, "state and log_decay must not be NULL");
     if (!aligned16(a->state)) return fail(SSU_ERR_INVALID, "state must be 16-byte aligned");
+    for (const void *q : {a->q, a->k, a->v, static_cast<const void *>(a->out)})
+        if (!aligned(q, dtype_size(a->io_dtype))) return fail(SSU_ERR_INVALID, "q, k, v and out must be aligned to their type");
+    if (!aligned(a->log_decay, 4) || !aligned(a->d_status, 4))
+        return fail(SSU_ERR_INVALID, "log_decay and d_status must be 4-byte aligned");
     if (a->rows > 0 && (!a->q || !a->k || !a->v || !a->out)) return fail(SSU_ERR_INVALID, "q, k, v and out must not be NULL");
     if (a->rows > 0 && (a->out == a->q || a->out == a->k || a->out == a->v || a->out == a->state))
         return fail(SSU_ERR_INVALID, "out must not alias an input");
@@ -593,6 +604,7 @@ ssu_status ssu_linear_attention_prefill(const ssu_linattn_args *args, int64_t ns
     if (args->io_dtype == SSU_F32) return fail(SSU_ERR_UNSUPPORTED, "the prefill takes fp16 or bf16 q, k, v and out");
     if (nseq == 0) return ok();
     if (!cu_seqlens) return fail(SSU_ERR_INVALID, "cu_seqlens must not be NULL");
+    if (!aligned(cu_seqlens, itype_size(meta_type))) return fail(SSU_ERR_INVALID, "cu_seqlens must be aligned to its type");
     if (lp.rows > 0) {
         for (const void *q : {args->q, args->k, args->v, static_cast<const void *>(args->out)})
             if (!aligned16(q)) return fail(SSU_ERR_INVALID, "q, k, v and out must be 16-byte aligned");
@@ -637,10 +649,12 @@ ssu_status ssu_add_rmsnorm(const ssu_norm_args *a, void *stream) {
         return fail(SSU_ERR_INVALID, "scales go with the E4M3 formats and only with them");
     if (!a->x || !a->weight || !a->y) return fail(SSU_ERR_INVALID, "x, weight and y must not be NULL");
     if (a->rows > kMaxGrid) return fail(SSU_ERR_INVALID, "more than 2^31-1 rows");
-    const int64_t size = a->dtype == SSU_F32 ? 4 : 2;
     for (const void *q : {a->x, a->residual, static_cast<const void *>(a->residual_out)})
-        if (reinterpret_cast<uintptr_t>(q) % size != 0)
+        if (!aligned(q, dtype_size(a->dtype)))
             return fail(SSU_ERR_INVALID, "x, residual and residual_out must be aligned to their type");
+    if (!aligned(a->weight, dtype_size(a->weight_dtype)) || !aligned(a->scales, 4) ||
+        (a->format == SSU_NORM_PLAIN && !aligned(a->y, dtype_size(a->dtype))))
+        return fail(SSU_ERR_INVALID, "weight, y and scales must be aligned to their type");
     if (a->y == a->x || a->y == a->residual || a->y == a->residual_out || (a->residual_out && a->residual_out == a->x))
         return fail(SSU_ERR_INVALID, "y must not alias x, residual or residual_out, nor residual_out x");
     ssu_status st = check_device(a->x, "x");
@@ -671,8 +685,12 @@ ssu_status ssu_token_logprobs(const ssu_logprob_args *a, void *stream) {
         return fail(SSU_ERR_INVALID, "logits, tokens, logprobs and entropy must not be NULL");
     if (a->top_k > 0 && (!a->top_ids || !a->top_logprobs))
         return fail(SSU_ERR_INVALID, "top_ids and top_logprobs must not be NULL");
-    if (reinterpret_cast<uintptr_t>(a->logits) % (a->dtype == SSU_F32 ? 4 : 2) != 0)
-        return fail(SSU_ERR_INVALID, "logits must be aligned to their type");
+    if (!aligned(a->logits, dtype_size(a->dtype))) return fail(SSU_ERR_INVALID, "logits must be aligned to their type");
+    if (!aligned(a->tokens, itype_size(a->token_type)) || !aligned(a->top_ids, itype_size(a->token_type)))
+        return fail(SSU_ERR_INVALID, "tokens and top_ids must be aligned to their type");
+    for (const void *q : {static_cast<const void *>(a->logprobs), static_cast<const void *>(a->entropy),
+                          static_cast<const void *>(a->top_logprobs), static_cast<const void *>(a->d_status)})
+        if (!aligned(q, 4)) return fail(SSU_ERR_INVALID, "logprobs, entropy, top_logprobs and d_status must be 4-byte aligned");
     if (a->rows > kMaxGrid / 8) return fail(SSU_ERR_INVALID, "too many rows for one launch");
     ssu_status st = check_device(a->logits, "logits");
     if (st != SSU_OK) return st;
