@@ -300,19 +300,22 @@ __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) nor
 
 bool aligned(const void *q, int64_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; }
 
-// CTAs of this kernel that the GPU holds at once, by threads (cached).
+// CTAs of this kernel that the device holds at once, by device and threads (cached).
 template <typename T, int VEC, int EPT, bool RES, bool LOOSE>
 int resident(int threads) {
-    static int cache[33];
-    int n = __atomic_load_n(&cache[threads / 32], __ATOMIC_RELAXED);
+    static int cache[64][33];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int *const kept = dev >= 0 && dev < 64 ? &cache[dev][threads / 32] : nullptr;
+    int n = kept ? __atomic_load_n(kept, __ATOMIC_RELAXED) : 0;
     if (n == 0) {
-        int dev = 0, sms = 0, per = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        int sms = 0, per = 0;
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, norm_kernel<T, VEC, EPT, RES, LOOSE>, threads, 0) != cudaSuccess ||
             per <= 0)
             return 0;
         n = per * sms;
-        __atomic_store_n(&cache[threads / 32], n, __ATOMIC_RELAXED);
+        if (kept) __atomic_store_n(kept, n, __ATOMIC_RELAXED);
     }
     return n;
 }
