@@ -1259,16 +1259,22 @@ int sm_count() {
 }
 
 template <int DK, bool BF, bool GROW>
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(linattn_prefill_kernel<DK, BF, GROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes);
+}
+template <int DK, bool BF, bool GROW>
 cudaError_t launch_one(const LinattnParams &p, const Maps &maps, const Plan &plan, int64_t grid, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(linattn_prefill_kernel<DK, BF, GROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Layout<DK>::kBytes);
-    if (e != cudaSuccess) return e;
     linattn_prefill_kernel<DK, BF, GROW><<<static_cast<unsigned>(grid), kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan);
     return cudaGetLastError();
 }
 
 template <int DK, bool BF>
 cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *workspace, cudaStream_t stream) {
+    // Before the maps: their encoder is a driver call and refuses a host thread
+    // that has no context yet, which this one gives it.
+    cudaError_t e = allow_smem<DK, BF, false>();
+    if (e == cudaSuccess && split.max_cuts > 0) e = allow_smem<DK, BF, true>();
+    if (e != cudaSuccess) return e;
     Maps maps;
     if (p.rows > 0 && !(encode(&maps.q, p, p.q, p.N, p.H, p.qs) && encode(&maps.k, p, p.k, p.N, p.G, p.ks) &&
                         encode(&maps.v, p, p.v, p.P, p.G, p.vs) && encode(&maps.out, p, p.out, p.P, p.H, p.os)))
@@ -1288,8 +1294,7 @@ cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *wo
         plan.max_states = split.max_states;
         grid = sms;
         linattn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, static_cast<int>(grid));
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if (split.max_cuts > 0) {
             if ((e = launch_one<DK, BF, true>(p, maps, plan, grid, stream)) != cudaSuccess) return e;
             const dim3 blocks(static_cast<unsigned>((static_cast<int64_t>(p.P) * p.N + 1023) / 1024), static_cast<unsigned>(p.H),
