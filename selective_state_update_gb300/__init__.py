@@ -512,6 +512,11 @@ def ssu_replay_verify(state, x, dt, A, B, C, x_buf, dt_buf, B_buf, count_in, cou
 _SSD_WORKSPACE = {}
 
 
+def _stream_object(device, stream) -> torch.cuda.Stream:
+    """A given stream (a ``torch.cuda.Stream`` or a raw handle) as torch's."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+
+
 def _ssd_workspace(device, nbytes: int, stream) -> torch.Tensor:
     """A workspace per (device, stream) that only grows (the "cached
     workspace" of the MATE page): a steady-state call allocates nothing, and
@@ -525,8 +530,7 @@ def _ssd_workspace(device, nbytes: int, stream) -> torch.Tensor:
         if stream is None:  # the call runs on the current stream
             ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         else:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
-            with torch.cuda.stream(s):
+            with torch.cuda.stream(_stream_object(device, stream)):
                 ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         _SSD_WORKSPACE[key] = ws
     return ws

@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import _DTYPE, _ITYPE, _raise, _ssd_workspace, _stream, _table, OK, SLOTS_STRIDED, SlotTable, lib
+from . import _DTYPE, _ITYPE, _raise, _stream, _stream_object, _table, OK, SLOTS_STRIDED, SlotTable, lib
 
 _I64x2 = ctypes.c_int64 * 2
 
@@ -188,10 +188,14 @@ def ssu_linear_attention_prefill(state, q, k, v, log_decay, cu_seqlens, scale: O
         _raise(rc)
     need, ws = nbytes.value, None
     if need:
-        # on the current stream a block of the caching allocator (also inside a
-        # graph's own pool); on another one the workspace kept for that stream
-        ws = (torch.empty(need, dtype=torch.uint8, device=q.device) if stream is None
-              else _ssd_workspace(q.device, need, stream))
+        # a block of the caching allocator for this call alone, on the stream
+        # that it runs on (in a capture, of the graph's own pool): the launches of
+        # another host thread's call may come between this one's
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(_stream_object(q.device, stream)):
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     _launch(L.ssu_linear_attention_prefill, state.get_device(), stream, a, nseq, cu_seqlens.data_ptr(),
             _ITYPE[cu_seqlens.dtype], longest, _slots(state_batch_indices), _slots(dst_state_batch_indices),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
