@@ -35,6 +35,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -510,6 +511,9 @@ def ssu_replay_verify(state, x, dt, A, B, C, x_buf, dt_buf, B_buf, count_in, cou
 
 
 _SSD_WORKSPACE = {}
+# Held from a call's look at the kept workspace to the last of its launches: those
+# of two host threads on one stream stay apart.
+_SSD_LAUNCHES = threading.Lock()
 
 
 def _stream_object(device, stream) -> torch.cuda.Stream:
@@ -566,7 +570,6 @@ def ssu_ssd_prefill(x, dt, A, B, C, chunk_size: int, cu_chunk_seqlens, seq_idx, 
     rc = lib().ssu_ssd_workspace_size(nchunks, heads, groups, dim, dstate, chunk_size, ctypes.byref(nbytes))
     if rc != OK:
         _raise(rc)
-    ws = _ssd_workspace(x.device, nbytes.value, stream)
     hi = float(dt_limit[1])
     a = SsdArgs(tokens=tokens, heads=heads, dim=dim, dstate=dstate, groups=groups, nseq=nseq, nchunks=nchunks,
                 chunk_size=chunk_size, io_dtype=_DTYPE.get(x.dtype, -1), dt_dtype=_DTYPE[dt.dtype],
@@ -576,9 +579,11 @@ def ssu_ssd_prefill(x, dt, A, B, C, chunk_size: int, cu_chunk_seqlens, seq_idx, 
                 x=x.data_ptr(), dt=dt.data_ptr(), B=B.data_ptr(), C=C.data_ptr(), z=_ptr(z), A=A.data_ptr(),
                 D=_ptr(D), dt_bias=_ptr(dt_bias), cu_chunk_seqlens=cu_chunk_seqlens.data_ptr(),
                 seq_idx=seq_idx.data_ptr(), last_chunk_indices=_ptr(last_chunk_indices),
-                initial_states=_ptr(initial_states), y=out.data_ptr(), states=states.data_ptr(),
-                workspace=ws.data_ptr(), workspace_bytes=ws.numel(), d_status=_ptr(status))
-    rc = lib().ssu_ssd_prefill(ctypes.byref(a), _stream(stream))
+                initial_states=_ptr(initial_states), y=out.data_ptr(), states=states.data_ptr(), d_status=_ptr(status))
+    with _SSD_LAUNCHES:
+        ws = _ssd_workspace(x.device, nbytes.value, stream)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        rc = lib().ssu_ssd_prefill(ctypes.byref(a), _stream(stream))
     if rc != OK:
         _raise(rc)
     return out, states

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import selective_state_update_gb300 as ssu
+import workloads
 from test_gpu_linear_attention import DEV, problem
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,39 @@ def test_linear_attention_prefill(libssu, raw):
         for out in outs:
             assert torch.equal(out, want)
     assert set(ssu._SSD_WORKSPACE) == kept  # nothing is held for the stream
+
+
+def test_ssd_prefill(libssu):
+    """On the workspace kept for the stream."""
+    side = torch.cuda.Stream()
+    calls, wants = [], []
+    for seed, lengths in ((300, [130, 257, 1, 312]), (301, [900, 33])):
+        g = workloads.ssd_problem(seed, lengths, heads=16, dim=64, dstate=128, groups=2, chunk_size=128).to(DEV)
+
+        def call(stream=side, g=g):
+            return ssu.ssu_ssd_prefill(g.x, g.dt, g.A, g.B, g.C, g.chunk_size, g.cu_chunk_seqlens, g.seq_idx, g.last_chunk_indices,
+                                       D=g.D, z=g.z, dt_bias=g.dt_bias, dt_softplus=g.dt_softplus, dt_limit=g.dt_limit,
+                                       initial_states=g.initial_states, state_dtype=g.state_dtype, nseq=g.nseq,
+                                       out=torch.empty_like(g.x), stream=stream)
+
+        calls.append(call)
+        wants.append([t.clone() for t in call(None)])
+    torch.cuda.synchronize()
+    for outs, want in zip(both(calls, 20), wants):
+        side.synchronize()
+        for out in outs:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_ssd_launches_stay_together(libssu, monkeypatch):
+    """No other thread gets at the kept workspace between a call's look at it and its launches."""
+    g = workloads.ssd_problem(302, [130], heads=16, dim=64, dstate=128, groups=2, chunk_size=128).to(DEV)
+    kept, held = ssu._ssd_workspace, []
+
+    def watched(*args):
+        held.append(ssu._SSD_LAUNCHES.locked())
+        return kept(*args)
+
+    monkeypatch.setattr(ssu, "_ssd_workspace", watched)
+    ssu.ssu_ssd_prefill(g.x, g.dt, g.A, g.B, g.C, g.chunk_size, g.cu_chunk_seqlens, g.seq_idx, g.last_chunk_indices, nseq=g.nseq)
+    assert held == [True]
