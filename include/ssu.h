@@ -26,7 +26,8 @@
  *    copies nothing between host and device, and never synchronizes: one
  *    call is one kernel launch on `stream` (a cudaStream_t; NULL = the
  *    legacy default stream).  After ssu_prewarm the calls may be captured in
- *    a CUDA graph.
+ *    a CUDA graph; linear attention, the norm and the log probabilities from
+ *    their first call on.
  *  - Host-detectable errors return a status, leave a message for
  *    ssu_last_error(), and launch nothing.
  *  - Errors only the device can see (a slot outside [0, slots) that is not
@@ -587,7 +588,8 @@ ssu_status ssu_token_logprobs(const ssu_logprob_args *args, void *stream);
  * Graph capture and prewarm_selective_state_update (kernels there are
  * compiled at first use; here they are compiled ahead of time, so this only
  * loads them).  `packed` selects the packed kernel instead of the one-token
- * kernel.  Returns SSU_ERR_UNSUPPORTED for a dstate or dtype the kernels do
+ * kernel.  Linear attention, the norm and the log probabilities need none of
+ * this.  Returns SSU_ERR_UNSUPPORTED for a dstate or dtype the kernels do
  * not cover.
  */
 ssu_status ssu_prewarm(int32_t state_dtype, int32_t io_dtype, int32_t dt_dtype,

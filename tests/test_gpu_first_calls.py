@@ -1,4 +1,8 @@
-"""Calls where nothing was done on the GPU before: the first of a host thread."""
+"""Calls where nothing was done before: the first of a host thread, the first of a
+process inside a graph capture."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -51,3 +55,28 @@ def test_first_call_of_a_host_thread(libssu, name):
     t.join()
     assert isinstance(got[0], torch.Tensor), got[0]
     assert torch.equal(got[0], want)
+
+
+CAPTURE = """
+import torch
+from test_gpu_first_calls import calls
+
+for name, call in calls().items():
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, call()), name
+print("captured")
+"""
+
+
+def test_first_calls_inside_a_capture(libssu):
+    """No kernel of these has been loaded before its capture: they need no ssu_prewarm."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    paths = os.pathsep.join([here, os.path.dirname(here)])
+    r = subprocess.run([sys.executable, "-c", CAPTURE], env=dict(os.environ, PYTHONPATH=paths), capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "captured", r.stderr[-2000:]
