@@ -17,6 +17,8 @@
 // and stores the current one (rows of up to 4096 columns; wider ones leave no
 // registers for it).  16384 x 8192 bf16 with residual and block scales: 155 us,
 // 6.1 TB/s, 0.90 of the copy rate.
+#include <type_traits>
+
 #include "ssu_device.cuh"
 #include "ssu_hybrid.h"
 
@@ -200,7 +202,21 @@ __global__ void __launch_bounds__(ept_threads(EPT), 1024 / ept_threads(EPT)) nor
 #pragma unroll
         for (int i = 0; i < EPT; ++i) ss = fmaf(r[i], r[i], ss);
         ss = block_reduce<false>(ss, part[0]);
-        const float inv = __frsqrt_rn(ss / static_cast<float>(p.hidden) + p.eps);
+        float inv = __frsqrt_rn(ss / static_cast<float>(p.hidden) + p.eps);
+        if constexpr (sizeof(T) == 4 || std::is_same<T, __nv_bfloat16>::value) {
+            if (ss > 3.402823466e38f) {
+                // squares past fp32's range (values from 1e17 on): again of r 2^-80, beside which eps is nothing
+                __syncthreads();  // `part` is read
+                ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) {
+                    const float small = r[i] * 0x1p-80f;
+                    ss = fmaf(small, small, ss);
+                }
+                ss = block_reduce<false>(ss, part[0]);
+                inv = __frsqrt_rn(ss / static_cast<float>(p.hidden)) * 0x1p-80f;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = (tid + j * nthr) * VEC - shift;
