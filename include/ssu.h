@@ -452,8 +452,15 @@ ssu_status ssu_shadow_refresh(const void *state, int32_t state_dtype, int64_t ro
  * The pool is the one of the update entry points: [slots, heads, dim,
  * dstate], any ssu_dtype, slots read and written through the same kind of
  * tables (ssu_batch_copy moves them).  S is carried in fp32 and rounded once,
- * to nearest even, into the pool's type; out is computed in fp32 and rounded
- * into the io type.
+ * to nearest even, into the pool's type.  The step computes out in fp32 and
+ * rounds it into the io type.  The prefill works in chunks of 128 tokens and
+ * rounds two operands to the io type on the way to out, once each: a score
+ * q . k after its decay, before it meets v, and the state that enters a chunk,
+ * before it meets q.  Beside fp32's own errors, and with u = 2^-8 (bf16) or 2^-11
+ * (fp16), out is thus within u (|out| + scale (sum over the chunk's j <= t of
+ * decay |q . k_j| |v_j|  +  decay |S| |q|)) of the formula: about one rounding
+ * of out more, unless its terms cancel.  The states go through neither.  Its
+ * scores q . k, before their decay, have to fit fp32.
  *
  * q, k, v and out may be slices of larger tensors: `*_stride` holds the token
  * and head strides in elements (not negative); the innermost stride is one.

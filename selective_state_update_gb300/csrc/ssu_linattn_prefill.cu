@@ -25,19 +25,24 @@
 //                                       whose rows have been scaled there by l^(i+1) in fp32
 //   growth   [p, n]  = (V decayed)^T K  the decayed V in three parts (bf16) or two
 //                                       (fp16), transposed, from tensor memory
-// Rounding: P and, where it meets Q, S to the io type (2^-8 bf16, 2^-11 fp16,
-// each once, as the output itself: together they take the output's error from
-// one rounding's to at most sqrt(2) of it); the decayed V to three parts
-// (2^-24) or two (2^-22), so that fp32 states keep fp32 accuracy.  S in two
-// parts as well took 260 us where one takes 235 (32768 tokens x 32 heads): eight
-// more products, and the shared memory that the second Q now has.  fp16 operands are scaled by powers of two (per state row, score row and value
-// tile), so neither overflow nor the subnormals cost accuracy.
+// Rounding: P and, where it meets Q, S to the io type (2^-8 bf16, 2^-11 fp16),
+// each once; the decayed V to three parts (2^-24) or two (2^-22), so that fp32
+// states keep fp32 accuracy.  The first two cost the outputs u sum |P| |V| and
+// u |S| |Q|, u being the io type's rounding: as much as one more rounding of Q
+// or V, which the caller has rounded to the same type.  On normal inputs in
+// bf16 the outputs are off by 0.0023 of their norm, where their own rounding
+// alone is 0.0017 of it; where a sum cancels it is more beside the output.  S in
+// two parts as well took 260 us where one took 235 (32768 tokens x 32 heads):
+// eight more products, and the shared memory that the second Q now has.  fp16
+// operands are scaled by powers of two (per state row, score row and chunk of
+// values), so neither overflow nor the subnormals cost accuracy.
 //
 // Warps, in groups of four (a warp reaches the tensor-memory lanes 32 (warp %
 // 4) ...):
 //   0-3    (thread = token) scores -> P, entering rows scaled, outputs stored;
 //   4-7    (thread = value dim) S: growth added, parts split off, first and last state;
-//   8-11   V decayed, transposed (ldmatrix) and split, 32 tokens at a time;
+//   8-11   V decayed, transposed (ldmatrix) and split, 32 tokens at a time, and
+//          looked through for what is no number;
 //   12     issues the products;  13 finds the units and loads Q, K, V by tiled copies,
 //          two chunks ahead of the outputs, which leave through Q's place;
 //   14     stores the outputs by tiled copies;  15 only completes the group.
@@ -46,14 +51,14 @@
 // (unrolled, 384 us instead of 257 at that stage).
 //
 // What it takes: 32768 tokens in 16 sequences x 32 heads of 128 x 128 (bf16, fp32
-// states, some read) 220 us, 5.1 TB/s of the bytes that have to move, 0.75 of the
-// copy rate; one sequence of 40001 tokens x 16 heads (4 of keys) 182 us, of which
-// the growth pass 58.  A chunk takes 4.9 to 5.2 thousand cycles: 48 products of
-// 128 x 128 x 16 and more keep the tensor pipe at work for 3.1 thousand of them, the
-// others go to the hand-overs between the groups; its 450 KB of shared-memory
-// traffic would take 3.5 thousand.  A unit costs 5 to 7 thousand cycles beside its
-// chunks (its state in and out, the partial chunk), the first one of a CTA 10 more
-// (cold instructions).
+// states, some read) 229 us, 4.9 TB/s of the bytes that have to move, 0.72 of the
+// copy rate; one sequence of 40001 tokens x 16 heads (4 of keys) 186 us, of which the
+// growth pass 60.  A chunk takes 2.95 us on every SM at once (3.3 with keys and
+// values of its own for every head, 3.8 in fp16): 48 products of 128 x 128 x 16 and
+// more keep the tensor pipe at work for 3.1 thousand cycles of it, the others go
+// to the hand-overs between the groups; its 450 KB of shared-memory traffic would
+// take 3.5 thousand.  A unit of one token takes 12 us by itself, launch and cold
+// instructions included.
 #include <cuda.h>
 
 #include "ssu_hybrid.h"
@@ -231,8 +236,10 @@ __device__ __forceinline__ void add_zero_times(uint32_t &sum, uint32_t v) {
 // tokens before it, by a zero of P.  So they are made zeros in shared memory, where
 // P meets them, once they have been read for the state; and the rows' group
 // makes the outputs of a dim NaN from the first one's token on, which this returns
-// (kC where there is none).  Looking for them and the room that this takes in the
-// instruction cache cost 2 to 4 %: 233 us for 225, 32768 tokens x 32 heads.
+// (kC where there is none).  Looking for them, and the room that this takes in the
+// instruction cache, costs 2 to 4 % (232 us for 223, 32768 tokens x 32 heads).  A
+// warp of its own that looked through every chunk cost 14 %, the products' warp
+// asking for it 5.
 template <bool BF>
 __device__ __forceinline__ int take_out(unsigned char *values, int dim, int tokens) {
     int first = kC;
@@ -1309,12 +1316,14 @@ cudaError_t launch_t(const LinattnParams &p, const LinattnSplit &split, void *wo
 }  // namespace
 
 // How a call is split.  Without cuts a call takes as long as its longest
-// sequence on one SM (2.3 us a chunk), or its share of the GPU, `even` chunks an
+// sequence on one SM (2.8 us a chunk), or its share of the GPU, `even` chunks an
 // SM; cut into pieces of about `even` chunks it takes those, the growth pass
 // over them (nearly as long again) and three more launches, worth 15 chunks.
-// Measured, one sequence of 128 x 128 bf16 heads, uncut and cut: 40001 tokens x 16
-// heads 733 and 185 us, 4096 x 16 86 and 57, 2048 x 16 48 and 50, 1024 x 16 30 and
-// 50, 4096 x 64 88 and 122, 16384 x 64 313 and 325.
+// Measured, one sequence of 128 x 128 bf16 heads, four to a head of keys, uncut and
+// cut: 40001 tokens x 16 heads 879 and 186 us, 4096 x 16 97 and 49, 2048 x 16 52 and
+// 44 (the rule leaves it whole), 1024 x 16 30 and 41, 4096 x 64 99 and 119,
+// 16384 x 64 367 and 348.  kSms, not the device's count: the workspace's size and
+// the launch have to agree on the split whatever device is current at either.
 LinattnSplit linattn_split(int64_t rows, int64_t nseq, int64_t heads, int64_t dim, int64_t dstate, int64_t max_seqlen) {
     constexpr int64_t kSms = 152;
     constexpr int64_t kCutCost = 15;

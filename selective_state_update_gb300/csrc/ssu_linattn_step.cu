@@ -17,8 +17,14 @@
 // not by registers.  Eight lanes share a row, each taking the 16-byte pieces lane,
 // lane + 8, ... of it: a quarter of a warp touches 128 contiguous bytes.
 //
-// 256 sequences x 32 heads of 128 x 128 fp32 states: 174 us, 6.2 TB/s, 0.92 of the
+// 256 sequences x 32 heads of 128 x 128 fp32 states: 173 us, 6.3 TB/s, 0.92 of the
 // copy rate (plain loads and stores by registers, 96 KB in flight an SM: 194 us).
+// Other heads (dim x dstate) with states of 0.5 GB: fp32 64 x 64, 64 x 128, 128 x 64,
+// 112 x 112 and 120 x 128 0.93 to 0.95, 80 x 96 and 96 x 80 0.90, 72 x 96 0.82, 32 x 32
+// 0.36; bf16 128 x 128 and 64 x 128 0.80, 120 x 128 0.76, 112 x 112 0.62, 64 x 64 and
+// 128 x 64 0.56, 80 x 96, 96 x 80 and 72 x 96 0.38 to 0.43, 32 x 32 0.17.  A unit costs
+// the same however few bytes its rows have, and a dim that is no multiple of 64 has a
+// unit of few rows.
 #include "ssu_device.cuh"
 #include "ssu_hybrid.h"
 

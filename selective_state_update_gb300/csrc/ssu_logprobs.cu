@@ -19,8 +19,8 @@
 // HBM-bound: every logit is read once.  A row is split over the CTAs of a
 // cluster when there are few rows, and the parts are joined through
 // distributed shared memory, so a call is one launch without a workspace.
-// 4096 x 131072 bf16 with 20 alternatives: 188 us, 5.7 TB/s, 0.84 of the copy rate;
-// without alternatives 168 us.  A row's end (sums, search) leaves its CTA's loads
+// 4096 x 131072 bf16 with 20 alternatives: 187 us, 5.7 TB/s, 0.85 of the copy rate;
+// without alternatives 166 us.  A row's end (sums, search) leaves its CTA's loads
 // idle, so CTAs are small and many: of 512 threads, three an SM, four vectors in
 // flight a thread it took 208 us, of 256 threads, six an SM 192, four an SM with
 // eight vectors 188.
