@@ -121,3 +121,29 @@ def test_prefill_fp16_later_keys_leave_earlier_outputs(libssu, late):
         kk[at] = late
         got = ssu.ssu_linear_attention_prefill(pool.clone(), q, kk, v, g, cu, scale=1.0)
         assert torch.equal(got[:at], want[:at])
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [0, 63, 128, 249])
+def test_prefill_queries_and_keys_that_are_no_numbers(libssu, at, poison, io):
+    """In q they stay in their token's outputs of that head, in k they reach no earlier token."""
+    pool, q, k, v, g = problem(250 + at, 250, 4, 2, 72, 40, io, torch.float32, 1)
+    cu = torch.tensor([0, 250], dtype=torch.int32, device=DEV)
+    first = pool.clone()
+    want = ssu.ssu_linear_attention_prefill(pool, q, k, v, g, cu)
+    bad_q, bad_k = q.clone(), k.clone()
+    bad_q[at, 1, 7] = poison
+    bad_k[at, 1, 7] = poison
+    state = first.clone()
+    got = ssu.ssu_linear_attention_prefill(state, bad_q, k, v, g, cu)
+    assert not torch.isfinite(got[at, 1].float()).any()
+    got[at, 1] = want[at, 1]
+    assert torch.equal(got, want) and torch.equal(state, pool)
+    state = first.clone()
+    got = ssu.ssu_linear_attention_prefill(state, q, bad_k, v, g, cu)
+    assert torch.equal(got[:at], want[:at]) and torch.equal(got[:, :2], want[:, :2])
+    assert not torch.isfinite(got[at:, 2:].float()).any()
+    assert torch.equal(state[:, :2], pool[:, :2])
+    columns = [n for n in range(40) if n != 7]
+    assert torch.equal(state[..., columns], pool[..., columns]) and not torch.isfinite(state[:, 2:, :, 7]).any()
