@@ -589,14 +589,101 @@ typedef struct ssu_logprob_args {
 ssu_status ssu_token_logprobs(const ssu_logprob_args *args, void *stream);
 
 /*
+ * A paged cache of keys and values, for the softmax-attention layers of a
+ * hybrid stack: `pages` pages of `page_size` tokens, [pages, page_size,
+ * kv_heads, dim] of fp16 or bf16 each for keys and values.
+ *
+ * The two calls share their description of a batch.  Sequence b holds
+ * kv_lens[b] tokens in the cache, of which the last n = cu_seqlens[b+1] -
+ * cu_seqlens[b] are the call's new ones, rows cu_seqlens[b] .. of q, k and v
+ * (without cu_seqlens: one each, row b; rows == nseq).  Its new token i has
+ * position kv_lens[b] - n + i, and the token at position j lies in page
+ * block_table[b, j / page_size], row j % page_size.  Entries behind a
+ * sequence's last page are not read, nor, with a window, those before its
+ * first one.  kv_lens may be smaller than n (a padded batch has 0): tokens at
+ * negative positions are not in the cache and see nothing.
+ *
+ * page_size is a multiple of 8 and dim one in [8, 128] (others return
+ * SSU_ERR_UNSUPPORTED), heads a multiple of kv_heads, at most 128 of them on
+ * one.  The caches, q, k, v and out may be slices of larger tensors (the two
+ * caches interleaved, heads before rows): strides are in elements, multiples
+ * of 8, and positive along the caches' extents above one; the innermost is one
+ * and all pointers are 16-byte aligned.  Offsets are 64-bit throughout.
+ *
+ * Device-side: cu_seqlens that decrease, are negative or pass `rows`, and
+ * kv_lens outside [0, table_width * page_size] (or above 2^30) set
+ * SSU_DEV_BAD_SEQLEN; nothing of such a sequence is written.  A page outside
+ * [0, pages) sets SSU_DEV_BAD_SLOT: append does not store its tokens,
+ * attention takes its keys and values for zeros.  Rows of no sequence are left
+ * as they are.  Both calls may be captured without a prewarm.
+ */
+typedef struct ssu_paged_args {
+    int64_t pages, page_size, heads, kv_heads, dim;
+    int64_t rows, nseq;
+    int32_t io_dtype;             /* SSU_F16 or SSU_BF16: the caches, q, k, v, out             */
+    int32_t table_type;           /* ssu_itype of block_table                                  */
+    int32_t meta_type;            /* ssu_itype of kv_lens and cu_seqlens                       */
+    int32_t reserved0;            /* must be 0                                                 */
+    void *k_cache, *v_cache;      /* device; read only by the attention                        */
+    int64_t k_cache_stride[3], v_cache_stride[3];  /* page, row, head                          */
+    const void *block_table;      /* device [nseq, table_width]                                */
+    int64_t table_stride, table_width;  /* elements from one sequence's entries to the next's  */
+    const void *kv_lens;          /* device [nseq]                                             */
+    const void *cu_seqlens;       /* device [nseq + 1] or NULL                                 */
+    const void *q;                /* device [rows, heads, dim]; append: or NULL                */
+    void *out;                    /* device [rows, heads, dim]; append: the turned q           */
+    int64_t q_stride[2], out_stride[2];
+    int32_t *d_status;            /* device int32 or NULL; SSU_DEV_* bits are ORed in          */
+} ssu_paged_args;
+
+/*
+ * Append the new tokens' keys k and values v, [rows, kv_heads, dim], to the
+ * cache, keys (and, where q is given, queries: q to out, which may be q itself)
+ * turned by their position.  The first `rotary` elements of a head are pairs
+ * (x, y) -- elements (j, j + rotary / 2), or (2 j, 2 j + 1) if `interleaved` --
+ * turned by the angle position * inv_freq[j] (device fp32 [rotary / 2]):
+ *     x' = x cos - y sin,   y' = y cos + x sin
+ * in fp32, rounded once; the angle is formed in fp64.  rotary is a multiple of
+ * 16, at most dim; 0 (inv_freq NULL) turns nothing.  Where two tokens of a call
+ * share a place in the cache, either may end up there.  One kernel launch;
+ * rows == 0 launches nothing.
+ */
+ssu_status ssu_paged_append(const ssu_paged_args *args, const void *k, const int64_t *k_stride, const void *v,
+                            const int64_t *v_stride, const float *inv_freq, int64_t rotary, int32_t interleaved,
+                            void *stream);
+
+/*
+ * Attention of the new tokens over the cache, their own keys and values among
+ * it: the token at position i sees the keys j <= i, with window > 0 only
+ * those j > i - window, and
+ *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j e^(scale q . k_j)
+ * (lse: device fp32 [rows, heads] or NULL).  A token that sees no key has out 0
+ * and lse -inf.  Scores, maxima and sums are fp32; e^(score - maximum) is rounded
+ * once to the io type where it meets v, which costs out as much as one more
+ * rounding of v.  scale is positive.  An infinity or a NaN in a key or a value
+ * reaches the tokens that see it and no other.
+ *
+ * `max_seqlen` and `max_kv_len` are the largest n and kv_len if the caller
+ * knows them, 0 if not.  They steer how the work is split over the GPU and
+ * never the result's validity.  `workspace` is caller-owned device memory of at
+ * least ssu_paged_attention_workspace_size() bytes for the same arguments,
+ * 256-byte aligned; its contents need no initialisation, and two calls that may
+ * run at once need one each.
+ */
+ssu_status ssu_paged_attention_workspace_size(const ssu_paged_args *args, int64_t max_seqlen, int64_t max_kv_len,
+                                              uint64_t *bytes);
+ssu_status ssu_paged_attention(const ssu_paged_args *args, float scale, int64_t window, int64_t max_seqlen,
+                               int64_t max_kv_len, float *lse, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/*
  * Get the kernel for one configuration ready before any CUDA graph capture:
  * checks that the configuration is supported, loads the kernel's module on
  * the current device and caches its launch attributes.  MATE "Mamba / SSU",
  * Graph capture and prewarm_selective_state_update (kernels there are
  * compiled at first use; here they are compiled ahead of time, so this only
  * loads them).  `packed` selects the packed kernel instead of the one-token
- * kernel.  Linear attention, the norm and the log probabilities need none of
- * this.  Returns SSU_ERR_UNSUPPORTED for a dstate or dtype the kernels do
+ * kernel.  Linear attention, the norm, the log probabilities and the paged
+ * cache's calls need none of this.  Returns SSU_ERR_UNSUPPORTED for a dstate or dtype the kernels do
  * not cover.
  */
 ssu_status ssu_prewarm(int32_t state_dtype, int32_t io_dtype, int32_t dt_dtype,

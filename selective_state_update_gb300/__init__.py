@@ -26,6 +26,10 @@ Entry points (same names as the C ABI):
   ssu_add_rmsnorm      RMS norm with the residual's addition, E4M3 output
   ssu_token_logprobs   log probabilities of given tokens, entropy and top
                        alternatives
+  ssu_paged_append, ssu_paged_attention
+                       the softmax-attention layers of a hybrid stack: keys
+                       and values into a paged cache, rotated on the way, and
+                       attention of new tokens over it
 and ``selective_state_update``, the MATE/FlashInfer-shaped call (MATE
 documentation, page "Mamba / SSU", API reference) that picks one of the two
 update entry points from the call shape.
@@ -46,6 +50,7 @@ __all__ = ["ssu_update_onetoken", "ssu_selftest_timeout", "ssu_update_packed", "
            "slot_copies", "ssu_prewarm",
            "selective_state_update",
            "ssu_linear_attention_step", "ssu_linear_attention_prefill", "ssu_add_rmsnorm", "ssu_token_logprobs",
+           "ssu_paged_append", "ssu_paged_attention",
            "SLOTS_STRIDED", "SLOTS_PER_ROW", "DEV_BAD_SLOT", "DEV_BAD_ENTRY", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
            "library_path", "lib"]
 
@@ -200,6 +205,7 @@ def lib():
                                   ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]
         L.ssu_prewarm.restype = ctypes.c_int
         hybrid.bind(L)
+        paged.bind(L)
         L.ssu_last_error.argtypes = []
         L.ssu_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -768,3 +774,5 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, 
 from . import hybrid  # noqa: E402  (needs the helpers above)
 from .hybrid import (ssu_add_rmsnorm, ssu_linear_attention_prefill, ssu_linear_attention_step,  # noqa: E402
                      ssu_token_logprobs)
+from . import paged  # noqa: E402
+from .paged import ssu_paged_append, ssu_paged_attention  # noqa: E402

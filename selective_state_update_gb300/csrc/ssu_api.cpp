@@ -9,6 +9,7 @@
 
 #include "ssu_hybrid.h"
 #include "ssu_internal.h"
+#include "ssu_paged.h"
 #include "ssu_ssd_params.h"
 #include "ssu_verify.h"
 
@@ -703,6 +704,152 @@ ssu_status ssu_token_logprobs(const ssu_logprob_args *a, void *stream) {
     p.top_ids = a->top_ids, p.top_logprob = a->top_logprobs;
     p.status = a->d_status;
     return launched(ssu::launch_logprobs(p, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks shared by the calls on a paged cache; fills `c`.
+static ssu_status paged_prepare(const ssu_paged_args *a, ssu::PagedParams *c) {
+    if (a == nullptr) return fail(SSU_ERR_INVALID, "args is NULL");
+    if (a->reserved0 != 0) return fail(SSU_ERR_INVALID, "reserved0 must be 0");
+    if (!valid_dtype(a->io_dtype)) return fail(SSU_ERR_INVALID, "io_dtype %d is not an ssu_dtype", a->io_dtype);
+    if (a->io_dtype == SSU_F32) return fail(SSU_ERR_UNSUPPORTED, "a paged cache holds fp16 or bf16");
+    if (!valid_itype(a->table_type)) return fail(SSU_ERR_INVALID, "table_type %d is not an ssu_itype", a->table_type);
+    if (!valid_itype(a->meta_type)) return fail(SSU_ERR_INVALID, "meta_type %d is not an ssu_itype", a->meta_type);
+    if (a->rows < 0 || a->nseq < 0) return fail(SSU_ERR_INVALID, "rows and nseq must not be negative");
+    if (a->pages <= 0 || a->pages > kMaxGrid) return fail(SSU_ERR_INVALID, "pages must be positive and below 2^31");
+    if (a->page_size <= 0) return fail(SSU_ERR_INVALID, "page_size must be positive");
+    if (a->page_size % 8 != 0 || a->page_size > (1 << 20))
+        return fail(SSU_ERR_UNSUPPORTED, "page_size %lld is not supported (multiples of 8 up to 2^20)", (long long)a->page_size);
+    if (a->heads <= 0 || a->kv_heads <= 0 || a->heads % a->kv_heads != 0)
+        return fail(SSU_ERR_INVALID, "heads (%lld) must be a positive multiple of kv_heads (%lld)", (long long)a->heads,
+                    (long long)a->kv_heads);
+    if (a->heads > 65535) return fail(SSU_ERR_INVALID, "more than 65535 heads");
+    if (a->heads / a->kv_heads > ssu::kPagedMaxShare)
+        return fail(SSU_ERR_UNSUPPORTED, "more than %d heads share a key/value head", ssu::kPagedMaxShare);
+    if (a->dim < 8 || a->dim > ssu::kPagedMaxDim || a->dim % 8 != 0)
+        return fail(SSU_ERR_UNSUPPORTED, "dim %lld is not supported (multiples of 8 from 8 to %d)", (long long)a->dim,
+                    ssu::kPagedMaxDim);
+    if (a->rows >= kMaxGrid || a->nseq >= kMaxGrid) return fail(SSU_ERR_INVALID, "more than 2^31-1 rows or sequences");
+    if (a->cu_seqlens == nullptr && a->rows != a->nseq)
+        return fail(SSU_ERR_INVALID, "without cu_seqlens every sequence has one row (rows %lld, nseq %lld)", (long long)a->rows,
+                    (long long)a->nseq);
+    if (a->table_width < 0 || a->table_stride < 0) return fail(SSU_ERR_INVALID, "table_width and table_stride must not be negative");
+    if (!a->k_cache || !a->v_cache) return fail(SSU_ERR_INVALID, "k_cache and v_cache must not be NULL");
+    if (a->k_cache == a->v_cache) return fail(SSU_ERR_INVALID, "k_cache and v_cache must not be the same");
+    if (!aligned16(a->k_cache) || !aligned16(a->v_cache)) return fail(SSU_ERR_INVALID, "the caches must be 16-byte aligned");
+    if (!aligned16(a->q) || !aligned16(a->out)) return fail(SSU_ERR_INVALID, "q and out must be 16-byte aligned");
+    const int64_t extents[3] = {a->pages, a->page_size, a->kv_heads};
+    for (int i = 0; i < 3; ++i)
+        for (const int64_t s : {a->k_cache_stride[i], a->v_cache_stride[i]}) {
+            if (extents[i] == 1) continue;
+            if (s <= 0 || s % 8 != 0) return fail(SSU_ERR_INVALID, "the caches' strides must be positive multiples of 8");
+            if (s >= (int64_t(1) << 39)) return fail(SSU_ERR_INVALID, "a stride of the caches is too large");
+        }
+    for (int i = 0; i < 2; ++i)
+        if (a->q_stride[i] < 0 || a->out_stride[i] < 0 || a->q_stride[i] % 8 || a->out_stride[i] % 8)
+            return fail(SSU_ERR_INVALID, "the strides of q and out must be multiples of 8 and not negative");
+    if (!aligned(a->d_status, 4)) return fail(SSU_ERR_INVALID, "d_status must be 4-byte aligned");
+    if (a->nseq > 0) {
+        if (!a->kv_lens) return fail(SSU_ERR_INVALID, "kv_lens must not be NULL");
+        if (a->table_width > 0 && !a->block_table) return fail(SSU_ERR_INVALID, "block_table must not be NULL");
+        if (!aligned(a->kv_lens, itype_size(a->meta_type)) || !aligned(a->cu_seqlens, itype_size(a->meta_type)) ||
+            !aligned(a->block_table, itype_size(a->table_type)))
+            return fail(SSU_ERR_INVALID, "kv_lens, cu_seqlens and block_table must be aligned to their type");
+    }
+    std::memset(c, 0, sizeof *c);
+    c->pages = a->pages, c->rows = a->rows, c->nseq = a->nseq;
+    c->page = static_cast<int32_t>(a->page_size);
+    c->H = static_cast<int32_t>(a->heads), c->G = static_cast<int32_t>(a->kv_heads), c->share = c->H / c->G;
+    c->D = static_cast<int32_t>(a->dim);
+    c->io_dtype = a->io_dtype;
+    c->table_is_i64 = a->table_type == SSU_I64, c->meta_is_i64 = a->meta_type == SSU_I64;
+    c->k_cache = a->k_cache, c->v_cache = a->v_cache;
+    for (int i = 0; i < 3; ++i) c->ks[i] = a->k_cache_stride[i], c->vs[i] = a->v_cache_stride[i];
+    c->table = a->block_table, c->table_stride = a->table_stride, c->table_width = a->table_width;
+    c->kv_lens = a->kv_lens, c->cu = a->cu_seqlens;
+    c->q = a->q, c->out = a->out;
+    for (int i = 0; i < 2; ++i) c->qs[i] = a->q_stride[i], c->os[i] = a->out_stride[i];
+    c->status = a->d_status;
+    return SSU_OK;
+}
+
+ssu_status ssu_paged_append(const ssu_paged_args *args, const void *k, const int64_t *k_stride, const void *v,
+                            const int64_t *v_stride, const float *inv_freq, int64_t rotary, int32_t interleaved,
+                            void *stream) {
+    ssu::AppendParams p{};
+    ssu_status st = paged_prepare(args, &p.c);
+    if (st != SSU_OK) return st;
+    if (rotary < 0 || rotary > args->dim) return fail(SSU_ERR_INVALID, "rotary must be in [0, dim]");
+    if (rotary % 16 != 0) return fail(SSU_ERR_UNSUPPORTED, "rotary %lld is not supported (multiples of 16)", (long long)rotary);
+    if ((rotary > 0) != (inv_freq != nullptr)) return fail(SSU_ERR_INVALID, "inv_freq and a positive rotary go together");
+    if (!aligned(inv_freq, 4)) return fail(SSU_ERR_INVALID, "inv_freq must be 4-byte aligned");
+    if ((args->q == nullptr) != (args->out == nullptr)) return fail(SSU_ERR_INVALID, "q and out go together");
+    if (args->out == args->q && args->q &&
+        (args->q_stride[0] != args->out_stride[0] || args->q_stride[1] != args->out_stride[1]))
+        return fail(SSU_ERR_INVALID, "q turned in place keeps its strides");
+    if (args->rows == 0 || args->nseq == 0) return ok();
+    if (!k || !v || !k_stride || !v_stride) return fail(SSU_ERR_INVALID, "k, v and their strides must not be NULL");
+    if (!aligned16(k) || !aligned16(v)) return fail(SSU_ERR_INVALID, "k and v must be 16-byte aligned");
+    for (int i = 0; i < 2; ++i) {
+        if (k_stride[i] < 0 || v_stride[i] < 0 || k_stride[i] % 8 || v_stride[i] % 8)
+            return fail(SSU_ERR_INVALID, "the strides of k and v must be multiples of 8 and not negative");
+        p.kstr[i] = k_stride[i], p.vstr[i] = v_stride[i];
+    }
+    for (const void *q : {k, v, args->q})
+        if (q == args->k_cache || q == args->v_cache) return fail(SSU_ERR_INVALID, "k, v and q must not alias the caches");
+    if (args->out && (args->out == k || args->out == v || args->out == args->k_cache || args->out == args->v_cache))
+        return fail(SSU_ERR_INVALID, "out must not alias k, v or the caches");
+    p.k = k, p.v = v;
+    p.inv_freq = inv_freq;
+    p.rotary = static_cast<int32_t>(rotary);
+    p.interleaved = interleaved != 0;
+    if ((st = check_device(args->k_cache, "k_cache")) != SSU_OK) return st;
+    return launched(ssu::launch_paged_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks of the attention's own arguments; fills `p` but for lse.
+static ssu_status attend_prepare(const ssu_paged_args *args, float scale, int64_t window, int64_t max_seqlen,
+                                 int64_t max_kv_len, ssu::AttendParams *p) {
+    const ssu_status st = paged_prepare(args, &p->c);
+    if (st != SSU_OK) return st;
+    if (!(scale > 0.f) || !(scale <= 3.402823466e38f)) return fail(SSU_ERR_INVALID, "scale must be positive and finite");
+    if (window < 0) return fail(SSU_ERR_INVALID, "window must not be negative");
+    if (max_seqlen < 0 || max_kv_len < 0) return fail(SSU_ERR_INVALID, "max_seqlen and max_kv_len must not be negative");
+    p->scale = scale;
+    // (a window longer than any sequence is none)
+    p->window = window > ssu::kPagedMaxLen ? 0 : static_cast<int32_t>(window);
+    p->lse = nullptr;
+    return SSU_OK;
+}
+
+ssu_status ssu_paged_attention_workspace_size(const ssu_paged_args *args, int64_t max_seqlen, int64_t max_kv_len,
+                                              uint64_t *bytes) {
+    if (!bytes) return fail(SSU_ERR_INVALID, "bytes is NULL");
+    ssu::AttendParams p{};
+    const ssu_status st = attend_prepare(args, 1.f, 0, max_seqlen, max_kv_len, &p);
+    if (st != SSU_OK) return st;
+    *bytes = p.c.rows == 0 || p.c.nseq == 0 ? 0 : ssu::attend_plan(p, max_seqlen, max_kv_len).bytes;
+    return ok();
+}
+
+ssu_status ssu_paged_attention(const ssu_paged_args *args, float scale, int64_t window, int64_t max_seqlen,
+                               int64_t max_kv_len, float *lse, void *workspace, uint64_t workspace_bytes, void *stream) {
+    ssu::AttendParams p{};
+    ssu_status st = attend_prepare(args, scale, window, max_seqlen, max_kv_len, &p);
+    if (st != SSU_OK) return st;
+    if (p.c.rows == 0 || p.c.nseq == 0) return ok();
+    if (!args->q || !args->out) return fail(SSU_ERR_INVALID, "q and out must not be NULL");
+    if (args->out == args->q || args->out == args->k_cache || args->out == args->v_cache)
+        return fail(SSU_ERR_INVALID, "out must not alias an input");
+    if (!aligned(lse, 4)) return fail(SSU_ERR_INVALID, "lse must be 4-byte aligned");
+    const ssu::AttendPlan plan = ssu::attend_plan(p, max_seqlen, max_kv_len);
+    if (plan.bytes > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+        return fail(SSU_ERR_INVALID, "workspace must be a 256-byte aligned device pointer");
+    if (workspace_bytes < plan.bytes)
+        return fail(SSU_ERR_INVALID, "workspace of %llu bytes is smaller than the %llu needed",
+                    (unsigned long long)workspace_bytes, (unsigned long long)plan.bytes);
+    p.lse = lse;
+    if ((st = check_device(args->k_cache, "k_cache")) != SSU_OK) return st;
+    return launched(ssu::launch_paged_attention(p, plan, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 ssu_status ssu_prewarm(int32_t state_dtype, int32_t io_dtype, int32_t dt_dtype, int64_t heads, int64_t dim,

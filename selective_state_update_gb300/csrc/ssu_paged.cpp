@@ -1,0 +1,70 @@
+// ssu_paged.cpp -- host side of the paged cache's kernels: how a call is
+// computed, tensor maps, device properties.
+#include "ssu_paged.h"
+
+#include "ssu.h"
+
+namespace ssu {
+
+namespace {
+
+// The driver's tensor-map encoder, looked up once.
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+}  // namespace
+
+bool encode_cache(CUtensorMap *m, const PagedParams &p, const void *base, const int64_t *stride, int box) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.G), static_cast<cuuint64_t>(p.page),
+                                static_cast<cuuint64_t>(p.pages)};
+    // [head, row, page]; a stride along an extent of one is never used: keep it legal
+    const int64_t at[3] = {p.G > 1 ? stride[2] : p.D, stride[1], p.pages > 1 ? stride[0] : p.D};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(at[i]) * 2;
+    const cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, unit[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = p.io_dtype == SSU_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(m, type, 4, const_cast<void *>(base), dims, strides, boxes, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int device_sms() {
+    static int cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int *const kept = dev >= 0 && dev < 64 ? &cache[dev] : nullptr;
+    int n = kept ? __atomic_load_n(kept, __ATOMIC_RELAXED) : 0;
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        if (kept) __atomic_store_n(kept, n, __ATOMIC_RELAXED);
+    }
+    return n;
+}
+
+AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv_len) {
+    (void)max_kv_len;
+    AttendPlan a{};
+    int64_t longest = p.c.cu == nullptr ? 1 : max_seqlen > 0 ? max_seqlen : (p.c.rows + p.c.nseq - 1) / p.c.nseq;
+    a.kind = longest * p.c.share <= 16 ? kAttendRows16 : kAttendRows32;
+    a.bytes = attend_rows_workspace(a.kind, p.c.D);
+    return a;
+}
+
+cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream) {
+    return launch_attend_rows(p, plan.kind, workspace, stream);
+}
+
+}  // namespace ssu

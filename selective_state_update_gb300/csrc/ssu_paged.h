@@ -1,0 +1,67 @@
+// ssu_paged.h -- parameters shared by the host layer and the kernels of the
+// paged key / value cache: appending to it and attention over it.  Not part of
+// the public ABI (that is include/ssu.h).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace ssu {
+
+// Sequence b has the rows [cu[b], cu[b + 1]) (row b without cu) of the new
+// tokens, the last ones of its kv_lens[b] tokens; key j of it lies in page
+// table[b][j / page], row j % page.  Strides are in elements, the innermost is
+// one: [page, row, head] of the caches, [row, head] of q and out.
+struct PagedParams {
+    int64_t pages, rows, nseq;
+    int32_t page;              // tokens of a page
+    int32_t H, G, share, D;    // heads, key/value heads, heads / key/value heads, head size
+    int32_t io_dtype;
+    int32_t table_is_i64, meta_is_i64;
+    void *k_cache, *v_cache;
+    int64_t ks[3], vs[3];
+    const void *table;
+    int64_t table_stride, table_width;
+    const void *kv_lens, *cu;
+    const void *q;
+    void *out;
+    int64_t qs[2], os[2];
+    int32_t *status;
+};
+constexpr int kPagedMaxDim = 128;      // largest head size
+constexpr int kPagedMaxShare = 128;    // most heads on one key/value head
+constexpr int64_t kPagedMaxLen = 1 << 30;  // longest sequence
+
+struct AppendParams {
+    PagedParams c;  // q -> out (rotated), or out == nullptr: no q
+    const void *k, *v;
+    int64_t kstr[2], vstr[2];
+    const float *inv_freq;  // nullptr: no rotation
+    int32_t rotary, interleaved;
+};
+cudaError_t launch_paged_append(const AppendParams &p, cudaStream_t stream);
+
+struct AttendParams {
+    PagedParams c;
+    float scale;       // positive
+    int32_t window;    // 0: all earlier keys
+    float *lse;        // [rows, H] or nullptr
+};
+// How a call is computed, and the workspace it needs for that.
+struct AttendPlan {
+    int32_t kind;      // kAttendRows*, kAttendTiles
+    uint64_t bytes;
+};
+enum : int32_t { kAttendRows16 = 0, kAttendRows32 = 1 };
+AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv_len);
+cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream);
+cudaError_t launch_attend_rows(const AttendParams &p, int kind, void *workspace, cudaStream_t stream);
+uint64_t attend_rows_workspace(int kind, int D);
+
+// The tensor maps of a cache: boxes of `box` tokens of one head by 64 elements.
+bool encode_cache(CUtensorMap *m, const PagedParams &p, const void *base, const int64_t *stride, int box);
+int device_sms();
+
+}  // namespace ssu

@@ -1,0 +1,657 @@
+// ssu_paged_rows.cu -- attention over the paged cache for few query rows: single
+// tokens and drafts.
+//
+// A tile is 16 or 32 query rows of one sequence that share a key/value head --
+// row m of the sequence is token m / share, head m % share of the group -- and
+// 64 keys.  One pass over the keys with a running maximum and sum:
+//     x_j = scale log2(e) q . k_j,  m' = max(m, x_j),
+//     l' = l 2^(m - m') + sum_j 2^(x_j - m'),  o' = o 2^(m - m') + sum_j 2^(x_j - m') v_j
+// and out = o / l, lse = (m + log2 l) ln 2, all of it in fp32; P = 2^(x - m') is
+// rounded once to the io type, as the product's operand.
+//
+// Bound by HBM: a key and its value are 4 D bytes and 4 D share operations.  So
+// what counts is that every SM reads all the time, whatever the lengths: all
+// (sequence, row tile, head, key tile) of the call are numbered in this order
+// and every CTA takes an equal share of the numbers, cut anywhere.  A CTA that
+// has a whole run of one row tile's keys stores its outputs; where the run is
+// cut, (o, l, m) go to the workspace and a second kernel joins the parts, always
+// in the order of the keys.  Every CTA finds its share from the metadata by
+// itself, in one block-wide sum: no plan, no counters, nothing to be cleared.
+//
+// One warp has the pages copied into a ring of stages by the TMA engine; four
+// warps take 16 keys of a stage each (mma.sync 16 x 8 x 16: the products are
+// far from the bound, and a quarter of a 128-row tcgen05 tile would be used).
+#include "ssu_paged.cuh"
+#include "ssu_tcgen05.cuh"
+
+namespace ssu {
+
+namespace {
+
+constexpr int kKeys = 64;             // keys of a stage
+constexpr int kPanel = kKeys * 128;   // bytes of 64 elements of its keys
+constexpr int kWarps = 4;             // consumers
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kCtas = 2;              // per SM
+
+template <int DK, int MT>
+struct Layout {
+    static constexpr int kPanels = DK / 64;
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kStageBytes = 2 * kPanels * kPanel;
+    static constexpr int kStages = DK == 64 ? 6 : 3;
+    static constexpr int kQ = kStages * kStageBytes;                 // [kRows][DK], 16-byte pieces swapped by row
+    static constexpr int kSlice = 32 / MT;                           // columns joined at a time
+    static constexpr int kJoin = kQ;                                 // [kWarps][kRows][kSlice] fp32, once the queries are done with
+    static constexpr int kJoinBytes = kWarps * kRows * kSlice * 4;
+    static constexpr int kML = kQ + (kRows * DK * 2 > kJoinBytes ? kRows * DK * 2 : kJoinBytes);  // [kWarps][kRows][2]
+    static constexpr int kBar = kML + kWarps * kRows * 8;
+    static constexpr int kMisc = kBar + 16 * kStages;
+    static constexpr int kBytes = kMisc + 128;
+    static constexpr int kPart = kRows * (DK + 2);                   // floats of a part in the workspace: o, l, m
+    static_assert(kBytes <= (227 * 1024) / kCtas - 1024, "shared memory");
+};
+
+// What the second kernel has to know of a CTA's first run: the row tile that it
+// continues (b < 0: none) and whether it is the tile's last.
+struct Joint {
+    int32_t b, g, tile, last;
+};
+
+__device__ __forceinline__ int row_tiles(const PagedParams &p, const Seq &s, int rows) {
+    return static_cast<int>((static_cast<int64_t>(s.n) * p.share + rows - 1) / rows);
+}
+
+// A row tile's keys.
+struct Range {
+    int pos_lo, pos_hi;  // positions of its first and last token
+    int lo, end;         // keys that any of its rows sees: [lo, end)
+    int first, count;    // key tiles; one at least
+};
+__device__ __forceinline__ Range range_of(const AttendParams &p, const Seq &s, int tile, int rows) {
+    Range r;
+    const int64_t m0 = static_cast<int64_t>(tile) * rows, all = static_cast<int64_t>(s.n) * p.c.share;
+    const int64_t m1 = min(m0 + rows, all) - 1;
+    r.pos_lo = s.kv - s.n + static_cast<int>(m0 / p.c.share);
+    r.pos_hi = s.kv - s.n + static_cast<int>(m1 / p.c.share);
+    r.end = max(r.pos_hi + 1, 0);
+    r.lo = p.window > 0 ? max(r.pos_lo - p.window + 1, 0) : 0;
+    if (r.lo > r.end) r.lo = r.end;
+    r.first = r.lo / kKeys;
+    r.count = max((r.end + kKeys - 1) / kKeys - r.first, 1);
+    return r;
+}
+// Key tiles of all row tiles of a sequence, for one head.
+__device__ __forceinline__ int64_t tiles_of(const AttendParams &p, const Seq &s, int rows) {
+    int64_t sum = 0;
+    const int n = row_tiles(p.c, s, rows);
+    for (int t = 0; t < n; ++t) sum += range_of(p, s, t, rows).count;
+    return sum;
+}
+
+// A CTA's share: where it begins, and how many key tiles it has.
+struct Share {
+    int64_t left;
+    int32_t b, g, tile, at;  // sequence, head, row tile, key tile of it
+};
+
+// The share's runs, one row tile after the other.
+struct Walk {
+    Share w;
+    Seq s;
+    int tiles;
+    Range r;
+    __device__ __forceinline__ void start(const AttendParams &p, const Share &share, int rows) {
+        w = share;
+        if (w.left <= 0) return;
+        s = load_seq(p.c, w.b, false);
+        tiles = row_tiles(p.c, s, rows);
+        r = range_of(p, s, w.tile, rows);
+    }
+    __device__ __forceinline__ bool more() const { return w.left > 0; }
+    // key tiles [at, at + run()) of the row tile
+    __device__ __forceinline__ int run() const { return static_cast<int>(min(static_cast<int64_t>(r.count - w.at), w.left)); }
+    __device__ __forceinline__ void next(const AttendParams &p, int rows) {
+        w.left -= run();
+        w.at = 0;
+        if (w.left <= 0) return;
+        if (++w.g == p.c.G) {
+            w.g = 0;
+            if (++w.tile >= tiles) {
+                w.tile = 0;
+                do {  // (the share ends within a sequence that has rows, unless the lengths changed meanwhile)
+                    if (++w.b >= p.c.nseq) {
+                        w.left = 0;
+                        return;
+                    }
+                    s = load_seq(p.c, w.b, false);
+                } while (s.n == 0);
+                tiles = row_tiles(p.c, s, rows);
+            }
+            r = range_of(p, s, w.tile, rows);
+        }
+    }
+};
+
+// This CTA's share, by all of its threads; `sums` holds one number per warp.
+__device__ __forceinline__ void find_share(const AttendParams &p, int rows, int64_t *sums, Share *out) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t per = (p.c.nseq + kThreads - 1) / kThreads;
+    const int64_t b0 = min(tid * per, p.c.nseq), b1 = min(b0 + per, p.c.nseq);
+    int64_t mine = 0;
+    for (int64_t b = b0; b < b1; ++b) mine += tiles_of(p, load_seq(p.c, b, blockIdx.x == 0), rows) * p.c.G;
+    int64_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+    }
+    if (lane == 31) sums[warp] = upto;
+    if (tid == 0) out->left = 0;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps + 1; ++w) {
+        if (w == warp) before = total;
+        total += sums[w];
+    }
+    const int64_t from = before + upto - mine;
+    // no share is empty but those of the last CTAs, where there are fewer key tiles than CTAs
+    const int64_t n = min(total, static_cast<int64_t>(gridDim.x)), c = blockIdx.x;
+    const auto start = [&](int64_t i) { return total / n * i + total % n * i / n; };
+    if (c >= n) return;
+    const int64_t w0 = start(c), w1 = start(c + 1);
+    if (w0 >= from && w0 < from + mine) {
+        int64_t at = w0 - from;
+        for (int64_t b = b0; b < b1; ++b) {
+            const Seq s = load_seq(p.c, b, false);
+            const int tiles = row_tiles(p.c, s, rows);
+            for (int t = 0; t < tiles; ++t) {
+                const int count = range_of(p, s, t, rows).count;
+                const int64_t all = static_cast<int64_t>(count) * p.c.G;
+                if (at < all) {
+                    out->b = static_cast<int32_t>(b);
+                    out->tile = t;
+                    out->g = static_cast<int32_t>(at / count);
+                    out->at = static_cast<int32_t>(at % count);
+                    out->left = w1 - w0;
+                    b = b1;
+                    break;
+                }
+                at -= all;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t saddr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+template <bool BF>
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, const uint32_t *b) {
+    if constexpr (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (BF) {
+        return pack_bf16x2(a, b);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <bool BF>
+__device__ __forceinline__ float value_of(unsigned short u) {
+    return bits_to_float(u, BF ? kBF16 : kF16);
+}
+// Where element `dim` of key `row` lies in a stage's panels.
+__device__ __forceinline__ uint32_t place(int row, int dim) {
+    return (dim >> 6) * kPanel + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) * 16);
+}
+
+struct Caches {
+    CUtensorMap k, v;
+};
+
+// What a row's outputs become: o / l, zeros where the row sees nothing.
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
+
+// Four columns of one row's outputs.
+template <bool BF>
+__device__ __forceinline__ void store_out(const AttendParams &p, const Seq &s, int g, int64_t m, int dim, const float *o, int n) {
+    if (dim >= p.c.D) return;
+    const int64_t row = s.t0 + m / p.c.share;
+    const int h = g * p.c.share + static_cast<int>(m % p.c.share);
+    unsigned short *out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1] + dim;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+        if (i < n) *reinterpret_cast<uint32_t *>(out + i) = pack2<BF>(o[i], o[i + 1]);
+}
+__device__ __forceinline__ void store_lse(const AttendParams &p, const Seq &s, int g, int64_t m, float lse) {
+    if (p.lse) p.lse[(s.t0 + m / p.c.share) * p.c.H + g * p.c.share + m % p.c.share] = lse;
+}
+
+// DK: the head size, rounded up to 64; MT: row tiles of 16; BF: bf16.
+template <int DK, int MT, bool BF>
+__global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const AttendParams p, const __grid_constant__ Caches maps,
+                                                                      int box, Joint *joints, float *parts) {
+    using LY = Layout<DK, MT>;
+    constexpr int R = LY::kRows;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    uint64_t *const full = reinterpret_cast<uint64_t *>(smem + LY::kBar), *const empty = full + LY::kStages;
+    Share *const share = reinterpret_cast<Share *>(smem + LY::kMisc);
+    int *const abort_flag = reinterpret_cast<int *>(smem + LY::kMisc + 32), *const odd_flag = abort_flag + 1;
+    int64_t *const sums = reinterpret_cast<int64_t *>(smem + LY::kMisc + 48);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        *abort_flag = 0;
+        *odd_flag = 0;
+        for (int i = 0; i < LY::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kWarps);
+    }
+    find_share(p, R, sums, share);  // (its barriers order the set-up too)
+    Walk walk;
+    walk.start(p, *share, R);
+    if (tid == 0) {
+        Joint j{-1, 0, 0, 0};
+        if (walk.more() && walk.w.at > 0) j = {walk.w.b, walk.w.g, walk.w.tile, walk.w.at + walk.run() == walk.r.count};
+        joints[blockIdx.x] = j;
+    }
+    bool ok = true;
+    if (warp == kWarps) {
+        // ---------------- copies: a lane each box ----------------
+        const int boxes = kKeys / box, copies = 2 * LY::kPanels * boxes;
+        const int which = lane % boxes, panel = lane / boxes % LY::kPanels;
+        const bool value = lane >= LY::kPanels * boxes;
+        int it = 0;
+        const auto page_at = [&](const Walk &w, int i) {
+            // the page of this lane's box of key tile i, past the last page (where the copies read zeros) for one that no row sees
+            const int token = (w.r.first + i) * kKeys + which * box;
+            int64_t page = -1;
+            if (lane < copies && token < w.r.end && token + box > w.r.lo) page = page_of(p.c, w.w.b, token);
+            return static_cast<int>(page < 0 ? p.c.pages : page);
+        };
+        int page = walk.more() ? page_at(walk, walk.w.at) : 0;
+        while (ok && walk.more()) {
+            const int from = walk.w.at, to = from + walk.run(), first = walk.r.first, g = walk.w.g;
+            for (int i = from; i < to; ++i, ++it) {
+                const int s = it % LY::kStages, here = page;
+                const int token = (first + i) * kKeys + which * box;
+                if (i + 1 < to) {
+                    page = page_at(walk, i + 1);
+                } else {
+                    walk.next(p, R);
+                    if (walk.more()) page = page_at(walk, walk.w.at);
+                }
+                if (it >= LY::kStages) ok = mbar_wait_bounded(&empty[s], (it / LY::kStages - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok && !*reinterpret_cast<volatile int *>(abort_flag));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect(&full[s], LY::kStageBytes);
+                __syncwarp();
+                if (lane < copies)
+                    tma_load_4d(smem + s * LY::kStageBytes + (value ? LY::kPanels * kPanel : 0) + panel * kPanel + which * box * 128,
+                                value ? &maps.v : &maps.k, 64 * panel, g, token % p.c.page, here, &full[s]);
+            }
+        }
+        if (!ok) {
+            if (lane == 0) flag(p.c.status, kDevTimeout);
+            *abort_flag = 1;
+        }
+        // what was asked for has landed before the CTA retires
+        if (lane == 0)
+            for (int k = max(it - LY::kStages, 0); k < it; ++k) mbar_wait_bounded(&full[k % LY::kStages], (k / LY::kStages) & 1);
+        __syncwarp();
+        return;
+    }
+
+    // ---------------- consumers: warp w has keys 16 w ... of a stage ----------------
+    const uint32_t s0 = smem_addr(smem);
+    float *const join = reinterpret_cast<float *>(smem + LY::kJoin);
+    float2 *const ml = reinterpret_cast<float2 *>(smem + LY::kML);
+    const float scale = p.scale * 1.4426950408889634f;
+    int it = 0;
+    bool first_run = true;
+    for (; ok && walk.more(); walk.next(p, R), first_run = false) {
+        const Seq s = walk.s;
+        const Range r = walk.r;
+        const int g = walk.w.g, from = walk.w.at, to = from + walk.run();
+        const int64_t m0 = static_cast<int64_t>(walk.w.tile) * R;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * p.c.share - m0));
+        // the queries
+        for (int i = tid; i < R * DK / 8; i += 32 * kWarps) {
+            const int row = i / (DK / 8), piece = i % (DK / 8);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (row < rows && 8 * piece < p.c.D) {
+                const int64_t m = m0 + row;
+                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p.c.q) + (s.t0 + m / p.c.share) * p.c.qs[0] +
+                                                          (g * p.c.share + m % p.c.share) * p.c.qs[1] + 8 * piece));
+            }
+            *reinterpret_cast<uint4 *>(smem + LY::kQ + row * DK * 2 + ((piece ^ (row & 7)) * 16)) = v;
+        }
+        named_barrier(1, 32 * kWarps);
+        uint32_t q[MT == 1 ? DK / 16 : 1][4];
+        const auto load_q = [&](int mt, int k, uint32_t *a) {
+            const int row = 16 * mt + (lane & 15), piece = 2 * k + (lane >> 4);
+            ldmatrix_x4(s0 + LY::kQ + row * DK * 2 + ((piece ^ (row & 7)) * 16), a);
+        };
+        if constexpr (MT == 1)
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) load_q(0, k, q[k]);
+        // this thread's rows: lane / 4 and lane / 4 + 8 of each 16
+        int hi[MT][2], lo[MT][2];  // they see keys [lo, hi)
+        float mx[MT][2], sum[MT][2], o[MT][DK / 8][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = min(16 * mt + 8 * h + lane / 4, rows - 1);
+                const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
+                hi[mt][h] = pos + 1;
+                lo[mt][h] = p.window > 0 ? pos + 1 - p.window : 0;
+                mx[mt][h] = -INFINITY;
+                sum[mt][h] = 0.f;
+            }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
+
+        for (int i = from; i < to; ++i, ++it) {
+            const int st = it % LY::kStages;
+            ok = mbar_wait_bounded(&full[st], (it / LY::kStages) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t sk = s0 + st * LY::kStageBytes, sv = sk + LY::kPanels * kPanel;
+            const int key0 = (r.first + i) * kKeys, mine = key0 + 16 * warp;
+            // all rows see all of the tile?
+            const bool masked = key0 + kKeys > r.pos_lo + 1 || (p.window > 0 && key0 < r.pos_hi + 1 - p.window);
+            float x[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[mt][n][j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
+                uint32_t b[4];
+                ldmatrix_x4(sk + place(16 * warp + (lane & 7) + ((lane >> 4) << 3), 16 * k + ((lane >> 3) & 1) * 8), b);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t a[4];
+                    if constexpr (MT > 1) load_q(mt, k, a);
+                    mma16816<BF>(x[mt][0], MT == 1 ? q[k] : a, b);
+                    mma16816<BF>(x[mt][1], MT == 1 ? q[k] : a, b + 2);
+                }
+            }
+            if (masked) {
+                // Values that some row does not see must not reach it by a zero
+                // of P: what no row sees becomes zeros, and so do infinities
+                // and NaN, which are added to the rows that see them at the end.
+                unsigned char *const values = smem + st * LY::kStageBytes + LY::kPanels * kPanel;
+                const bool partly = r.pos_lo != r.pos_hi;
+                bool odd = false;
+                for (int e = lane; e < 16 * (DK / 8); e += 32) {
+                    const int row = e / (DK / 8), key = mine + row;
+                    uint4 *const v = reinterpret_cast<uint4 *>(values + place(16 * warp + row, 8 * (e % (DK / 8))));
+                    if (key >= r.end || key < r.lo) {
+                        *v = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (partly && any_odd<BF>(*v)) {
+                        odd = true;
+                        *v = without_odd<BF>(*v);
+                    }
+                }
+                if (odd) *odd_flag = 1;
+                fence_proxy_async_smem();  // before the stage's next copy
+                __syncwarp();
+            }
+            // P and the running maximum and sum
+            uint32_t pa[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float e[4] = {x[mt][0][2 * h] * scale, x[mt][0][2 * h + 1] * scale, x[mt][1][2 * h] * scale,
+                                  x[mt][1][2 * h + 1] * scale};
+                    if (masked)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = mine + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+                            if (key >= hi[mt][h] || key < lo[mt][h]) e[j] = -INFINITY;
+                        }
+                    float top = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top = fmaxf(top, mx[mt][h]);
+                    const float base = top == -INFINITY ? 0.f : top, back = ex2(mx[mt][h] - base);
+                    mx[mt][h] = top;
+                    float add = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e[j] = ex2(e[j] - base);
+                        add += e[j];
+                    }
+                    sum[mt][h] = sum[mt][h] * back + add;
+                    if (back != 1.f)
+#pragma unroll
+                        for (int n = 0; n < DK / 8; ++n) o[mt][n][2 * h] *= back, o[mt][n][2 * h + 1] *= back;
+                    pa[mt][h] = pack2<BF>(e[0], e[1]);
+                    pa[mt][2 + h] = pack2<BF>(e[2], e[3]);
+                }
+#pragma unroll
+            for (int n = 0; n < DK / 16; ++n) {
+                uint32_t b[4];
+                ldmatrix_x4_t(sv + place(16 * warp + (lane & 15), 16 * n + ((lane >> 4) << 3)), b);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma16816<BF>(o[mt][2 * n], pa[mt], b);
+                    mma16816<BF>(o[mt][2 * n + 1], pa[mt], b + 2);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        ok = !barrier_or(1, 32 * kWarps, !ok);
+        if (!ok) break;
+
+        // ---------------- the warps' parts joined ----------------
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float t = sum[mt][h];
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
+                t += __shfl_xor_sync(0xffffffffu, t, 2);
+                if ((lane & 3) == 0) ml[warp * R + 16 * mt + 8 * h + lane / 4] = make_float2(mx[mt][h], t);
+            }
+        named_barrier(1, 32 * kWarps);
+        const auto top_of = [&](int row) {
+            float m = ml[row].x;
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, ml[w * R + row].x);
+            return m;
+        };
+        const bool whole = from == 0 && to == r.count, odd = *odd_flag != 0;
+        // (the part of a cut run: a continuation is its CTA's first run, another its last)
+        float *const part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (from > 0 ? 0 : 1)) * LY::kPart;
+        float down[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float m = top_of(16 * mt + 8 * h + lane / 4);
+                down[mt][h] = mx[mt][h] == -INFINITY ? 0.f : ex2(mx[mt][h] - m);
+            }
+        // a thread takes kWide columns of one row of each slice
+        constexpr int kWide = R * LY::kSlice / (32 * kWarps), kAcross = LY::kSlice / kWide;
+        static_assert(kWide == 4, "a thread's columns");
+        const int row = tid / kAcross, col = tid % kAcross * kWide;
+        const float m = top_of(row);
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 f = ml[w * R + row];
+            l += f.y * (f.x == -INFINITY ? 0.f : ex2(f.x - m));  // (a sum without a maximum is 0 or NaN)
+        }
+        const int pos = s.kv - s.n + static_cast<int>((m0 + min(row, rows - 1)) / p.c.share);
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int c = 0; c < DK; c += LY::kSlice) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = c / 8; n < (c + LY::kSlice) / 8; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2 *>(&join[(warp * R + 16 * mt + 8 * h + lane / 4) * LY::kSlice + 8 * n - c + 2 * (lane & 3)]) =
+                            make_float2(o[mt][n][2 * h] * down[mt][h], o[mt][n][2 * h + 1] * down[mt][h]);
+            named_barrier(1, 32 * kWarps);
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 f = *reinterpret_cast<const float4 *>(&join[(w * R + row) * LY::kSlice + col]);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+            }
+            named_barrier(1, 32 * kWarps);
+            if (__builtin_expect(odd, 0) && row < rows && c + col < p.c.D) {
+                // infinities and NaN that were left out, of the keys this row sees in the run
+                const int k0 = max((r.first + from) * kKeys, p.window > 0 ? pos + 1 - p.window : 0);
+                const int k1 = min((r.first + to) * kKeys, pos + 1);
+                for (int key = max(k0, 0); key < k1; ++key) {
+                    const int tile0 = key / kKeys * kKeys;
+                    if (!(tile0 + kKeys > r.pos_lo + 1 || (p.window > 0 && tile0 < r.pos_hi + 1 - p.window))) continue;
+                    const int64_t page = page_of(p.c, walk.w.b, key);
+                    if (page < 0) continue;
+                    const unsigned short *at = static_cast<const unsigned short *>(p.c.v_cache) + page * p.c.vs[0] +
+                                               (key % p.c.page) * p.c.vs[1] + g * p.c.vs[2] + c + col;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float f = value_of<BF>(__ldg(at + k));
+                        if (!(fabsf(f) <= 3.402823466e38f)) v[k] += f;
+                    }
+                }
+            }
+            if (whole) {
+                if (row < rows) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = pos < 0 ? 0.f : v[k] * inv;
+                    store_out<BF>(p, s, g, m0 + row, c + col, v, 4);
+                }
+            } else {
+                *reinterpret_cast<float4 *>(&part[row * DK + c + col]) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        if (tid % kAcross == 0) {
+            if (!whole) part[R * DK + row] = l, part[R * DK + R + row] = m;
+            else if (row < rows) store_lse(p, s, g, m0 + row, pos < 0 ? -INFINITY : lse_of(m, l));
+        }
+        named_barrier(1, 32 * kWarps);
+        if (odd && tid == 0) *odd_flag = 0;  // (read again after the next run's first barrier)
+    }
+    if (!ok) {
+        if (lane == 0) flag(p.c.status, kDevTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// CTA c joins the parts of the row tile that CTA c's share begins within, if it
+// is the first that does: the end of share c - 1, the beginnings of c, c + 1, ...
+template <int DK, int MT, bool BF>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p, int ctas, const Joint *joints, const float *parts) {
+    using LY = Layout<DK, MT>;
+    constexpr int R = LY::kRows;
+    const int c = blockIdx.x + 1;
+    const Joint j = joints[c];
+    if (j.b < 0) return;
+    const Joint before = joints[c - 1];
+    // (share c - 1 lies within the same tile: an earlier CTA joins it)
+    if (before.b == j.b && before.g == j.g && before.tile == j.tile && !before.last) return;
+    int last = c;
+    while (last + 1 < ctas && !joints[last].last) ++last;
+    const Seq s = load_seq(p.c, j.b, false);
+    const int64_t m0 = static_cast<int64_t>(j.tile) * R;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * p.c.share - m0));
+    const auto part = [&](int i) { return parts + (i < c ? 2 * static_cast<int64_t>(c - 1) + 1 : 2 * static_cast<int64_t>(i)) * LY::kPart; };
+    for (int e = threadIdx.x; e < rows * (DK / 4); e += 128) {
+        const int row = e / (DK / 4), dim = e % (DK / 4) * 4;
+        const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
+        float m = -INFINITY;
+        for (int i = c - 1; i <= last; ++i) m = fmaxf(m, part(i)[R * DK + R + row]);
+        float l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = c - 1; i <= last; ++i) {
+            const float *q = part(i);
+            const float top = q[R * DK + R + row], f = top == -INFINITY ? 0.f : ex2(top - m);
+            l += q[R * DK + row] * f;
+            const float4 o = *reinterpret_cast<const float4 *>(&q[row * DK + dim]);
+            v[0] += o.x * f, v[1] += o.y * f, v[2] += o.z * f, v[3] += o.w * f;
+        }
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = pos < 0 ? 0.f : v[k] * inv;
+        store_out<BF>(p, s, j.g, m0 + row, dim, v, 4);
+        if (dim == 0) store_lse(p, s, j.g, m0 + row, pos < 0 ? -INFINITY : lse_of(m, l));
+    }
+}
+
+int rows_grid() {
+    constexpr int kSms = 152;  // not the device's count: the workspace's size and the launch have to agree on it
+    return kCtas * kSms;
+}
+
+template <int DK, int MT, bool BF>
+cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream) {
+    using LY = Layout<DK, MT>;
+    cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<DK, MT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes);
+    if (e != cudaSuccess) return e;
+    int box = kKeys;
+    while (p.c.page % box != 0) box /= 2;
+    Caches maps;
+    if (!encode_cache(&maps.k, p.c, p.c.k_cache, p.c.ks, box) || !encode_cache(&maps.v, p.c, p.c.v_cache, p.c.vs, box))
+        return cudaErrorInvalidValue;
+    const int grid = rows_grid();
+    Joint *joints = static_cast<Joint *>(workspace);
+    float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + (grid * sizeof(Joint) + 255) / 256 * 256);
+    attend_rows_kernel<DK, MT, BF><<<grid, kThreads, LY::kBytes, stream>>>(p, maps, box, joints, parts);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    attend_join_kernel<DK, MT, BF><<<grid - 1, 128, 0, stream>>>(p, grid, joints, parts);
+    return cudaGetLastError();
+}
+template <int DK, int MT>
+cudaError_t launch_m(const AttendParams &p, void *workspace, cudaStream_t stream) {
+    return p.c.io_dtype == kBF16 ? launch_t<DK, MT, true>(p, workspace, stream) : launch_t<DK, MT, false>(p, workspace, stream);
+}
+
+}  // namespace
+
+uint64_t attend_rows_workspace(int kind, int D) {
+    const uint64_t rows = kind == kAttendRows16 ? 16 : 32, dk = D <= 64 ? 64 : 128;
+    return (rows_grid() * sizeof(Joint) + 255) / 256 * 256 + 2 * rows_grid() * rows * (dk + 2) * sizeof(float);
+}
+
+cudaError_t launch_attend_rows(const AttendParams &p, int kind, void *workspace, cudaStream_t stream) {
+    if (p.c.D <= 64)
+        return kind == kAttendRows16 ? launch_m<64, 1>(p, workspace, stream) : launch_m<64, 2>(p, workspace, stream);
+    return kind == kAttendRows16 ? launch_m<128, 1>(p, workspace, stream) : launch_m<128, 2>(p, workspace, stream);
+}
+
+}  // namespace ssu

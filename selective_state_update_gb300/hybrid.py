@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import _DTYPE, _ITYPE, _raise, _stream, _stream_object, _table, OK, SLOTS_STRIDED, SlotTable, lib
+from . import _DTYPE, _I64x3, _ITYPE, _raise, _stream, _stream_object, _table, OK, SLOTS_STRIDED, SlotTable, lib
 
 _I64x2 = ctypes.c_int64 * 2
 
@@ -60,7 +60,8 @@ class LogprobArgs(ctypes.Structure):
 def _packer(cls) -> struct.Struct:
     """The C layout of a ctypes structure for one struct.pack call: filling the
     structure field by field costs more than some of the kernels take."""
-    code = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "Q", _I64x2: "2q"}
+    code = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "Q", _I64x2: "2q",
+            _I64x3: "3q"}
     return struct.Struct("@" + "".join(code[f[1]] for f in cls._fields_))
 
 
