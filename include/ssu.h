@@ -607,8 +607,9 @@ ssu_status ssu_token_logprobs(const ssu_logprob_args *args, void *stream);
  * SSU_ERR_UNSUPPORTED), heads a multiple of kv_heads, at most 128 of them on
  * one.  The caches, q, k, v and out may be slices of larger tensors (the two
  * caches interleaved, heads before rows): strides are in elements, multiples
- * of 8, and positive along the caches' extents above one; the innermost is one
- * and all pointers are 16-byte aligned.  Offsets are 64-bit throughout.
+ * of 8, and positive (those of k and v may be 0) along extents above one; the
+ * innermost is one and all pointers are 16-byte aligned.  Offsets are 64-bit
+ * throughout.
  *
  * Device-side: cu_seqlens that decrease, are negative or pass `rows`, and
  * kv_lens outside [0, table_width * page_size] (or above 2^30) set

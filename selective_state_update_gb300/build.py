@@ -27,7 +27,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-Wall", "-I", I
 SOURCES = ["ssu_api.cpp", "ssu_onetoken.cu", "ssu_packed.cu", "ssu_packed_long.cu", "ssu_replay_f32.cu", "ssu_replay_f16.cu",
            "ssu_replay_bf16.cu", "ssu_copy.cu", "ssu_shadow.cu", "ssu_ssd.cu", "ssu_ssd_tc.cu", "ssu_verify.cu",
            "ssu_linattn_step.cu", "ssu_linattn_prefill.cu", "ssu_norm.cu", "ssu_logprobs.cu", "ssu_paged.cpp", "ssu_paged_append.cu",
-           "ssu_paged_rows.cu"]
+           "ssu_paged_rows.cu", "ssu_paged_tiles.cu"]
 HEADERS = ["ssu_internal.h", "ssu_device.cuh", "ssu_replay.cuh", "ssu_ssd_params.h", "ssu_verify.h", "ssu_hybrid.h",
            "ssu_tcgen05.cuh", "ssu_paged.h", "ssu_paged.cuh"]
 

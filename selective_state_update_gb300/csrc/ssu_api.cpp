@@ -729,6 +729,8 @@ static ssu_status paged_prepare(const ssu_paged_args *a, ssu::PagedParams *c) {
         return fail(SSU_ERR_UNSUPPORTED, "dim %lld is not supported (multiples of 8 from 8 to %d)", (long long)a->dim,
                     ssu::kPagedMaxDim);
     if (a->rows >= kMaxGrid || a->nseq >= kMaxGrid) return fail(SSU_ERR_INVALID, "more than 2^31-1 rows or sequences");
+    if (a->rows + a->nseq > (kMaxGrid - (1 << 20)) / a->kv_heads)
+        return fail(SSU_ERR_INVALID, "too many rows, sequences and heads for one call");
     if (a->cu_seqlens == nullptr && a->rows != a->nseq)
         return fail(SSU_ERR_INVALID, "without cu_seqlens every sequence has one row (rows %lld, nseq %lld)", (long long)a->rows,
                     (long long)a->nseq);
@@ -744,9 +746,11 @@ static ssu_status paged_prepare(const ssu_paged_args *a, ssu::PagedParams *c) {
             if (s <= 0 || s % 8 != 0) return fail(SSU_ERR_INVALID, "the caches' strides must be positive multiples of 8");
             if (s >= (int64_t(1) << 39)) return fail(SSU_ERR_INVALID, "a stride of the caches is too large");
         }
+    const int64_t across[2] = {a->rows, a->heads};
     for (int i = 0; i < 2; ++i)
-        if (a->q_stride[i] < 0 || a->out_stride[i] < 0 || a->q_stride[i] % 8 || a->out_stride[i] % 8)
-            return fail(SSU_ERR_INVALID, "the strides of q and out must be multiples of 8 and not negative");
+        for (const int64_t s : {a->q ? a->q_stride[i] : 8, a->out ? a->out_stride[i] : 8})
+            if (across[i] > 1 && (s <= 0 || s % 8 != 0 || s >= (int64_t(1) << 39)))
+                return fail(SSU_ERR_INVALID, "the strides of q and out must be positive multiples of 8");
     if (!aligned(a->d_status, 4)) return fail(SSU_ERR_INVALID, "d_status must be 4-byte aligned");
     if (a->nseq > 0) {
         if (!a->kv_lens) return fail(SSU_ERR_INVALID, "kv_lens must not be NULL");
@@ -790,7 +794,7 @@ ssu_status ssu_paged_append(const ssu_paged_args *args, const void *k, const int
     if (!k || !v || !k_stride || !v_stride) return fail(SSU_ERR_INVALID, "k, v and their strides must not be NULL");
     if (!aligned16(k) || !aligned16(v)) return fail(SSU_ERR_INVALID, "k and v must be 16-byte aligned");
     for (int i = 0; i < 2; ++i) {
-        if (k_stride[i] < 0 || v_stride[i] < 0 || k_stride[i] % 8 || v_stride[i] % 8)
+        if ((i == 0 ? args->rows : args->kv_heads) > 1 && (k_stride[i] < 0 || v_stride[i] < 0 || k_stride[i] % 8 || v_stride[i] % 8))
             return fail(SSU_ERR_INVALID, "the strides of k and v must be multiples of 8 and not negative");
         p.kstr[i] = k_stride[i], p.vstr[i] = v_stride[i];
     }

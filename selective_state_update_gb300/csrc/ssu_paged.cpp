@@ -41,6 +41,18 @@ bool encode_cache(CUtensorMap *m, const PagedParams &p, const void *base, const 
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_queries(CUtensorMap *m, const PagedParams &p, int tokens) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.rows)};
+    const int64_t hs = p.H > 1 ? p.qs[1] : p.D, ts = p.rows > 1 ? p.qs[0] : p.D;
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(ts) * 2};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(p.share), static_cast<cuuint32_t>(tokens)}, unit[3] = {1, 1, 1};
+    const CUtensorMapDataType type = p.io_dtype == SSU_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(m, type, 3, const_cast<void *>(p.q), dims, strides, boxes, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_sms() {
     static int cache[64];
     int dev = 0;
@@ -58,12 +70,13 @@ AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv
     (void)max_kv_len;
     AttendPlan a{};
     int64_t longest = p.c.cu == nullptr ? 1 : max_seqlen > 0 ? max_seqlen : (p.c.rows + p.c.nseq - 1) / p.c.nseq;
-    a.kind = longest * p.c.share <= 16 ? kAttendRows16 : kAttendRows32;
-    a.bytes = attend_rows_workspace(a.kind, p.c.D);
+    a.kind = longest * p.c.share <= 16 ? kAttendRows16 : longest * p.c.share <= 32 ? kAttendRows32 : kAttendTiles;
+    a.bytes = a.kind == kAttendTiles ? attend_tiles_workspace(p.c) : attend_rows_workspace(a.kind, p.c.D);
     return a;
 }
 
 cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream) {
+    if (plan.kind == kAttendTiles) return launch_attend_tiles(p, workspace, stream);
     return launch_attend_rows(p, plan.kind, workspace, stream);
 }
 

@@ -54,14 +54,18 @@ struct AttendPlan {
     int32_t kind;      // kAttendRows*, kAttendTiles
     uint64_t bytes;
 };
-enum : int32_t { kAttendRows16 = 0, kAttendRows32 = 1 };
+enum : int32_t { kAttendRows16 = 0, kAttendRows32 = 1, kAttendTiles = 2 };
 AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv_len);
 cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream);
 cudaError_t launch_attend_rows(const AttendParams &p, int kind, void *workspace, cudaStream_t stream);
 uint64_t attend_rows_workspace(int kind, int D);
+cudaError_t launch_attend_tiles(const AttendParams &p, void *workspace, cudaStream_t stream);
+uint64_t attend_tiles_workspace(const PagedParams &c);
 
 // The tensor maps of a cache: boxes of `box` tokens of one head by 64 elements.
 bool encode_cache(CUtensorMap *m, const PagedParams &p, const void *base, const int64_t *stride, int box);
+// ... and of the queries: boxes of `tokens` tokens by the heads of a group by 64 elements.
+bool encode_queries(CUtensorMap *m, const PagedParams &p, int tokens);
 int device_sms();
 
 }  // namespace ssu

@@ -1,0 +1,929 @@
+// ssu_paged_tiles.cu -- attention over the paged cache on the 5th-generation
+// tensor cores: chunks of prompts, and batches that hold some.
+//
+// A work unit is up to 2 x 128 query rows of one sequence and key/value head --
+// tile A and tile B, each floor(128 / share) tokens by `share` heads, the head
+// fastest -- over the 128-key tiles that its rows see.  One pass over the keys
+// with a running reference m and sum l, in units of log2:
+//     x_j = scale log2(e) q . k_j,   P_j = 2^(x_j - m),   l += sum P_j,   O += P V
+// and out = O / l, lse = (m + log2 l) ln 2.  m is the row's maximum when it was last
+// moved; it moves when the maximum has grown by more than 2^8, so that O, in
+// tensor memory, is rarely rescaled (P stays below 2^8, far inside both io types,
+// and l and O are fp32).  P is rounded once to the io type, as its product's operand.
+//
+// A plan kernel checks the metadata, lists the units and, where they are too few
+// or too uneven for the GPU, cuts their keys into parts; the main kernel's CTAs
+// take the list in turn.  Parts leave (O, l, m) in the workspace, and the CTA that
+// completes a unit's last part joins them in the order of the keys.
+//
+// Two products a key tile and query tile, fp32 accumulators in tensor memory:
+//     S = Q K^T  (both from shared memory, as copied),  O += P V  (P where S was)
+// Warps, in groups of four:
+//   0-3, 4-7  (thread = row of tile A, B) S -> P, O rescaled, outputs;
+//   8         issues the products;   9  finds the units and copies pages;
+//   10-11     look through the values of partly visible tiles (below).
+#include <type_traits>
+
+#include "ssu_paged.cuh"
+#include "ssu_tcgen05.cuh"
+
+namespace ssu {
+
+namespace {
+
+constexpr int kRows = 128;     // rows of a query tile
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kPanel = 16384;  // 128 rows of 128 bytes
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.f;  // log2 by which the maximum may grow before the reference moves
+
+// A part of a unit's keys, as planned.
+struct Piece {
+    int64_t row0;         // first row of the sequence's new tokens
+    int32_t b, n, kv;     // sequence, its new tokens, its tokens in the cache
+    int32_t pair;         // tokens [pair, pair + 1) * 2 * (128 / share) of it
+    int32_t first, last;  // key tiles
+    int32_t part, parts;  // of the unit's parts, which
+    int32_t slot, count;  // workspace: first part's place, the unit's counter (where parts > 1)
+};
+struct PlanHead {
+    int32_t pieces, cut, next;  // number of pieces; are there parts; the next one to be taken
+};
+struct Plan {
+    PlanHead *head;
+    Piece *units, *pieces;  // whole units; parts, where some are cut
+    int32_t *counters;      // [cut units][G][2]
+    float *parts;           // [slots][G][2][kRows][DK + 2]
+    int32_t max_units, max_slots;  // what there is room for: units; parts of cut units (a head)
+};
+
+// What the groups need to know of a piece.
+struct Work {
+    int64_t row[2];            // first row of tile A, B
+    int32_t b, g;
+    int32_t toks[2], pos[2];   // tokens, position of the first
+    int32_t from[2], to[2];    // key tiles
+    int32_t first, last;       // of either; last < 0: no more work
+    int32_t part, parts, slot, count;
+};
+
+__device__ __forceinline__ int tile_tokens(const PagedParams &p) { return kRows / p.share; }
+
+// Key tiles that tokens at positions [pos, pos + toks) see.
+__device__ __forceinline__ void key_tiles(const AttendParams &p, int pos, int toks, int &from, int &to) {
+    const int end = max(pos + toks, 0);
+    const int lo = p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
+    from = lo / kKeys;
+    to = toks > 0 && end > lo ? (end + kKeys - 1) / kKeys : from;
+}
+// Does every row of the tile see all of key tile j?
+__device__ __forceinline__ bool sees_all(int window, int pos, int toks, int j) {
+    return (j + 1) * kKeys <= pos + 1 && (window == 0 || j * kKeys >= pos + toks - window);
+}
+__device__ __forceinline__ bool partly_seen(const Work &w, int window, int j) {
+    bool some = false;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        some = some || (j >= w.from[x] && j < w.to[x] && !sees_all(window, w.pos[x], w.toks[x], j));
+    return some;
+}
+
+// ---------------------------------------------------------------------------
+// The plan: one CTA.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxParts = 16;
+
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[lane];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+// Sum of the threads before this one; `total` of all.
+__device__ __forceinline__ int block_scan(int v, int *red, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int upto = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = upto;
+    __syncthreads();
+    int w = red[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, w, off);
+        if (lane >= off) w += o;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return upto - v + (warp > 0 ? before : 0);
+}
+
+// Key tiles of a pair of tiles.
+__device__ __forceinline__ void pair_tiles(const AttendParams &p, const Seq &s, int pair, int &first, int &last) {
+    const int tt = tile_tokens(p.c), t0 = pair * 2 * tt, pos = s.kv - s.n + t0;
+    int f[2], l[2];
+    key_tiles(p, pos, min(tt, s.n - t0), f[0], l[0]);
+    key_tiles(p, pos + tt, max(min(tt, s.n - t0 - tt), 0), f[1], l[1]);
+    first = f[0], last = l[0];
+    if (l[1] > f[1]) {
+        if (last == first) first = f[1];
+        last = l[1];
+    }
+}
+
+__device__ __forceinline__ int block_max(int v, int *red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, red[lane]);
+}
+__device__ __forceinline__ int parts_of(const Piece &u, int len) { return max((u.last - u.first + len - 1) / len, 1); }
+
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p, const Plan plan, int ctas) {
+    __shared__ int64_t red64[32];
+    __shared__ int red[32], bounds[kPlanThreads + 1];
+    const int tid = threadIdx.x, tt2 = 2 * tile_tokens(p.c);
+    const auto pairs_of = [&](const Seq &s) { return (s.n + tt2 - 1) / tt2; };
+    // The units, in the order of the sequences, the last tokens of each first.
+    int64_t sum = 0;  // all key tiles, and one a unit
+    int most = 0;     // the longest unit's
+    int units = 0;
+    for (int64_t b0 = 0; b0 < p.c.nseq; b0 += kPlanThreads) {
+        Seq s{0, 0, 0};
+        if (b0 + tid < p.c.nseq) s = load_seq(p.c, b0 + tid, true);
+        int total;
+        const int before = block_scan(pairs_of(s), red, total);
+        bounds[tid] = before;
+        __syncthreads();
+        for (int i = tid; i < total; i += kPlanThreads) {
+            int lo = 0, hi = kPlanThreads;  // the sequence: bounds[lo] <= i, the last such
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (bounds[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const Seq q = load_seq(p.c, b0 + lo, false);
+            Piece u{};
+            u.row0 = q.t0, u.b = static_cast<int32_t>(b0 + lo), u.n = q.n, u.kv = q.kv;
+            u.pair = pairs_of(q) - 1 - (i - bounds[lo]);
+            u.parts = 1;
+            pair_tiles(p, q, u.pair, u.first, u.last);
+            if (units + i < plan.max_units) plan.units[units + i] = u;
+            sum += u.last - u.first + 1;
+            most = max(most, u.last - u.first);
+        }
+        units = min(units + total, plan.max_units);  // (more only where sequences overlap)
+        __syncthreads();
+    }
+    sum = block_sum(sum, red64) * p.c.G;
+    most = static_cast<int>(block_max(most, red));
+
+    // The longest part: the longest unit or a fraction of it.  Where the pieces
+    // are few the CTAs take them in rounds, else the time is the even share and
+    // about half a piece; a piece costs a tile of its own, a part kPartCost.
+    constexpr int kPartCost = 3;
+    int best = max(most, 1);
+    int64_t best_time = INT64_MAX;
+    for (int parts = 1; parts <= kMaxParts; ++parts) {
+        const int len = (most + parts - 1) / parts;
+        if (parts > 1 && (len < 4 || sum / ctas >= 4 * most)) break;
+        int64_t n = units, cut = 0;
+        if (parts > 1) {
+            n = 0;
+            for (int u = tid; u < units; u += kPlanThreads) {
+                const int c = parts_of(plan.units[u], len);
+                n += c;
+                cut += c > 1 ? c : 0;
+            }
+            n = block_sum(n, red64);
+            cut = block_sum(cut, red64);
+            if (cut > plan.max_slots) break;
+        }
+        n *= p.c.G;
+        const int64_t cost = parts > 1 ? kPartCost : 1;
+        const int64_t time = n <= 2 * ctas ? (n + ctas - 1) / ctas * (len + cost)
+                                           : min((n + ctas - 1) / ctas * (len + cost), sum / ctas + (cost - 1) * n / ctas + (len + 1) / 2);
+        if (time < best_time) best_time = time, best = max(len, 1);
+    }
+    if (best >= most) {
+        if (tid == 0) plan.head->pieces = units, plan.head->cut = 0, plan.head->next = ctas;
+        return;
+    }
+    // The pieces: all first parts, all second ones, ... so that CTAs that are at work at the same time read the same keys.
+    int pieces = 0;
+    for (int part = 0;; ++part) {
+        int slots = 0, cuts = 0;
+        const int begun = pieces;
+        for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
+            Piece q{};
+            int c = 0;
+            if (u0 + tid < units) {
+                q = plan.units[u0 + tid];
+                c = parts_of(q, best);
+            }
+            int t0, t1, t2;
+            const int at = block_scan(c > part, red, t0), slot = block_scan(c > 1 ? c : 0, red, t1), cut = block_scan(c > 1, red, t2);
+            if (c > part) {
+                const int f = q.first, l = q.last;
+                q.first = f + static_cast<int>(static_cast<int64_t>(l - f) * part / c);
+                q.last = f + static_cast<int>(static_cast<int64_t>(l - f) * (part + 1) / c);
+                q.part = part, q.parts = c, q.slot = slots + slot, q.count = cuts + cut;
+                plan.pieces[pieces + at] = q;
+                if (part == 0 && c > 1)
+                    for (int i = 0; i < 2 * p.c.G; ++i) plan.counters[static_cast<int64_t>(q.count) * 2 * p.c.G + i] = 0;
+            }
+            pieces += t0, slots += t1, cuts += t2;
+        }
+        if (pieces == begun) break;
+    }
+    if (tid == 0) plan.head->pieces = pieces, plan.head->cut = 1, plan.head->next = ctas;
+}
+
+// ---------------------------------------------------------------------------
+// The attention.
+// ---------------------------------------------------------------------------
+enum : int {
+    kQFull0, kQFull1, kQFree0, kQFree1,      // a tile's queries have landed, are done with
+    kUnitFull0, kUnitFull1, kUnitFree0, kUnitFree1,
+    kSFull0, kSFull1,                        // scores of tile A, B are there
+    kPFull0, kPFull1,                        // ... and have become P
+    kOFull0, kOFull1,                        // P has been added to O
+    kSync0, kSync1,                          // among the warps of a group
+    kFinal,
+    kRing,                                   // a buffer is full; then: is empty; then: its values are looked through
+};
+constexpr uint32_t kColS = 0, kColO = 256;   // tensor memory: S (then P) of A, B; O of A, B
+constexpr int kReaders = 11;                 // warps that read a piece of work
+constexpr int kWorks = 4;  // pieces of work kept: one is written when every warp has begun the one two before it, so a
+                           // warp finds its own in place until it begins the next but one
+
+template <int DK>
+struct Layout {
+    static constexpr int kPanels = DK / 64;
+    static constexpr int kTile = kPanels * kPanel;        // 128 queries, keys or values
+    static constexpr int kBufs = DK == 64 ? 10 : 5;
+    static constexpr int kBuf = 2 * kTile;                // after the queries of A and B
+    static constexpr int kBars = kBuf + kBufs * kTile;
+    static constexpr int kWork = kBars + 8 * (kRing + 3 * kBufs);
+    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort, is_last[2], odd[kWorks][2]
+    static constexpr int kBytes = kMisc + 48;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (BF) {
+        return pack_bf16x2(a, b);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Infinities and NaN that were taken out of partly visible tiles, of the keys
+// this row sees, added to what the row has stored (once one is added, the sum is
+// no number that rounding could change).
+template <bool BF, typename T>
+__device__ __noinline__ void add_odd(const AttendParams &p, const Work &w, int x, int pos, T *row) {
+    const int lo = p.window > 0 ? max(pos + 1 - p.window, 0) : 0;
+    for (int j = w.from[x]; j < w.to[x]; ++j) {
+        if (!partly_seen(w, p.window, j)) continue;
+        for (int key = max(j * kKeys, lo); key < min((j + 1) * kKeys, pos + 1); ++key) {
+            const int64_t page = page_of(p.c, w.b, key);
+            if (page < 0) continue;
+            const unsigned short *v = static_cast<const unsigned short *>(p.c.v_cache) + page * p.c.vs[0] +
+                                      (key % p.c.page) * p.c.vs[1] + w.g * p.c.vs[2];
+            for (int d = 0; d < p.c.D; ++d) {
+                const float f = bits_to_float(__ldg(v + d), BF ? kBF16 : kF16);
+                if (fabsf(f) <= 3.402823466e38f) continue;
+                if constexpr (sizeof(T) == 4) row[d] += f;
+                else row[d] = static_cast<T>(pack2<BF>(bits_to_float(row[d], BF ? kBF16 : kF16) + f, 0.f) & 0xffffu);
+            }
+        }
+    }
+}
+
+// DK: the head size, rounded up to 64; BF: bf16.
+template <int DK, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendParams p, const __grid_constant__ Maps maps, const Plan plan,
+                                                                   int box) {
+    using LY = Layout<DK>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + LY::kBars);
+    uint64_t *const full = bars + kRing, *const empty = full + LY::kBufs, *const clean = empty + LY::kBufs;
+    Work *const ring = reinterpret_cast<Work *>(smem + LY::kWork);
+    uint32_t *const tmem_at = reinterpret_cast<uint32_t *>(smem + LY::kMisc);
+    volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + LY::kMisc) + 1;
+    volatile int *const is_last = abort_flag + 1;
+    // by piece of work and warp: were there values that are no numbers?
+    volatile int *const odd = abort_flag + 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 8) tmem_alloc512(tmem_at);
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < kRing; ++i)
+            mbar_init(&bars[i], i == kUnitFree0 || i == kUnitFree1 ? kReaders
+                                : i == kPFull0 || i == kPFull1 || i == kSync0 || i == kSync1 ? 4 : 1);
+        for (int i = 0; i < LY::kBufs; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 3), mbar_init(&clean[i], 2);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+    bool ok = true;
+    int nu = 0;  // pieces of work read
+    const auto read_work = [&](const Work *&w) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) return false;
+        w = &ring[nu % kWorks];
+        if (lane == 0) mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+        ++nu;
+        return true;
+    };
+
+    if (warp >= 8) {
+        registers_down<80>();
+        if (warp == 9) {
+            // ---------------- units and copies ----------------
+            const int pieces = plan.head->pieces, units = pieces * p.c.G, tt = tile_tokens(p.c);
+            const Piece *const list = plan.head->cut ? plan.pieces : plan.units;
+            int u = blockIdx.x, made = 0;
+            const auto next_work = [&](Work &w) {
+                if (u >= units) {
+                    w = Work{};  // (no key tiles: first > last)
+                    w.last = -1;
+                    return;
+                }
+                const int i = u / p.c.G;
+                w.g = u - i * p.c.G;
+                const Piece q = list[i];
+                w.b = q.b;
+                w.first = q.last, w.last = q.first;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int t0 = (2 * q.pair + x) * tt;
+                    w.toks[x] = max(min(tt, q.n - t0), 0);
+                    w.row[x] = q.row0 + t0;
+                    w.pos[x] = q.kv - q.n + t0;
+                    key_tiles(p, w.pos[x], w.toks[x], w.from[x], w.to[x]);
+                    w.from[x] = max(w.from[x], q.first);
+                    w.to[x] = max(min(w.to[x], q.last), w.from[x]);
+                    if (w.to[x] > w.from[x]) w.first = min(w.first, w.from[x]), w.last = max(w.last, w.to[x]);
+                }
+                if (w.last < w.first) w.first = w.last = 0;
+                w.part = q.part, w.parts = q.parts, w.slot = q.slot, w.count = q.count;
+                int nextu = 0;
+                if (lane == 0) nextu = atomicAdd(&plan.head->next, 1);
+                u = __shfl_sync(0xffffffffu, nextu, 0);
+            };
+            const auto publish = [&](const Work &w) {
+                if (made >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[kUnitFree0 + (made & 1)], ((made >> 1) - 1) & 1)))
+                    return false;
+                if (lane == 0) {
+                    ring[made % kWorks] = w;
+                    mbar_arrive(&bars[kUnitFull0 + (made & 1)]);
+                }
+                __syncwarp();
+                ++made;
+                return true;
+            };
+            // a lane each box of a tile
+            const int boxes = kKeys / box, copies = LY::kPanels * boxes, which = lane % boxes, panel = lane / boxes;
+            const auto page_at = [&](const Work &w, int j) {
+                // past the last page, where the copies read zeros, for a box that no row sees
+                int end = 0, lo = INT_MAX;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (w.to[x] > w.from[x]) {
+                        end = max(end, w.pos[x] + w.toks[x]);
+                        lo = min(lo, p.window > 0 ? w.pos[x] + 1 - p.window : 0);
+                    }
+                const int token = j * kKeys + which * box;
+                int64_t page = -1;
+                if (lane < copies && token < end && token + box > lo) page = page_of(p.c, w.b, token);
+                return static_cast<int>(page < 0 ? p.c.pages : page);
+            };
+            int n = 0, nq0 = 0, nq1 = 0;  // tiles copied; queries of A and B
+            int buf = 0, turn = 0;
+            const auto copy = [&](const CUtensorMap *map, int g, int j, int page) {
+                if (n >= LY::kBufs) ok = mbar_wait_bounded(&empty[buf], (turn & 1) ^ 1);
+                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+                if (!ok) return false;
+                if (lane == 0) mbar_arrive_expect(&full[buf], LY::kTile);
+                __syncwarp();
+                if (lane < copies)
+                    tma_load_4d(smem + LY::kBuf + buf * LY::kTile + panel * kPanel + which * box * 128, map, 64 * panel, g,
+                                (j * kKeys + which * box) % p.c.page, page, &full[buf]);
+                ++n;
+                if (++buf == LY::kBufs) buf = 0, ++turn;
+                return true;
+            };
+            const auto queries = [&](const Work &w, int x, int &nq) {
+                if (w.to[x] <= w.from[x]) return true;
+                if (nq > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kQFree0 + x], (nq - 1) & 1));
+                if (!ok) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect(&bars[kQFull0 + x], LY::kPanels * p.c.share * tt * 128);
+                    for (int i = 0; i < LY::kPanels; ++i)
+                        tma_load_3d(smem + x * LY::kTile + i * kPanel, &maps.q, 64 * i, w.g * p.c.share, static_cast<int>(w.row[x]),
+                                    &bars[kQFull0 + x]);
+                }
+                __syncwarp();
+                ++nq;
+                return true;
+            };
+            Work w, after;
+            next_work(w);
+            ok = publish(w);
+            int page = 0;
+            if (ok && w.last > w.first) page = page_at(w, w.first);
+            while (ok && w.last >= 0) {
+                next_work(after);
+                if (!(ok = publish(after))) break;
+                for (int j = w.first; ok && j < w.last; ++j) {
+                    const int here = page;
+                    if (j + 1 < w.last) page = page_at(w, j + 1);
+                    else if (after.last > after.first) page = page_at(after, after.first);
+                    if (!copy(&maps.k, w.g, j, here)) break;
+                    if (j == w.first) {
+                        if (!queries(w, 0, nq0) || !queries(w, 1, nq1)) break;
+                    }
+                    if (!copy(&maps.v, w.g, j, here)) break;
+                }
+                if (w.last <= w.first && after.last > after.first) page = page_at(after, after.first);
+                w = after;
+            }
+            if (!ok && lane == 0) {
+                flag(p.c.status, kDevTimeout);
+                *abort_flag = 1;
+            }
+            // what was asked for has landed before the CTA retires
+            if (lane == 0) {
+                for (int i = 0; i < LY::kBufs && i < n; ++i) {
+                    buf = buf == 0 ? LY::kBufs - 1 : buf - 1;
+                    if (buf == LY::kBufs - 1) --turn;
+                    mbar_wait_bounded(&full[buf], turn & 1);
+                }
+                if (nq0 > 0) mbar_wait_bounded(&bars[kQFull0], (nq0 - 1) & 1);
+                if (nq1 > 0) mbar_wait_bounded(&bars[kQFull1], (nq1 - 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp == 8) {
+            // ---------------- products (the warp together, one lane issuing) ----------------
+            constexpr int bf = BF ? 1 : 0;
+            const int ksteps = (p.c.D + 15) / 16, dims = (p.c.D + 15) / 16 * 16;
+            const uint32_t id_s = idesc_f16(kRows, kKeys, 0, 0, bf), id_o = idesc_f16(kRows, dims, 0, 1, bf);
+            const uint32_t s0 = smem_addr(smem), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const Desc dQ(desc_k_sw128(s0)), dK(desc_k_sw128(s0 + LY::kBuf)), dV(desc_mn_sw128(s0 + LY::kBuf, kPanel));
+            constexpr auto along_k = [](int k) { return static_cast<uint32_t>(((k / 4) * kPanel + (k % 4) * 32) >> 4); };
+            constexpr auto along_mn = [](int k) { return static_cast<uint32_t>((k * 2048) >> 4); };
+            const auto wait = [&](uint64_t *bar, int phase) {
+                const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1));
+                tc_fence_after();
+                return got;
+            };
+            struct Ring {
+                int buf, turn;
+            } rk{0, 0}, rv{1, 0};
+            const auto advance = [&](Ring &r) {
+                r.buf += 2;
+                if (r.buf >= LY::kBufs) r.buf -= LY::kBufs, ++r.turn;
+            };
+            int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+            uint32_t cleaned = 0;  // by buffer: phase of its next partly visible values
+            const auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+            // A piece's key tiles as the products need them.
+            struct Span {
+                int from0, to0, from1, to1, first, last;
+                const Work *at;
+            };
+            const auto next_span = [&](Span &s) {
+                if (!read_work(s.at)) return false;
+                s.from0 = uniform(s.at->from[0]), s.to0 = uniform(s.at->to[0]);
+                s.from1 = uniform(s.at->from[1]), s.to1 = uniform(s.at->to[1]);
+                s.first = uniform(s.at->first), s.last = uniform(s.at->last);
+                return true;
+            };
+            // S of tile T and key tile j, if it sees that
+            const auto scores = [&](auto T, int from, int to, int j, int &nq) {
+                constexpr int t = decltype(T)::value;
+                if (j < from || j >= to) return true;
+                if (j == from && !wait(&bars[kQFull0 + t], nq)) return false;
+                const bool done = j + 1 == to;
+                if (elect_one()) {
+                    const Desc a = dQ + ((t * LY::kTile) >> 4), b = dK + ((rk.buf * LY::kTile) >> 4);
+#pragma unroll
+                    for (int i = 0; i < DK / 16; ++i)
+                        if (i < ksteps) mma(tm + kColS + t * kKeys, a + along_k(i), b + along_k(i), id_s, i > 0);
+                    mma_commit(&bars[kSFull0 + t]);
+                    if (done) mma_commit(&bars[kQFree0 + t]);
+                }
+                __syncwarp();
+                if (done) ++nq;
+                return true;
+            };
+            // O of tile T += P V
+            const auto outputs = [&](auto T, int from, int to, int j, int &np) {
+                constexpr int t = decltype(T)::value;
+                if (j < from || j >= to) return true;
+                if (!wait(&bars[kPFull0 + t], np)) return false;
+                ++np;
+                if (elect_one()) {
+                    const Desc b = dV + ((rv.buf * LY::kTile) >> 4);
+                    const uint32_t acc = j > from;
+#pragma unroll
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        mma_ts(tm + kColO + t * kKeys, tm + kColS + t * kKeys + 8 * i, b + along_mn(i), id_o, acc | (i > 0));
+                    mma_commit(&bars[kOFull0 + t]);
+                }
+                __syncwarp();
+                return true;
+            };
+            const std::integral_constant<int, 0> A;
+            const std::integral_constant<int, 1> B;
+            // The scores of the next key tile, of this piece or the next, are
+            // issued between the products of this one's P.  (A piece without keys
+            // is not looked past before this one's are: its readers may wait for them.)
+            Span w, n;
+            bool begun = false;  // the scores of w's tile j are issued
+            int j = 0;
+            ok = next_span(w);
+            while (ok && w.last >= 0) {
+                if (w.last == w.first) {
+                    ok = next_span(w);
+                    continue;
+                }
+                if (!begun) {
+                    j = w.first;
+                    ok = wait(&full[rk.buf], rk.turn) && scores(A, w.from0, w.to0, j, nq0) && scores(B, w.from1, w.to1, j, nq1);
+                    if (!ok) break;
+                    if (elect_one()) mma_commit(&empty[rk.buf]);
+                    __syncwarp();
+                    advance(rk);
+                }
+                const bool turnover = j + 1 >= w.last;
+                if (turnover) {
+                    if (!(ok = next_span(n))) break;
+                } else {
+                    n = w;
+                }
+                const int jn = turnover ? n.first : j + 1;
+                begun = n.last > n.first;
+                if (!(ok = wait(&full[rv.buf], rv.turn))) break;
+                if (partly_seen(*w.at, p.window, j)) {
+                    if (!(ok = wait(&clean[rv.buf], static_cast<int>(cleaned >> rv.buf)))) break;
+                    cleaned ^= 1u << rv.buf;
+                }
+                if (!(ok = outputs(A, w.from0, w.to0, j, np0))) break;
+                if (begun && !(ok = wait(&full[rk.buf], rk.turn) && scores(A, n.from0, n.to0, jn, nq0))) break;
+                if (!(ok = outputs(B, w.from1, w.to1, j, np1))) break;
+                if (begun && !(ok = scores(B, n.from1, n.to1, jn, nq1))) break;
+                if (elect_one()) {
+                    mma_commit(&empty[rv.buf]);
+                    if (begun) mma_commit(&empty[rk.buf]);
+                }
+                __syncwarp();
+                advance(rv);
+                if (begun) advance(rk);
+                w = n;
+                j = jn;
+            }
+            if (!ok && lane == 0) {
+                flag(p.c.status, kDevTimeout);
+                *abort_flag = 1;
+            }
+            // every product issued has completed before tensor memory is freed
+            if (elect_one()) mma_commit(&bars[kFinal]);
+            __syncwarp();
+            mbar_wait_bounded(&bars[kFinal], 0);
+            __syncwarp();
+        } else {
+            // ---------------- values of partly visible tiles ----------------
+            // What no row sees becomes zeros, and so do infinities and NaN,
+            // which a zero of P would spread to rows that do not see them: they
+            // are added at the end to those that do.
+            const Work *at;
+            const int half = warp - 10;
+            // They wait for every copy and release every buffer, whether or not
+            // there is something to do: a wait for a phase that is not the
+            // barrier's next one would mean nothing.
+            int buf = 0, turn = 0;
+            const auto arrived = [&] { return __all_sync(0xffffffffu, mbar_wait_bounded(&full[buf], turn & 1)) != 0; };
+            const auto release = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[buf]);
+                if (++buf == LY::kBufs) buf = 0, ++turn;
+            };
+            while ((ok = read_work(at)) && at->last >= 0) {
+                const Work w = *at;
+                volatile int *const found_odd = &odd[2 * ((nu - 1) % kWorks) + half];
+                if (lane == 0) *found_odd = 0;
+                __syncwarp();
+                int lo = INT_MAX, end = 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (w.to[x] > w.from[x]) {
+                        end = max(end, w.pos[x] + w.toks[x]);
+                        lo = min(lo, p.window > 0 ? w.pos[x] + 1 - p.window : 0);
+                    }
+                for (int j = w.first; j < w.last; ++j) {
+                    if (!(ok = arrived())) break;  // the keys
+                    release();
+                    if (!(ok = arrived())) break;
+                    if (partly_seen(w, p.window, j)) {
+                        unsigned char *const values = smem + LY::kBuf + buf * LY::kTile;
+                        bool found = false;
+                        for (int e = lane; e < kKeys / 2 * (DK / 8); e += 32) {
+                            const int row = kKeys / 2 * half + e / (DK / 8), key = j * kKeys + row, piece = e % (DK / 8);
+                            uint4 *const v = reinterpret_cast<uint4 *>(values + (piece / 8) * kPanel + row * 128 +
+                                                                       (((piece % 8) ^ (row & 7)) * 16));
+                            if (key >= end || key < lo) {
+                                *v = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (any_odd<BF>(*v)) {
+                                found = true;
+                                *v = without_odd<BF>(*v);
+                            }
+                        }
+                        if (found) *found_odd = 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&clean[buf]);
+                    }
+                    release();
+                }
+                if (!ok) break;
+            }
+            if (!ok && lane == 0) {
+                flag(p.c.status, kDevTimeout);
+                *abort_flag = 1;
+            }
+        }
+    } else {
+        registers_up<208>();
+        // ---------------- softmax and outputs (thread = row of tile x) ----------------
+        const int x = warp >> 2, m = tid & (kRows - 1), tok = m / p.c.share, head = m - tok * p.c.share;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t colS = lanes + kColS + x * kKeys, colO = lanes + kColO + x * kKeys;
+        const float scale = p.scale * 1.4426950408889634f;
+        int ns = 0, syncs = 0;  // score tiles seen (so many have been added to O); barriers of the group
+        const auto group_sync = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kSync0 + x]);
+            const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kSync0 + x], syncs & 1));
+            ++syncs;
+            return got;
+        };
+        const Work *at;
+        while ((ok = read_work(at)) && at->last >= 0) {
+            const struct {
+                int64_t row;
+                int g, toks, pos, from, to, part, parts, slot, count;
+            } w = {at->row[x], at->g, at->toks[x], at->pos[x], at->from[x], at->to[x], at->part, at->parts, at->slot, at->count};
+            const int from = w.from, to = w.to, pos = w.pos + tok;
+            const bool mine = tok < w.toks, live = __any_sync(0xffffffffu, mine);
+            const int hi = pos + 1, lo = p.window > 0 ? pos + 1 - p.window : 0;  // it sees keys [lo, hi)
+            float ref = -INFINITY, l = 0.f;
+            for (int j = from; j < to; ++j, ++ns) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kSFull0 + x], ns & 1)))) break;
+                tc_fence_after();
+                if (live) {
+                    uint32_t s[kKeys];
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 32) tmem_ld32(colS + c, s + c);
+                    tmem_wait_ld();
+                    if (!sees_all(p.window, w.pos, w.toks, j)) {
+                        const int h = hi - j * kKeys, o = lo - j * kKeys;
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            if (c >= h || c < o) s[c] = 0xff800000u;
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(s[i]);
+#pragma unroll
+                    for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
+                    const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                    const bool moves = now > ref + kSlack;
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float back = moves ? ex2(ref - now) : 1.f;
+                        if (moves) ref = now, l *= back;
+                        if (j > from) {
+                            if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kOFull0 + x], (ns - 1) & 1)))) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < DK; c += 16) {
+                                uint32_t r[16];
+                                tmem_ld16(colO + c, r);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * back);
+                                tmem_st16(colO + c, r);
+                            }
+                        }
+                    }
+                    const float base = ref == -INFINITY ? 0.f : ref;
+                    float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t pr[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float a = ex2(fmaf(__uint_as_float(s[c + 2 * i]), scale, -base));
+                            const float b = ex2(fmaf(__uint_as_float(s[c + 2 * i + 1]), scale, -base));
+                            add[(2 * i) & 3] += a;
+                            add[(2 * i + 1) & 3] += b;
+                            pr[i] = pack2<BF>(a, b);
+                        }
+                        tmem_st16(colS + c / 2, pr);
+                    }
+                    l += (add[0] + add[1]) + (add[2] + add[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kPFull0 + x]);
+            }
+            if (!ok) break;
+            if (to > from) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kOFull0 + x], (ns - 1) & 1)))) break;
+                tc_fence_after();
+            }
+            const bool fix = (odd[2 * ((nu - 1) % kWorks)] | odd[2 * ((nu - 1) % kWorks) + 1]) != 0;
+            const int64_t row = w.row + tok;
+            const int h = w.g * p.c.share + head;
+            unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
+            if (w.parts == 1) {
+                const float inv = pos < 0 ? 0.f : 1.f / l;
+                if (live) {
+#pragma unroll 1
+                    for (int c = 0; c < p.c.D; c += 16) {
+                        uint32_t r[16];
+                        if (to > from) {
+                            tmem_ld16(colO + c, r);
+                            tmem_wait_ld();
+                        }
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[i] = pos < 0 ? 0u : pack2<BF>(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
+                        if (mine) {
+                            *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (c + 8 < p.c.D) *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
+                    if (mine && p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(l)) * 0.6931471805599453f;
+                    if (__builtin_expect(fix, 0) && mine) add_odd<BF>(p, *at, x, pos, out);
+                }
+            } else {
+                // this part's O, l and reference; the last part to arrive joins them all
+                const auto part_at = [&](int part) {
+                    return plan.parts + (((static_cast<int64_t>(w.slot) + part) * p.c.G + w.g) * 2 + x) * (kRows * (DK + 2));
+                };
+                float *const part = part_at(w.part), *const mine_at = part + m * DK;
+                if (live) {
+#pragma unroll 1
+                    for (int c = 0; c < DK; c += 16) {
+                        uint32_t r[16];
+                        if (to > from) {
+                            tmem_ld16(colO + c, r);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = 0u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4 *>(mine_at + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                    }
+                    part[kRows * DK + m] = l;
+                    part[kRows * DK + kRows + m] = ref;
+                    if (__builtin_expect(fix, 0) && mine) add_odd<BF>(p, *at, x, pos, mine_at);
+                }
+                __threadfence();
+                if (!(ok = group_sync())) break;
+                if (m == 0)
+                    is_last[x] = atomicAdd(&plan.counters[(static_cast<int64_t>(w.count) * p.c.G + w.g) * 2 + x], 1) == w.parts - 1;
+                if (!(ok = group_sync())) break;
+                if (is_last[x] && mine) {
+                    __threadfence();
+                    float top = -INFINITY, sum = 0.f;
+                    for (int i = 0; i < w.parts; ++i) top = fmaxf(top, __ldcg(part_at(i) + kRows * DK + kRows + m));
+                    for (int i = 0; i < w.parts; ++i) {
+                        const float r = __ldcg(part_at(i) + kRows * DK + kRows + m);
+                        sum += __ldcg(part_at(i) + kRows * DK + m) * (r == -INFINITY ? 0.f : ex2(r - top));
+                    }
+                    const float inv = 1.f / sum;
+                    for (int c = 0; c < p.c.D; c += 8) {
+                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        for (int i = 0; i < w.parts; ++i) {
+                            const float r = __ldcg(part_at(i) + kRows * DK + kRows + m), f = r == -INFINITY ? 0.f : ex2(r - top);
+                            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + m * DK + c));
+                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + m * DK + c + 4));
+                            v[0] += a.x * f, v[1] += a.y * f, v[2] += a.z * f, v[3] += a.w * f;
+                            v[4] += b.x * f, v[5] += b.y * f, v[6] += b.z * f, v[7] += b.w * f;
+                        }
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = pos < 0 ? 0u : pack2<BF>(v[2 * i] * inv, v[2 * i + 1] * inv);
+                        *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    if (p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.6931471805599453f;
+                }
+            }
+            // O's columns have been read before the next P is announced
+            tc_fence_before();
+        }
+        if (!ok && lane == 0) {
+            flag(p.c.status, kDevTimeout);
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc512(tmem);
+}
+
+constexpr int64_t kSlots = 1024;  // parts of cut units, all heads together
+
+struct Split {
+    int64_t units, slots;  // most units; most parts of cut ones (a head)
+    uint64_t at_units, at_pieces, at_counters, at_parts, bytes;
+};
+Split split_of(const PagedParams &c) {
+    const auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
+    Split s{};
+    const int64_t pair = 2 * (kRows / c.share);
+    s.units = c.rows / pair + c.nseq;  // >= sum of ceil(n / pair)
+    const int64_t few = kMaxParts * s.units;
+    s.slots = kSlots / c.G < few ? kSlots / c.G : few;
+    const uint64_t dk = c.D <= 64 ? 64 : 128;
+    s.at_units = up(sizeof(PlanHead));
+    s.at_pieces = s.at_units + up(s.units * sizeof(Piece));
+    s.at_counters = s.at_pieces + up((s.units + s.slots) * sizeof(Piece));
+    s.at_parts = s.at_counters + up(s.slots * c.G * 2 * sizeof(int32_t));
+    s.bytes = s.at_parts + up(static_cast<uint64_t>(s.slots) * c.G * 2 * kRows * (dk + 2) * sizeof(float));
+    return s;
+}
+
+template <int DK, bool BF>
+cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream) {
+    // Before the maps: their encoder is a driver call and refuses a host thread
+    // that has no context yet, which this one gives it.
+    cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes);
+    if (e != cudaSuccess) return e;
+    int box = kKeys;
+    while (p.c.page % box != 0) box /= 2;
+    Maps maps;
+    if (!encode_queries(&maps.q, p.c, kRows / p.c.share) || !encode_cache(&maps.k, p.c, p.c.k_cache, p.c.ks, box) ||
+        !encode_cache(&maps.v, p.c, p.c.v_cache, p.c.vs, box))
+        return cudaErrorInvalidValue;
+    const int sms = device_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const Split s = split_of(p.c);
+    unsigned char *const at = static_cast<unsigned char *>(workspace);
+    Plan plan{};
+    plan.head = reinterpret_cast<PlanHead *>(at);
+    plan.units = reinterpret_cast<Piece *>(at + s.at_units);
+    plan.pieces = reinterpret_cast<Piece *>(at + s.at_pieces);
+    plan.counters = reinterpret_cast<int32_t *>(at + s.at_counters);
+    plan.parts = reinterpret_cast<float *>(at + s.at_parts);
+    plan.max_units = static_cast<int32_t>(s.units);
+    plan.max_slots = static_cast<int32_t>(s.slots);
+    attend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, sms);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    attend_tiles_kernel<DK, BF><<<sms, kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan, box);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+uint64_t attend_tiles_workspace(const PagedParams &c) { return split_of(c).bytes; }
+
+cudaError_t launch_attend_tiles(const AttendParams &p, void *workspace, cudaStream_t stream) {
+    const bool bf = p.c.io_dtype == kBF16;
+    if (p.c.D <= 64) return bf ? launch_t<64, true>(p, workspace, stream) : launch_t<64, false>(p, workspace, stream);
+    return bf ? launch_t<128, true>(p, workspace, stream) : launch_t<128, false>(p, workspace, stream);
+}
+
+}  // namespace ssu
