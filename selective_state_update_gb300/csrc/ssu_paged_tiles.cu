@@ -292,6 +292,36 @@ __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sy
 template <int N>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// The slow path of a wait, bounded like every other.
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+
+// Two floats at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float v;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+    return v;
+}
+
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     if constexpr (BF) {
@@ -490,7 +520,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             }
             __syncwarp();
         } else if (warp == 8) {
-            // ---------------- products (the warp together, one lane issuing) ----------------
+            // ---------------- products ----------------
+            // The warp runs this together, an elected lane issuing.  What matters
+            // is little code between the waits: this warp is on the path of
+            // every key tile, and shares its scheduler and instruction cache with
+            // two that run long straight stretches.  With votes and checks around
+            // each product a key tile took 4100 cycles, with the products
+            // predicated in place of an elected branch (their descriptors formed
+            // for each) 3300.  Loop counts and addresses are the same in every
+            // lane and known to be (shuffled from lane 0), so that descriptors stay
+            // in uniform registers.
             constexpr int bf = BF ? 1 : 0;
             const int ksteps = (p.c.D + 15) / 16, dims = (p.c.D + 15) / 16 * 16;
             const uint32_t id_s = idesc_f16(kRows, kKeys, 0, 0, bf), id_o = idesc_f16(kRows, dims, 0, 1, bf);
@@ -498,70 +537,82 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             const Desc dQ(desc_k_sw128(s0)), dK(desc_k_sw128(s0 + LY::kBuf)), dV(desc_mn_sw128(s0 + LY::kBuf, kPanel));
             constexpr auto along_k = [](int k) { return static_cast<uint32_t>(((k / 4) * kPanel + (k % 4) * 32) >> 4); };
             constexpr auto along_mn = [](int k) { return static_cast<uint32_t>((k * 2048) >> 4); };
+            // A wait that gives up only notes it: products of what is not there
+            // yet stay within shared and tensor memory, and the loop ends with
+            // this key tile.
             const auto wait = [&](uint64_t *bar, int phase) {
-                const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1));
-                tc_fence_after();
-                return got;
+                if (!mbar_try_wait(bar, phase & 1)) ok = wait_on(bar, phase & 1) && ok;
             };
-            struct Ring {
-                int buf, turn;
-            } rk{0, 0}, rv{1, 0};
-            const auto advance = [&](Ring &r) {
-                r.buf += 2;
-                if (r.buf >= LY::kBufs) r.buf -= LY::kBufs, ++r.turn;
+            int kbuf = 0, kturn = 0, vbuf = 1, vturn = 0;
+            const auto advance = [&](int &buf, int &turn) {
+                buf += 2;
+                if (buf >= LY::kBufs) buf -= LY::kBufs, ++turn;
             };
             int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
-            uint32_t cleaned = 0;  // by buffer: phase of its next partly visible values
-            const auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-            // A piece's key tiles as the products need them.
-            struct Span {
-                int from0, to0, from1, to1, first, last;
-                const Work *at;
-            };
-            const auto next_span = [&](Span &s) {
-                if (!read_work(s.at)) return false;
-                s.from0 = uniform(s.at->from[0]), s.to0 = uniform(s.at->to[0]);
-                s.from1 = uniform(s.at->from[1]), s.to1 = uniform(s.at->to[1]);
-                s.first = uniform(s.at->first), s.last = uniform(s.at->last);
-                return true;
-            };
-            // S of tile T and key tile j, if it sees that
-            const auto scores = [&](auto T, int from, int to, int j, int &nq) {
+            const auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+            const auto scores = [&](auto T, bool keys_done, bool queries_done) {  // S of tile T
                 constexpr int t = decltype(T)::value;
-                if (j < from || j >= to) return true;
-                if (j == from && !wait(&bars[kQFull0 + t], nq)) return false;
-                const bool done = j + 1 == to;
+                tc_fence_after();
+                Desc b = dK;
+                b.lo = uniform(b.lo + kbuf * (LY::kTile >> 4));
                 if (elect_one()) {
-                    const Desc a = dQ + ((t * LY::kTile) >> 4), b = dK + ((rk.buf * LY::kTile) >> 4);
+                    const Desc a = dQ + ((t * LY::kTile) >> 4);
 #pragma unroll
                     for (int i = 0; i < DK / 16; ++i)
                         if (i < ksteps) mma(tm + kColS + t * kKeys, a + along_k(i), b + along_k(i), id_s, i > 0);
                     mma_commit(&bars[kSFull0 + t]);
-                    if (done) mma_commit(&bars[kQFree0 + t]);
+                    if (keys_done) mma_commit(&empty[kbuf]);
+                    if (queries_done) mma_commit(&bars[kQFree0 + t]);
                 }
-                __syncwarp();
-                if (done) ++nq;
-                return true;
             };
-            // O of tile T += P V
-            const auto outputs = [&](auto T, int from, int to, int j, int &np) {
+            const auto outputs = [&](auto T, uint32_t acc, bool values_done) {  // O of tile T += P V
                 constexpr int t = decltype(T)::value;
-                if (j < from || j >= to) return true;
-                if (!wait(&bars[kPFull0 + t], np)) return false;
-                ++np;
+                tc_fence_after();
+                Desc b = dV;
+                b.lo = uniform(b.lo + vbuf * (LY::kTile >> 4));
                 if (elect_one()) {
-                    const Desc b = dV + ((rv.buf * LY::kTile) >> 4);
-                    const uint32_t acc = j > from;
 #pragma unroll
                     for (int i = 0; i < kKeys / 16; ++i)
-                        mma_ts(tm + kColO + t * kKeys, tm + kColS + t * kKeys + 8 * i, b + along_mn(i), id_o, acc | (i > 0));
+                        mma_ts(tm + kColO + t * kKeys, tm + kColS + t * kKeys + 8 * i, b + along_mn(i), id_o, i > 0 ? 1u : acc);
                     mma_commit(&bars[kOFull0 + t]);
+                    if (values_done) mma_commit(&empty[vbuf]);
                 }
-                __syncwarp();
-                return true;
+            };
+            const auto release = [&](int buf) {
+                if (elect_one()) mma_commit(&empty[buf]);
             };
             const std::integral_constant<int, 0> A;
             const std::integral_constant<int, 1> B;
+            // A piece's key tiles as the products need them.
+            struct Span {
+                int from0, to0, from1, to1, first, last;
+            };
+            const auto next_span = [&](Span &s) {
+                const Work *at;
+                if (!read_work(at)) return false;
+                s.from0 = uniform(at->from[0]), s.to0 = uniform(at->to[0]);
+                s.from1 = uniform(at->from[1]), s.to1 = uniform(at->to[1]);
+                s.first = uniform(at->first), s.last = uniform(at->last);
+                return true;
+            };
+            const auto begin = [&](auto T, const Span &s, int j) {  // S of tile T and key tile j, if it sees that
+                constexpr int t = decltype(T)::value;
+                const int from = t ? s.from1 : s.from0, to = t ? s.to1 : s.to0;
+                int &nq = t ? nq1 : nq0;
+                if (j < from || j >= to) return;
+                if (j == from) wait(&bars[kQFull0 + t], nq);
+                scores(T, false, j + 1 == to);
+                nq += j + 1 == to;
+            };
+            const auto finish = [&](auto T, const Span &s, int j) {
+                constexpr int t = decltype(T)::value;
+                const int from = t ? s.from1 : s.from0, to = t ? s.to1 : s.to0;
+                int &np = t ? np1 : np0;
+                if (j < from || j >= to) return;
+                wait(&bars[kPFull0 + t], np);
+                ++np;
+                outputs(T, j > from, false);
+            };
             // The scores of the next key tile, of this piece or the next, are
             // issued between the products of this one's P.  (A piece without keys
             // is not looked past before this one's are: its readers may wait for them.)
@@ -576,39 +627,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 }
                 if (!begun) {
                     j = w.first;
-                    ok = wait(&full[rk.buf], rk.turn) && scores(A, w.from0, w.to0, j, nq0) && scores(B, w.from1, w.to1, j, nq1);
-                    if (!ok) break;
-                    if (elect_one()) mma_commit(&empty[rk.buf]);
-                    __syncwarp();
-                    advance(rk);
+                    wait(&full[kbuf], kturn);
+                    begin(A, w, j);
+                    begin(B, w, j);
+                    release(kbuf);
+                    advance(kbuf, kturn);
+                }
+                // both tiles in the middle of their keys: nothing to decide
+                if (j > max(w.from0, w.from1)) {
+                    const int end = min(w.to0, w.to1) - 2;
+                    for (; j < end && ok; ++j) {
+                        wait(&clean[vbuf], vturn);
+                        wait(&bars[kPFull0], np0++);
+                        outputs(A, 1, false);
+                        wait(&full[kbuf], kturn);
+                        scores(A, false, false);
+                        wait(&bars[kPFull1], np1++);
+                        outputs(B, 1, true);
+                        scores(B, true, false);
+                        advance(vbuf, vturn);
+                        advance(kbuf, kturn);
+                    }
                 }
                 const bool turnover = j + 1 >= w.last;
-                if (turnover) {
-                    if (!(ok = next_span(n))) break;
-                } else {
-                    n = w;
-                }
+                n = w;
+                if (turnover && !(ok = next_span(n))) break;
                 const int jn = turnover ? n.first : j + 1;
                 begun = n.last > n.first;
-                if (!(ok = wait(&full[rv.buf], rv.turn))) break;
-                if (partly_seen(*w.at, p.window, j)) {
-                    if (!(ok = wait(&clean[rv.buf], static_cast<int>(cleaned >> rv.buf)))) break;
-                    cleaned ^= 1u << rv.buf;
+                wait(&clean[vbuf], vturn);
+                finish(A, w, j);
+                if (begun) {
+                    wait(&full[kbuf], kturn);
+                    begin(A, n, jn);
                 }
-                if (!(ok = outputs(A, w.from0, w.to0, j, np0))) break;
-                if (begun && !(ok = wait(&full[rk.buf], rk.turn) && scores(A, n.from0, n.to0, jn, nq0))) break;
-                if (!(ok = outputs(B, w.from1, w.to1, j, np1))) break;
-                if (begun && !(ok = scores(B, n.from1, n.to1, jn, nq1))) break;
-                if (elect_one()) {
-                    mma_commit(&empty[rv.buf]);
-                    if (begun) mma_commit(&empty[rk.buf]);
+                finish(B, w, j);
+                release(vbuf);
+                if (begun) {
+                    begin(B, n, jn);
+                    release(kbuf);
+                    advance(kbuf, kturn);
                 }
-                __syncwarp();
-                advance(rv);
-                if (begun) advance(rk);
+                advance(vbuf, vturn);
                 w = n;
                 j = jn;
+                ok = __all_sync(0xffffffffu, ok);
             }
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok && lane == 0) {
                 flag(p.c.status, kDevTimeout);
                 *abort_flag = 1;
@@ -625,14 +689,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             // are added at the end to those that do.
             const Work *at;
             const int half = warp - 10;
-            // They wait for every copy and release every buffer, whether or not
-            // there is something to do: a wait for a phase that is not the
-            // barrier's next one would mean nothing.
+            // They wait for every copy, keys and all, and pass on and release
+            // every buffer, whether or not there is something to do: a wait for
+            // a phase that is not the barrier's next one would mean nothing.
+            // (The products wait for the values by `clean` alone; having waited
+            // for the last key tile's, they know these two past any earlier use of
+            // a buffer.)
             int buf = 0, turn = 0;
             const auto arrived = [&] { return __all_sync(0xffffffffu, mbar_wait_bounded(&full[buf], turn & 1)) != 0; };
             const auto release = [&] {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[buf]);
+                if (lane == 0) mbar_arrive(&clean[buf]), mbar_arrive(&empty[buf]);
                 if (++buf == LY::kBufs) buf = 0, ++turn;
             };
             while ((ok = read_work(at)) && at->last >= 0) {
@@ -667,8 +734,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         }
                         if (found) *found_odd = 1;
                         fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&clean[buf]);
                     }
                     release();
                 }
@@ -722,8 +787,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(s[i]);
 #pragma unroll
-                    for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-                    const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                    for (int c = 4; c < kKeys - 4; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+                    top[0] = max3(top[0], __uint_as_float(s[kKeys - 4]), __uint_as_float(s[kKeys - 3]));
+                    top[1] = max3(top[1], __uint_as_float(s[kKeys - 2]), __uint_as_float(s[kKeys - 1]));
+                    const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
                     const bool moves = now > ref + kSlack;
                     if (__any_sync(0xffffffffu, moves)) {
                         const float back = moves ? ex2(ref - now) : 1.f;
@@ -743,21 +812,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         }
                     }
                     const float base = ref == -INFINITY ? 0.f : ref;
-                    float add[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
+                    uint64_t add[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 32) {
                         uint32_t pr[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float a = ex2(fmaf(__uint_as_float(s[c + 2 * i]), scale, -base));
-                            const float b = ex2(fmaf(__uint_as_float(s[c + 2 * i + 1]), scale, -base));
-                            add[(2 * i) & 3] += a;
-                            add[(2 * i + 1) & 3] += b;
+                            const float2 e = unpair(fma2(pair(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), scale2, base2));
+                            const float a = ex2(e.x), b = ex2(e.y);
+                            add[i & 3] = add2(add[i & 3], pair(a, b));
                             pr[i] = pack2<BF>(a, b);
                         }
                         tmem_st16(colS + c / 2, pr);
                     }
-                    l += (add[0] + add[1]) + (add[2] + add[3]);
+                    const float2 sum = unpair(add2(add2(add[0], add[1]), add2(add[2], add[3])));
+                    l += sum.x + sum.y;
                     tmem_wait_st();
                 }
                 tc_fence_before();
