@@ -26,19 +26,43 @@ EncodeFn encoder() {
 
 }  // namespace
 
-bool encode_cache(CUtensorMap *m, const PagedParams &p, const void *base, const int64_t *stride, int box) {
+namespace {
+
+bool encode_boxes(CUtensorMap *m, const PagedParams &p, const void *base, const int64_t *stride, int tokens, bool both) {
     const EncodeFn fn = encoder();
     if (!fn) return false;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.D), static_cast<cuuint64_t>(p.G), static_cast<cuuint64_t>(p.page),
-                                static_cast<cuuint64_t>(p.pages)};
-    // [head, row, page]; a stride along an extent of one is never used: keep it legal
-    const int64_t at[3] = {p.G > 1 ? stride[2] : p.D, stride[1], p.pages > 1 ? stride[0] : p.D};
-    cuuint64_t strides[3];
-    for (int i = 0; i < 3; ++i) strides[i] = static_cast<cuuint64_t>(at[i]) * 2;
-    const cuuint32_t boxes[4] = {64, 1, static_cast<cuuint32_t>(box), 1}, unit[4] = {1, 1, 1, 1};
+    // [element, row, half, head, page]
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(both ? 64 : p.D), static_cast<cuuint64_t>(p.page), both ? 2u : 1u,
+                                static_cast<cuuint64_t>(p.G), static_cast<cuuint64_t>(p.pages)};
+    // a stride along an extent of one is never used: keep it legal
+    const int64_t at[4] = {stride[1], both ? 64 : p.D, p.G > 1 ? stride[2] : p.D, p.pages > 1 ? stride[0] : p.D};
+    cuuint64_t strides[4];
+    for (int i = 0; i < 4; ++i) strides[i] = static_cast<cuuint64_t>(at[i]) * 2;
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(tokens), both ? 2u : 1u, 1, 1}, unit[5] = {1, 1, 1, 1, 1};
     const CUtensorMapDataType type = p.io_dtype == SSU_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return fn(m, type, 4, const_cast<void *>(base), dims, strides, boxes, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return fn(m, type, 5, const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int least_box(const PagedParams &p, int keys) {
+    int least = keys;
+    while (p.page % least != 0) least /= 2;
+    return least;
+}
+
+bool encode_cache(CacheMaps *m, const PagedParams &p, int keys) {
+    const int least = least_box(p, keys);
+    for (int i = 0; i < kBoxes; ++i) {
+        const int tokens = 8 << i;
+        if (tokens < least) continue;
+        if (tokens > keys || tokens > p.page) break;
+        const bool both = tokens == keys && p.D == 128;
+        if (!encode_boxes(&m->k[i], p, p.k_cache, p.ks, tokens, both) || !encode_boxes(&m->v[i], p, p.v_cache, p.vs, tokens, both))
+            return false;
+    }
+    return true;
 }
 
 bool encode_queries(CUtensorMap *m, const PagedParams &p, int tokens) {

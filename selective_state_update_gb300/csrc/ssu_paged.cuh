@@ -2,8 +2,8 @@
 // sequence's metadata, the cache's tiled copies, products of 16 x 8 x 16.
 #pragma once
 
-#include "ssu_device.cuh"
 #include "ssu_paged.h"
+#include "ssu_tcgen05.cuh"
 
 namespace ssu {
 
@@ -28,24 +28,79 @@ __device__ __forceinline__ Seq load_seq(const PagedParams &p, int64_t b, bool re
     return s;
 }
 
-// The page that holds tokens from `token` on of sequence b, or -1 (flagged)
-// where the table names none.
-__device__ __forceinline__ int64_t page_of(const PagedParams &p, int64_t b, int32_t token) {
-    const int64_t page = load_index(p.table, b * p.table_stride + token / p.page, p.table_is_i64);
+// Sequence b's page `i`, or -1 (flagged) where the table names none.
+__device__ __forceinline__ int64_t table_page(const PagedParams &p, int64_t b, int32_t i) {
+    const int64_t page = load_index(p.table, b * p.table_stride + i, p.table_is_i64);
     if (page >= 0 && page < p.pages) return page;
     flag(p.status, kDevBadSlot);
     return -1;
 }
+// The page of sequence b that holds its token `token`.
+__device__ __forceinline__ int64_t page_of(const PagedParams &p, int64_t b, int32_t token) { return table_page(p, b, token / p.page); }
 
-// Tiled copy global -> shared of a 4-D box, completed on `bar`.  x * element
+// Tiled copy global -> shared of a 5-D box, completed on `bar`.  x * element
 // size is a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_4d(void *dst_smem, const void *map, int x, int y, int z, int w, uint64_t *bar) {
+__device__ __forceinline__ void tma_load_5d(uint32_t dst_smem, const void *map, int x, int y, int z, int u, int w, uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            smem_addr(dst_smem)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            dst_smem),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(w), "r"(smem_addr(bar))
         : "memory");
 }
+
+// Copies tiles of KEYS keys or values, PANELS x 64 elements wide, from their
+// pages, a lane each box.  What there is to copy is found ahead of the wait for a
+// place to put it.
+template <int KEYS, int PANELS>
+struct PageCopier {
+    static constexpr int kPanelBytes = KEYS * 128;
+    const PagedParams &p;
+    int least;  // what tiles are rounded to
+    struct Tile {
+        uint32_t bytes;
+        int page;        // this lane's: entry `first` + lane of the table
+        int box, x, y;   // this lane's box: its map (-1: none), element, row of the page
+        int entry, dst;  // ... whose page which lane has, and where it goes
+    };
+    __device__ __forceinline__ PageCopier(const PagedParams &params, int box) : p(params), least(box) {}
+    // Tile j of sequence b, of which the keys [lo, end) are seen; the pages'
+    // numbers are on their way when this returns.
+    __device__ __forceinline__ Tile find(int64_t b, int j, int lo, int end) const {
+        const int lane = threadIdx.x & 31, token = j * KEYS;
+        int from = max(lo - token, 0) & -least;
+        const int to = min((max(end - token, 0) + least - 1) & -least, KEYS);
+        from = min(from, to);
+        const int first = (token + from) / p.page;
+        Tile t;
+        t.bytes = static_cast<uint32_t>(to - from) * (128 * PANELS);
+        t.page = 0;
+        // (past the last page the copies read zeros)
+        int y = token + from - first * p.page;
+        if (to > from && lane * p.page < y + to - from) {
+            const int64_t page = table_page(p, b, first + lane);
+            t.page = static_cast<int>(page < 0 ? p.pages : page);
+        }
+        t.box = -1, t.x = 0, t.y = 0, t.entry = 0, t.dst = 0;
+        // the largest boxes that the pages' ends allow: 32 at most, as many as pages of 8 tokens take
+        for (int at = from, entry = 0, op = 0; at < to;) {
+            const int h = 31 - __clz(min(min(to - at, p.page - y), KEYS)), rows = 1 << h;
+            // (a box of KEYS rows has both halves of 128 elements)
+            const int ops = PANELS == 2 && !(rows == KEYS && p.D == 128) ? 2 : 1;
+            if (lane >= op && lane < op + ops) {
+                const int half = lane - op;
+                t.box = h - 3, t.x = 64 * half, t.y = y, t.entry = entry, t.dst = half * kPanelBytes + at * 128;
+            }
+            op += ops, at += rows, y += rows;
+            if (y == p.page) y = 0, ++entry;
+        }
+        return t;
+    }
+    __device__ __forceinline__ void copy(const Tile &t, const CUtensorMap *maps, int g, uint32_t dst, uint64_t *bar) const {
+        const int page = __shfl_sync(0xffffffffu, t.page, t.entry);
+        if (t.box >= 0) tma_load_5d(dst + t.dst, maps + t.box, t.x, t.y, 0, g, page, bar);
+        __syncwarp();
+    }
+};
 
 // True where 16 bytes of 16-bit floats hold an infinity or a NaN.
 template <bool BF>

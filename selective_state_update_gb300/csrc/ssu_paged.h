@@ -62,8 +62,21 @@ uint64_t attend_rows_workspace(int kind, int D);
 cudaError_t launch_attend_tiles(const AttendParams &p, void *workspace, cudaStream_t stream);
 uint64_t attend_tiles_workspace(const PagedParams &c);
 
-// The tensor maps of a cache: boxes of `box` tokens of one head by 64 elements.
-bool encode_cache(CUtensorMap *m, const PagedParams &p, const void *base, const int64_t *stride, int box);
+// The tensor maps of a cache: map i has boxes of 8 << i tokens of one head by
+// 64 elements or, where it is as high as a tile of keys and the head size is 128,
+// by both halves of that.  A tile of keys
+// is copied in the largest boxes that the pages' ends allow: boxes of the
+// largest power of two that divides the page instead (16 tokens for pages of 272)
+// took 1065 us where these take 760 (2048 tokens behind 72000, 16 / 4 heads).
+constexpr int kBoxes = 5;
+struct CacheMaps {
+    CUtensorMap k[kBoxes], v[kBoxes];
+};
+// Tiles begin at multiples of `keys` tokens, so the distance to a page's end is a
+// multiple of the largest power of two that divides both; what a tile needs is rounded to that.
+int least_box(const PagedParams &p, int keys);
+// Maps of the boxes that tiles of `keys` tokens need.
+bool encode_cache(CacheMaps *m, const PagedParams &p, int keys);
 // ... and of the queries: boxes of `tokens` tokens by the heads of a group by 64 elements.
 bool encode_queries(CUtensorMap *m, const PagedParams &p, int tokens);
 int device_sms();

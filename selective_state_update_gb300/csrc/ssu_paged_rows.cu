@@ -228,10 +228,6 @@ __device__ __forceinline__ uint32_t place(int row, int dim) {
     return (dim >> 6) * kPanel + row * 128 + ((((dim & 63) >> 3) ^ (row & 7)) * 16);
 }
 
-struct Caches {
-    CUtensorMap k, v;
-};
-
 // What a row's outputs become: o / l, zeros where the row sees nothing.
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
@@ -252,7 +248,7 @@ __device__ __forceinline__ void store_lse(const AttendParams &p, const Seq &s, i
 
 // DK: the head size, rounded up to 64; MT: row tiles of 16; BF: bf16.
 template <int DK, int MT, bool BF>
-__global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const AttendParams p, const __grid_constant__ Caches maps,
+__global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const AttendParams p, const __grid_constant__ CacheMaps maps,
                                                                       int box, Joint *joints, float *parts) {
     using LY = Layout<DK, MT>;
     constexpr int R = LY::kRows;
@@ -277,38 +273,31 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
     }
     bool ok = true;
     if (warp == kWarps) {
-        // ---------------- copies: a lane each box ----------------
-        const int boxes = kKeys / box, copies = 2 * LY::kPanels * boxes;
-        const int which = lane % boxes, panel = lane / boxes % LY::kPanels;
-        const bool value = lane >= LY::kPanels * boxes;
+        // ---------------- copies ----------------
+        const PageCopier<kKeys, LY::kPanels> pages(p.c, box);
         int it = 0;
-        const auto page_at = [&](const Walk &w, int i) {
-            // the page of this lane's box of key tile i, past the last page (where the copies read zeros) for one that no row sees
-            const int token = (w.r.first + i) * kKeys + which * box;
-            int64_t page = -1;
-            if (lane < copies && token < w.r.end && token + box > w.r.lo) page = page_of(p.c, w.w.b, token);
-            return static_cast<int>(page < 0 ? p.c.pages : page);
-        };
-        int page = walk.more() ? page_at(walk, walk.w.at) : 0;
+        const auto find = [&](int at) { return pages.find(walk.w.b, walk.r.first + at, walk.r.lo, walk.r.end); };
+        auto tile = pages.find(0, 0, 0, 0);
+        if (walk.more()) tile = find(walk.w.at);
         while (ok && walk.more()) {
-            const int from = walk.w.at, to = from + walk.run(), first = walk.r.first, g = walk.w.g;
+            const int from = walk.w.at, to = from + walk.run(), g = walk.w.g;
             for (int i = from; i < to; ++i, ++it) {
-                const int s = it % LY::kStages, here = page;
-                const int token = (first + i) * kKeys + which * box;
+                const int s = it % LY::kStages;
+                const auto here = tile;
                 if (i + 1 < to) {
-                    page = page_at(walk, i + 1);
+                    tile = find(i + 1);
                 } else {
                     walk.next(p, R);
-                    if (walk.more()) page = page_at(walk, walk.w.at);
+                    if (walk.more()) tile = find(walk.w.at);
                 }
                 if (it >= LY::kStages) ok = mbar_wait_bounded(&empty[s], (it / LY::kStages - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok && !*reinterpret_cast<volatile int *>(abort_flag));
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect(&full[s], LY::kStageBytes);
+                if (lane == 0) mbar_arrive_expect(&full[s], 2 * here.bytes);
                 __syncwarp();
-                if (lane < copies)
-                    tma_load_4d(smem + s * LY::kStageBytes + (value ? LY::kPanels * kPanel : 0) + panel * kPanel + which * box * 128,
-                                value ? &maps.v : &maps.k, 64 * panel, g, token % p.c.page, here, &full[s]);
+                const uint32_t dst = smem_addr(smem + s * LY::kStageBytes);
+                pages.copy(here, maps.k, g, dst, &full[s]);
+                pages.copy(here, maps.v, g, dst + LY::kPanels * kPanel, &full[s]);
             }
         }
         if (!ok) {
@@ -623,15 +612,12 @@ cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream
     using LY = Layout<DK, MT>;
     cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<DK, MT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes);
     if (e != cudaSuccess) return e;
-    int box = kKeys;
-    while (p.c.page % box != 0) box /= 2;
-    Caches maps;
-    if (!encode_cache(&maps.k, p.c, p.c.k_cache, p.c.ks, box) || !encode_cache(&maps.v, p.c, p.c.v_cache, p.c.vs, box))
-        return cudaErrorInvalidValue;
+    CacheMaps maps;
+    if (!encode_cache(&maps, p.c, kKeys)) return cudaErrorInvalidValue;
     const int grid = rows_grid();
     Joint *joints = static_cast<Joint *>(workspace);
     float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + (grid * sizeof(Joint) + 255) / 256 * 256);
-    attend_rows_kernel<DK, MT, BF><<<grid, kThreads, LY::kBytes, stream>>>(p, maps, box, joints, parts);
+    attend_rows_kernel<DK, MT, BF><<<grid, kThreads, LY::kBytes, stream>>>(p, maps, least_box(p.c, kKeys), joints, parts);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     attend_join_kernel<DK, MT, BF><<<grid - 1, 128, 0, stream>>>(p, grid, joints, parts);
     return cudaGetLastError();

@@ -284,7 +284,8 @@ struct Layout {
 };
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q;
+    CacheMaps cache;
 };
 
 template <int N>
@@ -438,10 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 ++made;
                 return true;
             };
-            // a lane each box of a tile
-            const int boxes = kKeys / box, copies = LY::kPanels * boxes, which = lane % boxes, panel = lane / boxes;
-            const auto page_at = [&](const Work &w, int j) {
-                // past the last page, where the copies read zeros, for a box that no row sees
+            const PageCopier<kKeys, LY::kPanels> pages(p.c, box);
+            const auto find = [&](const Work &w, int j) {
                 int end = 0, lo = INT_MAX;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
@@ -449,22 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         end = max(end, w.pos[x] + w.toks[x]);
                         lo = min(lo, p.window > 0 ? w.pos[x] + 1 - p.window : 0);
                     }
-                const int token = j * kKeys + which * box;
-                int64_t page = -1;
-                if (lane < copies && token < end && token + box > lo) page = page_of(p.c, w.b, token);
-                return static_cast<int>(page < 0 ? p.c.pages : page);
+                return pages.find(w.b, j, lo, end);
             };
             int n = 0, nq0 = 0, nq1 = 0;  // tiles copied; queries of A and B
             int buf = 0, turn = 0;
-            const auto copy = [&](const CUtensorMap *map, int g, int j, int page) {
+            const auto copy = [&](const CUtensorMap *map, int g, const auto &tile) {
                 if (n >= LY::kBufs) ok = mbar_wait_bounded(&empty[buf], (turn & 1) ^ 1);
                 ok = __all_sync(0xffffffffu, ok && !*abort_flag);
                 if (!ok) return false;
-                if (lane == 0) mbar_arrive_expect(&full[buf], LY::kTile);
+                if (lane == 0) mbar_arrive_expect(&full[buf], tile.bytes);
                 __syncwarp();
-                if (lane < copies)
-                    tma_load_4d(smem + LY::kBuf + buf * LY::kTile + panel * kPanel + which * box * 128, map, 64 * panel, g,
-                                (j * kKeys + which * box) % p.c.page, page, &full[buf]);
+                pages.copy(tile, map, g, smem_addr(smem + LY::kBuf + buf * LY::kTile), &full[buf]);
                 ++n;
                 if (++buf == LY::kBufs) buf = 0, ++turn;
                 return true;
@@ -486,22 +480,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             Work w, after;
             next_work(w);
             ok = publish(w);
-            int page = 0;
-            if (ok && w.last > w.first) page = page_at(w, w.first);
+            auto tile = pages.find(0, 0, 0, 0);
+            if (ok && w.last > w.first) tile = find(w, w.first);
             while (ok && w.last >= 0) {
                 next_work(after);
                 if (!(ok = publish(after))) break;
                 for (int j = w.first; ok && j < w.last; ++j) {
-                    const int here = page;
-                    if (j + 1 < w.last) page = page_at(w, j + 1);
-                    else if (after.last > after.first) page = page_at(after, after.first);
-                    if (!copy(&maps.k, w.g, j, here)) break;
+                    const auto here = tile;
+                    if (j + 1 < w.last) tile = find(w, j + 1);
+                    else if (after.last > after.first) tile = find(after, after.first);
+                    if (!copy(maps.cache.k, w.g, here)) break;
                     if (j == w.first) {
                         if (!queries(w, 0, nq0) || !queries(w, 1, nq1)) break;
                     }
-                    if (!copy(&maps.v, w.g, j, here)) break;
+                    if (!copy(maps.cache.v, w.g, here)) break;
                 }
-                if (w.last <= w.first && after.last > after.first) page = page_at(after, after.first);
+                if (w.last <= w.first && after.last > after.first) tile = find(after, after.first);
                 w = after;
             }
             if (!ok && lane == 0) {
@@ -962,12 +956,8 @@ cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream
     // that has no context yet, which this one gives it.
     cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes);
     if (e != cudaSuccess) return e;
-    int box = kKeys;
-    while (p.c.page % box != 0) box /= 2;
     Maps maps;
-    if (!encode_queries(&maps.q, p.c, kRows / p.c.share) || !encode_cache(&maps.k, p.c, p.c.k_cache, p.c.ks, box) ||
-        !encode_cache(&maps.v, p.c, p.c.v_cache, p.c.vs, box))
-        return cudaErrorInvalidValue;
+    if (!encode_queries(&maps.q, p.c, kRows / p.c.share) || !encode_cache(&maps.cache, p.c, kKeys)) return cudaErrorInvalidValue;
     const int sms = device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const Split s = split_of(p.c);
@@ -982,7 +972,7 @@ cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream
     plan.max_slots = static_cast<int32_t>(s.slots);
     attend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, sms);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attend_tiles_kernel<DK, BF><<<sms, kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan, box);
+    attend_tiles_kernel<DK, BF><<<sms, kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan, least_box(p.c, kKeys));
     return cudaGetLastError();
 }
 
