@@ -102,17 +102,17 @@ struct PageCopier {
     }
 };
 
-// True where 16 bytes of 16-bit floats hold an infinity or a NaN.
+// True where 16 bytes of 16-bit floats hold an infinity or a NaN: a sum of zeros
+// times them is no zero.
 template <bool BF>
 __device__ __forceinline__ bool any_odd(const uint4 &v) {
-    constexpr uint32_t kExp = BF ? 0x7f80u : 0x7c00u;
-    bool odd = false;
+    uint32_t sum = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t u = (&v.x)[i];
-        odd = odd || (u & kExp) == kExp || ((u >> 16) & kExp) == kExp;
+        if constexpr (BF) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"((&v.x)[i]), "r"(0u));
+        else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"((&v.x)[i]), "r"(0u));
     }
-    return odd;
+    return (sum & 0x7fff7fffu) != 0u;
 }
 // The same 16 bytes with zeros for them.
 template <bool BF>

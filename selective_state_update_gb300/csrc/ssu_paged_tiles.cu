@@ -19,9 +19,10 @@
 // Two products a key tile and query tile, fp32 accumulators in tensor memory:
 //     S = Q K^T  (both from shared memory, as copied),  O += P V  (P where S was)
 // Warps, in groups of four:
-//   0-3, 4-7  (thread = row of tile A, B) S -> P, O rescaled, outputs;
+//   0-3, 4-7  (thread = row of tile A, B) S -> P, O rescaled;
 //   8         issues the products;   9  finds the units and copies pages;
-//   10-11     look through the values of partly visible tiles (below).
+//   10-11     look through the values of partly visible tiles (below);
+//   12-15     store the outputs.
 #include <type_traits>
 
 #include "ssu_paged.cuh"
@@ -34,7 +35,7 @@ namespace {
 constexpr int kRows = 128;     // rows of a query tile
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 128 bytes
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr float kSlack = 8.f;  // log2 by which the maximum may grow before the reference moves
 
 // A part of a unit's keys, as planned.
@@ -261,12 +262,14 @@ enum : int {
     kSFull0, kSFull1,                        // scores of tile A, B are there
     kPFull0, kPFull1,                        // ... and have become P
     kOFull0, kOFull1,                        // P has been added to O
-    kSync0, kSync1,                          // among the warps of a group
+    kORead0, kORead1,                        // a piece's O has been read
+    kStat0, kStat1, kStatFree0, kStatFree1,  // a piece's sums and references are there, have been read
+    kSync,                                   // among the warps that store outputs
     kFinal,
     kRing,                                   // a buffer is full; then: is empty; then: its values are looked through
 };
 constexpr uint32_t kColS = 0, kColO = 256;   // tensor memory: S (then P) of A, B; O of A, B
-constexpr int kReaders = 11;                 // warps that read a piece of work
+constexpr int kReaders = 15;                 // warps that read a piece of work
 constexpr int kWorks = 4;  // pieces of work kept: one is written when every warp has begun the one two before it, so a
                            // warp finds its own in place until it begins the next but one
 
@@ -278,8 +281,9 @@ struct Layout {
     static constexpr int kBuf = 2 * kTile;                // after the queries of A and B
     static constexpr int kBars = kBuf + kBufs * kTile;
     static constexpr int kWork = kBars + 8 * (kRing + 3 * kBufs);
-    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort, is_last[2], odd[kWorks][2]
-    static constexpr int kBytes = kMisc + 48;
+    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort, is_last, odd[kWorks][2]
+    static constexpr int kStat = kMisc + 48;              // [2][kRows] sum, reference
+    static constexpr int kBytes = kStat + 2 * kRows * 8;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -293,8 +297,25 @@ __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sy
 template <int N>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// The slow path of a wait, bounded like every other.
-__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+// A wait, bounded like every other, of warps that mostly wait: asleep for up to
+// 20 us at a time unless the phase completes.  (Polling, the warps that store
+// outputs cost the others on their schedulers 10 %.)
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    for (uint32_t i = 0; i < (1u << 26); ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (clock64() - t0 > kWaitCycles) break;
+    }
+    return false;
+}
 
 // Two floats at a time.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -349,10 +370,37 @@ __device__ __noinline__ void add_odd(const AttendParams &p, const Work &w, int x
             for (int d = 0; d < p.c.D; ++d) {
                 const float f = bits_to_float(__ldg(v + d), BF ? kBF16 : kF16);
                 if (fabsf(f) <= 3.402823466e38f) continue;
-                if constexpr (sizeof(T) == 4) row[d] += f;
+                if constexpr (sizeof(T) == 4) row[(d / 4) * (4 * kRows) + d % 4] += f;  // (a part's O)
                 else row[d] = static_cast<T>(pack2<BF>(bits_to_float(row[d], BF ? kBF16 : kF16) + f, 0.f) & 0xffffu);
             }
         }
+    }
+}
+
+// 16 lanes x 32 columns: registers 4 c + 2 i, + 1 are columns 8 c + 2 (lane % 4), + 1
+// of lane 8 i + lane / 4.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Among 4 neighbouring lanes: word i of lane q becomes word q of lane i.
+__device__ __forceinline__ void quad_transpose(uint32_t *w) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[i] : w[i + 1], 1);
+        if (odd) w[i] = got;
+        else w[i + 1] = got;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[i] : w[i + 2], 2);
+        if (high) w[i] = got;
+        else w[i + 2] = got;
     }
 }
 
@@ -368,15 +416,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     uint32_t *const tmem_at = reinterpret_cast<uint32_t *>(smem + LY::kMisc);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + LY::kMisc) + 1;
     volatile int *const is_last = abort_flag + 1;
+    float2 *const stat = reinterpret_cast<float2 *>(smem + LY::kStat);
     // by piece of work and warp: were there values that are no numbers?
-    volatile int *const odd = abort_flag + 3;
+    volatile int *const odd = abort_flag + 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 8) tmem_alloc512(tmem_at);
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < kRing; ++i)
             mbar_init(&bars[i], i == kUnitFree0 || i == kUnitFree1 ? kReaders
-                                : i == kPFull0 || i == kPFull1 || i == kSync0 || i == kSync1 ? 4 : 1);
+                                : i >= kPFull0 && i < kOFull0 ? 4 : i >= kORead0 && i <= kSync ? 4 : 1);
         for (int i = 0; i < LY::kBufs; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 3), mbar_init(&clean[i], 2);
     }
     tc_fence_before();
@@ -386,50 +435,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     bool ok = true;
     int nu = 0;  // pieces of work read
     const auto read_work = [&](const Work *&w) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) return false;
+        if (!__all_sync(0xffffffffu, wait_on(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) return false;
         w = &ring[nu % kWorks];
         if (lane == 0) mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
         ++nu;
         return true;
     };
 
-    if (warp >= 8) {
-        registers_down<80>();
+    if (warp >= 8 && warp < 12) {
+        registers_down<104>();
         if (warp == 9) {
             // ---------------- units and copies ----------------
             const int pieces = plan.head->pieces, units = pieces * p.c.G, tt = tile_tokens(p.c);
             const Piece *const list = plan.head->cut ? plan.pieces : plan.units;
             int u = blockIdx.x, made = 0;
-            const auto next_work = [&](Work &w) {
-                if (u >= units) {
-                    w = Work{};  // (no key tiles: first > last)
-                    w.last = -1;
-                    return;
-                }
-                const int i = u / p.c.G;
-                w.g = u - i * p.c.G;
-                const Piece q = list[i];
-                w.b = q.b;
-                w.first = q.last, w.last = q.first;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int t0 = (2 * q.pair + x) * tt;
-                    w.toks[x] = max(min(tt, q.n - t0), 0);
-                    w.row[x] = q.row0 + t0;
-                    w.pos[x] = q.kv - q.n + t0;
-                    key_tiles(p, w.pos[x], w.toks[x], w.from[x], w.to[x]);
-                    w.from[x] = max(w.from[x], q.first);
-                    w.to[x] = max(min(w.to[x], q.last), w.from[x]);
-                    if (w.to[x] > w.from[x]) w.first = min(w.first, w.from[x]), w.last = max(w.last, w.to[x]);
-                }
-                if (w.last < w.first) w.first = w.last = 0;
-                w.part = q.part, w.parts = q.parts, w.slot = q.slot, w.count = q.count;
-                int nextu = 0;
-                if (lane == 0) nextu = atomicAdd(&plan.head->next, 1);
-                u = __shfl_sync(0xffffffffu, nextu, 0);
+            // What the copies need of a piece; its place among the pieces kept.
+            struct Load {
+                int b, g, first, last, lo, end, at;
             };
-            const auto publish = [&](const Work &w) {
-                if (made >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[kUnitFree0 + (made & 1)], ((made >> 1) - 1) & 1)))
+            // The next piece, announced: false where a wait gave up.
+            const auto next_work = [&](Load &l) {
+                l.at = made % kWorks;
+                Work w{};
+                w.last = -1;  // (no key tiles: first > last)
+                l.lo = INT_MAX, l.end = 0;
+                if (u < units) {
+                    const int i = u / p.c.G;
+                    w.g = u - i * p.c.G;
+                    const Piece q = list[i];
+                    w.b = q.b;
+                    w.first = q.last, w.last = q.first;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int t0 = (2 * q.pair + x) * tt;
+                        w.toks[x] = max(min(tt, q.n - t0), 0);
+                        w.row[x] = q.row0 + t0;
+                        w.pos[x] = q.kv - q.n + t0;
+                        key_tiles(p, w.pos[x], w.toks[x], w.from[x], w.to[x]);
+                        w.from[x] = max(w.from[x], q.first);
+                        w.to[x] = max(min(w.to[x], q.last), w.from[x]);
+                        if (w.to[x] > w.from[x]) {
+                            w.first = min(w.first, w.from[x]), w.last = max(w.last, w.to[x]);
+                            l.end = max(l.end, w.pos[x] + w.toks[x]);
+                            l.lo = min(l.lo, p.window > 0 ? w.pos[x] + 1 - p.window : 0);
+                        }
+                    }
+                    if (w.last < w.first) w.first = w.last = 0;
+                    w.part = q.part, w.parts = q.parts, w.slot = q.slot, w.count = q.count;
+                    int nextu = 0;
+                    if (lane == 0) nextu = atomicAdd(&plan.head->next, 1);
+                    u = __shfl_sync(0xffffffffu, nextu, 0);
+                }
+                l.b = w.b, l.g = w.g, l.first = w.first, l.last = w.last;
+                if (made >= 2 && !__all_sync(0xffffffffu, wait_on(&bars[kUnitFree0 + (made & 1)], ((made >> 1) - 1) & 1)))
                     return false;
                 if (lane == 0) {
                     ring[made % kWorks] = w;
@@ -440,20 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 return true;
             };
             const PageCopier<kKeys, LY::kPanels> pages(p.c, box);
-            const auto find = [&](const Work &w, int j) {
-                int end = 0, lo = INT_MAX;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (w.to[x] > w.from[x]) {
-                        end = max(end, w.pos[x] + w.toks[x]);
-                        lo = min(lo, p.window > 0 ? w.pos[x] + 1 - p.window : 0);
-                    }
-                return pages.find(w.b, j, lo, end);
-            };
+            const auto find = [&](const Load &l, int j) { return pages.find(l.b, j, l.lo, l.end); };
             int n = 0, nq0 = 0, nq1 = 0;  // tiles copied; queries of A and B
             int buf = 0, turn = 0;
             const auto copy = [&](const CUtensorMap *map, int g, const auto &tile) {
-                if (n >= LY::kBufs) ok = mbar_wait_bounded(&empty[buf], (turn & 1) ^ 1);
+                if (n >= LY::kBufs) ok = wait_on(&empty[buf], (turn & 1) ^ 1);
                 ok = __all_sync(0xffffffffu, ok && !*abort_flag);
                 if (!ok) return false;
                 if (lane == 0) mbar_arrive_expect(&full[buf], tile.bytes);
@@ -465,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             };
             const auto queries = [&](const Work &w, int x, int &nq) {
                 if (w.to[x] <= w.from[x]) return true;
-                if (nq > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kQFree0 + x], (nq - 1) & 1));
+                if (nq > 0) ok = __all_sync(0xffffffffu, wait_on(&bars[kQFree0 + x], (nq - 1) & 1));
                 if (!ok) return false;
                 if (lane == 0) {
                     mbar_arrive_expect(&bars[kQFull0 + x], LY::kPanels * p.c.share * tt * 128);
@@ -477,22 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 ++nq;
                 return true;
             };
-            Work w, after;
-            next_work(w);
-            ok = publish(w);
+            Load w, after;
+            ok = next_work(w);
             auto tile = pages.find(0, 0, 0, 0);
             if (ok && w.last > w.first) tile = find(w, w.first);
             while (ok && w.last >= 0) {
-                next_work(after);
-                if (!(ok = publish(after))) break;
+                if (!(ok = next_work(after))) break;
                 for (int j = w.first; ok && j < w.last; ++j) {
                     const auto here = tile;
                     if (j + 1 < w.last) tile = find(w, j + 1);
                     else if (after.last > after.first) tile = find(after, after.first);
                     if (!copy(maps.cache.k, w.g, here)) break;
-                    if (j == w.first) {
-                        if (!queries(w, 0, nq0) || !queries(w, 1, nq1)) break;
-                    }
+                    if (j == w.first && (!queries(ring[w.at], 0, nq0) || !queries(ring[w.at], 1, nq1))) break;
                     if (!copy(maps.cache.v, w.g, here)) break;
                 }
                 if (w.last <= w.first && after.last > after.first) tile = find(after, after.first);
@@ -507,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 for (int i = 0; i < LY::kBufs && i < n; ++i) {
                     buf = buf == 0 ? LY::kBufs - 1 : buf - 1;
                     if (buf == LY::kBufs - 1) --turn;
-                    mbar_wait_bounded(&full[buf], turn & 1);
+                    wait_on(&full[buf], turn & 1);
                 }
-                if (nq0 > 0) mbar_wait_bounded(&bars[kQFull0], (nq0 - 1) & 1);
-                if (nq1 > 0) mbar_wait_bounded(&bars[kQFull1], (nq1 - 1) & 1);
+                if (nq0 > 0) wait_on(&bars[kQFull0], (nq0 - 1) & 1);
+                if (nq1 > 0) wait_on(&bars[kQFull1], (nq1 - 1) & 1);
             }
             __syncwarp();
         } else if (warp == 8) {
@@ -542,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 buf += 2;
                 if (buf >= LY::kBufs) buf -= LY::kBufs, ++turn;
             };
-            int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;
+            int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, no0 = 0, no1 = 0;
             const auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
             const auto scores = [&](auto T, bool keys_done, bool queries_done) {  // S of tile T
                 constexpr int t = decltype(T)::value;
@@ -605,6 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 if (j < from || j >= to) return;
                 wait(&bars[kPFull0 + t], np);
                 ++np;
+                if (j == from) {  // O's columns are the last piece's until it is stored
+                    int &no = t ? no1 : no0;
+                    if (no > 0) wait(&bars[kORead0 + t], no - 1);
+                    ++no;
+                }
                 outputs(T, j > from, false);
             };
             // The scores of the next key tile, of this piece or the next, are
@@ -674,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             // every product issued has completed before tensor memory is freed
             if (elect_one()) mma_commit(&bars[kFinal]);
             __syncwarp();
-            mbar_wait_bounded(&bars[kFinal], 0);
+            wait_on(&bars[kFinal], 0);
             __syncwarp();
         } else {
             // ---------------- values of partly visible tiles ----------------
@@ -690,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             // for the last key tile's, they know these two past any earlier use of
             // a buffer.)
             int buf = 0, turn = 0;
-            const auto arrived = [&] { return __all_sync(0xffffffffu, mbar_wait_bounded(&full[buf], turn & 1)) != 0; };
+            const auto arrived = [&] { return __all_sync(0xffffffffu, wait_on(&full[buf], turn & 1)) != 0; };
             const auto release = [&] {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&clean[buf]), mbar_arrive(&empty[buf]);
@@ -715,17 +765,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                     if (partly_seen(w, p.window, j)) {
                         unsigned char *const values = smem + LY::kBuf + buf * LY::kTile;
                         bool found = false;
-                        for (int e = lane; e < kKeys / 2 * (DK / 8); e += 32) {
-                            const int row = kKeys / 2 * half + e / (DK / 8), key = j * kKeys + row, piece = e % (DK / 8);
-                            uint4 *const v = reinterpret_cast<uint4 *>(values + (piece / 8) * kPanel + row * 128 +
-                                                                       (((piece % 8) ^ (row & 7)) * 16));
-                            if (key >= end || key < lo) {
-                                *v = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (any_odd<BF>(*v)) {
-                                found = true;
-                                *v = without_odd<BF>(*v);
+                        // rows [r0, r1) of the tile, in turns of the two warps
+                        const auto look = [&](int r0, int r1) {
+                            constexpr int kPieces = DK / 8, kAt = 32 / kPieces;  // rows a warp looks at at once
+                            const int piece = lane % kPieces;
+#pragma unroll 4
+                            for (int row = r0 + kAt * half + lane / kPieces; row < r1; row += 2 * kAt) {
+                                const int key = j * kKeys + row;
+                                uint4 *const v = reinterpret_cast<uint4 *>(values + (piece / 8) * kPanel + row * 128 +
+                                                                           (((piece % 8) ^ (row & 7)) * 16));
+                                if (key >= end || key < lo) {
+                                    *v = make_uint4(0u, 0u, 0u, 0u);
+                                } else if (any_odd<BF>(*v)) {
+                                    found = true;
+                                    *v = without_odd<BF>(*v);
+                                }
                             }
-                        }
+                        };
+                        // what some row sees and another does not lies behind the first row's own key, or before
+                        // the last one's window
+                        const bool a = j >= w.from[0] && j < w.to[0], b = j >= w.from[1] && j < w.to[1];
+                        const int pos = a ? w.pos[0] : w.pos[1], last = b ? w.pos[1] + w.toks[1] : w.pos[0] + w.toks[0];
+                        const int seen = p.window > 0 ? min(max(last - p.window - j * kKeys, 0), kKeys) : 0;
+                        look(0, seen);
+                        look(max(max(pos + 1 - j * kKeys, 0), seen), kKeys);
                         if (found) *found_odd = 1;
                         fence_proxy_async_smem();
                     }
@@ -738,54 +801,223 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 *abort_flag = 1;
             }
         }
-    } else {
-        registers_up<208>();
-        // ---------------- softmax and outputs (thread = row of tile x) ----------------
-        const int x = warp >> 2, m = tid & (kRows - 1), tok = m / p.c.share, head = m - tok * p.c.share;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t colS = lanes + kColS + x * kKeys, colO = lanes + kColO + x * kKeys;
-        const float scale = p.scale * 1.4426950408889634f;
-        int ns = 0, syncs = 0;  // score tiles seen (so many have been added to O); barriers of the group
+    } else if (warp >= 12) {
+        registers_down<104>();
+        // ---------------- outputs ----------------
+        // Beside the next piece's products, whose first P V waits until O has
+        // been read.  (By the softmax's own threads, a row each, a piece's end
+        // took 8600 cycles where a key tile takes 2900.)
+        const int warp_row = (warp & 3) * 32, m = warp_row + lane, tok = m / p.c.share, head = m - tok * p.c.share;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp_row) << 16);
+        int done0 = 0, done1 = 0, tiles0 = 0, tiles1 = 0, syncs = 0;  // of tile A, B: pieces with keys, key tiles
         const auto group_sync = [&] {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kSync0 + x]);
-            const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kSync0 + x], syncs & 1));
+            if (lane == 0) mbar_arrive(&bars[kSync]);
+            const bool got = __all_sync(0xffffffffu, wait_on(&bars[kSync], syncs & 1));
             ++syncs;
             return got;
         };
+        const auto store = [&](const Work *at, int x, int &done, int &tiles) {
+            const int from = at->from[x], to = at->to[x], toks = at->toks[x], pos = at->pos[x] + tok;
+            if (toks <= 0) return true;
+            const bool mine = tok < toks;
+            const uint32_t colO = lanes + kColO + x * kKeys;
+            float l = 0.f, ref = -INFINITY;
+            if (to > from) {
+                tiles += to - from;
+                if (!__all_sync(0xffffffffu, wait_on(&bars[kStat0 + x], done & 1))) return false;
+                const float2 f = stat[x * kRows + m];
+                l = f.x, ref = f.y;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kStatFree0 + x]);
+                ++done;
+                if (!__all_sync(0xffffffffu, wait_on(&bars[kOFull0 + x], (tiles - 1) & 1))) return false;
+                tc_fence_after();
+            }
+            const auto o_read = [&] {
+                if (to <= from) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kORead0 + x]);
+            };
+            const int slot = (nu - 1) % kWorks;
+            const bool fix = (odd[2 * slot] | odd[2 * slot + 1]) != 0;
+            const int64_t row = at->row[x] + tok;
+            const int h = at->g * p.c.share + head;
+            unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
+            const auto put_lse = [&](float top, float sum) {
+                if (p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.6931471805599453f;
+            };
+            // rows r, r + 8 of the warp's are lane 4 (r % 8) ...'s: 4 lanes hold 8 columns of a row, and after a transposition among
+            // them each holds 8 of 32
+            const auto row_of = [&](int r) { return reinterpret_cast<unsigned short *>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(out), r)); };
+            if (at->parts == 1) {
+                const float inv = pos < 0 ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int ra = 16 * half + lane / 4, q = lane & 3;
+                    unsigned short *const out_a = row_of(ra) + 8 * q, *const out_b = row_of(ra + 8) + 8 * q;
+                    const float inv_a = __shfl_sync(0xffffffffu, inv, ra), inv_b = __shfl_sync(0xffffffffu, inv, ra + 8);
+                    const uint32_t there = __ballot_sync(0xffffffffu, mine), none = __ballot_sync(0xffffffffu, pos < 0);
+                    const bool a = there >> ra & 1, b = there >> (ra + 8) & 1, zero_a = none >> ra & 1, zero_b = none >> (ra + 8) & 1;
+#pragma unroll 1
+                    for (int c = 0; c < p.c.D; c += 32) {
+                        uint32_t r[16];
+                        if (to > from) {
+                            tmem_ld_16x256b_x4(colO + (static_cast<uint32_t>(16 * half) << 16) + c, r);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = 0u;
+                        }
+                        uint32_t u[4], v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            u[i] = zero_a ? 0u : pack2<BF>(__uint_as_float(r[4 * i]) * inv_a, __uint_as_float(r[4 * i + 1]) * inv_a);
+                            v[i] = zero_b ? 0u : pack2<BF>(__uint_as_float(r[4 * i + 2]) * inv_b, __uint_as_float(r[4 * i + 3]) * inv_b);
+                        }
+                        quad_transpose(u);
+                        quad_transpose(v);
+                        if (c + 8 * q < p.c.D) {
+                            if (a) *reinterpret_cast<uint4 *>(out_a + c) = make_uint4(u[0], u[1], u[2], u[3]);
+                            if (b) *reinterpret_cast<uint4 *>(out_b + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                }
+                o_read();
+                if (mine) put_lse(ref, l);
+                if (__builtin_expect(fix, 0)) {
+                    __syncwarp();
+                    if (mine) add_odd<BF>(p, *at, x, pos, out);
+                }
+                return true;
+            }
+            // This part's O, l and reference; the last part to arrive joins them all.
+            const auto part_at = [&](int part) {
+                return plan.parts + (((static_cast<int64_t>(at->slot) + part) * p.c.G + at->g) * 2 + x) * (kRows * (DK + 2));
+            };
+            float *const part = part_at(at->part);  // O as [DK / 4][kRows][4]
+#pragma unroll 1
+            for (int c = 0; c < DK; c += 16) {
+                uint32_t r[16];
+                if (to > from) {
+                    tmem_ld16(colO + c, r);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(part + ((c / 4 + i) * kRows + m) * 4) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+            }
+            o_read();
+            part[kRows * DK + m] = l;
+            part[kRows * DK + kRows + m] = ref;
+            if (__builtin_expect(fix, 0) && mine) add_odd<BF>(p, *at, x, pos, part + m * 4);
+            __threadfence();
+            if (!group_sync()) return false;
+            if (m == 0) *is_last = atomicAdd(&plan.counters[(static_cast<int64_t>(at->count) * p.c.G + at->g) * 2 + x], 1) == at->parts - 1;
+            if (!group_sync()) return false;
+            if (!*is_last) return true;
+            __threadfence();
+            const int parts = at->parts;
+            const auto stat_of = [&](int i, int r, int k) { return __ldcg(part_at(i) + kRows * DK + k * kRows + r); };
+            {
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < parts; ++i) top = fmaxf(top, stat_of(i, m, 1));
+#pragma unroll 4
+                for (int i = 0; i < parts; ++i) {
+                    const float r = stat_of(i, m, 1);
+                    sum += stat_of(i, m, 0) * (r == -INFINITY ? 0.f : ex2(r - top));
+                }
+                l = sum, ref = top;
+                if (mine) put_lse(ref, l);
+            }
+            const float inv = 1.f / l;
+#pragma unroll 1
+            for (int r = lane / 4; r < 32; r += 8) {
+                unsigned short *const to_row = row_of(r);
+                const float top = __shfl_sync(0xffffffffu, ref, r), by = __shfl_sync(0xffffffffu, inv, r);
+                const bool there = __shfl_sync(0xffffffffu, mine, r), none = __shfl_sync(0xffffffffu, pos, r) < 0;
+#pragma unroll 1
+                for (int c = 4 * (lane & 3); c < p.c.D; c += 64) {
+                    float4 v[4] = {};
+                    for (int i = 0; i < parts; ++i) {
+                        const float s = stat_of(i, warp_row + r, 1), f = s == -INFINITY ? 0.f : ex2(s - top);
+                        float4 o[4] = {};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (c + 16 * k < p.c.D)
+                                o[k] = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + ((c / 4 + 4 * k) * kRows + warp_row + r) * 4));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k].x += o[k].x * f, v[k].y += o[k].y * f, v[k].z += o[k].z * f, v[k].w += o[k].w * f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (there && c + 16 * k < p.c.D)
+                            *reinterpret_cast<uint2 *>(to_row + c + 16 * k) =
+                                none ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[k].x * by, v[k].y * by), pack2<BF>(v[k].z * by, v[k].w * by));
+                }
+                __syncwarp();
+            }
+            return true;
+        };
+        const Work *at;
+        while ((ok = read_work(at)) && at->last >= 0)
+            if (!(ok = store(at, 0, done0, tiles0) && store(at, 1, done1, tiles1))) break;
+        if (!ok && lane == 0) {
+            flag(p.c.status, kDevTimeout);
+            *abort_flag = 1;
+        }
+    } else {
+        registers_up<152>();
+        // ---------------- softmax (thread = row of tile x) ----------------
+        const int x = warp >> 2, m = tid & (kRows - 1), tok = m / p.c.share;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t colS = lanes + kColS + x * kKeys, colO = lanes + kColO + x * kKeys;
+        const float scale = p.scale * 1.4426950408889634f;
+        int ns = 0, done = 0;  // score tiles seen (so many have been added to O); pieces with any
         const Work *at;
         while ((ok = read_work(at)) && at->last >= 0) {
-            const struct {
-                int64_t row;
-                int g, toks, pos, from, to, part, parts, slot, count;
-            } w = {at->row[x], at->g, at->toks[x], at->pos[x], at->from[x], at->to[x], at->part, at->parts, at->slot, at->count};
-            const int from = w.from, to = w.to, pos = w.pos + tok;
-            const bool mine = tok < w.toks, live = __any_sync(0xffffffffu, mine);
+            const int from = at->from[x], to = at->to[x], toks = at->toks[x], pos0 = at->pos[x], pos = pos0 + tok;
+            const bool live = __any_sync(0xffffffffu, tok < toks);
             const int hi = pos + 1, lo = p.window > 0 ? pos + 1 - p.window : 0;  // it sees keys [lo, hi)
             float ref = -INFINITY, l = 0.f;
             for (int j = from; j < to; ++j, ++ns) {
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kSFull0 + x], ns & 1)))) break;
                 tc_fence_after();
                 if (live) {
-                    uint32_t s[kKeys];
+                    if (!sees_all(p.window, pos0, toks, j)) {
+                        // (in place and in a loop: rarely run code must not stretch this path)
+#pragma unroll 1
+                        for (int c = 0; c < kKeys; c += 32) {
+                            uint32_t r[32];
+                            tmem_ld32(colS + c, r);
+                            tmem_wait_ld();
+                            const int h = hi - j * kKeys - c, o = lo - j * kKeys - c;
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) tmem_ld32(colS + c, s + c);
-                    tmem_wait_ld();
-                    if (!sees_all(p.window, w.pos, w.toks, j)) {
-                        const int h = hi - j * kKeys, o = lo - j * kKeys;
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c)
-                            if (c >= h || c < o) s[c] = 0xff800000u;
+                            for (int i = 0; i < 32; ++i)
+                                if (i >= h || i < o) r[i] = 0xff800000u;
+                            tmem_st16(colS + c, r);
+                            tmem_st16(colS + c + 16, r + 16);
+                        }
+                        tmem_wait_st();
                     }
-                    float top[4];
+                    // The scores are read twice, for their maximum and for P: held
+                    // between the two they take the registers that the other groups need.
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t s[2][32];
+                    tmem_ld32(colS, s[0]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(s[i]);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        tmem_ld32(colS + (c < 3 ? 32 * c + 32 : 0), s[(c + 1) & 1]);  // (last: the first again, for P)
 #pragma unroll
-                    for (int c = 4; c < kKeys - 4; c += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
-                    top[0] = max3(top[0], __uint_as_float(s[kKeys - 4]), __uint_as_float(s[kKeys - 3]));
-                    top[1] = max3(top[1], __uint_as_float(s[kKeys - 2]), __uint_as_float(s[kKeys - 1]));
+                        for (int i = 0; i < 32; i += 2)
+                            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[c & 1][i]), __uint_as_float(s[c & 1][i + 1]));
+                    }
                     const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
                     const bool moves = now > ref + kSlack;
                     if (__any_sync(0xffffffffu, moves)) {
@@ -809,16 +1041,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                     const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
                     uint64_t add[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) {
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld32(colS + 32 * c + 32, s[(c + 1) & 1]);
                         uint32_t pr[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 e = unpair(fma2(pair(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])), scale2, base2));
+                            const float2 e = unpair(fma2(pair(__uint_as_float(s[c & 1][2 * i]), __uint_as_float(s[c & 1][2 * i + 1])), scale2, base2));
                             const float a = ex2(e.x), b = ex2(e.y);
                             add[i & 3] = add2(add[i & 3], pair(a, b));
                             pr[i] = pack2<BF>(a, b);
                         }
-                        tmem_st16(colS + c / 2, pr);
+                        tmem_st16(colS + 16 * c, pr);
                     }
                     const float2 sum = unpair(add2(add2(add[0], add[1]), add2(add[2], add[3])));
                     l += sum.x + sum.y;
@@ -830,92 +1064,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             }
             if (!ok) break;
             if (to > from) {
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kOFull0 + x], (ns - 1) & 1)))) break;
-                tc_fence_after();
+                if (done > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kStatFree0 + x], (done - 1) & 1)))) break;
+                stat[x * kRows + m] = make_float2(l, ref);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kStat0 + x]);
+                ++done;
             }
-            const bool fix = (odd[2 * ((nu - 1) % kWorks)] | odd[2 * ((nu - 1) % kWorks) + 1]) != 0;
-            const int64_t row = w.row + tok;
-            const int h = w.g * p.c.share + head;
-            unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
-            if (w.parts == 1) {
-                const float inv = pos < 0 ? 0.f : 1.f / l;
-                if (live) {
-#pragma unroll 1
-                    for (int c = 0; c < p.c.D; c += 16) {
-                        uint32_t r[16];
-                        if (to > from) {
-                            tmem_ld16(colO + c, r);
-                            tmem_wait_ld();
-                        }
-                        uint32_t o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            o[i] = pos < 0 ? 0u : pack2<BF>(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
-                        if (mine) {
-                            *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                            if (c + 8 < p.c.D) *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                    }
-                    if (mine && p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(l)) * 0.6931471805599453f;
-                    if (__builtin_expect(fix, 0) && mine) add_odd<BF>(p, *at, x, pos, out);
-                }
-            } else {
-                // this part's O, l and reference; the last part to arrive joins them all
-                const auto part_at = [&](int part) {
-                    return plan.parts + (((static_cast<int64_t>(w.slot) + part) * p.c.G + w.g) * 2 + x) * (kRows * (DK + 2));
-                };
-                float *const part = part_at(w.part), *const mine_at = part + m * DK;
-                if (live) {
-#pragma unroll 1
-                    for (int c = 0; c < DK; c += 16) {
-                        uint32_t r[16];
-                        if (to > from) {
-                            tmem_ld16(colO + c, r);
-                            tmem_wait_ld();
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = 0u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4 *>(mine_at + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-                    }
-                    part[kRows * DK + m] = l;
-                    part[kRows * DK + kRows + m] = ref;
-                    if (__builtin_expect(fix, 0) && mine) add_odd<BF>(p, *at, x, pos, mine_at);
-                }
-                __threadfence();
-                if (!(ok = group_sync())) break;
-                if (m == 0)
-                    is_last[x] = atomicAdd(&plan.counters[(static_cast<int64_t>(w.count) * p.c.G + w.g) * 2 + x], 1) == w.parts - 1;
-                if (!(ok = group_sync())) break;
-                if (is_last[x] && mine) {
-                    __threadfence();
-                    float top = -INFINITY, sum = 0.f;
-                    for (int i = 0; i < w.parts; ++i) top = fmaxf(top, __ldcg(part_at(i) + kRows * DK + kRows + m));
-                    for (int i = 0; i < w.parts; ++i) {
-                        const float r = __ldcg(part_at(i) + kRows * DK + kRows + m);
-                        sum += __ldcg(part_at(i) + kRows * DK + m) * (r == -INFINITY ? 0.f : ex2(r - top));
-                    }
-                    const float inv = 1.f / sum;
-                    for (int c = 0; c < p.c.D; c += 8) {
-                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                        for (int i = 0; i < w.parts; ++i) {
-                            const float r = __ldcg(part_at(i) + kRows * DK + kRows + m), f = r == -INFINITY ? 0.f : ex2(r - top);
-                            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + m * DK + c));
-                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + m * DK + c + 4));
-                            v[0] += a.x * f, v[1] += a.y * f, v[2] += a.z * f, v[3] += a.w * f;
-                            v[4] += b.x * f, v[5] += b.y * f, v[6] += b.z * f, v[7] += b.w * f;
-                        }
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = pos < 0 ? 0u : pack2<BF>(v[2 * i] * inv, v[2 * i + 1] * inv);
-                        *reinterpret_cast<uint4 *>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                    if (p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.6931471805599453f;
-                }
-            }
-            // O's columns have been read before the next P is announced
-            tc_fence_before();
         }
         if (!ok && lane == 0) {
             flag(p.c.status, kDevTimeout);
