@@ -82,6 +82,7 @@ struct PageCopier {
         }
         t.box = -1, t.x = 0, t.y = 0, t.entry = 0, t.dst = 0;
         // the largest boxes that the pages' ends allow: 32 at most, as many as pages of 8 tokens take
+#pragma unroll 1
         for (int at = from, entry = 0, op = 0; at < to;) {
             const int h = 31 - __clz(min(min(to - at, p.page - y), KEYS)), rows = 1 << h;
             // (a box of KEYS rows has both halves of 128 elements)

@@ -256,10 +256,11 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
 // ---------------------------------------------------------------------------
 // The attention.
 // ---------------------------------------------------------------------------
+constexpr int kAhead = 4;  // pieces of work announced ahead of the slowest warp
 enum : int {
     kQFull0, kQFull1, kQFree0, kQFree1,      // a tile's queries have landed, are done with
-    kUnitFull0, kUnitFull1, kUnitFree0, kUnitFree1,
-    kSFull0, kSFull1,                        // scores of tile A, B are there
+    kUnitFull0, kUnitFree0 = kUnitFull0 + kAhead, kUnitEnd = kUnitFree0 + kAhead,  // pieces of work
+    kSFull0 = kUnitEnd, kSFull1,             // scores of tile A, B are there
     kPFull0, kPFull1,                        // ... and have become P
     kOFull0, kOFull1,                        // P has been added to O
     kORead0, kORead1,                        // a piece's O has been read
@@ -270,8 +271,10 @@ enum : int {
 };
 constexpr uint32_t kColS = 0, kColO = 256;   // tensor memory: S (then P) of A, B; O of A, B
 constexpr int kReaders = 15;                 // warps that read a piece of work
-constexpr int kWorks = 4;  // pieces of work kept: one is written when every warp has begun the one two before it, so a
-                           // warp finds its own in place until it begins the next but one
+// Pieces of work kept: one is written when every warp has begun the one kAhead
+// before it, and a warp looks at the one that it is at and, the products, at the next.
+constexpr int kWorks = 8;
+static_assert(kWorks >= kAhead + 2, "pieces of work");
 
 template <int DK>
 struct Layout {
@@ -281,8 +284,8 @@ struct Layout {
     static constexpr int kBuf = 2 * kTile;                // after the queries of A and B
     static constexpr int kBars = kBuf + kBufs * kTile;
     static constexpr int kWork = kBars + 8 * (kRing + 3 * kBufs);
-    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort, is_last, odd[kWorks][2]
-    static constexpr int kStat = kMisc + 48;              // [2][kRows] sum, reference
+    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort, is_last; odd[kWorks][2]
+    static constexpr int kStat = kMisc + 32;              // [2][kRows] sum, reference
     static constexpr int kBytes = kStat + 2 * kRows * 8;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -316,6 +319,13 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity) {
     }
     return false;
 }
+
+// A number that is known when this is compiled.
+template <int N>
+struct Known {
+    static constexpr int value = N;
+    __device__ __forceinline__ constexpr operator int() const { return N; }
+};
 
 // Two floats at a time.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -418,13 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     volatile int *const is_last = abort_flag + 1;
     float2 *const stat = reinterpret_cast<float2 *>(smem + LY::kStat);
     // by piece of work and warp: were there values that are no numbers?
-    volatile int *const odd = abort_flag + 2;
+    volatile unsigned char *const odd = smem + LY::kMisc + 12;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 8) tmem_alloc512(tmem_at);
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < kRing; ++i)
-            mbar_init(&bars[i], i == kUnitFree0 || i == kUnitFree1 ? kReaders
+            mbar_init(&bars[i], i >= kUnitFree0 && i < kUnitEnd ? kReaders
                                 : i >= kPFull0 && i < kOFull0 ? 4 : i >= kORead0 && i <= kSync ? 4 : 1);
         for (int i = 0; i < LY::kBufs; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 3), mbar_init(&clean[i], 2);
     }
@@ -435,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     bool ok = true;
     int nu = 0;  // pieces of work read
     const auto read_work = [&](const Work *&w) {
-        if (!__all_sync(0xffffffffu, wait_on(&bars[kUnitFull0 + (nu & 1)], (nu >> 1) & 1))) return false;
+        if (!__all_sync(0xffffffffu, wait_on(&bars[kUnitFull0 + nu % kAhead], nu / kAhead & 1))) return false;
         w = &ring[nu % kWorks];
-        if (lane == 0) mbar_arrive(&bars[kUnitFree0 + (nu & 1)]);
+        if (lane == 0) mbar_arrive(&bars[kUnitFree0 + nu % kAhead]);
         ++nu;
         return true;
     };
@@ -487,18 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                     u = __shfl_sync(0xffffffffu, nextu, 0);
                 }
                 l.b = w.b, l.g = w.g, l.first = w.first, l.last = w.last;
-                if (made >= 2 && !__all_sync(0xffffffffu, wait_on(&bars[kUnitFree0 + (made & 1)], ((made >> 1) - 1) & 1)))
+                if (made >= kAhead && !__all_sync(0xffffffffu, wait_on(&bars[kUnitFree0 + made % kAhead], (made / kAhead - 1) & 1)))
                     return false;
                 if (lane == 0) {
                     ring[made % kWorks] = w;
-                    mbar_arrive(&bars[kUnitFull0 + (made & 1)]);
+                    mbar_arrive(&bars[kUnitFull0 + made % kAhead]);
                 }
                 __syncwarp();
                 ++made;
                 return true;
             };
             const PageCopier<kKeys, LY::kPanels> pages(p.c, box);
-            const auto find = [&](const Load &l, int j) { return pages.find(l.b, j, l.lo, l.end); };
             int n = 0, nq0 = 0, nq1 = 0;  // tiles copied; queries of A and B
             int buf = 0, turn = 0;
             const auto copy = [&](const CUtensorMap *map, int g, const auto &tile) {
@@ -526,22 +535,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 ++nq;
                 return true;
             };
-            Load w, after;
-            ok = next_work(w);
+            // A tile is found while the one before it is copied, and a piece
+            // announced before the one ahead of it is copied.
+            Load w{}, after{};
             auto tile = pages.find(0, 0, 0, 0);
-            if (ok && w.last > w.first) tile = find(w, w.first);
-            while (ok && w.last >= 0) {
-                if (!(ok = next_work(after))) break;
-                for (int j = w.first; ok && j < w.last; ++j) {
-                    const auto here = tile;
-                    if (j + 1 < w.last) tile = find(w, j + 1);
-                    else if (after.last > after.first) tile = find(after, after.first);
+            int j = 0;
+            for (bool begun = false;; begun = true) {
+                // (w, j): the tile to copy, found; none the first time, and for a piece without keys
+                const bool some = begun && w.last > w.first;
+                const auto here = tile;
+                Load next = w;
+                int jn = j + 1;
+                if (!some || jn >= w.last) {
+                    next = after;
+                    if (!begun && !(ok = next_work(next))) break;
+                    jn = next.first;
+                    if (next.last >= 0 && !(ok = next_work(after))) break;
+                }
+                if (next.last > next.first) tile = pages.find(next.b, jn, next.lo, next.end);
+                if (some) {
                     if (!copy(maps.cache.k, w.g, here)) break;
                     if (j == w.first && (!queries(ring[w.at], 0, nq0) || !queries(ring[w.at], 1, nq1))) break;
                     if (!copy(maps.cache.v, w.g, here)) break;
                 }
-                if (w.last <= w.first && after.last > after.first) tile = find(after, after.first);
-                w = after;
+                w = next, j = jn;
+                if (w.last < 0) break;
             }
             if (!ok && lane == 0) {
                 flag(p.c.status, kDevTimeout);
@@ -589,30 +607,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             };
             int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, no0 = 0, no1 = 0;
             const auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
-            const auto scores = [&](auto T, bool keys_done, bool queries_done) {  // S of tile T
-                constexpr int t = decltype(T)::value;
+            // (a tile that is known when this is compiled needs no shuffle)
+            const auto of_tile = [&](auto t, uint32_t base, uint32_t step) {
+                if constexpr (std::is_same<decltype(t), int>::value) return uniform(base + t * step);
+                else return base + decltype(t)::value * step;
+            };
+            const auto scores = [&](auto t, bool keys_done, bool queries_done) {  // S of tile t
                 tc_fence_after();
-                Desc b = dK;
+                Desc b = dK, a = dQ;
                 b.lo = uniform(b.lo + kbuf * (LY::kTile >> 4));
+                a.lo = of_tile(t, a.lo, LY::kTile >> 4);
+                const uint32_t d = of_tile(t, tm + kColS, kKeys);
                 if (elect_one()) {
-                    const Desc a = dQ + ((t * LY::kTile) >> 4);
 #pragma unroll
                     for (int i = 0; i < DK / 16; ++i)
-                        if (i < ksteps) mma(tm + kColS + t * kKeys, a + along_k(i), b + along_k(i), id_s, i > 0);
+                        if (i < ksteps) mma(d, a + along_k(i), b + along_k(i), id_s, i > 0);
                     mma_commit(&bars[kSFull0 + t]);
                     if (keys_done) mma_commit(&empty[kbuf]);
                     if (queries_done) mma_commit(&bars[kQFree0 + t]);
                 }
             };
-            const auto outputs = [&](auto T, uint32_t acc, bool values_done) {  // O of tile T += P V
-                constexpr int t = decltype(T)::value;
+            const auto outputs = [&](auto t, uint32_t acc, bool values_done) {  // O of tile t += P V
                 tc_fence_after();
                 Desc b = dV;
                 b.lo = uniform(b.lo + vbuf * (LY::kTile >> 4));
+                const uint32_t d = of_tile(t, tm + kColO, kKeys), a = of_tile(t, tm + kColS, kKeys);
                 if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_ts(tm + kColO + t * kKeys, tm + kColS + t * kKeys + 8 * i, b + along_mn(i), id_o, i > 0 ? 1u : acc);
+                    for (int i = 0; i < kKeys / 16; ++i) mma_ts(d, a + 8 * i, b + along_mn(i), id_o, i > 0 ? 1u : acc);
                     mma_commit(&bars[kOFull0 + t]);
                     if (values_done) mma_commit(&empty[vbuf]);
                 }
@@ -620,8 +642,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             const auto release = [&](int buf) {
                 if (elect_one()) mma_commit(&empty[buf]);
             };
-            const std::integral_constant<int, 0> A;
-            const std::integral_constant<int, 1> B;
             // A piece's key tiles as the products need them.
             struct Span {
                 int from0, to0, from1, to1, first, last;
@@ -634,51 +654,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 s.first = uniform(at->first), s.last = uniform(at->last);
                 return true;
             };
-            const auto begin = [&](auto T, const Span &s, int j) {  // S of tile T and key tile j, if it sees that
-                constexpr int t = decltype(T)::value;
-                const int from = t ? s.from1 : s.from0, to = t ? s.to1 : s.to0;
-                int &nq = t ? nq1 : nq0;
-                if (j < from || j >= to) return;
-                if (j == from) wait(&bars[kQFull0 + t], nq);
-                scores(T, false, j + 1 == to);
-                nq += j + 1 == to;
-            };
-            const auto finish = [&](auto T, const Span &s, int j) {
-                constexpr int t = decltype(T)::value;
-                const int from = t ? s.from1 : s.from0, to = t ? s.to1 : s.to0;
-                int &np = t ? np1 : np0;
-                if (j < from || j >= to) return;
-                wait(&bars[kPFull0 + t], np);
-                ++np;
-                if (j == from) {  // O's columns are the last piece's until it is stored
-                    int &no = t ? no1 : no0;
-                    if (no > 0) wait(&bars[kORead0 + t], no - 1);
-                    ++no;
-                }
-                outputs(T, j > from, false);
-            };
             // The scores of the next key tile, of this piece or the next, are
             // issued between the products of this one's P.  (A piece without keys
             // is not looked past before this one's are: its readers may wait for them.)
-            Span w, n;
-            bool begun = false;  // the scores of w's tile j are issued
+            const Known<0> A;
+            const Known<1> B;
+            Span w{}, n{};  // (w, j): the key tile whose P is next, if `some`; (n, jn): the one after it, if `more`
+            bool some = false;
             int j = 0;
-            ok = next_span(w);
-            while (ok && w.last >= 0) {
-                if (w.last == w.first) {
-                    ok = next_span(w);
-                    continue;
-                }
-                if (!begun) {
-                    j = w.first;
-                    wait(&full[kbuf], kturn);
-                    begin(A, w, j);
-                    begin(B, w, j);
-                    release(kbuf);
-                    advance(kbuf, kturn);
-                }
+            for (;;) {
                 // both tiles in the middle of their keys: nothing to decide
-                if (j > max(w.from0, w.from1)) {
+                if (some && j > max(w.from0, w.from1)) {
                     const int end = min(w.to0, w.to1) - 2;
                     for (; j < end && ok; ++j) {
                         wait(&clean[vbuf], vturn);
@@ -693,28 +679,46 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         advance(kbuf, kturn);
                     }
                 }
-                const bool turnover = j + 1 >= w.last;
+                int jn = j + 1;
                 n = w;
-                if (turnover && !(ok = next_span(n))) break;
-                const int jn = turnover ? n.first : j + 1;
-                begun = n.last > n.first;
-                wait(&clean[vbuf], vturn);
-                finish(A, w, j);
-                if (begun) {
-                    wait(&full[kbuf], kturn);
-                    begin(A, n, jn);
+                if (!some || jn >= w.last) {
+                    if (!(ok = next_span(n) && ok)) break;
+                    jn = n.first;
                 }
-                finish(B, w, j);
-                release(vbuf);
-                if (begun) {
-                    begin(B, n, jn);
+                const bool more = n.last > n.first;
+                if (some) wait(&clean[vbuf], vturn);
+                if (more) wait(&full[kbuf], kturn);
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    const int from = t ? w.from1 : w.from0, to = t ? w.to1 : w.to0;
+                    if (some && j >= from && j < to) {
+                        wait(&bars[kPFull0 + t], t ? np1++ : np0++);
+                        if (j == from) {  // O's columns are the last piece's until it is stored
+                            const int no = t ? no1++ : no0++;
+                            if (no > 0) wait(&bars[kORead0 + t], no - 1);
+                        }
+                        outputs(t, j > from, false);
+                    }
+                    const int nfrom = t ? n.from1 : n.from0, nto = t ? n.to1 : n.to0;
+                    if (more && jn >= nfrom && jn < nto) {
+                        if (jn == nfrom) wait(&bars[kQFull0 + t], t ? nq1 : nq0);
+                        const bool done = jn + 1 == nto;
+                        scores(t, false, done);
+                        if (t) nq1 += done;
+                        else nq0 += done;
+                    }
+                }
+                if (some) {
+                    release(vbuf);
+                    advance(vbuf, vturn);
+                }
+                if (more) {
                     release(kbuf);
                     advance(kbuf, kturn);
                 }
-                advance(vbuf, vturn);
-                w = n;
-                j = jn;
+                w = n, j = jn, some = more;
                 ok = __all_sync(0xffffffffu, ok);
+                if (!ok || w.last < 0) break;
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok && lane == 0) {
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             };
             while ((ok = read_work(at)) && at->last >= 0) {
                 const Work w = *at;
-                volatile int *const found_odd = &odd[2 * ((nu - 1) % kWorks) + half];
+                volatile unsigned char *const found_odd = &odd[2 * ((nu - 1) % kWorks) + half];
                 if (lane == 0) *found_odd = 0;
                 __syncwarp();
                 int lo = INT_MAX, end = 0;
@@ -769,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         const auto look = [&](int r0, int r1) {
                             constexpr int kPieces = DK / 8, kAt = 32 / kPieces;  // rows a warp looks at at once
                             const int piece = lane % kPieces;
-#pragma unroll 4
+#pragma unroll 2
                             for (int row = r0 + kAt * half + lane / kPieces; row < r1; row += 2 * kAt) {
                                 const int key = j * kKeys + row;
                                 uint4 *const v = reinterpret_cast<uint4 *>(values + (piece / 8) * kPanel + row * 128 +
@@ -787,8 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         const bool a = j >= w.from[0] && j < w.to[0], b = j >= w.from[1] && j < w.to[1];
                         const int pos = a ? w.pos[0] : w.pos[1], last = b ? w.pos[1] + w.toks[1] : w.pos[0] + w.toks[0];
                         const int seen = p.window > 0 ? min(max(last - p.window - j * kKeys, 0), kKeys) : 0;
-                        look(0, seen);
-                        look(max(max(pos + 1 - j * kKeys, 0), seen), kKeys);
+#pragma unroll 1
+                        for (int r = 0; r < 2; ++r) look(r ? max(max(pos + 1 - j * kKeys, 0), seen) : 0, r ? kKeys : seen);
                         if (found) *found_odd = 1;
                         fence_proxy_async_smem();
                     }
@@ -817,20 +821,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             ++syncs;
             return got;
         };
-        const auto store = [&](const Work *at, int x, int &done, int &tiles) {
+        const auto store = [&](const Work *at, int x) {
             const int from = at->from[x], to = at->to[x], toks = at->toks[x], pos = at->pos[x] + tok;
             if (toks <= 0) return true;
             const bool mine = tok < toks;
             const uint32_t colO = lanes + kColO + x * kKeys;
             float l = 0.f, ref = -INFINITY;
             if (to > from) {
-                tiles += to - from;
+                const int done = x ? done1++ : done0++, tiles = x ? tiles1 += to - from : tiles0 += to - from;
                 if (!__all_sync(0xffffffffu, wait_on(&bars[kStat0 + x], done & 1))) return false;
                 const float2 f = stat[x * kRows + m];
                 l = f.x, ref = f.y;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[kStatFree0 + x]);
-                ++done;
                 if (!__all_sync(0xffffffffu, wait_on(&bars[kOFull0 + x], (tiles - 1) & 1))) return false;
                 tc_fence_after();
             }
@@ -925,9 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             const auto stat_of = [&](int i, int r, int k) { return __ldcg(part_at(i) + kRows * DK + k * kRows + r); };
             {
                 float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
+#pragma unroll 1
                 for (int i = 0; i < parts; ++i) top = fmaxf(top, stat_of(i, m, 1));
-#pragma unroll 4
+#pragma unroll 1
                 for (int i = 0; i < parts; ++i) {
                     const float r = stat_of(i, m, 1);
                     sum += stat_of(i, m, 0) * (r == -INFINITY ? 0.f : ex2(r - top));
@@ -941,32 +944,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 unsigned short *const to_row = row_of(r);
                 const float top = __shfl_sync(0xffffffffu, ref, r), by = __shfl_sync(0xffffffffu, inv, r);
                 const bool there = __shfl_sync(0xffffffffu, mine, r), none = __shfl_sync(0xffffffffu, pos, r) < 0;
+                constexpr int kN = DK / 16;  // four columns of every 16
+                const int c = 4 * (lane & 3);
+                float4 v[kN] = {};
 #pragma unroll 1
-                for (int c = 4 * (lane & 3); c < p.c.D; c += 64) {
-                    float4 v[4] = {};
-                    for (int i = 0; i < parts; ++i) {
-                        const float s = stat_of(i, warp_row + r, 1), f = s == -INFINITY ? 0.f : ex2(s - top);
-                        float4 o[4] = {};
+                for (int i = 0; i < parts; ++i) {
+                    const float s = stat_of(i, warp_row + r, 1);
+                    float4 o[kN];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (c + 16 * k < p.c.D)
-                                o[k] = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + ((c / 4 + 4 * k) * kRows + warp_row + r) * 4));
+                    for (int k = 0; k < kN; ++k)  // (columns past the head size hold anything)
+                        o[k] = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + ((c / 4 + 4 * k) * kRows + warp_row + r) * 4));
+                    const float f = s == -INFINITY ? 0.f : ex2(s - top);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k].x += o[k].x * f, v[k].y += o[k].y * f, v[k].z += o[k].z * f, v[k].w += o[k].w * f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (there && c + 16 * k < p.c.D)
-                            *reinterpret_cast<uint2 *>(to_row + c + 16 * k) =
-                                none ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[k].x * by, v[k].y * by), pack2<BF>(v[k].z * by, v[k].w * by));
+                    for (int k = 0; k < kN; ++k) v[k].x += o[k].x * f, v[k].y += o[k].y * f, v[k].z += o[k].z * f, v[k].w += o[k].w * f;
                 }
+#pragma unroll
+                for (int k = 0; k < kN; ++k)
+                    if (there && c + 16 * k < p.c.D)
+                        *reinterpret_cast<uint2 *>(to_row + c + 16 * k) =
+                            none ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[k].x * by, v[k].y * by), pack2<BF>(v[k].z * by, v[k].w * by));
                 __syncwarp();
             }
             return true;
         };
         const Work *at;
-        while ((ok = read_work(at)) && at->last >= 0)
-            if (!(ok = store(at, 0, done0, tiles0) && store(at, 1, done1, tiles1))) break;
+        while (ok && (ok = read_work(at)) && at->last >= 0)
+#pragma unroll 1
+            for (int x = 0; x < 2 && ok; ++x) ok = store(at, x);
         if (!ok && lane == 0) {
             flag(p.c.status, kDevTimeout);
             *abort_flag = 1;
