@@ -91,16 +91,16 @@ int device_sms() {
 }
 
 AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv_len) {
-    (void)max_kv_len;
     AttendPlan a{};
+    a.max_kv_len = max_kv_len;
     int64_t longest = p.c.cu == nullptr ? 1 : max_seqlen > 0 ? max_seqlen : (p.c.rows + p.c.nseq - 1) / p.c.nseq;
     a.kind = longest * p.c.share <= 16 ? kAttendRows16 : longest * p.c.share <= 32 ? kAttendRows32 : kAttendTiles;
-    a.bytes = a.kind == kAttendTiles ? attend_tiles_workspace(p.c) : attend_rows_workspace(a.kind, p.c.D);
+    a.bytes = a.kind == kAttendTiles ? attend_tiles_workspace(p.c, max_kv_len) : attend_rows_workspace(a.kind, p.c.D);
     return a;
 }
 
 cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream) {
-    if (plan.kind == kAttendTiles) return launch_attend_tiles(p, workspace, stream);
+    if (plan.kind == kAttendTiles) return launch_attend_tiles(p, plan.max_kv_len, workspace, stream);
     return launch_attend_rows(p, plan.kind, workspace, stream);
 }
 

@@ -63,23 +63,30 @@ struct PageCopier {
         int entry, dst;  // ... whose page which lane has, and where it goes
     };
     __device__ __forceinline__ PageCopier(const PagedParams &params, int box) : p(params), least(box) {}
-    // Tile j of sequence b, of which the keys [lo, end) are seen; the pages'
-    // numbers are on their way when this returns.
-    __device__ __forceinline__ Tile find(int64_t b, int j, int lo, int end) const {
-        const int lane = threadIdx.x & 31, token = j * KEYS;
-        int from = max(lo - token, 0) & -least;
-        const int to = min((max(end - token, 0) + least - 1) & -least, KEYS);
-        from = min(from, to);
-        const int first = (token + from) / p.page;
+    // The rows [from, to) of tile j that some query sees, where it sees the keys [lo, end).
+    __device__ __forceinline__ void rows(int j, int lo, int end, int &from, int &to) const {
+        to = min((max(end - j * KEYS, 0) + least - 1) & -least, KEYS);
+        from = min(max(lo - j * KEYS, 0) & -least, to);
+    }
+    // This lane's page of tile j of sequence b; the number is on its way when
+    // this returns.
+    __device__ __forceinline__ int look_up(int64_t b, int j, int lo, int end) const {
+        int from, to;
+        rows(j, lo, end, from, to);
+        const int entry = (j * KEYS + from) / p.page + (threadIdx.x & 31);
+        if (to <= from || entry * static_cast<int64_t>(p.page) >= j * KEYS + to) return 0;
+        const int64_t page = table_page(p, b, entry);
+        return static_cast<int>(page < 0 ? p.pages : page);  // past the last page the copies read zeros
+    }
+    // What tile j takes, its pages looked up.
+    __device__ __forceinline__ Tile find(int page, int j, int lo, int end) const {
+        const int lane = threadIdx.x & 31;
+        int from, to;
+        rows(j, lo, end, from, to);
         Tile t;
         t.bytes = static_cast<uint32_t>(to - from) * (128 * PANELS);
-        t.page = 0;
-        // (past the last page the copies read zeros)
-        int y = token + from - first * p.page;
-        if (to > from && lane * p.page < y + to - from) {
-            const int64_t page = table_page(p, b, first + lane);
-            t.page = static_cast<int>(page < 0 ? p.pages : page);
-        }
+        t.page = page;
+        int y = (j * KEYS + from) % p.page;
         t.box = -1, t.x = 0, t.y = 0, t.entry = 0, t.dst = 0;
         // the largest boxes that the pages' ends allow: 32 at most, as many as pages of 8 tokens take
 #pragma unroll 1

@@ -52,6 +52,7 @@ struct AttendParams {
 // How a call is computed, and the workspace it needs for that.
 struct AttendPlan {
     int32_t kind;      // kAttendRows*, kAttendTiles
+    int64_t max_kv_len;
     uint64_t bytes;
 };
 enum : int32_t { kAttendRows16 = 0, kAttendRows32 = 1, kAttendTiles = 2 };
@@ -59,8 +60,8 @@ AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv
 cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream);
 cudaError_t launch_attend_rows(const AttendParams &p, int kind, void *workspace, cudaStream_t stream);
 uint64_t attend_rows_workspace(int kind, int D);
-cudaError_t launch_attend_tiles(const AttendParams &p, void *workspace, cudaStream_t stream);
-uint64_t attend_tiles_workspace(const PagedParams &c);
+cudaError_t launch_attend_tiles(const AttendParams &p, int64_t max_kv_len, void *workspace, cudaStream_t stream);
+uint64_t attend_tiles_workspace(const PagedParams &c, int64_t max_kv_len);
 
 // The tensor maps of a cache: map i has boxes of 8 << i tokens of one head by
 // 64 elements or, where it is as high as a tile of keys and the head size is 128,

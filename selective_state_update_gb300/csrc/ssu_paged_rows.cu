@@ -276,19 +276,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
         // ---------------- copies ----------------
         const PageCopier<kKeys, LY::kPanels> pages(p.c, box);
         int it = 0;
-        const auto find = [&](int at) { return pages.find(walk.w.b, walk.r.first + at, walk.r.lo, walk.r.end); };
-        auto tile = pages.find(0, 0, 0, 0);
-        if (walk.more()) tile = find(walk.w.at);
+        const auto look_up = [&](int at) { return pages.look_up(walk.w.b, walk.r.first + at, walk.r.lo, walk.r.end); };
+        int page = walk.more() ? look_up(walk.w.at) : 0;
         while (ok && walk.more()) {
             const int from = walk.w.at, to = from + walk.run(), g = walk.w.g;
             for (int i = from; i < to; ++i, ++it) {
                 const int s = it % LY::kStages;
-                const auto here = tile;
+                const auto here = pages.find(page, walk.r.first + i, walk.r.lo, walk.r.end);
                 if (i + 1 < to) {
-                    tile = find(i + 1);
+                    page = look_up(i + 1);
                 } else {
                     walk.next(p, R);
-                    if (walk.more()) tile = find(walk.w.at);
+                    if (walk.more()) page = look_up(walk.w.at);
                 }
                 if (it >= LY::kStages) ok = mbar_wait_bounded(&empty[s], (it / LY::kStages - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok && !*reinterpret_cast<volatile int *>(abort_flag));

@@ -45,15 +45,16 @@ struct Piece {
     int32_t pair;         // tokens [pair, pair + 1) * 2 * (128 / share) of it
     int32_t first, last;  // key tiles
     int32_t part, parts;  // of the unit's parts, which
-    int32_t slot, count;  // workspace: first part's place, the unit's counter (where parts > 1)
+    int32_t slot;         // the first part's place in the workspace (where parts > 1)
+    int32_t spare;
 };
 struct PlanHead {
-    int32_t pieces, cut, next;  // number of pieces; are there parts; the next one to be taken
+    int32_t pieces, cuts, next;  // number of pieces, of units that are cut; the next piece to be taken
 };
 struct Plan {
     PlanHead *head;
     Piece *units, *pieces;  // whole units; parts, where some are cut
-    int32_t *counters;      // [cut units][G][2]
+    int32_t *cuts;          // the first part of every unit that is cut
     float *parts;           // [slots][G][2][kRows][DK + 2]
     int32_t max_units, max_slots;  // what there is room for: units; parts of cut units (a head)
 };
@@ -65,7 +66,7 @@ struct Work {
     int32_t toks[2], pos[2];   // tokens, position of the first
     int32_t from[2], to[2];    // key tiles
     int32_t first, last;       // of either; last < 0: no more work
-    int32_t part, parts, slot, count;
+    int32_t part, parts, slot;
 };
 
 __device__ __forceinline__ int tile_tokens(const PagedParams &p) { return kRows / p.share; }
@@ -108,28 +109,28 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
     return v;
 }
 // Sum of the threads before this one; `total` of all.
-__device__ __forceinline__ int block_scan(int v, int *red, int &total) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *red, T &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int upto = v;
+    T upto = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, upto, off);
+        const T o = __shfl_up_sync(0xffffffffu, upto, off);
         if (lane >= off) upto += o;
     }
     __syncthreads();
     if (lane == 31) red[warp] = upto;
     __syncthreads();
-    int w = red[lane];
+    T w = red[lane];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, w, off);
+        const T o = __shfl_up_sync(0xffffffffu, w, off);
         if (lane >= off) w += o;
     }
     total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    return upto - v + (warp > 0 ? before : 0);
+    const T before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return upto - v + (warp > 0 ? before : T(0));
 }
-
 // Key tiles of a pair of tiles.
 __device__ __forceinline__ void pair_tiles(const AttendParams &p, const Seq &s, int pair, int &first, int &last) {
     const int tt = tile_tokens(p.c), t0 = pair * 2 * tt, pos = s.kv - s.n + t0;
@@ -143,15 +144,31 @@ __device__ __forceinline__ void pair_tiles(const AttendParams &p, const Seq &s, 
     }
 }
 
-__device__ __forceinline__ int block_max(int v, int *red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    v = __reduce_max_sync(0xffffffffu, v);
-    __syncthreads();
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    return __reduce_max_sync(0xffffffffu, red[lane]);
+// How a unit of c key tiles is cut: `large` parts of `even` tiles, and the rest in
+// parts of about `fine`, at most kMaxParts in all.
+struct Cut {
+    int large, parts;
+};
+__device__ __forceinline__ Cut cut_of(int c, int even, int fine, bool whole) {
+    Cut k{0, 1};
+    if (whole) return k;
+    k.large = min(c / even, kMaxParts - 1);
+    const int rest = c - k.large * even;
+    k.parts = max(k.large + min((rest + fine - 1) / fine, kMaxParts - k.large), 1);
+    return k;
 }
-__device__ __forceinline__ int parts_of(const Piece &u, int len) { return max((u.last - u.first + len - 1) / len, 1); }
+// Key tiles [from, to) of its part i.
+__device__ __forceinline__ void part_of(const Cut &k, int c, int even, int i, int &from, int &to) {
+    const int large = min(k.large, k.parts);
+    if (i < large) {
+        from = i * even;
+        to = i + 1 == k.parts ? c : from + even;
+        return;
+    }
+    const int start = large * even, rest = c - start, n = k.parts - large, j = i - large;
+    from = start + static_cast<int>(static_cast<int64_t>(rest) * j / n);
+    to = start + static_cast<int>(static_cast<int64_t>(rest) * (j + 1) / n);
+}
 
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p, const Plan plan, int ctas) {
     __shared__ int64_t red64[32];
@@ -160,13 +177,12 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
     const auto pairs_of = [&](const Seq &s) { return (s.n + tt2 - 1) / tt2; };
     // The units, in the order of the sequences, the last tokens of each first.
     int64_t sum = 0;  // all key tiles, and one a unit
-    int most = 0;     // the longest unit's
     int units = 0;
     for (int64_t b0 = 0; b0 < p.c.nseq; b0 += kPlanThreads) {
         Seq s{0, 0, 0};
         if (b0 + tid < p.c.nseq) s = load_seq(p.c, b0 + tid, true);
         int total;
-        const int before = block_scan(pairs_of(s), red, total);
+        const int before = block_scan<int>(pairs_of(s), red, total);
         bounds[tid] = before;
         __syncthreads();
         for (int i = tid; i < total; i += kPlanThreads) {
@@ -184,73 +200,71 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
             pair_tiles(p, q, u.pair, u.first, u.last);
             if (units + i < plan.max_units) plan.units[units + i] = u;
             sum += u.last - u.first + 1;
-            most = max(most, u.last - u.first);
         }
         units = min(units + total, plan.max_units);  // (more only where sequences overlap)
         __syncthreads();
     }
     sum = block_sum(sum, red64) * p.c.G;
-    most = static_cast<int>(block_max(most, red));
 
-    // The longest part: the longest unit or a fraction of it.  Where the pieces
-    // are few the CTAs take them in rounds, else the time is the even share and
-    // about half a piece; a piece costs a tile of its own, a part kPartCost.
-    constexpr int kPartCost = 3;
-    int best = max(most, 1);
-    int64_t best_time = INT64_MAX;
-    for (int parts = 1; parts <= kMaxParts; ++parts) {
-        const int len = (most + parts - 1) / parts;
-        if (parts > 1 && (len < 4 || sum / ctas >= 4 * most)) break;
-        int64_t n = units, cut = 0;
-        if (parts > 1) {
-            n = 0;
-            for (int u = tid; u < units; u += kPlanThreads) {
-                const int c = parts_of(plan.units[u], len);
-                n += c;
-                cut += c > 1 ? c : 0;
-            }
-            n = block_sum(n, red64);
-            cut = block_sum(cut, red64);
-            if (cut > plan.max_slots) break;
+    // What is cut, with the even share of a CTA, `even`: a unit that is much longer
+    // than that, into parts of it and a rest; and, where the CTAs take the list in
+    // less than six rounds and the last one leaves many of them idle, that round's
+    // units.  The rests and those are cut finely.
+    const int64_t n = static_cast<int64_t>(units) * p.c.G, rounds = n / ctas, left = n - rounds * ctas;
+    const int64_t even64 = max((sum + ctas - 1) / ctas, static_cast<int64_t>(8));
+    const int even = static_cast<int>(min(even64, static_cast<int64_t>(1 << 30)));
+    const int64_t tail = rounds >= 6 || 20 * left >= 17 * ctas || (left == 0 && rounds > 0) ? units : (rounds * ctas + p.c.G - 1) / p.c.G;
+    int fine = max(even / 8, 4);
+    const auto cut_unit = [&](int u) {
+        const int c = plan.units[u].last - plan.units[u].first;
+        return cut_of(c, even, fine, u < tail && c <= even + even / 8);
+    };
+    bool cut_any = units > 0 && plan.max_slots > 1;
+    for (int turn = 0; cut_any; ++turn) {
+        int64_t cut = 0;
+        for (int u = tid; u < units; u += kPlanThreads) {
+            const int parts = cut_unit(u).parts;
+            cut += parts > 1 ? parts : 0;
         }
-        n *= p.c.G;
-        const int64_t cost = parts > 1 ? kPartCost : 1;
-        const int64_t time = n <= 2 * ctas ? (n + ctas - 1) / ctas * (len + cost)
-                                           : min((n + ctas - 1) / ctas * (len + cost), sum / ctas + (cost - 1) * n / ctas + (len + 1) / 2);
-        if (time < best_time) best_time = time, best = max(len, 1);
+        cut = block_sum(cut, red64);
+        if (cut == 0 || (turn == 4 && cut > plan.max_slots)) cut_any = false;
+        else if (cut <= plan.max_slots) break;
+        else fine *= 2;
     }
-    if (best >= most) {
-        if (tid == 0) plan.head->pieces = units, plan.head->cut = 0, plan.head->next = ctas;
+    if (!cut_any) {
+        if (tid == 0) plan.head->pieces = units, plan.head->cuts = 0, plan.head->next = ctas;
         return;
     }
     // The pieces: all first parts, all second ones, ... so that CTAs that are at work at the same time read the same keys.
-    int pieces = 0;
+    int pieces = 0, cuts = 0;
     for (int part = 0;; ++part) {
-        int slots = 0, cuts = 0;
+        int slots = 0;
+        cuts = 0;
         const int begun = pieces;
         for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
             Piece q{};
-            int c = 0;
+            Cut k{0, 0};
             if (u0 + tid < units) {
                 q = plan.units[u0 + tid];
-                c = parts_of(q, best);
+                k = cut_unit(u0 + tid);
             }
             int t0, t1, t2;
-            const int at = block_scan(c > part, red, t0), slot = block_scan(c > 1 ? c : 0, red, t1), cut = block_scan(c > 1, red, t2);
-            if (c > part) {
-                const int f = q.first, l = q.last;
-                q.first = f + static_cast<int>(static_cast<int64_t>(l - f) * part / c);
-                q.last = f + static_cast<int>(static_cast<int64_t>(l - f) * (part + 1) / c);
-                q.part = part, q.parts = c, q.slot = slots + slot, q.count = cuts + cut;
+            const int at = block_scan<int>(k.parts > part, red, t0), slot = block_scan<int>(k.parts > 1 ? k.parts : 0, red, t1),
+                      cut = block_scan<int>(k.parts > 1, red, t2);
+            if (k.parts > part) {
+                int from, to;
+                part_of(k, q.last - q.first, even, part, from, to);
+                q.last = q.first + to;
+                q.first += from;
+                q.part = part, q.parts = k.parts, q.slot = slots + slot;
                 plan.pieces[pieces + at] = q;
-                if (part == 0 && c > 1)
-                    for (int i = 0; i < 2 * p.c.G; ++i) plan.counters[static_cast<int64_t>(q.count) * 2 * p.c.G + i] = 0;
+                if (part == 0 && k.parts > 1) plan.cuts[cuts + cut] = pieces + at;
             }
             pieces += t0, slots += t1, cuts += t2;
         }
         if (pieces == begun) break;
     }
-    if (tid == 0) plan.head->pieces = pieces, plan.head->cut = 1, plan.head->next = ctas;
+    if (tid == 0) plan.head->pieces = pieces, plan.head->cuts = cuts, plan.head->next = ctas;
 }
 
 // ---------------------------------------------------------------------------
@@ -265,7 +279,6 @@ enum : int {
     kOFull0, kOFull1,                        // P has been added to O
     kORead0, kORead1,                        // a piece's O has been read
     kStat0, kStat1, kStatFree0, kStatFree1,  // a piece's sums and references are there, have been read
-    kSync,                                   // among the warps that store outputs
     kFinal,
     kRing,                                   // a buffer is full; then: is empty; then: its values are looked through
 };
@@ -284,12 +297,13 @@ struct Layout {
     static constexpr int kBuf = 2 * kTile;                // after the queries of A and B
     static constexpr int kBars = kBuf + kBufs * kTile;
     static constexpr int kWork = kBars + 8 * (kRing + 3 * kBufs);
-    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort, is_last; odd[kWorks][2]
+    static constexpr int kMisc = (kWork + kWorks * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;  // tensor-memory address, abort; odd[kWorks][2]
     static constexpr int kStat = kMisc + 32;              // [2][kRows] sum, reference
     static constexpr int kBytes = kStat + 2 * kRows * 8;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
+enum : int { kWideOut = 1 };  // the rows of out lie on 32-byte boundaries
 struct Maps {
     CUtensorMap q;
     CacheMaps cache;
@@ -348,6 +362,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
     return v;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float v;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
@@ -362,6 +381,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+}
+
+__device__ __forceinline__ float lse_of(float ref, float l) {
+    return ((ref == -INFINITY ? 0.f : ref) + log2f(l)) * 0.6931471805599453f;
+}
+// The place of a part of tile x: O as [DK / 4][kRows][4], l [kRows], reference [kRows].
+template <int DK>
+__device__ __forceinline__ float *part_at(const Plan &plan, int G, int slot, int g, int x) {
+    return plan.parts + ((static_cast<int64_t>(slot) * G + g) * 2 + x) * (kRows * (DK + 2));
 }
 
 // Infinities and NaN that were taken out of partly visible tiles, of the keys
@@ -387,37 +415,16 @@ __device__ __noinline__ void add_odd(const AttendParams &p, const Work &w, int x
     }
 }
 
-// 16 lanes x 32 columns: registers 4 c + 2 i, + 1 are columns 8 c + 2 (lane % 4), + 1
-// of lane 8 i + lane / 4.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-// Among 4 neighbouring lanes: word i of lane q becomes word q of lane i.
-__device__ __forceinline__ void quad_transpose(uint32_t *w) {
-    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[i] : w[i + 1], 1);
-        if (odd) w[i] = got;
-        else w[i + 1] = got;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[i] : w[i + 2], 2);
-        if (high) w[i] = got;
-        else w[i + 2] = got;
-    }
+__device__ __forceinline__ void store32(void *p, const uint32_t *u) {  // 32-byte aligned
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
+                 "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
 }
 
 // DK: the head size, rounded up to 64; BF: bf16.
 template <int DK, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendParams p, const __grid_constant__ Maps maps, const Plan plan,
-                                                                   int box) {
+                                                                   int box, int flags) {
     using LY = Layout<DK>;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + LY::kBars);
@@ -425,7 +432,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     Work *const ring = reinterpret_cast<Work *>(smem + LY::kWork);
     uint32_t *const tmem_at = reinterpret_cast<uint32_t *>(smem + LY::kMisc);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(smem + LY::kMisc) + 1;
-    volatile int *const is_last = abort_flag + 1;
     float2 *const stat = reinterpret_cast<float2 *>(smem + LY::kStat);
     // by piece of work and warp: were there values that are no numbers?
     volatile unsigned char *const odd = smem + LY::kMisc + 12;
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
         *abort_flag = 0;
         for (int i = 0; i < kRing; ++i)
             mbar_init(&bars[i], i >= kUnitFree0 && i < kUnitEnd ? kReaders
-                                : i >= kPFull0 && i < kOFull0 ? 4 : i >= kORead0 && i <= kSync ? 4 : 1);
+                                : i >= kPFull0 && i < kOFull0 ? 4 : i >= kORead0 && i < kFinal ? 4 : 1);
         for (int i = 0; i < LY::kBufs; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 3), mbar_init(&clean[i], 2);
     }
     tc_fence_before();
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
         if (warp == 9) {
             // ---------------- units and copies ----------------
             const int pieces = plan.head->pieces, units = pieces * p.c.G, tt = tile_tokens(p.c);
-            const Piece *const list = plan.head->cut ? plan.pieces : plan.units;
+            const Piece *const list = plan.head->cuts > 0 ? plan.pieces : plan.units;
             int u = blockIdx.x, made = 0;
             // What the copies need of a piece; its place among the pieces kept.
             struct Load {
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         }
                     }
                     if (w.last < w.first) w.first = w.last = 0;
-                    w.part = q.part, w.parts = q.parts, w.slot = q.slot, w.count = q.count;
+                    w.part = q.part, w.parts = q.parts, w.slot = q.slot;
                     int nextu = 0;
                     if (lane == 0) nextu = atomicAdd(&plan.head->next, 1);
                     u = __shfl_sync(0xffffffffu, nextu, 0);
@@ -535,31 +541,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 ++nq;
                 return true;
             };
-            // A tile is found while the one before it is copied, and a piece
-            // announced before the one ahead of it is copied.
-            Load w{}, after{};
-            auto tile = pages.find(0, 0, 0, 0);
-            int j = 0;
-            for (bool begun = false;; begun = true) {
-                // (w, j): the tile to copy, found; none the first time, and for a piece without keys
-                const bool some = begun && w.last > w.first;
-                const auto here = tile;
-                Load next = w;
-                int jn = j + 1;
-                if (!some || jn >= w.last) {
-                    next = after;
-                    if (!begun && !(ok = next_work(next))) break;
-                    jn = next.first;
-                    if (next.last >= 0 && !(ok = next_work(after))) break;
-                }
-                if (next.last > next.first) tile = pages.find(next.b, jn, next.lo, next.end);
-                if (some) {
-                    if (!copy(maps.cache.k, w.g, here)) break;
+            // A piece is announced before the one ahead of it is copied, and a
+            // tile's pages are looked up while the one before it is.
+            Load w, after;
+            ok = next_work(w);
+            int page = ok && w.last > w.first ? pages.look_up(w.b, w.first, w.lo, w.end) : 0;
+            while (ok && w.last >= 0) {
+                if (!(ok = next_work(after))) break;
+                for (int j = w.first; j < w.last; ++j) {
+                    const auto tile = pages.find(page, j, w.lo, w.end);
+                    const bool last = j + 1 == w.last;
+                    if (!last || after.last > after.first)
+                        page = pages.look_up(last ? after.b : w.b, last ? after.first : j + 1, last ? after.lo : w.lo, last ? after.end : w.end);
+                    if (!copy(maps.cache.k, w.g, tile)) break;
                     if (j == w.first && (!queries(ring[w.at], 0, nq0) || !queries(ring[w.at], 1, nq1))) break;
-                    if (!copy(maps.cache.v, w.g, here)) break;
+                    if (!copy(maps.cache.v, w.g, tile)) break;
                 }
-                w = next, j = jn;
-                if (w.last < 0) break;
+                if (w.last <= w.first && after.last > after.first) page = pages.look_up(after.b, after.first, after.lo, after.end);
+                w = after;
             }
             if (!ok && lane == 0) {
                 flag(p.c.status, kDevTimeout);
@@ -751,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 if (++buf == LY::kBufs) buf = 0, ++turn;
             };
             while ((ok = read_work(at)) && at->last >= 0) {
-                const Work w = *at;
+                const Work &w = *at;
                 volatile unsigned char *const found_odd = &odd[2 * ((nu - 1) % kWorks) + half];
                 if (lane == 0) *found_odd = 0;
                 __syncwarp();
@@ -766,33 +765,45 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                     if (!(ok = arrived())) break;  // the keys
                     release();
                     if (!(ok = arrived())) break;
-                    if (partly_seen(w, p.window, j)) {
+                    if (__builtin_expect(partly_seen(w, p.window, j), 0)) {
                         unsigned char *const values = smem + LY::kBuf + buf * LY::kTile;
+                        constexpr int kPieces = DK / 8, kAt = 32 / kPieces, kTurn = 2 * kAt;  // rows a warp, the two look at at once
                         bool found = false;
+                        const int piece = lane % kPieces, mine = kAt * half + lane / kPieces;
+                        const auto at_row = [&](int row) {
+                            return reinterpret_cast<uint4 *>(values + (piece / 8) * kPanel + row * 128 + (((piece % 8) ^ (row & 7)) * 16));
+                        };
                         // rows [r0, r1) of the tile, in turns of the two warps
                         const auto look = [&](int r0, int r1) {
-                            constexpr int kPieces = DK / 8, kAt = 32 / kPieces;  // rows a warp looks at at once
-                            const int piece = lane % kPieces;
-#pragma unroll 2
-                            for (int row = r0 + kAt * half + lane / kPieces; row < r1; row += 2 * kAt) {
-                                const int key = j * kKeys + row;
-                                uint4 *const v = reinterpret_cast<uint4 *>(values + (piece / 8) * kPanel + row * 128 +
-                                                                           (((piece % 8) ^ (row & 7)) * 16));
-                                if (key >= end || key < lo) {
-                                    *v = make_uint4(0u, 0u, 0u, 0u);
-                                } else if (any_odd<BF>(*v)) {
+#pragma unroll 1
+                            for (int r = r0 + mine; r < r1; r += 4 * kTurn) {
+                                uint4 v[4];
+                                bool some = false;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[i] = r + i * kTurn < r1 ? *at_row(r + i * kTurn) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) some = any_odd<BF>(v[i]) || some;
+                                if (__builtin_expect(some, 0)) {
                                     found = true;
-                                    *v = without_odd<BF>(*v);
+#pragma unroll 1
+                                    for (int row = r; row < min(r1, r + 4 * kTurn); row += kTurn) *at_row(row) = without_odd<BF>(*at_row(row));
                                 }
                             }
+                        };
+                        const auto clear = [&](int r0, int r1) {
+#pragma unroll 1
+                            for (int r = r0 + mine; r < r1; r += kTurn) *at_row(r) = make_uint4(0u, 0u, 0u, 0u);
                         };
                         // what some row sees and another does not lies behind the first row's own key, or before
                         // the last one's window
                         const bool a = j >= w.from[0] && j < w.to[0], b = j >= w.from[1] && j < w.to[1];
                         const int pos = a ? w.pos[0] : w.pos[1], last = b ? w.pos[1] + w.toks[1] : w.pos[0] + w.toks[0];
                         const int seen = p.window > 0 ? min(max(last - p.window - j * kKeys, 0), kKeys) : 0;
+                        const int r0 = min(max(lo - j * kKeys, 0), kKeys), r1 = min(max(end - j * kKeys, 0), kKeys);  // that some row sees
+                        clear(0, r0);
+                        clear(r1, kKeys);
 #pragma unroll 1
-                        for (int r = 0; r < 2; ++r) look(r ? max(max(pos + 1 - j * kKeys, 0), seen) : 0, r ? kKeys : seen);
+                        for (int r = 0; r < 2; ++r) look(r ? max(max(pos + 1 - j * kKeys, 0), seen) : r0, r ? r1 : seen);
                         if (found) *found_odd = 1;
                         fence_proxy_async_smem();
                     }
@@ -806,21 +817,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             }
         }
     } else if (warp >= 12) {
-        registers_down<104>();
+        registers_down<120>();
         // ---------------- outputs ----------------
         // Beside the next piece's products, whose first P V waits until O has
         // been read.  (By the softmax's own threads, a row each, a piece's end
         // took 8600 cycles where a key tile takes 2900.)
         const int warp_row = (warp & 3) * 32, m = warp_row + lane, tok = m / p.c.share, head = m - tok * p.c.share;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp_row) << 16);
-        int done0 = 0, done1 = 0, tiles0 = 0, tiles1 = 0, syncs = 0;  // of tile A, B: pieces with keys, key tiles
-        const auto group_sync = [&] {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kSync]);
-            const bool got = __all_sync(0xffffffffu, wait_on(&bars[kSync], syncs & 1));
-            ++syncs;
-            return got;
-        };
+        int done0 = 0, done1 = 0, tiles0 = 0, tiles1 = 0;  // of tile A, B: pieces with keys, key tiles
         const auto store = [&](const Work *at, int x) {
             const int from = at->from[x], to = at->to[x], toks = at->toks[x], pos = at->pos[x] + tok;
             if (toks <= 0) return true;
@@ -848,58 +852,45 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             const int64_t row = at->row[x] + tok;
             const int h = at->g * p.c.share + head;
             unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
-            const auto put_lse = [&](float top, float sum) {
-                if (p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * 0.6931471805599453f;
-            };
-            // rows r, r + 8 of the warp's are lane 4 (r % 8) ...'s: 4 lanes hold 8 columns of a row, and after a transposition among
-            // them each holds 8 of 32
-            const auto row_of = [&](int r) { return reinterpret_cast<unsigned short *>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(out), r)); };
             if (at->parts == 1) {
-                const float inv = pos < 0 ? 0.f : 1.f / l;
+                const float inv = 1.f / l;
+                const bool zero = to <= from || pos < 0, wide = flags & kWideOut;
+                const uint64_t inv2 = pair(inv, inv);
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const int ra = 16 * half + lane / 4, q = lane & 3;
-                    unsigned short *const out_a = row_of(ra) + 8 * q, *const out_b = row_of(ra + 8) + 8 * q;
-                    const float inv_a = __shfl_sync(0xffffffffu, inv, ra), inv_b = __shfl_sync(0xffffffffu, inv, ra + 8);
-                    const uint32_t there = __ballot_sync(0xffffffffu, mine), none = __ballot_sync(0xffffffffu, pos < 0);
-                    const bool a = there >> ra & 1, b = there >> (ra + 8) & 1, zero_a = none >> ra & 1, zero_b = none >> (ra + 8) & 1;
-#pragma unroll 1
-                    for (int c = 0; c < p.c.D; c += 32) {
-                        uint32_t r[16];
-                        if (to > from) {
-                            tmem_ld_16x256b_x4(colO + (static_cast<uint32_t>(16 * half) << 16) + c, r);
-                            tmem_wait_ld();
+                for (int c = 0; c < p.c.D; c += 32) {
+                    uint32_t r[32], u[16];
+                    if (to > from) {
+                        tmem_ld32(colO + c, r);
+                        tmem_wait_ld();
+                    }
+                    if (c + 32 >= p.c.D) o_read();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 f = unpair(mul2(pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), inv2));
+                        u[i] = zero ? 0u : pack2<BF>(f.x, f.y);
+                    }
+                    // a row a thread: 32 bytes at a time where the rows lie for that, so that every sector is written at once
+#pragma unroll
+                    for (int i = 0; i < 16; i += 8) {
+                        const int at = c + 2 * i;
+                        if (!mine || at >= p.c.D) continue;
+                        if (wide && at + 16 <= p.c.D) {
+                            store32(out + at, u + i);
                         } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = 0u;
-                        }
-                        uint32_t u[4], v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            u[i] = zero_a ? 0u : pack2<BF>(__uint_as_float(r[4 * i]) * inv_a, __uint_as_float(r[4 * i + 1]) * inv_a);
-                            v[i] = zero_b ? 0u : pack2<BF>(__uint_as_float(r[4 * i + 2]) * inv_b, __uint_as_float(r[4 * i + 3]) * inv_b);
-                        }
-                        quad_transpose(u);
-                        quad_transpose(v);
-                        if (c + 8 * q < p.c.D) {
-                            if (a) *reinterpret_cast<uint4 *>(out_a + c) = make_uint4(u[0], u[1], u[2], u[3]);
-                            if (b) *reinterpret_cast<uint4 *>(out_b + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<uint4 *>(out + at) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                            if (at + 8 < p.c.D) *reinterpret_cast<uint4 *>(out + at + 8) = make_uint4(u[i + 4], u[i + 5], u[i + 6], u[i + 7]);
                         }
                     }
                 }
-                o_read();
-                if (mine) put_lse(ref, l);
+                if (mine && p.lse) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : lse_of(ref, l);
                 if (__builtin_expect(fix, 0)) {
                     __syncwarp();
                     if (mine) add_odd<BF>(p, *at, x, pos, out);
                 }
                 return true;
             }
-            // This part's O, l and reference; the last part to arrive joins them all.
-            const auto part_at = [&](int part) {
-                return plan.parts + (((static_cast<int64_t>(at->slot) + part) * p.c.G + at->g) * 2 + x) * (kRows * (DK + 2));
-            };
-            float *const part = part_at(at->part);  // O as [DK / 4][kRows][4]
+            // this part's O, l and reference, for the kernel that joins the parts
+            float *const part = part_at<DK>(plan, p.c.G, at->slot + at->part, at->g, x);  // O as [DK / 4][kRows][4]
 #pragma unroll 1
             for (int c = 0; c < DK; c += 16) {
                 uint32_t r[16];
@@ -918,53 +909,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             part[kRows * DK + m] = l;
             part[kRows * DK + kRows + m] = ref;
             if (__builtin_expect(fix, 0) && mine) add_odd<BF>(p, *at, x, pos, part + m * 4);
-            __threadfence();
-            if (!group_sync()) return false;
-            if (m == 0) *is_last = atomicAdd(&plan.counters[(static_cast<int64_t>(at->count) * p.c.G + at->g) * 2 + x], 1) == at->parts - 1;
-            if (!group_sync()) return false;
-            if (!*is_last) return true;
-            __threadfence();
-            const int parts = at->parts;
-            const auto stat_of = [&](int i, int r, int k) { return __ldcg(part_at(i) + kRows * DK + k * kRows + r); };
-            {
-                float top = -INFINITY, sum = 0.f;
-#pragma unroll 1
-                for (int i = 0; i < parts; ++i) top = fmaxf(top, stat_of(i, m, 1));
-#pragma unroll 1
-                for (int i = 0; i < parts; ++i) {
-                    const float r = stat_of(i, m, 1);
-                    sum += stat_of(i, m, 0) * (r == -INFINITY ? 0.f : ex2(r - top));
-                }
-                l = sum, ref = top;
-                if (mine) put_lse(ref, l);
-            }
-            const float inv = 1.f / l;
-#pragma unroll 1
-            for (int r = lane / 4; r < 32; r += 8) {
-                unsigned short *const to_row = row_of(r);
-                const float top = __shfl_sync(0xffffffffu, ref, r), by = __shfl_sync(0xffffffffu, inv, r);
-                const bool there = __shfl_sync(0xffffffffu, mine, r), none = __shfl_sync(0xffffffffu, pos, r) < 0;
-                constexpr int kN = DK / 16;  // four columns of every 16
-                const int c = 4 * (lane & 3);
-                float4 v[kN] = {};
-#pragma unroll 1
-                for (int i = 0; i < parts; ++i) {
-                    const float s = stat_of(i, warp_row + r, 1);
-                    float4 o[kN];
-#pragma unroll
-                    for (int k = 0; k < kN; ++k)  // (columns past the head size hold anything)
-                        o[k] = __ldcg(reinterpret_cast<const float4 *>(part_at(i) + ((c / 4 + 4 * k) * kRows + warp_row + r) * 4));
-                    const float f = s == -INFINITY ? 0.f : ex2(s - top);
-#pragma unroll
-                    for (int k = 0; k < kN; ++k) v[k].x += o[k].x * f, v[k].y += o[k].y * f, v[k].z += o[k].z * f, v[k].w += o[k].w * f;
-                }
-#pragma unroll
-                for (int k = 0; k < kN; ++k)
-                    if (there && c + 16 * k < p.c.D)
-                        *reinterpret_cast<uint2 *>(to_row + c + 16 * k) =
-                            none ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[k].x * by, v[k].y * by), pack2<BF>(v[k].z * by, v[k].w * by));
-                __syncwarp();
-            }
             return true;
         };
         const Work *at;
@@ -976,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             *abort_flag = 1;
         }
     } else {
-        registers_up<152>();
+        registers_up<144>();
         // ---------------- softmax (thread = row of tile x) ----------------
         const int x = warp >> 2, m = tid & (kRows - 1), tok = m / p.c.share;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -993,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kSFull0 + x], ns & 1)))) break;
                 tc_fence_after();
                 if (live) {
-                    if (!sees_all(p.window, pos0, toks, j)) {
+                    if (__builtin_expect(!sees_all(p.window, pos0, toks, j), 0)) {
                         // (in place and in a loop: rarely run code must not stretch this path)
 #pragma unroll 1
                         for (int c = 0; c < kKeys; c += 32) {
@@ -1024,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                     }
                     const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
                     const bool moves = now > ref + kSlack;
-                    if (__any_sync(0xffffffffu, moves)) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, moves), 0)) {
                         const float back = moves ? ex2(ref - now) : 1.f;
                         if (moves) ref = now, l *= back;
                         if (j > from) {
@@ -1086,30 +1030,74 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     if (warp == 8) tmem_dealloc512(tmem);
 }
 
+// The parts of units that were cut, joined in the order of the keys: a warp
+// eight rows of a tile, four lanes a row.  (By the CTA that stored a unit's last
+// part, with one warp's loads in flight on a scheduler, a join took up to 140 us.)
+template <int DK, bool BF>
+__global__ void __launch_bounds__(128) attend_tiles_join_kernel(const AttendParams p, const Plan plan) {
+    constexpr int kGroups = kRows / 8;
+    const int lane = threadIdx.x & 31, G = p.c.G, tt = tile_tokens(p.c);
+    const int64_t items = static_cast<int64_t>(plan.head->cuts) * G * 2 * kGroups;
+    for (int64_t i = blockIdx.x * 4 + (threadIdx.x >> 5); i < items; i += gridDim.x * 4) {
+        const int group = static_cast<int>(i % kGroups), x = static_cast<int>(i / kGroups % 2), g = static_cast<int>(i / (2 * kGroups) % G);
+        const Piece q = plan.pieces[plan.cuts[i / (2 * kGroups * G)]];
+        const int m = 8 * group + lane / 4, tok = m / p.c.share, t0 = (2 * q.pair + x) * tt + tok;
+        if (tok >= tt || t0 >= q.n) continue;
+        const int pos = q.kv - q.n + t0;
+        float top = -INFINITY;
+        for (int k = 0; k < q.parts; ++k) top = fmaxf(top, part_at<DK>(plan, G, q.slot + k, g, x)[kRows * (DK + 1) + m]);
+        float sum = 0.f;
+        float4 v[DK / 16] = {};  // columns 16 c + 4 (lane % 4) ...
+        for (int k = 0; k < q.parts; ++k) {
+            const float *const part = part_at<DK>(plan, G, q.slot + k, g, x);
+            const float ref = part[kRows * (DK + 1) + m], f = ref == -INFINITY ? 0.f : ex2(ref - top);
+            sum += part[kRows * DK + m] * f;
+#pragma unroll
+            for (int c = 0; c < DK / 16; ++c) {  // (columns past the head size hold anything)
+                const float4 o = *reinterpret_cast<const float4 *>(part + ((4 * c + (lane & 3)) * kRows + m) * 4);
+                v[c].x += o.x * f, v[c].y += o.y * f, v[c].z += o.z * f, v[c].w += o.w * f;
+            }
+        }
+        const float inv = 1.f / sum;
+        const int64_t row = q.row0 + t0;
+        const int h = g * p.c.share + (m - tok * p.c.share);
+        unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) {
+            const int at = 16 * c + 4 * (lane & 3);
+            if (at < p.c.D)
+                *reinterpret_cast<uint2 *>(out + at) =
+                    pos < 0 ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[c].x * inv, v[c].y * inv), pack2<BF>(v[c].z * inv, v[c].w * inv));
+        }
+        if (p.lse && (lane & 3) == 0) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : lse_of(top, sum);
+    }
+}
+
 constexpr int64_t kSlots = 1024;  // parts of cut units, all heads together
 
 struct Split {
     int64_t units, slots;  // most units; most parts of cut ones (a head)
-    uint64_t at_units, at_pieces, at_counters, at_parts, bytes;
+    uint64_t at_units, at_pieces, at_cuts, at_parts, bytes;
 };
-Split split_of(const PagedParams &c) {
+Split split_of(const PagedParams &c, int64_t max_kv_len) {
     const auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
     Split s{};
     const int64_t pair = 2 * (kRows / c.share);
     s.units = c.rows / pair + c.nseq;  // >= sum of ceil(n / pair)
     const int64_t few = kMaxParts * s.units;
-    s.slots = kSlots / c.G < few ? kSlots / c.G : few;
+    // (a few key tiles are not worth cutting: 3 us for the joining kernel, a part's own cost)
+    s.slots = max_kv_len > 0 && max_kv_len <= 8 * kKeys ? 0 : kSlots / c.G < few ? kSlots / c.G : few;
     const uint64_t dk = c.D <= 64 ? 64 : 128;
     s.at_units = up(sizeof(PlanHead));
     s.at_pieces = s.at_units + up(s.units * sizeof(Piece));
-    s.at_counters = s.at_pieces + up((s.units + s.slots) * sizeof(Piece));
-    s.at_parts = s.at_counters + up(s.slots * c.G * 2 * sizeof(int32_t));
+    s.at_cuts = s.at_pieces + up((s.slots > 0 ? s.units + s.slots : 0) * sizeof(Piece));
+    s.at_parts = s.at_cuts + up(s.slots * sizeof(int32_t));
     s.bytes = s.at_parts + up(static_cast<uint64_t>(s.slots) * c.G * 2 * kRows * (dk + 2) * sizeof(float));
     return s;
 }
 
 template <int DK, bool BF>
-cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream) {
+cudaError_t launch_t(const AttendParams &p, int64_t max_kv_len, void *workspace, cudaStream_t stream) {
     // Before the maps: their encoder is a driver call and refuses a host thread
     // that has no context yet, which this one gives it.
     cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes);
@@ -1118,30 +1106,33 @@ cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream
     if (!encode_queries(&maps.q, p.c, kRows / p.c.share) || !encode_cache(&maps.cache, p.c, kKeys)) return cudaErrorInvalidValue;
     const int sms = device_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const Split s = split_of(p.c);
+    const bool wide = reinterpret_cast<uintptr_t>(p.c.out) % 32 == 0 && (p.c.rows == 1 || p.c.os[0] % 16 == 0) && (p.c.H == 1 || p.c.os[1] % 16 == 0);
+    const Split s = split_of(p.c, max_kv_len);
     unsigned char *const at = static_cast<unsigned char *>(workspace);
     Plan plan{};
     plan.head = reinterpret_cast<PlanHead *>(at);
     plan.units = reinterpret_cast<Piece *>(at + s.at_units);
     plan.pieces = reinterpret_cast<Piece *>(at + s.at_pieces);
-    plan.counters = reinterpret_cast<int32_t *>(at + s.at_counters);
+    plan.cuts = reinterpret_cast<int32_t *>(at + s.at_cuts);
     plan.parts = reinterpret_cast<float *>(at + s.at_parts);
     plan.max_units = static_cast<int32_t>(s.units);
     plan.max_slots = static_cast<int32_t>(s.slots);
     attend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, sms);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attend_tiles_kernel<DK, BF><<<sms, kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan, least_box(p.c, kKeys));
+    attend_tiles_kernel<DK, BF><<<sms, kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan, least_box(p.c, kKeys), wide ? kWideOut : 0);
+    if ((e = cudaGetLastError()) != cudaSuccess || s.slots == 0) return e;
+    attend_tiles_join_kernel<DK, BF><<<8 * sms, 128, 0, stream>>>(p, plan);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-uint64_t attend_tiles_workspace(const PagedParams &c) { return split_of(c).bytes; }
+uint64_t attend_tiles_workspace(const PagedParams &c, int64_t max_kv_len) { return split_of(c, max_kv_len).bytes; }
 
-cudaError_t launch_attend_tiles(const AttendParams &p, void *workspace, cudaStream_t stream) {
+cudaError_t launch_attend_tiles(const AttendParams &p, int64_t max_kv_len, void *workspace, cudaStream_t stream) {
     const bool bf = p.c.io_dtype == kBF16;
-    if (p.c.D <= 64) return bf ? launch_t<64, true>(p, workspace, stream) : launch_t<64, false>(p, workspace, stream);
-    return bf ? launch_t<128, true>(p, workspace, stream) : launch_t<128, false>(p, workspace, stream);
+    if (p.c.D <= 64) return bf ? launch_t<64, true>(p, max_kv_len, workspace, stream) : launch_t<64, false>(p, max_kv_len, workspace, stream);
+    return bf ? launch_t<128, true>(p, max_kv_len, workspace, stream) : launch_t<128, false>(p, max_kv_len, workspace, stream);
 }
 
 }  // namespace ssu
