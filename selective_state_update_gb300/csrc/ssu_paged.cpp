@@ -94,7 +94,7 @@ AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv
     AttendPlan a{};
     a.max_kv_len = max_kv_len;
     int64_t longest = p.c.cu == nullptr ? 1 : max_seqlen > 0 ? max_seqlen : (p.c.rows + p.c.nseq - 1) / p.c.nseq;
-    a.kind = longest * p.c.share <= 16 ? kAttendRows16 : longest * p.c.share <= 32 ? kAttendRows32 : kAttendTiles;
+    a.kind = longest * p.c.share <= 16 ? kAttendRows16 : longest * p.c.share <= 32 ? kAttendRows32 : longest * p.c.share <= 64 ? kAttendRows64 : kAttendTiles;
     a.bytes = a.kind == kAttendTiles ? attend_tiles_workspace(p.c, max_kv_len) : attend_rows_workspace(a.kind, p.c.D);
     return a;
 }

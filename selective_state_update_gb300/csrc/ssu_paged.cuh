@@ -48,21 +48,48 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst_smem, const void *map, 
         : "memory");
 }
 
+// Division by a page's length: by its reciprocal, rounded down, which is at most
+// one too small for numbers below 2^30.
+struct PageDivider {
+    uint32_t page, inverse;
+    __device__ __forceinline__ explicit PageDivider(int p) : page(p), inverse(0xffffffffu / static_cast<uint32_t>(p)) {}
+    __device__ __forceinline__ int divide(int n, int &rest) const {
+        uint32_t q = __umulhi(static_cast<uint32_t>(n), inverse), r = static_cast<uint32_t>(n) - q * page;
+        if (r >= page) ++q, r -= page;
+        rest = static_cast<int>(r);
+        return static_cast<int>(q);
+    }
+};
+
 // Copies tiles of KEYS keys or values, PANELS x 64 elements wide, from their
 // pages, a lane each box.  What there is to copy is found ahead of the wait for a
-// place to put it.
+// place to put it, with little arithmetic: one warp does it, an instruction at a
+// time.  (With divisions and the general case for every tile, single tokens took
+// 1.6 us a tile of 64 keys on every CTA whatever its size.)
 template <int KEYS, int PANELS>
 struct PageCopier {
     static constexpr int kPanelBytes = KEYS * 128;
     const PagedParams &p;
     int least;  // what tiles are rounded to
+    PageDivider by_page;
+    bool regular;              // every box of a tile is `least` rows of a page of its own, or the tile lies within one page
+    int box, x, at, dst;       // this lane's box where that is so: its map, element, first row of the tile; where it goes
     struct Tile {
         uint32_t bytes;
-        int page;        // this lane's: entry `first` + lane of the table
+        int page;        // this lane's: entry `first` + lane of the table; where regular, its box's
         int box, x, y;   // this lane's box: its map (-1: none), element, row of the page
         int entry, dst;  // ... whose page which lane has, and where it goes
     };
-    __device__ __forceinline__ PageCopier(const PagedParams &params, int box) : p(params), least(box) {}
+    __device__ __forceinline__ PageCopier(const PagedParams &params, int least_rows)
+        : p(params), least(least_rows), by_page(params.page) {
+        const int lane = threadIdx.x & 31;
+        regular = least == KEYS || least == p.page;
+        const int halves = PANELS == 2 && !(least == KEYS && p.D == 128) ? 2 : 1, half = lane % halves;
+        at = lane / halves * least;
+        box = at < KEYS ? 28 - __clz(least) : -1;
+        x = 64 * half;
+        dst = half * kPanelBytes + at * 128;
+    }
     // The rows [from, to) of tile j that some query sees, where it sees the keys [lo, end).
     __device__ __forceinline__ void rows(int j, int lo, int end, int &from, int &to) const {
         to = min((max(end - j * KEYS, 0) + least - 1) & -least, KEYS);
@@ -71,10 +98,16 @@ struct PageCopier {
     // This lane's page of tile j of sequence b; the number is on its way when
     // this returns.
     __device__ __forceinline__ int look_up(int64_t b, int j, int lo, int end) const {
-        int from, to;
+        int from, to, rest;
         rows(j, lo, end, from, to);
-        const int entry = (j * KEYS + from) / p.page + (threadIdx.x & 31);
-        if (to <= from || entry * static_cast<int64_t>(p.page) >= j * KEYS + to) return 0;
+        int entry;
+        if (regular) {
+            entry = by_page.divide(j * KEYS + at, rest);
+            if (at < from || at >= to) return 0;
+        } else {
+            entry = by_page.divide(j * KEYS + from, rest) + (threadIdx.x & 31);
+            if (to <= from || entry * static_cast<int64_t>(p.page) >= j * KEYS + to) return 0;
+        }
         const int64_t page = table_page(p, b, entry);
         return static_cast<int>(page < 0 ? p.pages : page);  // past the last page the copies read zeros
     }
@@ -86,26 +119,32 @@ struct PageCopier {
         Tile t;
         t.bytes = static_cast<uint32_t>(to - from) * (128 * PANELS);
         t.page = page;
-        int y = (j * KEYS + from) % p.page;
+        if (regular) {
+            by_page.divide(j * KEYS + at, t.y);
+            t.box = at >= from && at < to ? box : -1, t.x = x, t.entry = lane, t.dst = dst;
+            return t;
+        }
         t.box = -1, t.x = 0, t.y = 0, t.entry = 0, t.dst = 0;
+        int y;
+        by_page.divide(j * KEYS + from, y);
         // the largest boxes that the pages' ends allow: 32 at most, as many as pages of 8 tokens take
 #pragma unroll 1
-        for (int at = from, entry = 0, op = 0; at < to;) {
-            const int h = 31 - __clz(min(min(to - at, p.page - y), KEYS)), rows = 1 << h;
+        for (int row = from, entry = 0, op = 0; row < to;) {
+            const int h = 31 - __clz(min(min(to - row, p.page - y), KEYS)), count = 1 << h;
             // (a box of KEYS rows has both halves of 128 elements)
-            const int ops = PANELS == 2 && !(rows == KEYS && p.D == 128) ? 2 : 1;
+            const int ops = PANELS == 2 && !(count == KEYS && p.D == 128) ? 2 : 1;
             if (lane >= op && lane < op + ops) {
                 const int half = lane - op;
-                t.box = h - 3, t.x = 64 * half, t.y = y, t.entry = entry, t.dst = half * kPanelBytes + at * 128;
+                t.box = h - 3, t.x = 64 * half, t.y = y, t.entry = entry, t.dst = half * kPanelBytes + row * 128;
             }
-            op += ops, at += rows, y += rows;
+            op += ops, row += count, y += count;
             if (y == p.page) y = 0, ++entry;
         }
         return t;
     }
-    __device__ __forceinline__ void copy(const Tile &t, const CUtensorMap *maps, int g, uint32_t dst, uint64_t *bar) const {
+    __device__ __forceinline__ void copy(const Tile &t, const CUtensorMap *maps, int g, uint32_t to, uint64_t *bar) const {
         const int page = __shfl_sync(0xffffffffu, t.page, t.entry);
-        if (t.box >= 0) tma_load_5d(dst + t.dst, maps + t.box, t.x, t.y, 0, g, page, bar);
+        if (t.box >= 0) tma_load_5d(to + t.dst, maps + t.box, t.x, t.y, 0, g, page, bar);
         __syncwarp();
     }
 };

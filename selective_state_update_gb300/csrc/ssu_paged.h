@@ -55,7 +55,7 @@ struct AttendPlan {
     int64_t max_kv_len;
     uint64_t bytes;
 };
-enum : int32_t { kAttendRows16 = 0, kAttendRows32 = 1, kAttendTiles = 2 };
+enum : int32_t { kAttendRows16 = 0, kAttendRows32 = 1, kAttendRows64 = 2, kAttendTiles = 3 };
 AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv_len);
 cudaError_t launch_paged_attention(const AttendParams &p, const AttendPlan &plan, void *workspace, cudaStream_t stream);
 cudaError_t launch_attend_rows(const AttendParams &p, int kind, void *workspace, cudaStream_t stream);

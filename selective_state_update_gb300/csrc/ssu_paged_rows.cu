@@ -19,8 +19,9 @@
 // itself, in one block-wide sum: no plan, no counters, nothing to be cleared.
 //
 // One warp has the pages copied into a ring of stages by the TMA engine; four
-// warps take 16 keys of a stage each (mma.sync 16 x 8 x 16: the products are
-// far from the bound, and a quarter of a 128-row tcgen05 tile would be used).
+// warps take 16 rows by the keys of a stage, or by a half or a quarter of them
+// (mma.sync 16 x 8 x 16: the products are far from the bound, and at most half of
+// a 128-row tcgen05 tile would be used).
 #include "ssu_paged.cuh"
 #include "ssu_tcgen05.cuh"
 
@@ -36,20 +37,21 @@ constexpr int kCtas = 2;              // per SM
 
 template <int DK, int MT>
 struct Layout {
-    static constexpr int kPanels = DK / 64;
+    static constexpr int kPanels = (DK + 63) / 64;
     static constexpr int kRows = 16 * MT;
     static constexpr int kStageBytes = 2 * kPanels * kPanel;
     static constexpr int kStages = DK == 64 ? 6 : 3;
-    static constexpr int kQ = kStages * kStageBytes;                 // [kRows][DK], 16-byte pieces swapped by row
+    static constexpr int kQ = kStages * kStageBytes;                 // [kRows][64 kPanels], 16-byte pieces swapped by row
+    static constexpr int kQRow = kPanels * 128;
     static constexpr int kSlice = 32 / MT;                           // columns joined at a time
-    static constexpr int kJoin = kQ;                                 // [kWarps][kRows][kSlice] fp32, once the queries are done with
-    static constexpr int kJoinBytes = kWarps * kRows * kSlice * 4;
-    static constexpr int kML = kQ + (kRows * DK * 2 > kJoinBytes ? kRows * DK * 2 : kJoinBytes);  // [kWarps][kRows][2]
-    static constexpr int kBar = kML + kWarps * kRows * 8;
+    static constexpr int kJoin = kQ;                                 // [kWarps / MT][kRows][kSlice] fp32, once the queries are done with
+    static constexpr int kJoinBytes = kWarps / MT * kRows * kSlice * 4;
+    static constexpr int kML = kQ + (kRows * kQRow > kJoinBytes ? kRows * kQRow : kJoinBytes);  // [kWarps / MT][kRows][2]
+    static constexpr int kBar = kML + kWarps / MT * kRows * 8;
     static constexpr int kMisc = kBar + 16 * kStages;
     static constexpr int kBytes = kMisc + 128;
     static constexpr int kPart = kRows * (DK + 2);                   // floats of a part in the workspace: o, l, m
-    static_assert(kBytes <= (227 * 1024) / kCtas - 1024, "shared memory");
+    static_assert(kBytes <= (228 * 1024) / kCtas - 1024, "shared memory");  // (1 KB of an SM's goes with every CTA)
 };
 
 // What the second kernel has to know of a CTA's first run: the row tile that it
@@ -246,7 +248,7 @@ __device__ __forceinline__ void store_lse(const AttendParams &p, const Seq &s, i
     if (p.lse) p.lse[(s.t0 + m / p.c.share) * p.c.H + g * p.c.share + m % p.c.share] = lse;
 }
 
-// DK: the head size, rounded up to 64; MT: row tiles of 16; BF: bf16.
+// DK: the head size, rounded up to 64, 96 or 128; MT: row tiles of 16; BF: bf16.
 template <int DK, int MT, bool BF>
 __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const AttendParams p, const __grid_constant__ CacheMaps maps,
                                                                       int box, Joint *joints, float *parts) {
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
         return;
     }
 
-    // ---------------- consumers: warp w has keys 16 w ... of a stage ----------------
+    // ---------------- consumers ----------------
     const uint32_t s0 = smem_addr(smem);
     float *const join = reinterpret_cast<float *>(smem + LY::kJoin);
     float2 *const ml = reinterpret_cast<float2 *>(smem + LY::kML);
@@ -332,37 +334,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p.c.q) + (s.t0 + m / p.c.share) * p.c.qs[0] +
                                                           (g * p.c.share + m % p.c.share) * p.c.qs[1] + 8 * piece));
             }
-            *reinterpret_cast<uint4 *>(smem + LY::kQ + row * DK * 2 + ((piece ^ (row & 7)) * 16)) = v;
+            *reinterpret_cast<uint4 *>(smem + LY::kQ + row * LY::kQRow + ((piece ^ (row & 7)) * 16)) = v;
         }
         named_barrier(1, 32 * kWarps);
-        uint32_t q[MT == 1 ? DK / 16 : 1][4];
-        const auto load_q = [&](int mt, int k, uint32_t *a) {
-            const int row = 16 * mt + (lane & 15), piece = 2 * k + (lane >> 4);
-            ldmatrix_x4(s0 + LY::kQ + row * DK * 2 + ((piece ^ (row & 7)) * 16), a);
-        };
-        if constexpr (MT == 1)
+        // this warp's 16 rows, and its keys of a tile: 16 of every MT x 16 that it shares with the warps of the other rows
+        const int row0 = 16 * (warp % MT), keys0 = 16 * MT * (warp / MT);
+        uint32_t q[DK / 16][4];
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) load_q(0, k, q[k]);
-        // this thread's rows: lane / 4 and lane / 4 + 8 of each 16
-        int hi[MT][2], lo[MT][2];  // they see keys [lo, hi)
-        float mx[MT][2], sum[MT][2], o[MT][DK / 8][4];
+        for (int k = 0; k < DK / 16; ++k) {
+            const int row = row0 + (lane & 15), piece = 2 * k + (lane >> 4);
+            ldmatrix_x4(s0 + LY::kQ + row * LY::kQRow + ((piece ^ (row & 7)) * 16), q[k]);
+        }
+        // this thread's rows: lane / 4 and lane / 4 + 8 of those
+        float mx[2], sum[2], o[DK / 8][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) mx[h] = -INFINITY, sum[h] = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = min(16 * mt + 8 * h + lane / 4, rows - 1);
-                const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
-                hi[mt][h] = pos + 1;
-                lo[mt][h] = p.window > 0 ? pos + 1 - p.window : 0;
-                mx[mt][h] = -INFINITY;
-                sum[mt][h] = 0.f;
-            }
+        for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
         for (int i = from; i < to; ++i, ++it) {
             const int st = it % LY::kStages;
@@ -370,38 +360,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint32_t sk = s0 + st * LY::kStageBytes, sv = sk + LY::kPanels * kPanel;
-            const int key0 = (r.first + i) * kKeys, mine = key0 + 16 * warp;
+            const int key0 = (r.first + i) * kKeys;
             // all rows see all of the tile?
             const bool masked = key0 + kKeys > r.pos_lo + 1 || (p.window > 0 && key0 < r.pos_hi + 1 - p.window);
-            float x[MT][2][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[mt][n][j] = 0.f;
-#pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {
-                uint32_t b[4];
-                ldmatrix_x4(sk + place(16 * warp + (lane & 7) + ((lane >> 4) << 3), 16 * k + ((lane >> 3) & 1) * 8), b);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t a[4];
-                    if constexpr (MT > 1) load_q(mt, k, a);
-                    mma16816<BF>(x[mt][0], MT == 1 ? q[k] : a, b);
-                    mma16816<BF>(x[mt][1], MT == 1 ? q[k] : a, b + 2);
-                }
-            }
             if (masked) {
                 // Values that some row does not see must not reach it by a zero
                 // of P: what no row sees becomes zeros, and so do infinities
                 // and NaN, which are added to the rows that see them at the end.
+                // (A warp its own keys, or its part of those it shares.)
                 unsigned char *const values = smem + st * LY::kStageBytes + LY::kPanels * kPanel;
                 const bool partly = r.pos_lo != r.pos_hi;
                 bool odd = false;
                 for (int e = lane; e < 16 * (DK / 8); e += 32) {
-                    const int row = e / (DK / 8), key = mine + row;
-                    uint4 *const v = reinterpret_cast<uint4 *>(values + place(16 * warp + row, 8 * (e % (DK / 8))));
+                    const int row = 16 * warp + e / (DK / 8), key = key0 + row;
+                    uint4 *const v = reinterpret_cast<uint4 *>(values + place(row, 8 * (e % (DK / 8))));
                     if (key >= r.end || key < r.lo) {
                         *v = make_uint4(0u, 0u, 0u, 0u);
                     } else if (partly && any_odd<BF>(*v)) {
@@ -411,49 +383,64 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                 }
                 if (odd) *odd_flag = 1;
                 fence_proxy_async_smem();  // before the stage's next copy
-                __syncwarp();
+                if (MT == 1) __syncwarp();
+                else named_barrier(1, 32 * kWarps);
             }
-            // P and the running maximum and sum
-            uint32_t pa[MT][4];
+#pragma unroll 1
+            for (int sub = 0; sub < MT; ++sub) {
+                const int mine = keys0 + 16 * sub;
+                float x[2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k) {
+                    uint32_t b[4];
+                    ldmatrix_x4(sk + place(mine + (lane & 7) + ((lane >> 4) << 3), 16 * k + ((lane >> 3) & 1) * 8), b);
+                    mma16816<BF>(x[0], q[k], b);
+                    mma16816<BF>(x[1], q[k], b + 2);
+                }
+                // P and the running maximum and sum
+                uint32_t pa[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float e[4] = {x[mt][0][2 * h] * scale, x[mt][0][2 * h + 1] * scale, x[mt][1][2 * h] * scale,
-                                  x[mt][1][2 * h + 1] * scale};
-                    if (masked)
+                    float e[4] = {x[0][2 * h] * scale, x[0][2 * h + 1] * scale, x[1][2 * h] * scale, x[1][2 * h + 1] * scale};
+                    if (masked) {
+                        // (the row's position, found here: kept it would cost registers on every tile)
+                        const int row = min(row0 + 8 * h + lane / 4, rows - 1);
+                        const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int key = mine + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
-                            if (key >= hi[mt][h] || key < lo[mt][h]) e[j] = -INFINITY;
+                            const int key = key0 + mine + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+                            if (key > pos || (p.window > 0 && key + p.window <= pos)) e[j] = -INFINITY;
                         }
+                    }
                     float top = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    top = fmaxf(top, mx[mt][h]);
-                    const float base = top == -INFINITY ? 0.f : top, back = ex2(mx[mt][h] - base);
-                    mx[mt][h] = top;
+                    top = fmaxf(top, mx[h]);
+                    const float base = top == -INFINITY ? 0.f : top, back = ex2(mx[h] - base);
+                    mx[h] = top;
                     float add = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         e[j] = ex2(e[j] - base);
                         add += e[j];
                     }
-                    sum[mt][h] = sum[mt][h] * back + add;
+                    sum[h] = sum[h] * back + add;
                     if (back != 1.f)
 #pragma unroll
-                        for (int n = 0; n < DK / 8; ++n) o[mt][n][2 * h] *= back, o[mt][n][2 * h + 1] *= back;
-                    pa[mt][h] = pack2<BF>(e[0], e[1]);
-                    pa[mt][2 + h] = pack2<BF>(e[2], e[3]);
+                        for (int n = 0; n < DK / 8; ++n) o[n][2 * h] *= back, o[n][2 * h + 1] *= back;
+                    pa[h] = pack2<BF>(e[0], e[1]);
+                    pa[2 + h] = pack2<BF>(e[2], e[3]);
                 }
 #pragma unroll
-            for (int n = 0; n < DK / 16; ++n) {
-                uint32_t b[4];
-                ldmatrix_x4_t(sv + place(16 * warp + (lane & 15), 16 * n + ((lane >> 4) << 3)), b);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816<BF>(o[mt][2 * n], pa[mt], b);
-                    mma16816<BF>(o[mt][2 * n + 1], pa[mt], b + 2);
+                for (int n = 0; n < DK / 16; ++n) {
+                    uint32_t b[4];
+                    ldmatrix_x4_t(sv + place(mine + (lane & 15), 16 * n + ((lane >> 4) << 3)), b);
+                    mma16816<BF>(o[2 * n], pa, b);
+                    mma16816<BF>(o[2 * n + 1], pa, b + 2);
                 }
             }
             __syncwarp();
@@ -464,32 +451,29 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
 
         // ---------------- the warps' parts joined ----------------
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float t = sum[mt][h];
-                t += __shfl_xor_sync(0xffffffffu, t, 1);
-                t += __shfl_xor_sync(0xffffffffu, t, 2);
-                if ((lane & 3) == 0) ml[warp * R + 16 * mt + 8 * h + lane / 4] = make_float2(mx[mt][h], t);
-            }
+        for (int h = 0; h < 2; ++h) {
+            float t = sum[h];
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            if ((lane & 3) == 0) ml[warp / MT * R + row0 + 8 * h + lane / 4] = make_float2(mx[h], t);
+        }
         named_barrier(1, 32 * kWarps);
+        constexpr int kSets = kWarps / MT;  // warps that share a row
         const auto top_of = [&](int row) {
             float m = ml[row].x;
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, ml[w * R + row].x);
+            for (int w = 1; w < kSets; ++w) m = fmaxf(m, ml[w * R + row].x);
             return m;
         };
         const bool whole = from == 0 && to == r.count, odd = *odd_flag != 0;
         // (the part of a cut run: a continuation is its CTA's first run, another its last)
         float *const part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (from > 0 ? 0 : 1)) * LY::kPart;
-        float down[MT][2];
+        float down[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float m = top_of(16 * mt + 8 * h + lane / 4);
-                down[mt][h] = mx[mt][h] == -INFINITY ? 0.f : ex2(mx[mt][h] - m);
-            }
+        for (int h = 0; h < 2; ++h) {
+            const float m = top_of(row0 + 8 * h + lane / 4);
+            down[h] = mx[h] == -INFINITY ? 0.f : ex2(mx[h] - m);
+        }
         // a thread takes kWide columns of one row of each slice
         constexpr int kWide = R * LY::kSlice / (32 * kWarps), kAcross = LY::kSlice / kWide;
         static_assert(kWide == 4, "a thread's columns");
@@ -497,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
         const float m = top_of(row);
         float l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kSets; ++w) {
             const float2 f = ml[w * R + row];
             l += f.y * (f.x == -INFINITY ? 0.f : ex2(f.x - m));  // (a sum without a maximum is 0 or NaN)
         }
@@ -506,17 +490,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
 #pragma unroll
         for (int c = 0; c < DK; c += LY::kSlice) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int n = c / 8; n < (c + LY::kSlice) / 8; ++n)
 #pragma unroll
-                for (int n = c / 8; n < (c + LY::kSlice) / 8; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float2 *>(&join[(warp * R + 16 * mt + 8 * h + lane / 4) * LY::kSlice + 8 * n - c + 2 * (lane & 3)]) =
-                            make_float2(o[mt][n][2 * h] * down[mt][h], o[mt][n][2 * h + 1] * down[mt][h]);
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2 *>(&join[(warp / MT * R + row0 + 8 * h + lane / 4) * LY::kSlice + 8 * n - c + 2 * (lane & 3)]) =
+                        make_float2(o[n][2 * h] * down[h], o[n][2 * h + 1] * down[h]);
             named_barrier(1, 32 * kWarps);
             float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < kSets; ++w) {
                 const float4 f = *reinterpret_cast<const float4 *>(&join[(w * R + row) * LY::kSlice + col]);
                 v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
             }
@@ -562,43 +544,74 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
     }
 }
 
-// CTA c joins the parts of the row tile that CTA c's share begins within, if it
-// is the first that does: the end of share c - 1, the beginnings of c, c + 1, ...
+// The parts of the row tile that CTA c's share begins within, if it is the first
+// that does: the end of share c - 1, the beginnings of c, c + 1, ...  Four warps
+// take a row, each a quarter of its parts, a lane four columns; what they sum is
+// added in the order of the keys' quarters.
+constexpr int kJoinRows = 4, kJoinSlices = 4;
 template <int DK, int MT, bool BF>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p, int ctas, const Joint *joints, const float *parts) {
+__global__ void __launch_bounds__(32 * kJoinRows * kJoinSlices) attend_join_kernel(const AttendParams p, int ctas, const Joint *joints,
+                                                                                   const float *parts) {
     using LY = Layout<DK, MT>;
     constexpr int R = LY::kRows;
-    const int c = blockIdx.x + 1;
+    __shared__ float4 sums[kJoinRows][kJoinSlices][32];
+    __shared__ float ls[kJoinRows][kJoinSlices];
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Joint j = joints[c];
     if (j.b < 0) return;
     const Joint before = joints[c - 1];
     // (share c - 1 lies within the same tile: an earlier CTA joins it)
     if (before.b == j.b && before.g == j.g && before.tile == j.tile && !before.last) return;
     int last = c;
-    while (last + 1 < ctas && !joints[last].last) ++last;
+    for (;; last += 32) {
+        const uint32_t ends = __ballot_sync(0xffffffffu, last + lane >= ctas - 1 || joints[last + lane].last);
+        if (ends != 0) {
+            last += __ffs(ends) - 1;
+            break;
+        }
+    }
     const Seq s = load_seq(p.c, j.b, false);
     const int64_t m0 = static_cast<int64_t>(j.tile) * R;
     const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * p.c.share - m0));
+    const int row = blockIdx.y * kJoinRows + warp / kJoinSlices, slice = warp % kJoinSlices;
     const auto part = [&](int i) { return parts + (i < c ? 2 * static_cast<int64_t>(c - 1) + 1 : 2 * static_cast<int64_t>(i)) * LY::kPart; };
-    for (int e = threadIdx.x; e < rows * (DK / 4); e += 128) {
-        const int row = e / (DK / 4), dim = e % (DK / 4) * 4;
-        const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
-        float m = -INFINITY;
-        for (int i = c - 1; i <= last; ++i) m = fmaxf(m, part(i)[R * DK + R + row]);
-        float l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i = c - 1; i <= last; ++i) {
+    const bool mine = 4 * lane < DK;
+    float m = -INFINITY;
+    if (row < rows) {
+        for (int i = c - 1 + lane; i <= last; i += 32) m = fmaxf(m, part(i)[R * DK + R + row]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const int n = last - c + 2, i0 = c - 1 + n * slice / kJoinSlices, i1 = c - 1 + n * (slice + 1) / kJoinSlices;
+        float l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = i0; i < i1; ++i) {
             const float *q = part(i);
             const float top = q[R * DK + R + row], f = top == -INFINITY ? 0.f : ex2(top - m);
             l += q[R * DK + row] * f;
-            const float4 o = *reinterpret_cast<const float4 *>(&q[row * DK + dim]);
-            v[0] += o.x * f, v[1] += o.y * f, v[2] += o.z * f, v[3] += o.w * f;
+            if (mine) {
+                const float4 o = *reinterpret_cast<const float4 *>(&q[row * DK + 4 * lane]);
+                v.x += o.x * f, v.y += o.y * f, v.z += o.z * f, v.w += o.w * f;
+            }
         }
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = pos < 0 ? 0.f : v[k] * inv;
-        store_out<BF>(p, s, j.g, m0 + row, dim, v, 4);
-        if (dim == 0) store_lse(p, s, j.g, m0 + row, pos < 0 ? -INFINITY : lse_of(m, l));
+        sums[warp / kJoinSlices][slice][lane] = v;
+        if (lane == 0) ls[warp / kJoinSlices][slice] = l;
     }
+    __syncthreads();
+    if (row >= rows || slice != 0) return;
+    float l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kJoinSlices; ++k) {
+        const float4 o = sums[warp / kJoinSlices][k][lane];
+        l += ls[warp / kJoinSlices][k];
+        v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
+    }
+    const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = pos < 0 ? 0.f : v[k] * inv;
+    if (mine) store_out<BF>(p, s, j.g, m0 + row, 4 * lane, v, 4);
+    if (lane == 0) store_lse(p, s, j.g, m0 + row, pos < 0 ? -INFINITY : lse_of(m, l));
 }
 
 int rows_grid() {
@@ -618,7 +631,7 @@ cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream
     float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + (grid * sizeof(Joint) + 255) / 256 * 256);
     attend_rows_kernel<DK, MT, BF><<<grid, kThreads, LY::kBytes, stream>>>(p, maps, least_box(p.c, kKeys), joints, parts);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attend_join_kernel<DK, MT, BF><<<grid - 1, 128, 0, stream>>>(p, grid, joints, parts);
+    attend_join_kernel<DK, MT, BF><<<dim3(grid - 1, LY::kRows / kJoinRows), 32 * kJoinRows * kJoinSlices, 0, stream>>>(p, grid, joints, parts);
     return cudaGetLastError();
 }
 template <int DK, int MT>
@@ -626,17 +639,24 @@ cudaError_t launch_m(const AttendParams &p, void *workspace, cudaStream_t stream
     return p.c.io_dtype == kBF16 ? launch_t<DK, MT, true>(p, workspace, stream) : launch_t<DK, MT, false>(p, workspace, stream);
 }
 
+template <int DK>
+cudaError_t launch_d(const AttendParams &p, int kind, void *workspace, cudaStream_t stream) {
+    if (kind == kAttendRows16) return launch_m<DK, 1>(p, workspace, stream);
+    if (kind == kAttendRows32) return launch_m<DK, 2>(p, workspace, stream);
+    return launch_m<DK, 4>(p, workspace, stream);
+}
+
 }  // namespace
 
 uint64_t attend_rows_workspace(int kind, int D) {
-    const uint64_t rows = kind == kAttendRows16 ? 16 : 32, dk = D <= 64 ? 64 : 128;
+    const uint64_t rows = kind == kAttendRows16 ? 16 : kind == kAttendRows32 ? 32 : 64, dk = D <= 64 ? 64 : D <= 96 ? 96 : 128;
     return (rows_grid() * sizeof(Joint) + 255) / 256 * 256 + 2 * rows_grid() * rows * (dk + 2) * sizeof(float);
 }
 
 cudaError_t launch_attend_rows(const AttendParams &p, int kind, void *workspace, cudaStream_t stream) {
-    if (p.c.D <= 64)
-        return kind == kAttendRows16 ? launch_m<64, 1>(p, workspace, stream) : launch_m<64, 2>(p, workspace, stream);
-    return kind == kAttendRows16 ? launch_m<128, 1>(p, workspace, stream) : launch_m<128, 2>(p, workspace, stream);
+    if (p.c.D <= 64) return launch_d<64>(p, kind, workspace, stream);
+    if (p.c.D <= 96) return launch_d<96>(p, kind, workspace, stream);
+    return launch_d<128>(p, kind, workspace, stream);
 }
 
 }  // namespace ssu
