@@ -2,10 +2,44 @@
 // sequence's metadata, the cache's tiled copies, products of 16 x 8 x 16.
 #pragma once
 
+#include <utility>
+
 #include "ssu_paged.h"
 #include "ssu_tcgen05.cuh"
 
 namespace ssu {
+
+// A kernel that is launched to start while the one before it on the stream ends:
+// it waits here until that has ended and what it wrote is there.
+__device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// ... which lets it start, once all of its CTAs have come here.
+__device__ __forceinline__ void start_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Args, typename... Given>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Given &&...args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid, config.blockDim = dim3(threads), config.dynamicSmemBytes = smem, config.stream = stream;
+    config.attrs = &attr, config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, std::forward<Given>(args)...);
+}
+
+// Runs something once on every device (again where that failed).
+struct DeviceOnce {
+    int done[64] = {};
+    template <typename F>
+    cudaError_t run(F f) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        int *const mine = dev >= 0 && dev < 64 ? &done[dev] : nullptr;
+        if (mine && __atomic_load_n(mine, __ATOMIC_RELAXED)) return cudaSuccess;
+        e = f();
+        if (e == cudaSuccess && mine) __atomic_store_n(mine, 1, __ATOMIC_RELAXED);
+        return e;
+    }
+};
 
 struct Seq {
     int64_t t0;  // first row of its new tokens

@@ -34,6 +34,18 @@ __device__ __forceinline__ uint4 pack8(const float *v) {
     else return StateChunk<__half>::pack(v);
 }
 
+// Division by a small number, by its reciprocal rounded down (exact below 2^16).
+struct Divider {
+    uint32_t by, inverse;
+    __device__ __forceinline__ explicit Divider(int n) : by(n), inverse(0xffffffffu / static_cast<uint32_t>(n)) {}
+    __device__ __forceinline__ int divide(int n, int &rest) const {
+        uint32_t q = __umulhi(static_cast<uint32_t>(n), inverse), r = static_cast<uint32_t>(n) - q * by;
+        if (r >= by) ++q, r -= by;
+        rest = static_cast<int>(r);
+        return static_cast<int>(q);
+    }
+};
+
 struct Item {
     const unsigned short *src;
     int token, head, a, b;  // b < 0: one piece only
@@ -52,11 +64,11 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     const int qheads = c.out ? c.H : 0, heads = qheads + 2 * c.G, per = (c.D + 15) / 16;
     const int items = tokens * heads * per, half = p.rotary / 2;
 
+    const Divider by_per(per), by_heads(heads);
     const auto item = [&](int i) {
         Item it;
-        const int th = i / per, u = i - th * per;
-        it.token = th / heads;
-        it.head = th - it.token * heads;
+        int u;
+        it.token = by_heads.divide(by_per.divide(i, u), it.head);
         const int64_t row = r0 + it.token;
         if (it.head < qheads) it.src = static_cast<const unsigned short *>(c.q) + row * c.qs[0] + it.head * c.qs[1];
         else if (it.head < qheads + c.G)
@@ -164,10 +176,14 @@ cudaError_t launch_t(const AppendParams &p, cudaStream_t stream) {
     paged_append_kernel<BF, T><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
+// As many rows a CTA as its threads hold in one turn (32768 rows of 32 + 2 x 8
+// heads of 128: two rows 140 us, four, in two turns, 168); one where the rows are few,
+// so that as many SMs as possible take part.
 template <bool BF>
 cudaError_t launch_b(const AppendParams &p, cudaStream_t stream) {
-    // few rows: one a CTA, so that as many SMs as possible take part
-    return p.c.rows <= 8 * device_sms() ? launch_t<BF, 1>(p, stream) : launch_t<BF, 4>(p, stream);
+    const int items = ((p.c.out ? p.c.H : 0) + 2 * p.c.G) * ((p.c.D + 15) / 16);
+    if (p.c.rows <= 8 * device_sms() || 2 * items > kItems * kThreads) return launch_t<BF, 1>(p, stream);
+    return 4 * items <= kItems * kThreads ? launch_t<BF, 4>(p, stream) : launch_t<BF, 2>(p, stream);
 }
 
 }  // namespace

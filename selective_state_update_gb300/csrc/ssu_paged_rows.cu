@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
         *odd_flag = 0;
         for (int i = 0; i < LY::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kWarps);
     }
+    start_dependents();
     find_share(p, R, sums, share);  // (its barriers order the set-up too)
     Walk walk;
     walk.start(p, *share, R);
@@ -386,45 +387,51 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                 if (MT == 1) __syncwarp();
                 else named_barrier(1, 32 * kWarps);
             }
+            constexpr int kSub = MT == 1 ? 1 : 2;  // 16 keys at a time, or 32
 #pragma unroll 1
-            for (int sub = 0; sub < MT; ++sub) {
+            for (int sub = 0; sub < MT; sub += kSub) {
                 const int mine = keys0 + 16 * sub;
-                float x[2][4];
+                float x[2 * kSub][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2 * kSub; ++n)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[n][j] = 0.f;
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    uint32_t b[4];
-                    ldmatrix_x4(sk + place(mine + (lane & 7) + ((lane >> 4) << 3), 16 * k + ((lane >> 3) & 1) * 8), b);
-                    mma16816<BF>(x[0], q[k], b);
-                    mma16816<BF>(x[1], q[k], b + 2);
-                }
+                for (int k = 0; k < DK / 16; ++k)
+#pragma unroll
+                    for (int n = 0; n < kSub; ++n) {
+                        uint32_t b[4];
+                        ldmatrix_x4(sk + place(mine + 16 * n + (lane & 7) + ((lane >> 4) << 3), 16 * k + ((lane >> 3) & 1) * 8), b);
+                        mma16816<BF>(x[2 * n], q[k], b);
+                        mma16816<BF>(x[2 * n + 1], q[k], b + 2);
+                    }
                 // P and the running maximum and sum
-                uint32_t pa[4];
+                uint32_t pa[kSub][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float e[4] = {x[0][2 * h] * scale, x[0][2 * h + 1] * scale, x[1][2 * h] * scale, x[1][2 * h + 1] * scale};
+                    float e[4 * kSub];  // keys 8 (j / 2) + 2 (lane % 4) + j % 2 of the row
+#pragma unroll
+                    for (int j = 0; j < 4 * kSub; ++j) e[j] = x[j / 2][2 * h + j % 2] * scale;
                     if (masked) {
                         // (the row's position, found here: kept it would cost registers on every tile)
                         const int row = min(row0 + 8 * h + lane / 4, rows - 1);
                         const int pos = s.kv - s.n + static_cast<int>((m0 + row) / p.c.share);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 4 * kSub; ++j) {
                             const int key = key0 + mine + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
                             if (key > pos || (p.window > 0 && key + p.window <= pos)) e[j] = -INFINITY;
                         }
                     }
-                    float top = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+                    float top = mx[h];
+#pragma unroll
+                    for (int j = 0; j < 4 * kSub; ++j) top = fmaxf(top, e[j]);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    top = fmaxf(top, mx[h]);
                     const float base = top == -INFINITY ? 0.f : top, back = ex2(mx[h] - base);
                     mx[h] = top;
                     float add = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 4 * kSub; ++j) {
                         e[j] = ex2(e[j] - base);
                         add += e[j];
                     }
@@ -432,16 +439,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                     if (back != 1.f)
 #pragma unroll
                         for (int n = 0; n < DK / 8; ++n) o[n][2 * h] *= back, o[n][2 * h + 1] *= back;
-                    pa[h] = pack2<BF>(e[0], e[1]);
-                    pa[2 + h] = pack2<BF>(e[2], e[3]);
+#pragma unroll
+                    for (int n = 0; n < kSub; ++n) pa[n][h] = pack2<BF>(e[4 * n], e[4 * n + 1]), pa[n][2 + h] = pack2<BF>(e[4 * n + 2], e[4 * n + 3]);
                 }
 #pragma unroll
-                for (int n = 0; n < DK / 16; ++n) {
-                    uint32_t b[4];
-                    ldmatrix_x4_t(sv + place(mine + (lane & 15), 16 * n + ((lane >> 4) << 3)), b);
-                    mma16816<BF>(o[2 * n], pa, b);
-                    mma16816<BF>(o[2 * n + 1], pa, b + 2);
-                }
+                for (int n = 0; n < DK / 16; ++n)
+#pragma unroll
+                    for (int k = 0; k < kSub; ++k) {
+                        uint32_t b[4];
+                        ldmatrix_x4_t(sv + place(mine + 16 * k + (lane & 15), 16 * n + ((lane >> 4) << 3)), b);
+                        mma16816<BF>(o[2 * n], pa[k], b);
+                        mma16816<BF>(o[2 * n + 1], pa[k], b + 2);
+                    }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
@@ -557,6 +566,7 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinSlices) attend_join_kern
     __shared__ float4 sums[kJoinRows][kJoinSlices][32];
     __shared__ float ls[kJoinRows][kJoinSlices];
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_prior();
     const Joint j = joints[c];
     if (j.b < 0) return;
     const Joint before = joints[c - 1];
@@ -622,7 +632,8 @@ int rows_grid() {
 template <int DK, int MT, bool BF>
 cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream) {
     using LY = Layout<DK, MT>;
-    cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<DK, MT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes);
+    static DeviceOnce once;
+    cudaError_t e = once.run([] { return cudaFuncSetAttribute(attend_rows_kernel<DK, MT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes); });
     if (e != cudaSuccess) return e;
     CacheMaps maps;
     if (!encode_cache(&maps, p.c, kKeys)) return cudaErrorInvalidValue;
@@ -631,8 +642,8 @@ cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream
     float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + (grid * sizeof(Joint) + 255) / 256 * 256);
     attend_rows_kernel<DK, MT, BF><<<grid, kThreads, LY::kBytes, stream>>>(p, maps, least_box(p.c, kKeys), joints, parts);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attend_join_kernel<DK, MT, BF><<<dim3(grid - 1, LY::kRows / kJoinRows), 32 * kJoinRows * kJoinSlices, 0, stream>>>(p, grid, joints, parts);
-    return cudaGetLastError();
+    return launch_after(attend_join_kernel<DK, MT, BF>, dim3(grid - 1, LY::kRows / kJoinRows), 32 * kJoinRows * kJoinSlices, 0, stream, p, grid,
+                        joints, parts);
 }
 template <int DK, int MT>
 cudaError_t launch_m(const AttendParams &p, void *workspace, cudaStream_t stream) {

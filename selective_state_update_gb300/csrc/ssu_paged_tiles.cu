@@ -46,7 +46,6 @@ struct Piece {
     int32_t first, last;  // key tiles
     int32_t part, parts;  // of the unit's parts, which
     int32_t slot;         // the first part's place in the workspace (where parts > 1)
-    int32_t spare;
 };
 struct PlanHead {
     int32_t pieces, cuts, next;  // number of pieces, of units that are cut; the next piece to be taken
@@ -93,7 +92,7 @@ __device__ __forceinline__ bool partly_seen(const Work &w, int window, int j) {
 // ---------------------------------------------------------------------------
 // The plan: one CTA.
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 constexpr int kMaxParts = 16;
 
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
@@ -103,7 +102,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
     __syncthreads();
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = red[lane];
+    v = lane < kPlanThreads / 32 ? red[lane] : 0;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
@@ -121,7 +120,7 @@ __device__ __forceinline__ T block_scan(T v, T *red, T &total) {
     __syncthreads();
     if (lane == 31) red[warp] = upto;
     __syncthreads();
-    T w = red[lane];
+    T w = lane < kPlanThreads / 32 ? red[lane] : T(0);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const T o = __shfl_up_sync(0xffffffffu, w, off);
@@ -171,6 +170,7 @@ __device__ __forceinline__ void part_of(const Cut &k, int c, int even, int i, in
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p, const Plan plan, int ctas) {
+    start_dependents();
     __shared__ int64_t red64[32];
     __shared__ int red[32], bounds[kPlanThreads + 1];
     const int tid = threadIdx.x, tt2 = 2 * tile_tokens(p.c);
@@ -235,36 +235,39 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
         if (tid == 0) plan.head->pieces = units, plan.head->cuts = 0, plan.head->next = ctas;
         return;
     }
-    // The pieces: all first parts, all second ones, ... so that CTAs that are at work at the same time read the same keys.
-    int pieces = 0, cuts = 0;
-    for (int part = 0;; ++part) {
-        int slots = 0;
-        cuts = 0;
-        const int begun = pieces;
-        for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
-            Piece q{};
-            Cut k{0, 0};
-            if (u0 + tid < units) {
-                q = plan.units[u0 + tid];
-                k = cut_unit(u0 + tid);
-            }
-            int t0, t1, t2;
-            const int at = block_scan<int>(k.parts > part, red, t0), slot = block_scan<int>(k.parts > 1 ? k.parts : 0, red, t1),
-                      cut = block_scan<int>(k.parts > 1, red, t2);
-            if (k.parts > part) {
-                int from, to;
-                part_of(k, q.last - q.first, even, part, from, to);
-                q.last = q.first + to;
-                q.first += from;
-                q.part = part, q.parts = k.parts, q.slot = slots + slot;
-                plan.pieces[pieces + at] = q;
-                if (part == 0 && k.parts > 1) plan.cuts[cuts + cut] = pieces + at;
-            }
-            pieces += t0, slots += t1, cuts += t2;
-        }
-        if (pieces == begun) break;
+    // The pieces: all first parts, all second ones, ... so that CTAs that are at
+    // work at the same time read the same keys.  (Among those the units come in any
+    // order, which nothing but the time depends on.)
+    __shared__ int next_piece[kMaxParts + 1], next_slot, next_cut;
+    if (tid <= kMaxParts) next_piece[tid] = 0;
+    if (tid == 0) next_slot = next_cut = 0;
+    __syncthreads();
+    for (int u = tid; u < units; u += kPlanThreads) {
+        const int parts = cut_unit(u).parts;
+        for (int i = 0; i < parts; ++i) atomicAdd(&next_piece[i + 1], 1);
     }
-    if (tid == 0) plan.head->pieces = pieces, plan.head->cuts = cuts, plan.head->next = ctas;
+    __syncthreads();
+    if (tid == 0)
+        for (int i = 0; i < kMaxParts; ++i) next_piece[i + 1] += next_piece[i];
+    __syncthreads();
+    const int pieces = next_piece[kMaxParts];
+    __syncthreads();
+    for (int u = tid; u < units; u += kPlanThreads) {
+        const Cut k = cut_unit(u);
+        Piece q = plan.units[u];
+        const int first = q.first, c = q.last - q.first, slot = k.parts > 1 ? atomicAdd(&next_slot, k.parts) : 0;
+        for (int i = 0; i < k.parts; ++i) {
+            int from, to;
+            part_of(k, c, even, i, from, to);
+            q.first = first + from, q.last = first + to;
+            q.part = i, q.parts = k.parts, q.slot = slot;
+            const int at = atomicAdd(&next_piece[i], 1);
+            plan.pieces[at] = q;
+            if (i == 0 && k.parts > 1) plan.cuts[atomicAdd(&next_cut, 1)] = at;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) plan.head->pieces = pieces, plan.head->cuts = next_cut, plan.head->next = ctas;
 }
 
 // ---------------------------------------------------------------------------
@@ -448,6 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
+    start_dependents();
+    wait_for_prior();  // the plan
     bool ok = true;
     int nu = 0;  // pieces of work read
     const auto read_work = [&](const Work *&w) {
@@ -1036,6 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
 template <int DK, bool BF>
 __global__ void __launch_bounds__(128) attend_tiles_join_kernel(const AttendParams p, const Plan plan) {
     constexpr int kGroups = kRows / 8;
+    wait_for_prior();
     const int lane = threadIdx.x & 31, G = p.c.G, tt = tile_tokens(p.c);
     const int64_t items = static_cast<int64_t>(plan.head->cuts) * G * 2 * kGroups;
     for (int64_t i = blockIdx.x * 4 + (threadIdx.x >> 5); i < items; i += gridDim.x * 4) {
@@ -1100,7 +1106,8 @@ template <int DK, bool BF>
 cudaError_t launch_t(const AttendParams &p, int64_t max_kv_len, void *workspace, cudaStream_t stream) {
     // Before the maps: their encoder is a driver call and refuses a host thread
     // that has no context yet, which this one gives it.
-    cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes);
+    static DeviceOnce once;
+    cudaError_t e = once.run([] { return cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes); });
     if (e != cudaSuccess) return e;
     Maps maps;
     if (!encode_queries(&maps.q, p.c, kRows / p.c.share) || !encode_cache(&maps.cache, p.c, kKeys)) return cudaErrorInvalidValue;
@@ -1119,10 +1126,10 @@ cudaError_t launch_t(const AttendParams &p, int64_t max_kv_len, void *workspace,
     plan.max_slots = static_cast<int32_t>(s.slots);
     attend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, sms);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attend_tiles_kernel<DK, BF><<<sms, kThreads, Layout<DK>::kBytes, stream>>>(p, maps, plan, least_box(p.c, kKeys), wide ? kWideOut : 0);
-    if ((e = cudaGetLastError()) != cudaSuccess || s.slots == 0) return e;
-    attend_tiles_join_kernel<DK, BF><<<8 * sms, 128, 0, stream>>>(p, plan);
-    return cudaGetLastError();
+    e = launch_after(attend_tiles_kernel<DK, BF>, dim3(sms), kThreads, Layout<DK>::kBytes, stream, p, maps, plan, least_box(p.c, kKeys),
+                     wide ? kWideOut : 0);
+    if (e != cudaSuccess || s.slots == 0) return e;
+    return launch_after(attend_tiles_join_kernel<DK, BF>, dim3(8 * sms), 128, 0, stream, p, plan);
 }
 
 }  // namespace
