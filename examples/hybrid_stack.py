@@ -2,7 +2,7 @@
 prompts through the chunked prefill, single tokens through the step, every
 layer's input normed to 8 bits, and every token's log probability.
 
-    python examples/hybrid_stack.py [--layers 4] [--new 16]
+    python examples/hybrid_stack.py [--layers 4] [--new 16] [--attention-every 2]
 
 The weights are random; what the example shows is how the calls fit together.
 Per layer and call:
@@ -11,6 +11,12 @@ Per layer and call:
     projection                          q, k, v as slices of one tensor (no copies)
     ssu_linear_attention_prefill/_step  on the layer's pool, through the sequences' slots
     projection
+
+With --attention-every n every n-th layer is softmax attention instead, over a paged
+cache of its own whose pages the sequences share:
+
+    ssu_paged_append                    keys and values into their pages, keys and queries turned by their position
+    ssu_paged_attention                 of the new tokens over what the cache then holds
 
 and at the end ssu_add_rmsnorm (16-bit), the vocabulary's projection and
 ssu_token_logprobs.  It closes by scoring the generated text in one prefill: the
@@ -32,7 +38,7 @@ PAD = -1
 
 class HybridStack:
     def __init__(self, vocab=2048, hidden=512, layers=4, heads=8, kv_heads=2, head_size=64, slots=16, quant="row", seed=0,
-                 device="cuda"):
+                 device="cuda", attention_every=0, page=16, pages=128):
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weight(rows, cols):
@@ -46,7 +52,13 @@ class HybridStack:
         # one decay rate per head, from a memory of two tokens to one of a thousand
         self.log_decay = -torch.exp2(-torch.linspace(1.0, 10.0, heads, device=device))
         # one pool per layer; a sequence has the same slot in all of them
-        self.pools = [torch.zeros(slots, heads, head_size, head_size, device=device) for _ in range(layers)]
+        # (an attention layer has pages of keys and values instead)
+        attends = [attention_every > 0 and i % attention_every == attention_every - 1 for i in range(layers)]
+        self.pools = [tuple(torch.zeros(pages, page, kv_heads, head_size, device=device, dtype=torch.bfloat16) for _ in range(2)) if a
+                      else torch.zeros(slots, heads, head_size, head_size, device=device) for a in attends]
+        self.page, self.free = page, list(range(pages))
+        self.inv_freq = 10000.0 ** -(torch.arange(0, head_size, 2, device=device) / head_size)
+        self.held = {}  # slot -> its pages and its number of tokens
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
     def _project(self, x, scales, w):
@@ -67,24 +79,57 @@ class HybridStack:
         x, _, _ = ssu.ssu_add_rmsnorm(delta, self.norms[-1], residual=stream, residual_out=stream)
         return x @ self.unembed.t()
 
+    def _grow(self, slots, new):
+        """Room for ``new`` more tokens in each slot's pages: (block table, lengths with them)."""
+        for slot, n in zip(slots, new):
+            pages, length = self.held.setdefault(slot, ([], 0))
+            while len(pages) * self.page < length + n:
+                pages.append(self.free.pop())
+            self.held[slot] = pages, length + n
+        rows = [self.held[slot][0] for slot in slots]
+        wide = max(len(r) for r in rows)
+        table = torch.tensor([r + [PAD] * (wide - len(r)) for r in rows], dtype=torch.int32, device=self.embed.device)
+        return table, torch.tensor([self.held[slot][1] for slot in slots], dtype=torch.int32, device=self.embed.device)
+
+    def _attend(self, cache, q, k, v, table, lengths, **kw):
+        q = ssu.ssu_paged_append(*cache, k, v, table, lengths, q=q, inv_freq=self.inv_freq, cu_seqlens=kw.get("cu_seqlens"),
+                                 status=self.status)
+        return ssu.ssu_paged_attention(q, *cache, table, lengths, status=self.status, **kw)
+
     def prefill(self, tokens, lengths, slots):
         """New prompts, packed: their states go to ``slots``."""
         cu = torch.tensor([0, *lengths], device=tokens.device).cumsum(0).int()
         fresh = torch.full_like(slots, PAD)  # every prompt starts from a zero state
-        return self.forward(tokens, lambda pool, q, k, v: ssu.ssu_linear_attention_prefill(
-            pool, q, k, v, self.log_decay, cu, state_batch_indices=fresh, dst_state_batch_indices=slots, pad_slot_id=PAD,
-            max_seqlen=max(lengths), status=self.status))
+        for slot in slots.tolist():  # ... and with no pages
+            self.free += self.held.pop(slot, ([], 0))[0]
+        table, kv_lens = self._grow(slots.tolist(), lengths)
+
+        def mix(pool, q, k, v):
+            if isinstance(pool, tuple):
+                return self._attend(pool, q, k, v, table, kv_lens, cu_seqlens=cu, max_seqlen=max(lengths), max_kv_len=max(lengths))
+            return ssu.ssu_linear_attention_prefill(
+                pool, q, k, v, self.log_decay, cu, state_batch_indices=fresh, dst_state_batch_indices=slots, pad_slot_id=PAD,
+                max_seqlen=max(lengths), status=self.status)
+
+        return self.forward(tokens, mix)
 
     def step(self, tokens, slots):
         """One token for the sequence in each slot."""
-        return self.forward(tokens, lambda pool, q, k, v: ssu.ssu_linear_attention_step(
-            pool, q, k, v, self.log_decay, state_batch_indices=slots, pad_slot_id=PAD, status=self.status))
+        table, kv_lens = self._grow(slots.tolist(), [1] * len(slots))
+
+        def mix(pool, q, k, v):
+            if isinstance(pool, tuple):
+                return self._attend(pool, q, k, v, table, kv_lens)
+            return ssu.ssu_linear_attention_step(
+                pool, q, k, v, self.log_decay, state_batch_indices=slots, pad_slot_id=PAD, status=self.status)
+
+        return self.forward(tokens, mix)
 
 
-def run(layers=4, new=16, lengths=(37, 200, 5), quant="row", top_k=5, seed=0):
+def run(layers=4, new=16, lengths=(37, 200, 5), quant="row", top_k=5, seed=0, attention_every=0):
     """Generates ``new`` tokens for prompts of the given lengths.  Returns the generated tokens' log probabilities as
     the steps saw them and as one prefill over the whole texts sees them, [sequences, new] each."""
-    model = HybridStack(layers=layers, quant=quant, seed=seed)
+    model = HybridStack(layers=layers, quant=quant, seed=seed, attention_every=attention_every)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     prompts = [torch.randint(2048, (n,), generator=g, device="cuda") for n in lengths]
     slots = torch.arange(len(lengths), device="cuda", dtype=torch.int32) * 2 + 1
@@ -119,8 +164,9 @@ if __name__ == "__main__":
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--new", type=int, default=16)
     ap.add_argument("--quant", default="row", choices=["none", "row"])
+    ap.add_argument("--attention-every", type=int, default=0)
     a = ap.parse_args()
-    seen, again, made, entropy = run(layers=a.layers, new=a.new, quant=a.quant)
+    seen, again, made, entropy = run(layers=a.layers, new=a.new, quant=a.quant, attention_every=a.attention_every)
     for i, (t, s) in enumerate(zip(made.tolist(), seen.tolist())):
         print(f"sequence {i}: " + " ".join(f"{x}({lp:.2f})" for x, lp in zip(t, s)))
     print("entropy of the next token:", [round(x, 3) for x in entropy.tolist()])

@@ -25,22 +25,6 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t
     return cudaLaunchKernelEx(&config, kernel, std::forward<Given>(args)...);
 }
 
-// Runs something once on every device (again where that failed).
-struct DeviceOnce {
-    int done[64] = {};
-    template <typename F>
-    cudaError_t run(F f) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        int *const mine = dev >= 0 && dev < 64 ? &done[dev] : nullptr;
-        if (mine && __atomic_load_n(mine, __ATOMIC_RELAXED)) return cudaSuccess;
-        e = f();
-        if (e == cudaSuccess && mine) __atomic_store_n(mine, 1, __ATOMIC_RELAXED);
-        return e;
-    }
-};
-
 struct Seq {
     int64_t t0;  // first row of its new tokens
     int32_t n;   // new tokens; 0 as well where the sequence is to be skipped

@@ -632,8 +632,9 @@ int rows_grid() {
 template <int DK, int MT, bool BF>
 cudaError_t launch_t(const AttendParams &p, void *workspace, cudaStream_t stream) {
     using LY = Layout<DK, MT>;
-    static DeviceOnce once;
-    cudaError_t e = once.run([] { return cudaFuncSetAttribute(attend_rows_kernel<DK, MT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes); });
+    // Before the maps: their encoder is a driver call and refuses a host thread
+    // that has no context yet, which this one gives it.
+    cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<DK, MT, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes);
     if (e != cudaSuccess) return e;
     CacheMaps maps;
     if (!encode_cache(&maps, p.c, kKeys)) return cudaErrorInvalidValue;

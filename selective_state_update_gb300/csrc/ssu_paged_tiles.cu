@@ -1106,8 +1106,7 @@ template <int DK, bool BF>
 cudaError_t launch_t(const AttendParams &p, int64_t max_kv_len, void *workspace, cudaStream_t stream) {
     // Before the maps: their encoder is a driver call and refuses a host thread
     // that has no context yet, which this one gives it.
-    static DeviceOnce once;
-    cudaError_t e = once.run([] { return cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes); });
+    cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<DK, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DK>::kBytes);
     if (e != cudaSuccess) return e;
     Maps maps;
     if (!encode_queries(&maps.q, p.c, kRows / p.c.share) || !encode_cache(&maps.cache, p.c, kKeys)) return cudaErrorInvalidValue;

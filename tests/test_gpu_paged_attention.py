@@ -241,3 +241,34 @@ def test_nothing_to_do(libssu):
     out = torch.full_like(b.q, 3.0)
     ssu.ssu_paged_attention(b.q, b.k_cache, b.v_cache, b.table, b.kv_lens, cu_seqlens=b.cu, out=out)
     assert (out == 3.0).all()
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads", [
+    ([(2400, 5000)], 8, 2),                    # one unit a CTA and a little more
+    ([(1, 6000)] * 5 + [(130, 400)] * 3, 24, 8),  # long and short ones in one call
+    ([(3, 30000)], 128, 1),                    # a single row of units, cut many times
+    ([(700, 700), (900, 4000), (60, 9000)], 12, 4),
+])
+@pytest.mark.parametrize("io,dim,page", [("bf16", 128, 272), ("f16", 72, 24)])
+def test_units_cut_or_not(libssu, lens, heads, kv_heads, io, dim, page):
+    b = Batch(lens, heads, kv_heads, dim, page, io)
+    out, lse = call(b)
+    check(b, out, lse, attention(b))
+    again, lse2 = call(b, hints=False)
+    check(b, again, lse2, attention(b))
+
+
+@pytest.mark.parametrize("page", [8, 24, 40, 56, 104, 120, 136, 248, 264, 400])
+@pytest.mark.parametrize("lens", [[(1, 1), (1, 513), (1, 299)], [(200, 513), (70, 130)]], ids=["single", "chunks"])
+def test_pages_that_end_inside_a_tile(libssu, page, lens):
+    b = Batch(lens, 8, 2, 128 if page % 16 else 80, page, single=lens[0][0] == 1)
+    check(b, *call(b, window=0), attention(b))
+    check(b, *call(b, window=150), attention(b, window=150))
+
+
+@pytest.mark.parametrize("rows,heads,kv_heads", [(16, 16, 1), (17, 17, 1), (32, 8, 1), (33, 33, 1), (64, 16, 1), (65, 65, 1), (24, 12, 2)])
+@pytest.mark.parametrize("window", [0, 90])
+def test_each_number_of_rows(libssu, rows, heads, kv_heads, window):
+    n = rows // (heads // kv_heads)
+    b = Batch([(n, n), (n, n + 63), (n, 1500), (max(n - 1, 0), 200)], heads, kv_heads, 128, 32)
+    check(b, *call(b, window), attention(b, window=window))
