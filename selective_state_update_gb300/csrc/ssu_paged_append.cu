@@ -8,19 +8,20 @@
 //     x' = x cos a - y sin a,   y' = y cos a + x sin a
 // in fp32, rounded once.  The angle is formed and brought into [-pi, pi] in 64
 // bits (positions reach millions, where fp32 angles are off by whole radians);
-// what is left of it is exact to 2^-24, and so are its sine and cosine.
+// rounded to fp32 there it is off by 2^-23, and its sine and cosine by a little
+// more than their own rounding.
 //
-// HBM-bound: q, k and v are read once and written once.  A CTA takes kTokens
-// rows; a thread's item is 32 bytes of one head, two 16-byte pieces that hold
-// whole pairs.  The first items are asked for before the metadata, whose reads
-// depend on one another (sequence, length, page).
+// HBM-bound: q, k and v are read once and written once.  A CTA takes T rows; a
+// thread's item is 32 bytes of one head, two 16-byte pieces that hold whole
+// pairs.  The first items are asked for before the metadata, whose reads depend
+// on one another (sequence, length, page).  32768 rows of 32 + 2 x 8 heads of 128:
+// 150 us, 5.4 TB/s, 0.80 of the copy rate.
 #include "ssu_paged.cuh"
 
 namespace ssu {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kItems = 4;  // of a thread at a time
 
 template <bool BF>
@@ -52,10 +53,10 @@ struct Item {
     bool turn;
 };
 
-template <bool BF, int T>
+template <bool BF, int T, int kThreads>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendParams p) {
-    __shared__ int seq_of[T];
-    __shared__ int64_t pos_of[T], page_of_row[T];  // kAway: no row of the cache
+    __shared__ int seq_of[T], row_of[T];  // row of its page
+    __shared__ int64_t pos_of[T], page_of_row[T];  // page -1: none
     __shared__ float2 turn_by[T][kPagedMaxDim / 2];
     const PagedParams &c = p.c;
     const int tid = threadIdx.x;
@@ -94,8 +95,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
 
     if (tid < T) seq_of[tid] = -1;
     __syncthreads();
-    for (int64_t s = tid; s < c.nseq; s += kThreads) {
-        const Seq q = load_seq(c, s, blockIdx.x == 0);
+    // (with a row each, a row's sequence is known)
+    const bool each = c.cu == nullptr;
+    for (int64_t s = each ? r0 + tid : tid; s < (each ? r0 + tokens : c.nseq); s += kThreads) {
+        const Seq q = load_seq(c, s, each || blockIdx.x == 0);
         const int64_t from = max(q.t0, r0), to = min(q.t0 + q.n, r0 + tokens);
         for (int64_t t = from; t < to; ++t) {
             // (where sequences overlap, which the last check does not exclude, one of them has the token)
@@ -105,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
             }
             const int64_t pos = q.kv - q.n + (t - q.t0);
             pos_of[t - r0] = pos;
+            row_of[t - r0] = pos < 0 ? 0 : static_cast<int>(pos) % c.page;
             page_of_row[t - r0] = pos < 0 ? -1 : page_of(c, s, static_cast<int32_t>(pos));
         }
     }
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
                 const bool key = it.head < qheads + c.G;
                 const int64_t *str = key ? c.ks : c.vs;
                 dst = static_cast<unsigned short *>(key ? c.k_cache : c.v_cache) + page * str[0] +
-                      (pos_of[it.token] % c.page) * str[1] + (it.head - qheads - (key ? 0 : c.G)) * str[2];
+                      row_of[it.token] * str[1] + (it.head - qheads - (key ? 0 : c.G)) * str[2];
             }
             if (it.turn) {
                 float x[8], y[8];
@@ -170,20 +174,24 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     }
 }
 
-template <bool BF, int T>
+template <bool BF, int T, int THREADS>
 cudaError_t launch_t(const AppendParams &p, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>((p.c.rows + T - 1) / T);
-    paged_append_kernel<BF, T><<<grid, kThreads, 0, stream>>>(p);
+    paged_append_kernel<BF, T, THREADS><<<grid, THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
-// As many rows a CTA as its threads hold in one turn (32768 rows of 32 + 2 x 8
-// heads of 128: two rows 140 us, four, in two turns, 168); one where the rows are few,
-// so that as many SMs as possible take part.
+// Few rows: one a CTA of 256 threads, so that as many SMs as possible take part
+// (3 rows 3.3 us in a graph, 3.7 with 128 threads).  More: CTAs of 128 threads, as
+// many rows as those hold in one turn, one at least: 32768 rows of 32 + 2 x 8 heads
+// of 128 150 us with one row, 4 in two turns 168; CTAs of 256 threads and two rows
+// 156 to 164.
 template <bool BF>
 cudaError_t launch_b(const AppendParams &p, cudaStream_t stream) {
+    constexpr int kHeld = 128 * kItems;
     const int items = ((p.c.out ? p.c.H : 0) + 2 * p.c.G) * ((p.c.D + 15) / 16);
-    if (p.c.rows <= 8 * device_sms() || 2 * items > kItems * kThreads) return launch_t<BF, 1>(p, stream);
-    return 4 * items <= kItems * kThreads ? launch_t<BF, 4>(p, stream) : launch_t<BF, 2>(p, stream);
+    if (p.c.rows <= 8 * device_sms()) return launch_t<BF, 1, 256>(p, stream);
+    if (2 * items > kHeld) return launch_t<BF, 1, 128>(p, stream);
+    return 4 * items <= kHeld ? launch_t<BF, 4, 128>(p, stream) : launch_t<BF, 2, 128>(p, stream);
 }
 
 }  // namespace

@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
 #pragma unroll
                         for (int j = 0; j < 4 * kSub; ++j) {
                             const int key = key0 + mine + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
-                            if (key > pos || (p.window > 0 && key + p.window <= pos)) e[j] = -INFINITY;
+                            if (key > pos || (p.window > 0 && key <= pos - p.window)) e[j] = -INFINITY;
                         }
                     }
                     float top = mx[h];

@@ -93,7 +93,7 @@ __device__ __forceinline__ bool partly_seen(const Work &w, int window, int j) {
 // The plan: one CTA.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
-constexpr int kMaxParts = 16;
+constexpr int kMaxParts = 64;
 
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -151,7 +151,12 @@ struct Cut {
 __device__ __forceinline__ Cut cut_of(int c, int even, int fine, bool whole) {
     Cut k{0, 1};
     if (whole) return k;
-    k.large = min(c / even, kMaxParts - 1);
+    k.large = c / even;
+    if (k.large >= kMaxParts) {  // (alike, then)
+        k.large = 0;
+        k.parts = kMaxParts;
+        return k;
+    }
     const int rest = c - k.large * even;
     k.parts = max(k.large + min((rest + fine - 1) / fine, kMaxParts - k.large), 1);
     return k;
@@ -1035,47 +1040,71 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     if (warp == 8) tmem_dealloc512(tmem);
 }
 
-// The parts of units that were cut, joined in the order of the keys: a warp
-// eight rows of a tile, four lanes a row.  (By the CTA that stored a unit's last
+// The parts of units that were cut, joined: a CTA eight rows of a tile, four
+// lanes of each warp a row, and a warp a quarter of the parts, whose sums are added in
+// the order of the keys.  (By the CTA that stored a unit's last
 // part, with one warp's loads in flight on a scheduler, a join took up to 140 us.)
 template <int DK, bool BF>
 __global__ void __launch_bounds__(128) attend_tiles_join_kernel(const AttendParams p, const Plan plan) {
-    constexpr int kGroups = kRows / 8;
+    constexpr int kGroups = kRows / 8, kSlices = 4;
     wait_for_prior();
     const int lane = threadIdx.x & 31, G = p.c.G, tt = tile_tokens(p.c);
     const int64_t items = static_cast<int64_t>(plan.head->cuts) * G * 2 * kGroups;
-    for (int64_t i = blockIdx.x * 4 + (threadIdx.x >> 5); i < items; i += gridDim.x * 4) {
+    __shared__ float4 sums[kSlices - 1][DK / 16][32];
+    __shared__ float ls[kSlices - 1][32];
+    const int slice = threadIdx.x >> 5;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const int group = static_cast<int>(i % kGroups), x = static_cast<int>(i / kGroups % 2), g = static_cast<int>(i / (2 * kGroups) % G);
         const Piece q = plan.pieces[plan.cuts[i / (2 * kGroups * G)]];
         const int m = 8 * group + lane / 4, tok = m / p.c.share, t0 = (2 * q.pair + x) * tt + tok;
-        if (tok >= tt || t0 >= q.n) continue;
-        const int pos = q.kv - q.n + t0;
-        float top = -INFINITY;
-        for (int k = 0; k < q.parts; ++k) top = fmaxf(top, part_at<DK>(plan, G, q.slot + k, g, x)[kRows * (DK + 1) + m]);
-        float sum = 0.f;
+        const bool there = tok < tt && t0 < q.n;
+        float top = -INFINITY, sum = 0.f;
         float4 v[DK / 16] = {};  // columns 16 c + 4 (lane % 4) ...
-        for (int k = 0; k < q.parts; ++k) {
-            const float *const part = part_at<DK>(plan, G, q.slot + k, g, x);
-            const float ref = part[kRows * (DK + 1) + m], f = ref == -INFINITY ? 0.f : ex2(ref - top);
-            sum += part[kRows * DK + m] * f;
+        if (there) {
+#pragma unroll 4
+            for (int k = 0; k < q.parts; ++k) top = fmaxf(top, part_at<DK>(plan, G, q.slot + k, g, x)[kRows * (DK + 1) + m]);
+            for (int k = q.parts * slice / kSlices; k < q.parts * (slice + 1) / kSlices; ++k) {
+                const float *const part = part_at<DK>(plan, G, q.slot + k, g, x);
+                const float ref = part[kRows * (DK + 1) + m], f = ref == -INFINITY ? 0.f : ex2(ref - top);
+                sum += part[kRows * DK + m] * f;
 #pragma unroll
-            for (int c = 0; c < DK / 16; ++c) {  // (columns past the head size hold anything)
-                const float4 o = *reinterpret_cast<const float4 *>(part + ((4 * c + (lane & 3)) * kRows + m) * 4);
-                v[c].x += o.x * f, v[c].y += o.y * f, v[c].z += o.z * f, v[c].w += o.w * f;
+                for (int c = 0; c < DK / 16; ++c) {  // (columns past the head size hold anything)
+                    const float4 o = *reinterpret_cast<const float4 *>(part + ((4 * c + (lane & 3)) * kRows + m) * 4);
+                    v[c].x += o.x * f, v[c].y += o.y * f, v[c].z += o.z * f, v[c].w += o.w * f;
+                }
             }
         }
-        const float inv = 1.f / sum;
-        const int64_t row = q.row0 + t0;
-        const int h = g * p.c.share + (m - tok * p.c.share);
-        unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
+        if (slice > 0) {
 #pragma unroll
-        for (int c = 0; c < DK / 16; ++c) {
-            const int at = 16 * c + 4 * (lane & 3);
-            if (at < p.c.D)
-                *reinterpret_cast<uint2 *>(out + at) =
-                    pos < 0 ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[c].x * inv, v[c].y * inv), pack2<BF>(v[c].z * inv, v[c].w * inv));
+            for (int c = 0; c < DK / 16; ++c) sums[slice - 1][c][lane] = v[c];
+            ls[slice - 1][lane] = sum;
         }
-        if (p.lse && (lane & 3) == 0) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : lse_of(top, sum);
+        __syncthreads();
+        if (slice == 0 && there) {
+#pragma unroll
+            for (int k = 0; k < kSlices - 1; ++k) {
+                sum += ls[k][lane];
+#pragma unroll
+                for (int c = 0; c < DK / 16; ++c) {
+                    const float4 o = sums[k][c][lane];
+                    v[c].x += o.x, v[c].y += o.y, v[c].z += o.z, v[c].w += o.w;
+                }
+            }
+            const int pos = q.kv - q.n + t0;
+            const float inv = 1.f / sum;
+            const int64_t row = q.row0 + t0;
+            const int h = g * p.c.share + (m - tok * p.c.share);
+            unsigned short *const out = static_cast<unsigned short *>(p.c.out) + row * p.c.os[0] + h * p.c.os[1];
+#pragma unroll
+            for (int c = 0; c < DK / 16; ++c) {
+                const int at = 16 * c + 4 * (lane & 3);
+                if (at < p.c.D)
+                    *reinterpret_cast<uint2 *>(out + at) =
+                        pos < 0 ? make_uint2(0u, 0u) : make_uint2(pack2<BF>(v[c].x * inv, v[c].y * inv), pack2<BF>(v[c].z * inv, v[c].w * inv));
+            }
+            if (p.lse && (lane & 3) == 0) p.lse[row * p.c.H + h] = pos < 0 ? -INFINITY : lse_of(top, sum);
+        }
+        __syncthreads();  // `sums` are read
     }
 }
 
