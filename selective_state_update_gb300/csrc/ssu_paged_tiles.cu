@@ -13,8 +13,8 @@
 //
 // A plan kernel checks the metadata, lists the units and, where they are too few
 // or too uneven for the GPU, cuts their keys into parts; the main kernel's CTAs
-// take the list in turn.  Parts leave (O, l, m) in the workspace, and the CTA that
-// completes a unit's last part joins them in the order of the keys.
+// take the list in turn.  Parts leave (O, l, m) in the workspace, where a third
+// kernel joins them in the order of the keys.
 //
 // Two products a key tile and query tile, fp32 accumulators in tensor memory:
 //     S = Q K^T  (both from shared memory, as copied),  O += P V  (P where S was)
@@ -23,6 +23,14 @@
 //   8         issues the products;   9  finds the units and copies pages;
 //   10-11     look through the values of partly visible tiles (below);
 //   12-15     store the outputs.
+//
+// What it takes: 32768 tokens in 16 prompts, 32 / 8 heads of 128 bf16, 550 us, 1280
+// TFLOP/s, 0.66 of the measured product rate; 2432 tokens behind 65536, 16 / 4 heads,
+// 750 us, 1770 TFLOP/s, the measured sustained rate.  A key tile takes 2800 cycles
+// for both row tiles, of which the products alone would be 2048: S reads both its
+// operands from shared memory at the pipe's whole rate while copies are written, and
+// a tile's chain -- scores, 1450 cycles of softmax, P V and the next scores -- is as
+// long.  A unit's turnover takes about 5000 more.
 #include <type_traits>
 
 #include "ssu_paged.cuh"
@@ -323,8 +331,8 @@ template <int N>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // A wait, bounded like every other, of warps that mostly wait: asleep for up to
-// 20 us at a time unless the phase completes.  (Polling, the warps that store
-// outputs cost the others on their schedulers 10 %.)
+// 20 us at a time unless the phase completes.  (Polling, 32768 tokens in 16 prompts
+// took 570 us where they take 552.)
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity) {
     const long long t0 = clock64();
     for (uint32_t i = 0; i < (1u << 26); ++i) {
