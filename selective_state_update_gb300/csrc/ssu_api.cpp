@@ -815,7 +815,8 @@ static ssu_status attend_prepare(const ssu_paged_args *args, float scale, int64_
                                  int64_t max_kv_len, ssu::AttendParams *p) {
     const ssu_status st = paged_prepare(args, &p->c);
     if (st != SSU_OK) return st;
-    if (!(scale > 0.f) || !(scale <= 3.402823466e38f)) return fail(SSU_ERR_INVALID, "scale must be positive and finite");
+    // (scores are taken in units of log2)
+    if (!(scale > 0.f) || !(scale <= 2e38f)) return fail(SSU_ERR_INVALID, "scale must be positive and at most 2e38");
     if (window < 0) return fail(SSU_ERR_INVALID, "window must not be negative");
     if (max_seqlen < 0 || max_kv_len < 0) return fail(SSU_ERR_INVALID, "max_seqlen and max_kv_len must not be negative");
     p->scale = scale;

@@ -99,7 +99,8 @@ int device_sms() {
 AttendPlan attend_plan(const AttendParams &p, int64_t max_seqlen, int64_t max_kv_len) {
     AttendPlan a{};
     a.max_kv_len = max_kv_len;
-    const int64_t longest = p.c.cu == nullptr ? 1 : max_seqlen > 0 ? max_seqlen : (p.c.rows + p.c.nseq - 1) / p.c.nseq;
+    const int64_t given = max_seqlen < p.c.rows ? max_seqlen : p.c.rows;  // (no sequence is longer)
+    const int64_t longest = p.c.cu == nullptr ? 1 : max_seqlen > 0 ? given : (p.c.rows + p.c.nseq - 1) / p.c.nseq;
     const int64_t rows = longest * p.c.share;
     a.kind = rows <= 16 ? kAttendRows16 : rows <= 32 ? kAttendRows32 : rows <= 64 ? kAttendRows64 : kAttendTiles;
     a.bytes = a.kind == kAttendTiles ? attend_tiles_workspace(p.c, max_kv_len) : attend_rows_workspace(a.kind, p.c.D);

@@ -147,6 +147,23 @@ def test_refusals_of_attention(libssu, kw, call, code, needle):
     assert needle in libssu.ssu_last_error().decode()
 
 
+def test_scales_that_leave_fp32_in_units_of_log2(libssu):
+    assert attend(libssu, args(), scale=3e38) == ssu.ERR_INVALID  # 3e38 log2 e is infinite
+    assert "scale" in libssu.ssu_last_error().decode()
+    assert attend(libssu, args(rows=0), scale=2e38) == ssu.OK  # 2e38 log2 e is 2.89e38
+
+
+def test_a_hint_past_the_call_is_the_call(libssu):
+    # every max_seqlen of `rows` or more asks for the same workspace, those too whose rows 64 bits do not hold
+    sizes = []
+    for seqlen in (6, 7, 1 << 40, (1 << 63) - 1):
+        size = ctypes.c_uint64(0)
+        a = args(heads=256, q_stride=(16384, 64), out_stride=(16384, 64))
+        assert libssu.ssu_paged_attention_workspace_size(ctypes.byref(a), seqlen, 0, ctypes.byref(size)) == ssu.OK
+        sizes.append(size.value)
+    assert len(set(sizes)) == 1
+
+
 def test_null_and_nothing(libssu):
     assert append(libssu, None) == ssu.ERR_INVALID and attend(libssu, None) == ssu.ERR_INVALID
     for kw in (dict(rows=0), dict(nseq=0, kv_lens=None, block_table=None)):
