@@ -116,27 +116,26 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
     return v;
 }
 // Sum of the threads before this one; `total` of all.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T *red, T &total) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *red, int64_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T upto = v;
+    int64_t upto = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const T o = __shfl_up_sync(0xffffffffu, upto, off);
+        const int64_t o = __shfl_up_sync(0xffffffffu, upto, off);
         if (lane >= off) upto += o;
     }
     __syncthreads();
     if (lane == 31) red[warp] = upto;
     __syncthreads();
-    T w = lane < kPlanThreads / 32 ? red[lane] : T(0);
+    int64_t w = lane < kPlanThreads / 32 ? red[lane] : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const T o = __shfl_up_sync(0xffffffffu, w, off);
+        const int64_t o = __shfl_up_sync(0xffffffffu, w, off);
         if (lane >= off) w += o;
     }
     total = __shfl_sync(0xffffffffu, w, 31);
-    const T before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-    return upto - v + (warp > 0 ? before : T(0));
+    const int64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return upto - v + (warp > 0 ? before : 0);
 }
 // Key tiles of a pair of tiles.
 __device__ __forceinline__ void pair_tiles(const AttendParams &p, const Seq &s, int pair, int &first, int &last) {
@@ -185,7 +184,7 @@ __device__ __forceinline__ void part_of(const Cut &k, int c, int even, int i, in
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendParams p, const Plan plan, int ctas) {
     start_dependents();
     __shared__ int64_t red64[32];
-    __shared__ int red[32], bounds[kPlanThreads + 1];
+    __shared__ int bounds[kPlanThreads];
     const int tid = threadIdx.x, tt2 = 2 * tile_tokens(p.c);
     const auto pairs_of = [&](const Seq &s) { return (s.n + tt2 - 1) / tt2; };
     // The units, in the order of the sequences, the last tokens of each first.
@@ -194,9 +193,11 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
     for (int64_t b0 = 0; b0 < p.c.nseq; b0 += kPlanThreads) {
         Seq s{0, 0, 0};
         if (b0 + tid < p.c.nseq) s = load_seq(p.c, b0 + tid, true);
-        int total;
-        const int before = block_scan<int>(pairs_of(s), red, total);
-        bounds[tid] = before;
+        // (where sequences overlap there may be more units than there is room for, or than 32 bits count: those stay away)
+        int64_t wanted;
+        const int room = plan.max_units - units;
+        bounds[tid] = static_cast<int>(min(block_scan(pairs_of(s), red64, wanted), static_cast<int64_t>(room)));
+        const int total = static_cast<int>(min(wanted, static_cast<int64_t>(room)));
         __syncthreads();
         for (int i = tid; i < total; i += kPlanThreads) {
             int lo = 0, hi = kPlanThreads;  // the sequence: bounds[lo] <= i, the last such
@@ -211,10 +212,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const AttendP
             u.pair = pairs_of(q) - 1 - (i - bounds[lo]);
             u.parts = 1;
             pair_tiles(p, q, u.pair, u.first, u.last);
-            if (units + i < plan.max_units) plan.units[units + i] = u;
+            plan.units[units + i] = u;
             sum += u.last - u.first + 1;
         }
-        units = min(units + total, plan.max_units);  // (more only where sequences overlap)
+        units += total;
         __syncthreads();
     }
     sum = block_sum(sum, red64) * p.c.G;

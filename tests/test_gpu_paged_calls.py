@@ -1,6 +1,7 @@
 """The paged cache's calls where others are under way: the first call of a host
 thread, the first of a process inside a capture, two host threads on one stream,
 and the example stack with attention layers."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -10,7 +11,8 @@ import pytest
 import torch
 
 import selective_state_update_gb300 as ssu
-from paged_testlib import DEV, Batch
+from paged_testlib import DEV, Batch, attention, check
+from selective_state_update_gb300 import paged
 
 pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,6 +76,32 @@ def test_first_call_of_a_process_in_a_capture(libssu, name):
     code = CAPTURE.format(root=os.path.dirname(HERE), here=HERE, name=name)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n,kv", [(600, 900), (600, 5000), (5, 900)])
+@pytest.mark.parametrize("copies", [3, 300])
+def test_bounds_that_overlap(libssu, n, kv, copies):
+    """Bounds that go back and forth: every other sequence is the same rows again, those between them are bad.  What
+    the call would list then passes what its workspace holds; nothing behind that is touched, and the rows hold what
+    one of their sequences gives them."""
+    b = Batch([(n, kv)], heads=8, kv_heads=2, dim=64, page=48, seed=5)
+    want = attention(b)
+    nseq = 2 * copies - 1
+    table = b.table.expand(nseq, -1).contiguous()
+    kv_lens = torch.full((nseq,), kv, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, n] * copies, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = torch.empty_like(b.q), torch.empty(n, 8, device=DEV)
+    a = paged._paged_args(b.k_cache, b.v_cache, table, kv_lens, cu, n, 8, b.q, out, status)
+    size = ctypes.c_uint64(0)
+    assert libssu.ssu_paged_attention_workspace_size(a, n, 0, ctypes.byref(size)) == ssu.OK
+    ws = torch.full((size.value + 4096,), 0x5a, dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert libssu.ssu_paged_attention(a, 64 ** -0.5, 0, n, 0, lse.data_ptr(), ws.data_ptr(), size.value, stream) == ssu.OK
+    torch.cuda.synchronize()
+    assert int(status) == ssu.DEV_BAD_SEQLEN
+    assert (ws[size.value:] == 0x5a).all()
+    check(b, out, lse, want)
 
 
 @pytest.mark.parametrize("raw", [False, True])
