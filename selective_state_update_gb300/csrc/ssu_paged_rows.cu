@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
+        bool ended = false;
         for (int i = from; i < to; ++i, ++it) {
             const int st = it % LY::kStages;
             ok = mbar_wait_bounded(&full[st], (it / LY::kStages) & 1);
@@ -391,8 +392,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                 }
                 if (odd) *odd_flag = 1;
                 fence_proxy_async_smem();  // before the stage's next copy
-                if (MT == 1) __syncwarp();
-                else named_barrier(1, 32 * kWarps);
+                if (MT == 1) {
+                    __syncwarp();
+                } else if (barrier_or(1, 32 * kWarps, false)) {  // a warp whose wait gave up is at the run's end: this was it
+                    ok = false, ended = true;
+                    break;
+                }
             }
             constexpr int kSub = MT == 1 ? 1 : 2;  // 16 keys at a time, or 32
 #pragma unroll 1
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
-        ok = !barrier_or(1, 32 * kWarps, !ok);
+        if (!ended) ok = !barrier_or(1, 32 * kWarps, !ok);
         if (!ok) break;
 
         // ---------------- the warps' parts joined ----------------
