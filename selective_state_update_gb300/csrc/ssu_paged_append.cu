@@ -6,16 +6,19 @@
 // elements (j, j + rotary / 2), or (2 j, 2 j + 1) -- turned by the angle
 // a = pos inv_freq[j]:
 //     x' = x cos a - y sin a,   y' = y cos a + x sin a
-// in fp32, rounded once.  The angle is formed and brought into [-pi, pi] in 64
-// bits (positions reach millions, where fp32 angles are off by whole radians);
-// rounded to fp32 there it is off by 2^-23, and its sine and cosine by a little
-// more than their own rounding.
+// in fp32, rounded once.  The angle is formed and whole turns are taken off it in
+// 64 bits (positions reach millions, where fp32 angles are off by whole radians);
+// what is left, in half turns within [-1, 1], is rounded to fp32, by 2^-25 at most
+// (2^-23 of an angle), and its sine and cosine are off by a little more than their
+// own rounding.  (Of half turns: sincosf, with a path for large angles, made 150 us
+// of 146 below.)
 //
 // HBM-bound: q, k and v are read once and written once.  A CTA takes T rows; a
 // thread's item is 32 bytes of one head, two 16-byte pieces that hold whole
 // pairs.  The first items are asked for before the metadata, whose reads depend
 // on one another (sequence, length, page).  32768 rows of 32 + 2 x 8 heads of 128:
-// 150 us, 5.4 TB/s, 0.80 of the copy rate.
+// 146 us, 5.5 TB/s, 0.82 of the copy rate: eight rows are at work on an SM, for
+// 5.5 us each, and registers hold no more (48 or 56 a thread spill: 183, 148 us).
 #include "ssu_paged.cuh"
 
 namespace ssu {
@@ -116,10 +119,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendPara
     for (int i = tid; i < tokens * half; i += kThreads) {
         const int t = i / half, j = i - t * half;
         if (seq_of[t] < 0) continue;
-        const double angle = static_cast<double>(pos_of[t]) * static_cast<double>(__ldg(p.inv_freq + j));
-        const double turns = rint(angle * 0.15915494309189535);
+        const double turns = static_cast<double>(pos_of[t]) * static_cast<double>(__ldg(p.inv_freq + j)) * 0.15915494309189535;
         float s, co;
-        sincosf(static_cast<float>(fma(-turns, 6.283185307179586, angle)), &s, &co);
+        sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &co);
         turn_by[t][j] = make_float2(co, s);
     }
     __syncthreads();
@@ -184,7 +186,7 @@ cudaError_t launch_t(const AppendParams &p, cudaStream_t stream) {
 // (3 rows 3.3 us in a graph, 3.7 with 128 threads).  More: CTAs of 128 threads, as
 // many rows as those hold in one turn, one at least: 32768 rows of 32 + 2 x 8 heads
 // of 128 150 us with one row, 4 in two turns 168; CTAs of 256 threads and two rows
-// 156 to 164.
+// 156 to 164 (all with sincosf).
 template <bool BF>
 cudaError_t launch_b(const AppendParams &p, cudaStream_t stream) {
     constexpr int kHeld = 128 * kItems;
