@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                 for (int h = 0; h < 2; ++h) {
                     float e[4 * kSub];  // keys 8 (j / 2) + 2 (lane % 4) + j % 2 of the row
 #pragma unroll
-                    for (int j = 0; j < 4 * kSub; ++j) e[j] = x[j / 2][2 * h + j % 2] * scale;
+                    for (int j = 0; j < 4 * kSub; ++j) e[j] = __fmul_rn(x[j / 2][2 * h + j % 2], scale);  // (rounded, as the maximum is: none is above it)
                     if (masked) {
                         // (the row's position, found here: kept it would cost registers on every tile)
                         const int row = min(row0 + 8 * h + lane / 4, rows - 1);

@@ -9,7 +9,8 @@
 // and out = O / l, lse = (m + log2 l) ln 2.  m is the row's maximum when it was last
 // moved; it moves when the maximum has grown by more than 2^8, so that O, in
 // tensor memory, is rarely rescaled (P stays below 2^8, far inside both io types,
-// and l and O are fp32).  P is rounded once to the io type, as its product's operand.
+// and l and O are fp32; scores are scaled and their difference taken in one rounding,
+// in two where |m| is so large that this would not keep P there).  P is rounded once to the io type, as its product's operand.
 //
 // A plan kernel checks the metadata, lists the units and, where they are too few
 // or too uneven for the GPU, cuts their keys into parts; the main kernel's CTAs
@@ -45,6 +46,9 @@ constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 128 bytes
 constexpr int kThreads = 512;
 constexpr float kSlack = 8.f;  // log2 by which the maximum may grow before the reference moves
+// References from here on are too coarse for exponents formed in one rounding, scale s - m: the
+// reference is a rounded product, half a step of which is 2^-4 here and whole units of log2 soon.
+constexpr float kCoarse = 1048576.f;
 
 // A part of a unit's keys, as planned.
 struct Piece {
@@ -436,6 +440,22 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *u) {  // 32-byt
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
                  "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
+}
+
+// A row's scores of a key tile times `scale`, in place, each product rounded.  (A function of its
+// own, which nearly no call comes to: in the softmax's loop, never run, it made 566 us of the 552
+// that 32768 tokens in 16 prompts took without it; here 559.)
+__device__ __noinline__ void scale_scores(uint32_t at, float scale) {
+#pragma unroll 1
+    for (int c = 0; c < kKeys; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(at + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), scale));
+        tmem_st16(at + c, r);
+    }
+    tmem_wait_st();
 }
 
 // DK: the head size, rounded up to 64; BF: bf16.
@@ -952,6 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             const bool live = __any_sync(0xffffffffu, tok < toks);
             const int hi = pos + 1, lo = p.window > 0 ? pos + 1 - p.window : 0;  // it sees keys [lo, hi)
             float ref = -INFINITY, l = 0.f;
+            float factor = scale;  // exponents are factor s - ref; 1 once a row of the warp has a coarse reference
             for (int j = from; j < to; ++j, ++ns) {
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kSFull0 + x], ns & 1)))) break;
                 tc_fence_after();
@@ -985,11 +1006,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         for (int i = 0; i < 32; i += 2)
                             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[c & 1][i]), __uint_as_float(s[c & 1][i + 1]));
                     }
-                    const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
-                    const bool moves = now > ref + kSlack;
+                    const float now = __fmul_rn(fmaxf(max3(top[0], top[1], top[2]), top[3]), scale);
+                    const bool moves = now - ref > kSlack;  // (a difference: the sum would be rounded to the reference's step)
                     if (__builtin_expect(__any_sync(0xffffffffu, moves), 0)) {
                         const float back = moves ? ex2(ref - now) : 1.f;
                         if (moves) ref = now, l *= back;
+                        if (__any_sync(0xffffffffu, moves && fabsf(now) > kCoarse)) factor = 1.f;
                         if (j > from) {
                             if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kOFull0 + x], (ns - 1) & 1)))) break;
                             tc_fence_after();
@@ -1005,7 +1027,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                         }
                     }
                     const float base = ref == -INFINITY ? 0.f : ref;
-                    const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
+                    if (__builtin_expect(factor != scale, 0)) {
+                        // scaled ones, rounded as the reference was: none of a row's is above its maximum then
+                        tmem_wait_ld();
+                        scale_scores(colS, scale);
+                        tmem_ld32(colS, s[0]);
+                    }
+                    const uint64_t scale2 = pair(factor, factor), base2 = pair(-base, -base);
                     uint64_t add[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {

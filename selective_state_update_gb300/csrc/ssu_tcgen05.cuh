@@ -92,7 +92,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// 2^x by the special-function unit (relative error below 2^-22); x <= 0 here.
+// 2^x by the special-function unit (relative error below 2^-22; results below the
+// smallest normal number are zeros).
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
