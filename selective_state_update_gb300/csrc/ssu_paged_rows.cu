@@ -7,7 +7,10 @@
 //     x_j = scale log2(e) q . k_j,  m' = max(m, x_j),
 //     l' = l 2^(m - m') + sum_j 2^(x_j - m'),  o' = o 2^(m - m') + sum_j 2^(x_j - m') v_j
 // and out = o / l, lse = (m + log2 l) ln 2, all of it in fp32; P = 2^(x - m') is
-// rounded once to the io type, as the product's operand.
+// rounded once to the io type, as the product's operand.  For fp16 m is the maximum
+// less 15 (kLift), so that P goes up to 2^15 and is rounded by half a step down to 2^-29 of
+// the largest weight, and by 2^-40 of it below: without, the tokens of a long context
+// beside one that takes nearly all the weight, 2^-25 of it each, were nothing.
 //
 // Bound by HBM: a key and its value are 4 D bytes and 4 D share operations.  So
 // what counts is that every SM reads all the time, whatever the lengths: all
@@ -41,6 +44,8 @@ constexpr int kPanel = kKeys * 128;   // bytes of 64 elements of its keys
 constexpr int kWarps = 4;             // consumers
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kCtas = 2;              // per SM
+
+constexpr float kLift = 15.f;         // log2 by which fp16 weights are larger than the softmax's before its division
 
 template <int DK, int MT>
 struct Layout {
@@ -434,11 +439,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) attend_rows_kernel(const Atte
                             if (key > pos || (p.window > 0 && key <= pos - p.window)) e[j] = -INFINITY;
                         }
                     }
-                    float top = mx[h];
+                    float top = BF ? mx[h] : -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 4 * kSub; ++j) top = fmaxf(top, e[j]);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // (where fp32 has no halves left the difference might be rounded up, past fp16's range)
+                    if constexpr (!BF) top = fmaxf(mx[h], fabsf(top) < 8388608.f ? top - kLift : top);
                     const float base = top == -INFINITY ? 0.f : top, back = ex2(mx[h] - base);
                     mx[h] = top;
                     float add = 0.f;

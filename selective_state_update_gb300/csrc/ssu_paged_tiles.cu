@@ -7,8 +7,8 @@
 // with a running reference m and sum l, in units of log2:
 //     x_j = scale log2(e) q . k_j,   P_j = 2^(x_j - m),   l += sum P_j,   O += P V
 // and out = O / l, lse = (m + log2 l) ln 2.  m is the row's maximum when it was last
-// moved; it moves when the maximum has grown by more than 2^8, so that O, in
-// tensor memory, is rarely rescaled (P stays below 2^8, far inside both io types,
+// moved (fp16: less 7); it moves when P would pass 2^8 (fp16: 2^15), so that O, in
+// tensor memory, is rarely rescaled (that is inside both io types,
 // and l and O are fp32; scores are scaled and their difference taken in one rounding,
 // in two where |m| is so large that this would not keep P there).  P is rounded once to the io type, as its product's operand.
 //
@@ -45,7 +45,16 @@ constexpr int kRows = 128;     // rows of a query tile
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 128 bytes
 constexpr int kThreads = 512;
-constexpr float kSlack = 8.f;  // log2 by which the maximum may grow before the reference moves
+// The reference moves to the maximum less kLift when that is more than kMost above it.
+// For fp16 P is between 2^7 and 2^15 where it is largest, so that it is rounded by half a step down
+// to 2^-21 of the largest weight and by 2^-32 of it below, 2^21 tokens of which come to half a step
+// of the whole: with 0 and 8 as for bf16, the tokens of a long context beside one that takes nearly
+// all the weight, 2^-25 of it each, were nothing.  (With 11 and 15 O is rescaled more often: 43
+// sequences of single tokens and chunks 257 us, 246 so.)
+template <bool BF>
+constexpr float kLift = BF ? 0.f : 7.f;
+template <bool BF>
+constexpr float kMost = BF ? 8.f : 15.f;
 // References from here on are too coarse for exponents formed in one rounding, scale s - m: the
 // reference is a rounded product, half a step of which is 2^-4 here and whole units of log2 soon.
 constexpr float kCoarse = 1048576.f;
@@ -1007,10 +1016,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                             top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(s[c & 1][i]), __uint_as_float(s[c & 1][i + 1]));
                     }
                     const float now = __fmul_rn(fmaxf(max3(top[0], top[1], top[2]), top[3]), scale);
-                    const bool moves = now - ref > kSlack;  // (a difference: the sum would be rounded to the reference's step)
+                    const bool moves = now - ref > kMost<BF>;  // (a difference: the sum would be rounded to the reference's step)
                     if (__builtin_expect(__any_sync(0xffffffffu, moves), 0)) {
-                        const float back = moves ? ex2(ref - now) : 1.f;
-                        if (moves) ref = now, l *= back;
+                        const float level = fabsf(now) > kCoarse ? now : now - kLift<BF>, back = moves ? ex2(ref - level) : 1.f;
+                        if (moves) ref = level, l *= back;
                         if (__any_sync(0xffffffffu, moves && fabsf(now) > kCoarse)) factor = 1.f;
                         if (j > from) {
                             if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[kOFull0 + x], (ns - 1) & 1)))) break;

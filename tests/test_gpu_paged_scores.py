@@ -70,3 +70,48 @@ def test_one_key_far_above_the_others(libssu, form, io, size_q, size_k, scale, h
     assert not wrong.any(), (int(wrong.sum()), wrong.nonzero()[0].tolist(), out[wrong][:4].tolist(), value[wrong][:4].tolist())
     off = ((lse.double() - score).abs() / score).max()
     assert math.isfinite(float(off)) and off <= (dim + 8) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("lens,single", [([(1, 20000), (1, 3000)], True), ([(3, 20000), (3, 3000)], False), ([(9, 20000), (9, 3000)], False),
+                                         ([(40, 20000), (300, 3000)], False), ([(2000, 2600)], False)])
+@pytest.mark.parametrize("io", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", [20.0, 25.0, 27.5])
+def test_many_small_weights_beside_a_large_one(libssu, lens, single, io, gap):
+    """A sequence's first token, whose value is zero, is ahead of the others by about 2^gap.  What is left is their
+    part of the weight, right to the roundings of the weights, which for fp16 are half a step u of each and, of those
+    below 2^-21 of the largest one, 2^-32 of it (the largest is held as 2^7 or more, and below 2^-14 fp16 rounds by
+    2^-25); the other terms are those of ``paged_testlib.attention``."""
+    b = Batch(lens, 4, 2, 64, 48, io, single=single)
+    u = torch.finfo(b.io).eps / 2
+    g = torch.Generator(device=DEV).manual_seed(3)
+    b.q[:b.rows] = 0.0
+    b.q[:b.rows, :, 0] = 1.0
+    b.q[:b.rows, :, 1] = (torch.randn(b.rows, 4, generator=g, device=DEV) * 0.5).to(b.io)
+    for s, (n, kv) in enumerate(lens):
+        i = torch.arange(kv, device=DEV)
+        where = (b.table[s].long()[i // 48], i % 48)
+        k = b.tokens(b.k_cache, s).float() * 0.5
+        k[:, :, 0] = 0.0
+        k[0, :, 0], k[0, :, 1] = gap, 0.0
+        v = b.tokens(b.v_cache, s).float().abs() + 0.5
+        v[0] = 0.0
+        b.k_cache[where], b.v_cache[where] = k.to(b.io), v.to(b.io)
+    scale = math.log(2.0)
+    out, lse = call(b, scale=scale)
+    for s, (n, kv) in enumerate(lens):
+        q = b.q[b.starts[s]:b.starts[s] + n].double()
+        k, v = (b.tokens(c, s).double().repeat_interleave(2, 1) for c in (b.k_cache, b.v_cache))
+        x = scale * torch.einsum("ihd,jhd->ihj", q, k)
+        size = scale * torch.einsum("ihd,jhd->ihj", q.abs(), k.abs()).amax(-1)
+        seen = torch.arange(kv, device=DEV) <= torch.arange(kv - n, kv, device=DEV)[:, None]
+        x = x.masked_fill(~seen[:, None], -math.inf)
+        p = torch.softmax(x, -1)
+        want = torch.einsum("ihj,jhd->ihd", p, v)
+        r = 64 * 2.0 ** -24 * size + 2.0 ** -22 * (scale * gap + 1)
+        tol = (2 * u + 2 * r[..., None] + kv * 2.0 ** -24) * want + (2.0 ** -25 if io == "f16" else 0.0)
+        tol += p.amax(-1)[..., None] * 2.0 ** -32 * torch.einsum("ij,jhd->ihd", seen.double(), v)
+        got = out[b.starts[s]:b.starts[s] + n].double()
+        wrong = ~((got - want).abs() <= tol)
+        assert not wrong.any(), (s, int(wrong.sum()), got[wrong][:4].tolist(), want[wrong][:4].tolist(), tol[wrong][:4].tolist())
+        z = torch.logsumexp(x, -1)
+        assert ((lse[b.starts[s]:b.starts[s] + n].double() - z).abs() <= r + kv * 2.0 ** -24 + 2.0 ** -22 * z.abs()).all()
