@@ -56,7 +56,7 @@ class HybridStack:
         attends = [attention_every > 0 and i % attention_every == attention_every - 1 for i in range(layers)]
         self.pools = [tuple(torch.zeros(pages, page, kv_heads, head_size, device=device, dtype=torch.bfloat16) for _ in range(2)) if a
                       else torch.zeros(slots, heads, head_size, head_size, device=device) for a in attends]
-        self.page, self.free = page, list(range(pages))
+        self.page, self.free = page, list(range(pages)) if any(attends) else None  # (None: no layer has pages)
         self.inv_freq = 10000.0 ** -(torch.arange(0, head_size, 2, device=device) / head_size)
         self.held = {}  # slot -> its pages and its number of tokens
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
@@ -79,17 +79,25 @@ class HybridStack:
         x, _, _ = ssu.ssu_add_rmsnorm(delta, self.norms[-1], residual=stream, residual_out=stream)
         return x @ self.unembed.t()
 
-    def _grow(self, slots, new):
-        """Room for ``new`` more tokens in each slot's pages: (block table, lengths with them)."""
-        for slot, n in zip(slots, new):
-            pages, length = self.held.setdefault(slot, ([], 0))
-            while len(pages) * self.page < length + n:
-                pages.append(self.free.pop())
-            self.held[slot] = pages, length + n
-        rows = [self.held[slot][0] for slot in slots]
-        wide = max(len(r) for r in rows)
-        table = torch.tensor([r + [PAD] * (wide - len(r)) for r in rows], dtype=torch.int32, device=self.embed.device)
-        return table, torch.tensor([self.held[slot][1] for slot in slots], dtype=torch.int32, device=self.embed.device)
+    def _grow(self, slots, new, fresh=False):
+        """Room for ``new`` more tokens in each slot's pages, all of them where it is ``fresh``: (block table, lengths
+        with them).  Padding has neither."""
+        if self.free is None:
+            return None, None
+        slots = slots.tolist()
+        held = {s: ([], 0) if fresh else self.held.get(s, ([], 0)) for s in slots if s != PAD}
+        free = self.free + [p for s in held if fresh for p in self.held.get(s, ([], 0))[0]]
+        more = {s: (held[s][1] + n + self.page - 1) // self.page - len(held[s][0]) for s, n in zip(slots, new) if s != PAD}
+        if sum(more.values()) > len(free):
+            raise RuntimeError(f"{sum(more.values())} more pages are needed and {len(free)} are free")
+        for s, n in zip(slots, new):
+            if s != PAD:
+                self.held[s] = held[s][0] + [free.pop() for _ in range(more[s])], held[s][1] + n
+        self.free = free
+        rows = [self.held[s] if s != PAD else ([], 0) for s in slots]
+        wide = max((len(pages) for pages, _ in rows), default=0)
+        table = torch.tensor([pages + [PAD] * (wide - len(pages)) for pages, _ in rows], dtype=torch.int32, device=self.embed.device)
+        return table.view(len(rows), wide), torch.tensor([n for _, n in rows], dtype=torch.int32, device=self.embed.device)
 
     def _attend(self, cache, q, k, v, table, lengths, **kw):
         q = ssu.ssu_paged_append(*cache, k, v, table, lengths, q=q, inv_freq=self.inv_freq, cu_seqlens=kw.get("cu_seqlens"),
@@ -100,9 +108,7 @@ class HybridStack:
         """New prompts, packed: their states go to ``slots``."""
         cu = torch.tensor([0, *lengths], device=tokens.device).cumsum(0).int()
         fresh = torch.full_like(slots, PAD)  # every prompt starts from a zero state
-        for slot in slots.tolist():  # ... and with no pages
-            self.free += self.held.pop(slot, ([], 0))[0]
-        table, kv_lens = self._grow(slots.tolist(), lengths)
+        table, kv_lens = self._grow(slots, lengths, fresh=True)  # ... and with no pages
 
         def mix(pool, q, k, v):
             if isinstance(pool, tuple):
@@ -115,7 +121,7 @@ class HybridStack:
 
     def step(self, tokens, slots):
         """One token for the sequence in each slot."""
-        table, kv_lens = self._grow(slots.tolist(), [1] * len(slots))
+        table, kv_lens = self._grow(slots, [1] * len(slots))
 
         def mix(pool, q, k, v):
             if isinstance(pool, tuple):
