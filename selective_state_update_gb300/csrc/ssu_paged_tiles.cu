@@ -641,9 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
             const Desc dQ(desc_k_sw128(s0)), dK(desc_k_sw128(s0 + LY::kBuf)), dV(desc_mn_sw128(s0 + LY::kBuf, kPanel));
             constexpr auto along_k = [](int k) { return static_cast<uint32_t>(((k / 4) * kPanel + (k % 4) * 32) >> 4); };
             constexpr auto along_mn = [](int k) { return static_cast<uint32_t>((k * 2048) >> 4); };
-            // A wait that gives up only notes it: products of what is not there
-            // yet stay within shared and tensor memory, and the loop ends with
-            // this key tile.
+            // A wait that gives up only notes it, by lane: products of what is not
+            // there yet stay within shared and tensor memory.  The lanes agree on it
+            // once a key tile, ahead of every branch that it decides, and the loop
+            // ends with that tile.
             const auto wait = [&](uint64_t *bar, int phase) {
                 if (!mbar_try_wait(bar, phase & 1)) ok = wait_on(bar, phase & 1) && ok;
             };
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 // both tiles in the middle of their keys: nothing to decide
                 if (some && j > max(w.from0, w.from1)) {
                     const int end = min(w.to0, w.to1) - 2;
-                    for (; j < end && ok; ++j) {
+                    for (; j < end && (ok = __all_sync(0xffffffffu, ok)); ++j) {
                         wait(&clean[vbuf], vturn);
                         wait(&bars[kPFull0], np0++);
                         outputs(A, 1, false);
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
                 int jn = j + 1;
                 n = w;
                 if (!some || jn >= w.last) {
-                    if (!(ok = next_span(n) && ok)) break;
+                    if (!(ok = __all_sync(0xffffffffu, next_span(n) && ok))) break;
                     jn = n.first;
                 }
                 const bool more = n.last > n.first;
