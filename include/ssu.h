@@ -662,7 +662,8 @@ ssu_status ssu_paged_append(const ssu_paged_args *args, const void *k, const int
  * and lse -inf.  Scores, maxima and sums are fp32; e^(score - maximum) is rounded
  * once to the io type where it meets v, which costs out as much as one more
  * rounding of v (fp16: for weights of 2^-21 of the largest or more; smaller ones are
- * off by 2^-32 of that at most).  scale is positive, at most 2e38; a score that leaves fp32's range, in units of
+ * off by 2^-32 of that at most); the products' sums are the tensor cores' own, off by kv_len 2^-25
+ * of sum |weight v| at most.  scale is positive, at most 2e38; a score that leaves fp32's range, in units of
  * log2 (1.44 times itself), is an infinity.  An infinity or a NaN in a key or a value
  * reaches the tokens that see it and no other.
  *

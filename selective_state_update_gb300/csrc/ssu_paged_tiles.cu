@@ -346,8 +346,9 @@ __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.
 
 // A wait, bounded like every other, of warps that mostly wait: asleep for up to
 // 20 us at a time unless the phase completes.  (Polling, 32768 tokens in 16 prompts
-// took 570 us where they take 552.)
-__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity) {
+// took 570 us where they take 552.)  Some wait for as long as a piece takes: `limit` is
+// the call's (waits_of).
+__device__ __forceinline__ bool sleep_on(uint64_t *bar, uint32_t parity, long long limit) {
     const long long t0 = clock64();
     for (uint32_t i = 0; i < (1u << 26); ++i) {
         uint32_t done;
@@ -359,9 +360,16 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity) {
             : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
             : "memory");
         if (done) return true;
-        if (clock64() - t0 > kWaitCycles) break;
+        if (clock64() - t0 > limit) break;
     }
     return false;
+}
+// Cycles after which a wait gives up: what is enough for a copy or a product, and five times what
+// the key tiles of the longest sequence that the table has room for take one CTA, as they may be
+// one piece's.  (Waits that start anew while tiles are copied need no length: 592 us of those prompts' 560.)
+long long waits_of(const PagedParams &p) {
+    const int64_t room = p.table_width < kPagedMaxLen / p.page ? p.table_width * p.page : kPagedMaxLen;
+    return kWaitCycles + room / kKeys * 16384;
 }
 
 // A number that is known when this is compiled.
@@ -470,7 +478,7 @@ __device__ __noinline__ void scale_scores(uint32_t at, float scale) {
 // DK: the head size, rounded up to 64; BF: bf16.
 template <int DK, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendParams p, const __grid_constant__ Maps maps, const Plan plan,
-                                                                   int box, int flags) {
+                                                                   int box, int flags, long long limit) {
     using LY = Layout<DK>;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + LY::kBars);
@@ -482,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendP
     // by piece of work and warp: were there values that are no numbers?
     volatile unsigned char *const odd = smem + LY::kMisc + 12;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto wait_on = [&](uint64_t *bar, uint32_t parity) { return sleep_on(bar, parity, limit); };
     if (warp == 8) tmem_alloc512(tmem_at);
     if (tid == 0) {
         *abort_flag = 0;
@@ -1202,7 +1211,7 @@ cudaError_t launch_t(const AttendParams &p, int64_t max_kv_len, void *workspace,
     attend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, plan, sms);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_after(attend_tiles_kernel<DK, BF>, dim3(sms), kThreads, Layout<DK>::kBytes, stream, p, maps, plan, least_box(p.c, kKeys),
-                     wide ? kWideOut : 0);
+                     wide ? kWideOut : 0, waits_of(p.c));
     if (e != cudaSuccess || s.slots == 0) return e;
     return launch_after(attend_tiles_join_kernel<DK, BF>, dim3(8 * sms), 128, 0, stream, p, plan);
 }
