@@ -672,7 +672,9 @@ ssu_status ssu_paged_append(const ssu_paged_args *args, const void *k, const int
  * never the result's validity.  `workspace` is caller-owned device memory of at
  * least ssu_paged_attention_workspace_size() bytes for the same arguments,
  * 256-byte aligned; its contents need no initialisation, and two calls that may
- * run at once need one each.
+ * run at once need one each.  It grows with the parts that chunks may be cut into, which
+ * max_kv_len, or the room of the block table, bounds: 0.5 MB a part of four heads of 128,
+ * 137 MB and 48 bytes a row and 96 a sequence at most.
  */
 ssu_status ssu_paged_attention_workspace_size(const ssu_paged_args *args, int64_t max_seqlen, int64_t max_kv_len,
                                               uint64_t *bytes);

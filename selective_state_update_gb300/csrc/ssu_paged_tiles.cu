@@ -364,13 +364,12 @@ __device__ __forceinline__ bool sleep_on(uint64_t *bar, uint32_t parity, long lo
     }
     return false;
 }
+// The longest sequence that the block table has room for.
+int64_t room_of(const PagedParams &p) { return p.table_width < kPagedMaxLen / p.page ? p.table_width * p.page : kPagedMaxLen; }
 // Cycles after which a wait gives up: what is enough for a copy or a product, and five times what
 // the key tiles of the longest sequence that the table has room for take one CTA, as they may be
 // one piece's.  (Waits that start anew while tiles are copied need no length: 592 us of those prompts' 560.)
-long long waits_of(const PagedParams &p) {
-    const int64_t room = p.table_width < kPagedMaxLen / p.page ? p.table_width * p.page : kPagedMaxLen;
-    return kWaitCycles + room / kKeys * 16384;
-}
+long long waits_of(const PagedParams &p) { return kWaitCycles + room_of(p) / kKeys * 16384; }
 
 // A number that is known when this is compiled.
 template <int N>
@@ -1175,7 +1174,10 @@ Split split_of(const PagedParams &c, int64_t max_kv_len) {
     Split s{};
     const int64_t pair = 2 * (kRows / c.share);
     s.units = c.rows / pair + c.nseq;  // >= sum of ceil(n / pair)
-    const int64_t few = kMaxParts * s.units;
+    // cut_of makes no parts of less than four key tiles but one, and no more of a unit than its longest
+    // sequence has room for (a hint that is too small leaves units whole)
+    const int64_t room = room_of(c), longest = max_kv_len > 0 && max_kv_len < room ? max_kv_len : room;
+    const int64_t each = ((longest + kKeys - 1) / kKeys + 3) / 4 + 1, few = (each < kMaxParts ? each : kMaxParts) * s.units;
     // (a few key tiles are not worth cutting: 3 us for the joining kernel, a part's own cost)
     s.slots = max_kv_len > 0 && max_kv_len <= 8 * kKeys ? 0 : kSlots / c.G < few ? kSlots / c.G : few;
     const uint64_t dk = c.D <= 64 ? 64 : 128;
