@@ -26,12 +26,12 @@
 // (mma.sync 16 x 8 x 16: the products are far from the bound, and at most half of
 // a 128-row tcgen05 tile would be used).
 //
-// What it takes: 256 sequences of 500 to 4000, 32 / 8 heads of 128 bf16, 385 to 400 us,
-// 6.0 to 6.2 TB/s, 0.90 to 0.93 of the copy rate; two of 130000 and less, 16 / 2 heads,
-// 50 us for 27; 32 of 5 drafts, 20 / 4 heads of 96, 50 us for 24.  A CTA takes 1750
-// cycles a key tile (2000 with 32 rows), a warp's chain of products and powers, which
-// is less than its share of the memory rate for 128 elements and more for 96; a
-// call starts with 6 us until the first product.
+// What it takes, in a graph: 256 sequences of 500 to 4000, 32 / 8 heads of 128 bf16, 392 us,
+// 6.1 TB/s, 0.92 of the copy rate; two of 130000 and less, 16 / 2 heads, 50 us for 27; 32
+// of 5 drafts, 20 / 4 heads of 96, 50 us for 24 (launched one by one 397, 54 and 54 to 57).  The
+// first is 1.6 us a key tile and CTA, the memory's rate; the other two have 18 and 21 of
+// them, and beside those a part that every call has: 6 us until the first product, the
+// runs' ends, the join (7 to 17 us by itself with cold caches).
 #include "ssu_paged.cuh"
 #include "ssu_tcgen05.cuh"
 
@@ -644,7 +644,9 @@ __global__ void __launch_bounds__(32 * kJoinRows * kJoinSlices) attend_join_kern
 }
 
 int rows_grid() {
-    constexpr int kSms = 152;  // not the device's count: the workspace's size and the launch have to agree on it
+    // not the device's count: the workspace's size and the launch have to agree on it (with fewer SMs
+    // some take a second CTA's share)
+    constexpr int kSms = 152;
     return kCtas * kSms;
 }
 

@@ -25,9 +25,9 @@
 //   10-11     look through the values of partly visible tiles (below);
 //   12-15     store the outputs.
 //
-// What it takes: 32768 tokens in 16 prompts, 32 / 8 heads of 128 bf16, 550 us, 1280
-// TFLOP/s, 0.66 of the measured product rate; 2432 tokens behind 65536, 16 / 4 heads,
-// 750 us, 1770 TFLOP/s, the measured sustained rate.  A key tile takes 2800 cycles
+// What it takes: 32768 tokens in 16 prompts, 32 / 8 heads of 128 bf16, 562 us in a graph, 1250
+// TFLOP/s, 0.65 of the measured product rate (571 us launched one by one); 2432 tokens
+// behind 65536, 16 / 4 heads, 751 us, 1770 TFLOP/s, the measured sustained rate.  A key tile takes 2800 cycles
 // for both row tiles, of which the products alone would be 2048: S reads both its
 // operands from shared memory at the pipe's whole rate while copies are written, and
 // a tile's chain -- scores, 1450 cycles of softmax, P V and the next scores -- is as
